@@ -5,11 +5,13 @@ library.  The library is built in-tree by :func:`build` (nvcc, sm_103a) and
 loaded with ctypes; if it is missing, every entry point raises -- there is no
 CPU fallback.  PyTorch is used for device memory and the current stream.
 
-The C ABI is declared in ``include/mk.h`` (step) and ``include/mk_debug.h``
-(host-side planning, simulation and inspection).
+The C ABI is declared in ``include/mk.h`` (step), ``include/mk_chunk.h`` (chunks of new
+tokens over the paged cache) and ``include/mk_debug.h`` (host-side planning, simulation
+and inspection).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -136,7 +138,8 @@ EXPORTS = ("mk_create", "mk_decode_step", "mk_decode_step_greedy", "mk_get_statu
            "mk_plan_attention", "mk_simulate", "mk_debug_read", "mk_debug_inject_stall", "mk_num_ctas",
            "mk_debug_trace", "mk_debug_trace_read", "mk_paged_attention_noalloc", "mk_kv_pool_create",
            "mk_kv_pool_destroy", "mk_kv_admit", "mk_kv_reserve", "mk_kv_evict", "mk_kv_fill", "mk_kv_free_pages",
-           "mk_kv_len", "mk_graph_create", "mk_graph_launch", "mk_graph_destroy")
+           "mk_kv_len", "mk_graph_create", "mk_graph_launch", "mk_graph_destroy", "mk_rope_frequencies",
+           "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache")
 
 _lib = None
 _lock = threading.Lock()
@@ -178,6 +181,12 @@ def lib():
             L.mk_graph_launch.argtypes = [vp, vp, vp]
             L.mk_graph_destroy.argtypes = [vp]
             L.mk_graph_destroy.restype = None
+            f64, i64, sz = ctypes.c_double, ctypes.c_int64, ctypes.c_size_t
+            L.mk_rope_frequencies.argtypes = [i32, f64, f64, i32, f64, f64, vp]
+            L.mk_append_chunk.argtypes = [vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp]
+            L.mk_chunk_attention_workspace.argtypes = [vp, i32, vp, vp, ctypes.POINTER(sz)]
+            L.mk_chunk_attention.argtypes = [vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+            L.mk_read_cache.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
             L.mk_debug_trace.argtypes = [vp, i32, i32]
             L.mk_debug_trace_read.argtypes = [vp, vp, ctypes.c_size_t]
             _lib = L
@@ -287,6 +296,184 @@ class KvPool:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- chunks of new tokens over the paged cache
+class CacheShape(ctypes.Structure):
+    """One layer's heads and pages (``mk_cache_shape``); see :func:`cache_shape` for a model's."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "page_size", "num_pages",
+                                               "max_pages_per_seq", "flags")]
+
+
+def cache_shape(model: dict, page_size: int, num_pages: int, max_pages_per_seq: int, flags: int = 0) -> CacheShape:
+    return CacheShape(model["n_q"], model["n_kv"], model["head_dim"], page_size, num_pages, max_pages_per_seq, flags)
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_float)]
+
+
+class Rope:
+    """Rotary positions of :func:`append_chunk`: ``inv_freq`` radians per position of each pair of
+    the head's first ``2 * len(inv_freq)`` dims (float64, see :func:`rope_frequencies`); pair i is
+    dims (i, i + n) of the n pairs, or (2i, 2i + 1) with ``interleaved``."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, mscale: float = 1.0):
+        self.inv_freq = np.array(inv_freq, dtype=np.float64).reshape(-1)
+        self.struct = _RopeStruct(2 * self.inv_freq.size, int(interleaved), self.inv_freq.ctypes.data, float(mscale))
+
+
+def rope_frequencies(rotary_dim: int, theta: float, factor: float = 1.0, original_len: int = 0,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0) -> np.ndarray:
+    """``theta**(-2i/rotary_dim)``, scaled for contexts ``factor`` times longer (``mk_rope_frequencies``)."""
+    out = np.empty(max(int(rotary_dim), 0) // 2, dtype=np.float64)
+    _check(lib().mk_rope_frequencies(int(rotary_dim), float(theta), float(factor), int(original_len), float(beta_fast),
+                                     float(beta_slow), out.ctypes.data if out.size else None))
+    return out
+
+
+def _need(ok, what):
+    if not ok:
+        raise MkError(MK_ERR_INVALID_ARG, what)
+
+
+def _chunk_args(shape, chunk_lens, seq_lens, block_tables, kv_layer):
+    """(chunk_lens, seq_lens as host int32, rows) after checks of what the C call cannot see."""
+    import torch
+    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
+    _need(cl.ndim == 1 and cl.shape == sl.shape, "chunk_lens and seq_lens: one length per sequence each")
+    rows = sum(cl.tolist())
+    _need(0 <= rows < 1 << 24, "chunk_lens: fewer than 2^24 rows")
+    _need(block_tables.is_cuda and block_tables.dtype is torch.int32 and block_tables.is_contiguous(),
+          "block_tables: contiguous int32 CUDA tensor")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] >= cl.size
+          and block_tables.shape[1] == shape.max_pages_per_seq, "block_tables: [num_seqs, max_pages_per_seq]")
+    q8 = shape.flags & FLAG_KV_Q8
+    n = shape.num_pages * 2 * shape.num_kv_heads * shape.page_size * shape.head_dim
+    _need(kv_layer.is_cuda and kv_layer.is_contiguous() and kv_layer.dtype is (torch.uint8 if q8 else torch.bfloat16)
+          and kv_layer.numel() == (n + n // 16 if q8 else n),
+          "kv_layer: one layer of the shape's cache, contiguous CUDA tensor, bf16 (q8_0: uint8 codes, then f16 scales)")
+    _need(block_tables.device == kv_layer.device, "block_tables and kv_layer are on different devices")
+    return cl, sl, rows
+
+
+def _rows_arg(t, rows, heads, dim, device, what):
+    """The row stride of t, bf16 rows of heads*dim contiguous values as [rows, heads*dim] or [rows, heads, dim]."""
+    import torch
+    shape, stride = t.shape, t.stride()
+    _need(t.is_cuda and t.device == device and t.dtype is torch.bfloat16 and shape[0] >= rows
+          and (shape[1:] == (heads * dim,) and stride[1] == 1
+               or shape[1:] == (heads, dim) and stride[2] == 1 and (stride[1] == dim or heads == 1)),
+          f"{what}: bf16 CUDA rows of {heads} heads of {dim} contiguous values, at least {rows} rows")
+    return stride[0] if shape[0] > 1 else heads * dim
+
+
+def _out_arg(t, shape, device, what):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _need(t.is_cuda and t.device == device and t.dtype is torch.bfloat16 and t.is_contiguous()
+          and t.shape[1:] == shape[1:] and t.shape[0] >= shape[0],
+          f"{what}: contiguous bf16 CUDA tensor of at least {list(shape)}")
+    return t
+
+
+def _status_arg(t, device):
+    import torch
+    if t is not None:
+        _need(t.is_cuda and t.device == device and t.dtype is torch.int32 and t.numel() == 1,
+              "status: int32 CUDA tensor of one value")
+    return _ptr(t)
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Makes ``device`` and ``stream`` (default: torch's current one of the device) current, so that new
+    outputs and workspaces belong to the stream that writes them; yields the stream as a C argument."""
+    import torch
+    if stream is None:
+        with torch.cuda.device(device):
+            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    else:
+        _need(stream.device == device, "stream is on another device than the tensors")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, rope: Rope | None = None,
+                 q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, status=None, stream=None):
+    """Take the fused QKV rows of new tokens into the cache (``mk_append_chunk``).
+
+    qkv: bf16 CUDA [rows, (Hq + 2*Hkv)*D] (rows may be strided); chunk_lens / seq_lens: host int32
+    [num_seqs], new tokens and length including them; block_tables: int32 CUDA [num_seqs,
+    max_pages_per_seq]; kv_layer: the layer's cache, written; rope: rotation or None; q_norm /
+    k_norm: bf16 CUDA [D] gains or None; status: int32 CUDA [1] or None; stream: default torch's
+    current one.  Returns the query rows, bf16 [rows, Hq, D] (``q_out`` or a new tensor).
+    """
+    import torch
+    cl, sl, rows = _chunk_args(shape, chunk_lens, seq_lens, block_tables, kv_layer)
+    dev, Hq, D = kv_layer.device, shape.num_q_heads, shape.head_dim
+    stride = _rows_arg(qkv, rows, Hq + 2 * shape.num_kv_heads, D, dev, "qkv")
+    for t in (q_norm, k_norm):
+        _need(t is None or (t.is_cuda and t.device == dev and t.dtype is torch.bfloat16 and t.is_contiguous()
+                            and t.numel() == D), "q_norm / k_norm: contiguous bf16 CUDA [head_dim]")
+    with _on(dev, stream) as st:
+        q_out = _out_arg(q_out, (rows, Hq, D), dev, "q_out")
+        _check(lib().mk_append_chunk(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, _ptr(block_tables),
+                                     _ptr(qkv), stride, None if rope is None else ctypes.byref(rope.struct),
+                                     _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out), _ptr(kv_layer),
+                                     _status_arg(status, dev), st))
+    return q_out
+
+
+def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
+    """Bytes of workspace :func:`chunk_attention` needs for these lengths (0: none)."""
+    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
+    _need(cl.ndim == 1 and cl.shape == sl.shape, "chunk_lens and seq_lens: one length per sequence each")
+    n = ctypes.c_size_t()
+    _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
+                                              ctypes.byref(n)))
+    return n.value
+
+
+def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv_layer, out=None, workspace=None,
+                    status=None, stream=None):
+    """Causal attention of the new tokens' query rows over their sequences' cached positions
+    (``mk_chunk_attention``; arguments as :func:`append_chunk`).  q: bf16 CUDA [rows, Hq, D] (rows
+    may be strided); workspace: CUDA tensor of at least :func:`chunk_attention_workspace` bytes, or
+    None to take it from torch's allocator.  Returns bf16 [rows, Hq, D]."""
+    import torch
+    cl, sl, rows = _chunk_args(shape, chunk_lens, seq_lens, block_tables, kv_layer)
+    dev, Hq, D = kv_layer.device, shape.num_q_heads, shape.head_dim
+    stride = _rows_arg(q, rows, Hq, D, dev, "q")
+    with _on(dev, stream) as st:
+        out = _out_arg(out, (rows, Hq, D), dev, "out")
+        if workspace is None:
+            need = chunk_attention_workspace(shape, cl, sl)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace.is_cuda and workspace.device == dev and workspace.is_contiguous(),
+                  "workspace: contiguous CUDA tensor")
+        _check(lib().mk_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
+                                        _ptr(block_tables), _ptr(q), stride, _ptr(kv_layer), _ptr(out),
+                                        _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                                        _status_arg(status, dev), st))
+    return out
+
+
+def read_cache(shape: CacheShape, counts, seq_lens, block_tables, kv_layer, k_out=None, v_out=None, status=None,
+               stream=None):
+    """The last ``counts[s]`` cached positions of every sequence as packed bf16 rows
+    (``mk_read_cache``).  Returns (k, v), each [rows, Hkv, D]."""
+    cl, sl, rows = _chunk_args(shape, counts, seq_lens, block_tables, kv_layer)
+    dev, size = kv_layer.device, (rows, shape.num_kv_heads, shape.head_dim)
+    with _on(dev, stream) as st:
+        k_out, v_out = _out_arg(k_out, size, dev, "k_out"), _out_arg(v_out, size, dev, "v_out")
+        _check(lib().mk_read_cache(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, _ptr(block_tables),
+                                   _ptr(kv_layer), _ptr(k_out), _ptr(v_out), _status_arg(status, dev), st))
+    return k_out, v_out
 
 
 # ---------------------------------------------------------------- the engine

@@ -1,0 +1,144 @@
+"""Host tests of the chunk operators (include/mk_chunk.h): what they refuse before anything is
+launched, and the rotary frequencies.  No GPU needed."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import persistent_moe_decode_megakernel_gb300 as mk
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    mk.build()
+
+
+def i32(*v):
+    return np.array(v, dtype=np.int32)
+
+
+def shape(**over):
+    s = mk.CacheShape(8, 2, 128, 16, 32, 8, 0)
+    for k, v in over.items():
+        setattr(s, k, v)
+    return s
+
+
+PTR = 1 << 20    # an aligned address that no refused call reads
+
+
+def append(sh, cl=(3,), sl=(5,), n=None, rope=None, eps=1e-6, stride=None, qkv=PTR, kv=PTR, bt=PTR, q_out=PTR, qn=None,
+           status=None):
+    cl, sl = i32(*cl), i32(*sl)
+    stride = (sh.num_q_heads + 2 * sh.num_kv_heads) * sh.head_dim if stride is None else stride
+    return mk.lib().mk_append_chunk(ctypes.byref(sh), len(cl) if n is None else n, cl.ctypes.data, sl.ctypes.data, bt, qkv,
+                                    stride, None if rope is None else ctypes.byref(rope.struct), qn, None, eps, q_out, kv,
+                                    status, None)
+
+
+def attend(sh, cl=(3,), sl=(5,), n=None, stride=None, q=PTR, kv=PTR, bt=PTR, out=PTR, ws=None, ws_bytes=0, status=None):
+    cl, sl = i32(*cl), i32(*sl)
+    stride = sh.num_q_heads * sh.head_dim if stride is None else stride
+    return mk.lib().mk_chunk_attention(ctypes.byref(sh), len(cl) if n is None else n, cl.ctypes.data, sl.ctypes.data, bt, q,
+                                       stride, kv, out, ws, ws_bytes, status, None)
+
+
+def read(sh, cl=(3,), sl=(5,), n=None, kv=PTR, bt=PTR, k=PTR, v=PTR, status=None):
+    cl, sl = i32(*cl), i32(*sl)
+    return mk.lib().mk_read_cache(ctypes.byref(sh), len(cl) if n is None else n, cl.ctypes.data, sl.ctypes.data, bt, kv, k, v,
+                                  status, None)
+
+
+BAD, NO = mk.MK_ERR_INVALID_ARG, mk.MK_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", [append, attend, read])
+@pytest.mark.parametrize("over,code", [
+    (dict(num_q_heads=0), BAD), (dict(num_kv_heads=-1), BAD), (dict(num_kv_heads=3), BAD), (dict(page_size=0), BAD),
+    (dict(num_pages=0), BAD), (dict(max_pages_per_seq=0), BAD), (dict(flags=1), BAD), (dict(flags=4), BAD),
+    (dict(head_dim=96), NO), (dict(num_q_heads=18), NO), (dict(page_size=12), NO), (dict(flags=2, head_dim=64), NO),
+    (dict(num_q_heads=2048, num_kv_heads=2048), NO), (dict(page_size=1 << 28, max_pages_per_seq=8), NO),
+    (dict(num_pages=1 << 30), NO)])
+def test_refuses_shapes(call, over, code):
+    assert call(shape(**over)) == code
+    assert mk.lib().mk_last_error().decode() != ""
+
+
+@pytest.mark.parametrize("call", [append, attend, read])
+@pytest.mark.parametrize("cl,sl,n,code", [
+    ((-1,), (5,), None, BAD), ((6,), (5,), None, BAD), ((1,), (129,), None, BAD), ((3,), (5,), 0, BAD),
+    ((1,) * 65, (1,) * 65, None, BAD), ((1, 2, 9), (1, 2, 8), None, BAD)])
+def test_refuses_lengths(call, cl, sl, n, code):
+    assert call(shape(), cl, sl, n) == code
+
+
+def test_refuses_too_many_rows():
+    sh = shape(max_pages_per_seq=1 << 26)
+    for call in (append, attend, read):
+        assert call(sh, (1 << 24,), (1 << 24,)) == NO
+    assert attend(shape(num_q_heads=1024, num_kv_heads=128, max_pages_per_seq=1 << 20), (1 << 21,), (1 << 21,)) == NO
+
+
+def test_refuses_pointers_and_strides():
+    sh = shape()
+    for k in ("qkv", "kv", "q_out"):
+        assert append(sh, **{k: None}) == BAD and append(sh, **{k: PTR + 8}) == BAD
+    assert append(sh, bt=None) == BAD and append(sh, bt=PTR + 2) == BAD and append(sh, qn=PTR + 4) == BAD
+    assert append(sh, stride=12 * 128 - 8) == BAD and append(sh, stride=12 * 128 + 4) == BAD
+    for k in ("q", "kv", "out"):
+        assert attend(sh, **{k: None}) == BAD and attend(sh, **{k: PTR + 8}) == BAD
+    assert attend(sh, bt=None) == BAD and attend(sh, stride=8 * 128 - 8) == BAD and attend(sh, stride=8 * 128 + 2) == BAD
+    assert attend(sh, ws=PTR + 4) == BAD
+    for k in ("kv", "k", "v"):
+        assert read(sh, **{k: None}) == BAD and read(sh, **{k: PTR + 8}) == BAD
+    for call in (append, attend, read):
+        assert call(sh, status=PTR + 1) == BAD
+    assert mk.lib().mk_append_chunk(None, 1, None, None, None, None, 0, None, None, None, 0.0, None, None, None, None) == BAD
+
+
+@pytest.mark.parametrize("eps", [-1.0, math.nan, math.inf])
+def test_refuses_eps(eps):
+    assert append(shape(), eps=eps) == BAD
+
+
+def test_refuses_rotations():
+    def rope(n, **over):
+        r = mk.Rope(np.ones(n))
+        for k, v in over.items():
+            setattr(r.struct, k, v)
+        return r
+    for r in (rope(4), rope(72), rope(8, rotary_dim=-16), rope(8, interleaved=2), rope(8, mscale=math.nan),
+              rope(8, inv_freq=None), mk.Rope([1.0] * 7 + [math.inf])):
+        assert append(shape(), rope=r) == BAD
+
+
+def test_no_rows_is_no_work():
+    # nothing is launched, so no device is needed and pointers may be NULL
+    for call in (append, attend, read):
+        assert call(shape(), (0, 0), (5, 0)) == mk.MK_OK
+    assert attend(shape(), (0,), (0,), q=None, kv=None, bt=None, out=None) == mk.MK_OK
+    assert mk.chunk_attention_workspace(shape(), [0], [0]) == 0
+
+
+def test_rope_frequencies():
+    f = mk.rope_frequencies(128, 1e4)
+    assert np.allclose(f, 1e4 ** (-2.0 * np.arange(64) / 128), rtol=1e-15)
+    assert np.allclose(mk.rope_frequencies(128, 1e4, factor=4), f / 4, rtol=1e-15)
+    # by parts: fast pairs kept, slow ones divided, a falling ramp of the kept share between
+    g = mk.rope_frequencies(128, 1e4, factor=8, original_len=4096)
+    turns = 4096 * f / (2 * math.pi)
+    assert np.array_equal(g[turns > 33], f[turns > 33]) or np.allclose(g[turns > 40], f[turns > 40], rtol=1e-15)
+    assert np.allclose(g[turns < 0.8], f[turns < 0.8] / 8, rtol=1e-12)
+    share = (g / f - 1 / 8) / (1 - 1 / 8)
+    assert np.all(np.diff(share) <= 1e-12) and share.min() >= -1e-12 and share.max() <= 1 + 1e-12
+    lo = math.floor(128 * math.log(4096 / (32 * 2 * math.pi)) / (2 * math.log(1e4)))
+    hi = math.ceil(128 * math.log(4096 / (1 * 2 * math.pi)) / (2 * math.log(1e4)))
+    assert np.allclose(share, 1 - np.clip((np.arange(64) - lo) / (hi - lo), 0, 1), atol=1e-12)
+    for bad in ((127, 1e4), (0, 1e4), (128, 1.0), (128, math.inf)):
+        with pytest.raises(mk.MkError):
+            mk.rope_frequencies(*bad)
+    for bad in (dict(factor=0.5), dict(factor=math.nan), dict(original_len=-1), dict(original_len=9, beta_fast=1.0),
+                dict(original_len=9, beta_slow=0.0)):
+        with pytest.raises(mk.MkError):
+            mk.rope_frequencies(128, 1e4, **bad)

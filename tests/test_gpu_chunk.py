@@ -1,0 +1,420 @@
+"""GPU tests of the operators on chunks of new tokens over the paged cache (include/mk_chunk.h):
+append (norms, rotary positions, the bf16 and q8_0 write), causal attention, read-back, each
+against its definition in 64 bits (tests/chunk_ref.py), and a run of them together with the
+decode step.  Pages that no sequence owns and positions behind a last one hold NaNs throughout."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+import persistent_moe_decode_megakernel_gb300 as mk
+from tests import chunk_ref as R
+
+pytestmark = pytest.mark.gpu
+
+H = 2.0 ** -8    # a bf16 rounding is off by at most this much of the value
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    mk.build()
+
+
+def bits(t):
+    return t.view(torch.uint8) if t.dtype == torch.uint8 else t.view(torch.int16)
+
+
+# ---------------------------------------------------------------- append
+def append_case(st, rot, inter, norm, theta=1e4, mscale=1.0, seed=1, extra_rows=0, stride_pad=0, freq=None):
+    width = (st.hq + 2 * st.hkv) * st.d
+    buf = st.normal(st.rows + extra_rows, width + stride_pad, std=1.3)
+    qkv = buf[:, :width]
+    freq = (mk.rope_frequencies(rot, theta) if rot else ()) if freq is None else freq
+    gains = [(1 + 0.2 * torch.randn(st.d, generator=st.g, device="cuda")).to(torch.bfloat16) if norm else None
+             for _ in range(2)]
+    return qkv, mk.Rope(freq, inter, mscale) if rot else None, torch.from_numpy(np.asarray(freq)), gains
+
+
+def check_append(st, rot, inter, norm, eps=1e-6, mscale=1.0, **kw):
+    qkv, rope, freq, gains = append_case(st, rot, inter, norm, mscale=mscale, **kw)
+    before = st.kv.clone()
+    extra = qkv.shape[0] - st.rows
+    q_out = torch.full((st.rows + extra, st.hq, st.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+    got = mk.append_chunk(st.shape(mk), qkv, st.news, st.lens, st.bt, st.kv, rope=rope, q_norm=gains[0], k_norm=gains[1],
+                          eps=eps, q_out=q_out, status=status)
+    assert got is q_out and int(status) == mk.MK_OK
+    assert torch.all(q_out[st.rows:] == 7.0)        # rows behind the last sequence's
+    x = qkv[:st.rows].double().reshape(st.rows, st.hq + 2 * st.hkv, st.d)
+    seq, pos = st.positions()
+    q, k, v = x[:, :st.hq], x[:, st.hq:st.hq + st.hkv], x[:, st.hq + st.hkv:]
+    if norm:
+        q, k = R.head_norm(q, gains[0], eps), R.head_norm(k, gains[1], eps)
+    # fp32 noise: the norm's sum of D squares and its square root (D/8 + 16 roundings of 2^-24), the
+    # angle's cos and sin (4 of 2^-24, scaled by mscale) and two products, all of the pair's magnitude
+    scale = max(1.0, abs(mscale))
+    pair = lambda t: scale * t.abs().amax(-1, keepdim=True)  # noqa: E731
+    nq, nk = pair(q) * 64 * 2.0 ** -24, pair(k) * 64 * 2.0 ** -24
+    if rot:
+        q, k = R.rotate(q, pos, freq, inter, mscale), R.rotate(k, pos, freq, inter, mscale)
+    assert torch.all((q_out[:st.rows].double() - q).abs() <= q.abs() * H + nq * (1 + H))
+    page, off = st.bt[seq, pos // st.ps].long(), pos % st.ps
+    if st.q8:
+        codes, scales = st.planes()
+        c, s = codes[page, :, :, off].double(), scales[page, :, :, off]
+        want = torch.stack([k, v], 1)                # [rows][2][Hkv][D]
+        step = want.unflatten(-1, (-1, 32)).abs().amax(-1) / 127
+        noise = torch.stack([nk.expand_as(k), torch.zeros_like(v)], 1)
+        # the scale: fp32 noise, then half a step of f16 (2^-11 of it)
+        sn = noise.unflatten(-1, (-1, 32)).amax(-1) / 127 + step * 2.0 ** -23
+        assert torch.all((s.double() - step).abs() <= (step + sn) * 2.0 ** -11 + sn + 2.0 ** -25)
+        full = step.repeat_interleave(32, -1)
+        # the code: half a step, and the noise of the value and of the scale over 127 steps
+        assert torch.all((c * full - want).abs() <= full * (0.5 + 127 * 2.0 ** -22) + 2 * noise + 1e-30)
+        assert c.abs().max() <= 127
+    else:
+        assert torch.all((st.kv[page, 0, :, off].double() - k).abs() <= k.abs() * H + nk * (1 + H))
+        assert torch.equal(st.kv[page, 1, :, off], v.to(torch.bfloat16))
+    # nothing but the new positions was written
+    touched = torch.zeros(st.P, st.ps, dtype=torch.bool, device="cuda")
+    touched[page, off] = True
+    if st.q8:
+        for a, b in zip(st.planes(), st.planes(before)):
+            same = (a.contiguous().view(torch.uint8) == b.contiguous().view(torch.uint8)).all(-1)
+            assert torch.all(same | touched[:, None, None, :])
+    else:
+        same = (bits(st.kv) == bits(before)).all(-1)
+        assert torch.all(same | touched[:, None, None, :])
+
+
+APPEND_SHAPES = [
+    # hq, hkv, d, ps, lens, news
+    (4, 2, 64, 16, [65], [65]),
+    (32, 4, 128, 16, [1, 512, 33], [1, 1, 1]),
+    (7, 1, 128, 24, [100, 40], [37, 40]),
+    (8, 8, 64, 8, [9, 300], [2, 299]),
+    (6, 2, 128, 40, [2000, 77, 5], [1400, 0, 5]),
+    (5, 5, 128, 128, [129], [129]),
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("rot,inter,norm", [(1.0, False, False), (1.0, True, True), (0.5, False, True), (0.25, True, False),
+                                            (0, False, True), (0.75, False, False)])
+@pytest.mark.parametrize("hq,hkv,d,ps,lens,news", APPEND_SHAPES)
+def test_append(hq, hkv, d, ps, lens, news, rot, inter, norm, q8):
+    if q8 and d != 128:
+        d = 128
+    st = R.Setup(hq, hkv, d, ps, lens, news, q8=q8, seed=3)
+    check_append(st, int(rot * d), inter, norm, extra_rows=2)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_append_strided_rows_eps_and_mscale(q8):
+    st = R.Setup(8, 2, 128, 16, [70, 3], [50, 3], q8=q8, seed=4)
+    check_append(st, 128, False, True, eps=0.5, mscale=1.37, stride_pad=72, extra_rows=1)
+
+
+@pytest.mark.parametrize("pos", [0, 1, 131071, 1048575, (1 << 29) + 12345])
+def test_rotary_angles_of_far_positions(pos):
+    # one token at a far position: its page alone exists (earlier block-table entries are not read)
+    ps = 128
+    maxpg = pos // ps + 1
+    sh = mk.CacheShape(2, 1, 128, ps, 2, maxpg)
+    kv = torch.zeros(2, 2, 1, ps, 128, dtype=torch.bfloat16, device="cuda")
+    bt = torch.full((1, maxpg), -1, dtype=torch.int32, device="cuda")
+    bt[0, pos // ps] = 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    qkv = torch.randn(1, 4 * 128, generator=g, device="cuda").to(torch.bfloat16)
+    freq = mk.rope_frequencies(128, 1e4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = mk.append_chunk(sh, qkv, [1], [pos + 1], bt, kv, rope=mk.Rope(freq), status=status)
+    x = qkv.double().view(1, 4, 128)
+    want = R.rotate(x, torch.tensor([pos], device="cuda"), torch.from_numpy(freq), False)
+    # the angle itself: a 64-bit frequency is off by 2^-53 of itself and its turns by as much
+    far = pos * 2.0 ** -52 * x.abs().max()
+    assert int(status) == 0
+    assert torch.all((q.double() - want[:, :2]).abs() <= want[:, :2].abs() * H + 2.0 ** -18 * x.abs().max() + far)
+    assert torch.all((kv[1, 0, :, pos % ps].double() - want[:, 2]).abs()
+                     <= want[:, 2].abs() * H + 2.0 ** -18 * x.abs().max() + far)
+
+
+def test_append_reports_pages_out_of_range():
+    st = R.Setup(4, 2, 128, 16, [40, 20], [40, 20], seed=6)
+    good = st.bt.clone()
+    st.bt[0, 1], st.bt[1, 0] = st.P, -7
+    qkv, rope, freq, _ = append_case(st, 128, False, False)
+    before = st.kv.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = mk.append_chunk(st.shape(mk), qkv, st.news, st.lens, st.bt, st.kv, rope=rope, status=status)
+    assert int(status) == mk.MK_ERR_DEVICE_BOUNDS
+    kv_bad, st.kv = st.kv, before
+    q2 = mk.append_chunk(st.shape(mk), qkv, st.news, st.lens, good, st.kv, rope=rope, status=status)
+    assert int(status) == mk.MK_OK and torch.equal(q, q2)
+    for s, p in ((0, 0), (0, 2), (1, 1)):            # the pages that were in range hold the same
+        n = min(st.lens[s] - p * 16, 16)
+        assert torch.equal(bits(kv_bad[good[s, p].long(), :, :, :n]), bits(st.kv[good[s, p].long(), :, :, :n]))
+
+
+# ---------------------------------------------------------------- read-back
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("hkv,d,ps,lens,counts", [(2, 64, 16, [65], [65]), (4, 128, 24, [100, 7, 1], [33, 0, 1]),
+                                                  (1, 128, 8, [1000], [999]), (8, 128, 64, [64, 129], [64, 2])])
+def test_read_cache(hkv, d, ps, lens, counts, q8):
+    st = R.Setup(hkv, hkv, 128 if q8 else d, ps, lens, counts, q8=q8, seed=7)
+    k, v = mk.read_cache(st.shape(mk), counts, lens, st.bt, st.kv)
+    want = torch.cat([st.cached(st.kv, s, ln)[:, :, ln - n:] for s, (ln, n) in enumerate(zip(lens, counts))], 2)
+    want = want.transpose(1, 2)
+    assert torch.equal(k, want[0].float().to(torch.bfloat16))     # code * scale is exact in fp32
+    assert torch.equal(v, want[1].float().to(torch.bfloat16))
+
+
+def test_read_cache_zeros_for_pages_out_of_range():
+    st = R.Setup(2, 2, 64, 16, [40], [40], seed=8)
+    st.bt[0, 1] = 1 << 30
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = mk.read_cache(st.shape(mk), [40], [40], st.bt, st.kv, status=status)
+    assert int(status) == mk.MK_ERR_DEVICE_BOUNDS
+    assert torch.all(k[16:32] == 0) and torch.all(v[16:32] == 0) and torch.all(k[:16] != 0) and torch.all(v[32:] != 0)
+
+
+# ---------------------------------------------------------------- attention
+def check_attention(st, std=1.5, drop=None, status_want=mk.MK_OK, q=None, extra_rows=0):
+    q = st.normal(st.rows + extra_rows, st.hq, st.d, std=std) if q is None else q
+    status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+    out = torch.full((st.rows + extra_rows, st.hq, st.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, out=out, status=status)
+    assert got is out and int(status) == status_want
+    assert torch.all(out[st.rows:] == 7.0)
+    ref, weight, shift = R.attention(st, q, st.kv, drop)
+    far = (out[:st.rows].double() - ref).abs()
+    bound = R.attention_bound(ref, weight, shift, st.q8)
+    assert torch.all(far <= bound), float((far / bound).max())
+    return q, out
+
+
+ATTN_SHAPES = [
+    # hq, hkv, d, ps, lens, news: one token, one position, page edges, tiles' edges, ragged, odd groups
+    (4, 2, 64, 16, [65], [65]),
+    (1, 1, 128, 8, [1], [1]),
+    (8, 1, 128, 16, [16, 17, 128, 129], [1, 1, 1, 1]),
+    (8, 1, 128, 16, [16, 17, 128, 129, 1], [16, 17, 128, 129, 1]),
+    (32, 4, 128, 16, [513, 40, 1000], [100, 0, 3]),
+    (3, 1, 64, 24, [200, 300], [200, 47]),
+    (10, 2, 128, 40, [333], [333]),
+    (12, 2, 128, 64, [400, 64], [31, 64]),
+    (7, 1, 64, 8, [700], [69]),
+    (16, 16, 64, 128, [130, 257], [130, 129]),
+    (14, 2, 128, 256, [700], [300]),
+    (32, 4, 128, 16, [5000], [1]),
+    (16, 2, 128, 64, [9001, 3], [2, 1]),
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,ps,lens,news", ATTN_SHAPES)
+def test_attention(hq, hkv, d, ps, lens, news, q8):
+    st = R.Setup(hq, hkv, 128 if q8 else d, ps, lens, news, q8=q8, seed=9)
+    check_attention(st, extra_rows=1)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_attention_64_sequences(q8):
+    g = np.random.default_rng(1)
+    lens = [int(x) for x in np.exp(g.uniform(0, np.log(3000), 64)).astype(int)]
+    news = [min(ln, int(g.choice([0, 1, 1, 1, 5, 67]))) for ln in lens]
+    check_attention(R.Setup(16, 2, 128, 16, lens, news, q8=q8, seed=10))
+
+
+@pytest.mark.parametrize("std", [0.0, 30.0])
+def test_attention_flat_and_peaked_scores(std):
+    # all scores equal; and scores so far apart that the running maximum moves often and by much
+    check_attention(R.Setup(8, 2, 128, 16, [1500], [70], seed=11), std=std)
+
+
+def test_attention_rising_scores():
+    # every later key scores higher than all before: the running maximum moves with every tile
+    st = R.Setup(8, 1, 128, 16, [2000], [50], seed=12)
+    pos = torch.arange(2000, device="cuda")
+    page, off = st.bt[0, pos // 16].long(), pos % 16
+    k = torch.zeros(2000, 128, device="cuda")
+    k[:, 0] = pos * 0.25
+    st.kv[page, 0, 0, off] = k.to(torch.bfloat16)
+    q = st.normal(50, 8, 128)
+    q[..., 0] = 4.0
+    check_attention(st, q=q)
+
+
+def test_attention_strided_query_rows():
+    st = R.Setup(6, 2, 128, 16, [300, 30], [111, 30], seed=13)
+    qkv = st.normal(141, (6 + 4) * 128 + 8)
+    check_attention(st, q=qkv[:, :6 * 128].unflatten(1, (6, 128)))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_attention_skips_pages_out_of_range(q8):
+    st = R.Setup(8, 2, 128, 16, [100, 300, 20], [100, 3, 20], q8=q8, seed=14)
+    drop = torch.zeros(3, 300, dtype=torch.bool, device="cuda")
+    for s, p, bad in ((0, 0, st.P), (0, 3, -1), (1, 18, 1 << 30), (1, 2, -(1 << 31)), (2, 0, -5), (2, 1, 1 << 20)):
+        drop[s, p * 16:p * 16 + 16] = True          # rows 0..15 of sequence 0 and all of sequence 2 see nothing
+    ref_bt = st.bt.clone()
+    bad_bt = st.bt.clone()
+    for s, p, bad in ((0, 0, st.P), (0, 3, -1), (1, 18, 1 << 30), (1, 2, -(1 << 31)), (2, 0, -5), (2, 1, 1 << 20)):
+        bad_bt[s, p] = bad
+    q = st.normal(st.rows, 8, 128)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, bad_bt, st.kv, status=status)
+    assert int(status) == mk.MK_ERR_DEVICE_BOUNDS
+    st.bt = ref_bt
+    ref, weight, shift = R.attention(st, q, st.kv, drop)
+    assert torch.all((out.double() - ref).abs() <= R.attention_bound(ref, weight, shift, q8))
+    assert torch.all(out[:16] == 0) and torch.all(out[103:] == 0)
+
+
+def test_attention_nan_in_a_later_position_stays_there():
+    # a NaN value of the sequence reaches the rows that see it, and no other row of its chunk
+    st = R.Setup(4, 1, 64, 16, [90], [90], seed=15)
+    q = st.normal(90, 4, 64)
+    clean = mk.chunk_attention(st.shape(mk), q, [90], [90], st.bt, st.kv)
+    st.kv[st.bt[0, 80 // 16].long(), 0, 0, 80 % 16, 5] = float("nan")       # a key
+    out = mk.chunk_attention(st.shape(mk), q, [90], [90], st.bt, st.kv)
+    assert torch.isfinite(out[:80]).all() and torch.isnan(out[80:]).all()
+    assert torch.equal(out[:80], clean[:80])
+
+
+def test_attention_pool_beyond_32_bit_offsets():
+    # a 5 GB layer whose used pages lie at its end
+    ps, hkv, d = 128, 8, 128
+    P = 5 * (1 << 30) // (2 * hkv * ps * d * 2)
+    st = R.Setup(16, hkv, d, ps, [300], [40], seed=16)
+    big = torch.empty(P, 2, hkv, ps, d, dtype=torch.bfloat16, device="cuda")
+    n = st.kv.shape[0]
+    big[P - n:] = st.kv
+    bt = torch.where(st.bt >= 0, st.bt + (P - n), st.bt)
+    sh = mk.CacheShape(16, hkv, d, ps, P, st.maxpg)
+    q = st.normal(40, 16, d)
+    assert torch.equal(mk.chunk_attention(sh, q, [40], [300], bt, big),
+                       mk.chunk_attention(st.shape(mk), q, [40], [300], st.bt, st.kv))
+    k, v = mk.read_cache(sh, [300], [300], bt, big)
+    k2, v2 = mk.read_cache(st.shape(mk), [300], [300], st.bt, st.kv)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    qkv = st.normal(40, (16 + 2 * hkv) * d)
+    mk.append_chunk(sh, qkv, [40], [300], bt, big)
+    mk.append_chunk(st.shape(mk), qkv, [40], [300], st.bt, st.kv)
+    assert torch.equal(bits(big[P - n:]), bits(st.kv))
+
+
+# ---------------------------------------------------------------- streams, graphs, repeats
+@pytest.mark.parametrize("q8", [False, True])
+def test_repeats_are_bit_identical_on_any_stream_and_in_graphs(q8):
+    st = R.Setup(16, 2, 128, 16, [4000, 70, 333], [1, 70, 40], q8=q8, seed=17)
+    width = (16 + 4) * 128
+    qkv = st.normal(st.rows, width)
+    rope = mk.Rope(mk.rope_frequencies(128, 1e4))
+    sh = st.shape(mk)
+
+    def layer(kv, stream=None):
+        q = mk.append_chunk(sh, qkv, st.news, st.lens, st.bt, kv, rope=rope, stream=stream)
+        o = mk.chunk_attention(sh, q, st.news, st.lens, st.bt, kv, stream=stream)
+        return q, o, *mk.read_cache(sh, st.news, st.lens, st.bt, kv, stream=stream)
+
+    kv0 = st.kv.clone()
+    first = layer(st.kv)
+    again = layer(st.kv)                     # appending the same rows again changes nothing
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kv2 = kv0.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    other = layer(kv2, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    kv3 = kv0.clone()
+    graphs, outs = [], []
+    for _ in range(2):                       # two graphs over the same inputs, replayed at once
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer(kv3))
+        graphs.append(g)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            graphs[0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for r in (again, other, *outs):
+        for a, b in zip(first, r):
+            assert torch.equal(bits(a), bits(b))
+    assert torch.equal(bits(st.kv), bits(kv2)) and torch.equal(bits(st.kv), bits(kv3))
+
+
+def test_splitting_a_prompt_gives_the_same_cache_and_close_rows():
+    # a prompt in one call, and in slices with another sequence's tokens between
+    st = R.Setup(8, 2, 128, 16, [300, 9], [300, 9], seed=18)
+    sh = st.shape(mk)
+    qkv = st.normal(309, 12 * 128)
+    rope = mk.Rope(mk.rope_frequencies(128, 1e4))
+    kv1, kv2 = st.kv.clone(), st.kv.clone()
+    q1 = mk.append_chunk(sh, qkv, [300, 9], [300, 9], st.bt, kv1, rope=rope)
+    o1 = mk.chunk_attention(sh, q1, [300, 9], [300, 9], st.bt, kv1)
+    got = []
+    for a, b, n2, l2 in ((0, 129, 0, 0), (129, 130, 9, 9), (130, 300, 0, 9)):
+        rows = torch.cat([qkv[a:b], qkv[300:300 + n2]])
+        q2 = mk.append_chunk(sh, rows, [b - a, n2], [b, l2], st.bt, kv2, rope=rope)
+        got.append((mk.chunk_attention(sh, q2, [b - a, n2], [b, l2], st.bt, kv2), b - a))
+    assert torch.equal(bits(kv1), bits(kv2))
+    o2 = torch.cat([o[:n] for o, n in got] + [got[1][0][1:]])
+    st.kv = kv1
+    ref, weight, shift = R.attention(st, q1, kv1)
+    bound = R.attention_bound(ref, weight, shift, False)
+    assert torch.all((o1.double() - ref).abs() <= bound) and torch.all((o2.double() - ref).abs() <= bound)
+
+
+# ---------------------------------------------------------------- together with the decode step
+@pytest.mark.parametrize("q8", [False, True])
+def test_prefill_then_decode_step(q8):
+    """A prompt goes through every layer with the chunk operators (the products in between are plain
+    torch in fp32), then mk_decode_step decodes the next token from the cache they left: its logits
+    against the oracle's, which prefilled token by token."""
+    from oracle import Oracle
+    from tests.gpu_common import MEDIUM, check_rows, engine_for, gpu_step, to_device
+    from tests.helpers import tiny_setup
+    lens = [90, 33]
+    s = tiny_setup(MEDIUM, lens, kv_q8=q8)
+    m = s["model"]
+    w = to_device(s["wt"])
+    ps, P = s["page_size"], s["num_pages"]
+    flags = mk.FLAG_KV_Q8 if q8 else 0
+    sh = mk.cache_shape(m, ps, P, s["max_pages"], flags)
+    kv = (torch.zeros(m["layers"], W.kv_q8_layer_bytes(m, P, ps), dtype=torch.uint8, device="cuda") if q8 else
+          torch.zeros(W.kv_shape(m, P, ps), dtype=torch.bfloat16, device="cuda"))
+    bt = torch.from_numpy(s["bt"]).cuda()
+    news = [ln - 1 for ln in lens]
+    tokens = torch.from_numpy(np.concatenate([s["seqs"][b][:news[b]] for b in range(2)])).cuda().long()
+    rope = mk.Rope(mk.rope_frequencies(m["head_dim"], m["rope_theta"]))
+
+    def norm(x, g):
+        return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + m["rms_eps"]) * g.float()
+
+    x = w["embed"][tokens].float()
+    for l, lw in enumerate(w["layers"]):
+        qkv = (norm(x, lw["attn_norm"]) @ lw["w_qkv"].float().T).to(torch.bfloat16)
+        q = mk.append_chunk(sh, qkv, news, news, bt, kv[l], rope=rope)
+        o = mk.chunk_attention(sh, q, news, news, bt, kv[l])
+        x = x + o.flatten(1).float() @ lw["w_o"].float().T
+        y = norm(x, lw["ffn_norm"])
+        top, ids = torch.softmax(y @ lw["w_router"].float().T, -1).topk(m["top_k"])
+        top = top / top.sum(-1, keepdim=True)
+        for k in range(m["top_k"]):
+            gu = torch.einsum("th,tfh->tf", y, lw["w_gate_up"][ids[:, k]].float())
+            act = torch.nn.functional.silu(gu[:, :m["ffn"]]) * gu[:, m["ffn"]:]
+            x = x + top[:, k:k + 1] * torch.einsum("tf,thf->th", act, lw["w_down"][ids[:, k]].float())
+    eng = engine_for(s, w, flags=flags)
+    got = gpu_step(eng, s["tokens"], s["seq_lens"], s["bt"], kv)
+    ref = Oracle("f32").decode_step(s["dims"], s["wn"], s["tokens"], s["seq_lens"], s["bt"], s["kv"].copy())
+    # bf16 q, k, v rows and attention outputs where the oracle keeps fp32: 2^-9 each on average, over
+    # three layers; the bound of the step's own parity tests holds
+    errs = check_rows(got, ref)
+    print("prefill + step: rel L2", errs)
+    eng.close()
