@@ -19,6 +19,7 @@
 #define MK_DEBUG_H
 
 #include "mk.h"
+#include "mk_chunk.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -135,6 +136,15 @@ int mk_debug_trace_read(mk_ctx* ctx, void* host_dst, size_t bytes);
 
 /* Number of SMs (persistent thread blocks) a step of this context launches. */
 int mk_num_ctas(mk_ctx* ctx);
+
+/*
+ * The schedule mk_chunk_attention takes for these lengths (host only): *n_out segments, the first
+ * max_segments of them written as 8 int32 each, block by block in the order a block runs them:
+ * block, sequence, unit (up to two tiles of 128/G tokens), KV head, first position tile, position
+ * tiles, position tiles of the unit, partial written (-1: the segment is the whole unit).
+ */
+int mk_plan_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                            const int32_t* seq_lens, int32_t* segments, int32_t max_segments, int32_t* n_out);
 
 #ifdef __cplusplus
 }

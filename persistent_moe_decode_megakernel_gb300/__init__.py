@@ -139,7 +139,8 @@ EXPORTS = ("mk_create", "mk_decode_step", "mk_decode_step_greedy", "mk_get_statu
            "mk_debug_trace", "mk_debug_trace_read", "mk_paged_attention_noalloc", "mk_kv_pool_create",
            "mk_kv_pool_destroy", "mk_kv_admit", "mk_kv_reserve", "mk_kv_evict", "mk_kv_fill", "mk_kv_free_pages",
            "mk_kv_len", "mk_graph_create", "mk_graph_launch", "mk_graph_destroy", "mk_rope_frequencies",
-           "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache")
+           "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache",
+           "mk_plan_chunk_attention")
 
 _lib = None
 _lock = threading.Lock()
@@ -186,6 +187,7 @@ def lib():
             L.mk_append_chunk.argtypes = [vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp]
             L.mk_chunk_attention_workspace.argtypes = [vp, i32, vp, vp, ctypes.POINTER(sz)]
             L.mk_chunk_attention.argtypes = [vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+            L.mk_plan_chunk_attention.argtypes = [vp, i32, vp, vp, vp, i32, ctypes.POINTER(i32)]
             L.mk_read_cache.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
             L.mk_debug_trace.argtypes = [vp, i32, i32]
             L.mk_debug_trace_read.argtypes = [vp, vp, ctypes.c_size_t]
@@ -435,6 +437,18 @@ def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
     _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
                                               ctypes.byref(n)))
     return n.value
+
+
+def plan_chunk_attention(shape: CacheShape, chunk_lens, seq_lens) -> np.ndarray:
+    """The schedule of :func:`chunk_attention` (``mk_plan_chunk_attention``): int32 [segments, 8]."""
+    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
+    n = ctypes.c_int32()
+    _check(lib().mk_plan_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, None, 0,
+                                         ctypes.byref(n)))
+    out = np.zeros((n.value, 8), dtype=np.int32)
+    _check(lib().mk_plan_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, out.ctypes.data,
+                                         n.value, ctypes.byref(n)))
+    return out
 
 
 def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv_layer, out=None, workspace=None,

@@ -14,17 +14,26 @@
 // Two tiles in turn keep the tensor cores busy while the other tile's softmax runs: tensor
 // memory holds S and O of both (512 columns at D = 128).  A unit with one tile only (a few new
 // tokens, as in decoding) runs two STREAMS instead: even and odd position tiles, each with its own
-// S, O, m and l, merged at the end.
+// S, O, m and l, joined at the end.
 //
 // Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warp 8: loads.  Warp
-// 9: issues the MMAs.  Over a q8_0 cache warps 12-15 decode codes into the bf16 tiles.  Every
-// wait is bounded: one that runs out raises the block's abort flag, every role leaves its loop,
-// copies in flight are waited for and tensor memory is returned.
+// 9: issues the MMAs.  Warp 10: query rows.  Over a q8_0 cache warps 12-15 decode codes into fp16 operand tiles.  Blocks
+// are persistent (mk_chunk_plan.h): loads and scores of the next segment run under the epilogue of
+// this one.  Every wait is bounded: one that runs out raises the block's abort flag, every
+// role leaves its loop, copies in flight are let land and tensor memory is returned.
 //
-// Long contexts with few rows are split over the positions (the host's plan); the partial
-// (O, m, l) of each split go to the workspace and a second kernel merges them in split order.
+// Operands.  bf16 cache: Q, K, V as they are, P rounded to bf16 (2^-8; its sum uses the unrounded
+// values).  q8_0 cache: fp16, whose 2^-11 keeps a decoded value three bits better than bf16 would
+// and whose decode is one byte permute, one subtract and one multiply per two codes: K and V are
+// code * scale; a row of Q is divided by a power of two (undone in the softmax's constant), so that
+// it fits; P carries a factor 2^6, so that small weights stay clear of fp16's subnormals.
+//
+// What a row does not see must not reach it, and what fp16 cannot hold must still come out right: a row
+// whose result is not finite is computed again from the cache in fp32, position by position
+// (exact_row).  A NaN or infinity among later V rows of the same tile (0 * NaN) and scales whose values
+// overflow fp16 (the decode makes them NaN) end there; a row that really holds a NaN stays one.
 
-#include "mk_chunk.h"
+#include "mk_chunk_plan.h"
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -37,25 +46,13 @@
 namespace mk {
 namespace {
 
-constexpr int kTile = 128;          // positions of a tile, and rows of a tile
-constexpr int kRawPos = 64;         // q8_0: positions of one raw stage
-constexpr int kRawBytes = kRawPos * (128 + 8);
+constexpr int kRawBytes = kTile * (128 + 8);   // q8_0: the codes and scales of a K or V tile
 constexpr int kMasks = 8;           // tiles whose page masks are kept (more than can be in flight)
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Which work each block takes.  Sequences with rows, longest first; within one, units from the
-// last tokens (most positions) to the first, then KV heads, then splits.
-struct AttnPlan {
-  int32_t n;                        // sequences with rows
-  int32_t split_tiles;              // position tiles of a split
-  int32_t seq[kMaxSeqs];
-  int32_t item0[kMaxSeqs + 1];      // first block of the i-th
-  int32_t nsplit[kMaxSeqs];         // by sequence; 1: its blocks write the output
-  int64_t part0[kMaxSeqs];          // by sequence: first float of its partials
-};
-
 struct AttnParams {
   CUtensorMap map;                  // bf16 pages (see encode_pages)
+  CUtensorMap qmap;                 // query rows (see encode_queries)
   ChunkSeqs seqs;
   AttnPlan plan;
   const uint8_t* kv;
@@ -66,7 +63,7 @@ struct AttnParams {
   uint16_t* out;
   float* part;
   size_t code_bytes;
-  int32_t Hq, Hkv, G, TT, ps, P, maxpg;
+  int32_t Hq, ps, P, maxpg;
   int32_t box;                      // positions of one copy: a power of two that divides ps
   float c;                          // log2(e) / sqrt(D)
 };
@@ -103,6 +100,13 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const void* map, int z, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(z), "r"(pg), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_4d(uint32_t dst, const void* map, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -117,9 +121,9 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// bf16 operands, fp32 accumulator; b_mn: B is stored with its N dimension contiguous
-__device__ __forceinline__ constexpr uint32_t tc_idesc(int M, int N, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+// bf16 (or fp16) operands, fp32 accumulator; b_mn: B is stored with its N dimension contiguous
+__device__ __forceinline__ constexpr uint32_t tc_idesc(bool bf16, int M, int N, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 // one elected lane of the converged warp issues
@@ -171,6 +175,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t x = *reinterpret_cast<uint64_t*>(&a), y = *reinterpret_cast<uint64_t*>(&b), z = *reinterpret_cast<uint64_t*>(&c), d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
@@ -190,6 +199,12 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {   // a in the low
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -199,30 +214,31 @@ template <int D, bool Q8>
 struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;           // one operand tile
   static constexpr int kGroup = D / 64 * 1024;               // 8 positions of a K or V tile
-  static constexpr int kQ = 0;                               // two Q tiles
-  static constexpr int kRaw = 2 * kTileBytes;                // q8_0: raw stages (a one-tile unit's start at
-  static constexpr int kRawStages = Q8 ? 3 : 0;              // the second Q tile)
-  static constexpr int kRawStages1 = Q8 ? (kTileBytes + 3 * kRawBytes) / kRawBytes : 0;
+  static constexpr int kRawStages = Q8 ? 3 : 0;
+  static constexpr int kRaw = 2 * kTileBytes;                // behind the two Q tiles
   static constexpr int kKv = (kRaw + kRawStages * kRawBytes + 1023) / 1024 * 1024;
-  static constexpr int kStages = Q8 ? 4 : D == 128 ? 5 : 8;
+  static constexpr int kStages = Q8 ? 3 : D == 128 ? 5 : 8;
   static constexpr int kCtl = kKv + kStages * kTileBytes;
   static constexpr int kThreads = Q8 ? 512 : 384;
 };
 
 struct Ctl {
-  uint64_t full[8], empty[8];        // K and V tiles: position tile j is ring entries 2j (K) and 2j+1 (V)
+  uint64_t full[8], empty[8];        // K and V tiles: a block's j-th position tile is ring entries 2j (K), 2j+1 (V)
   uint64_t raw_full[8], raw_empty[8];
-  uint64_t qbar[2], sfull[2], pfull[2], ofull;
+  uint64_t qraw[2], qbar[2], qfree;  // query tiles: landed, in the operand type (bf16: qraw itself), read by the last S
+  uint64_t sfull[2], pfull[2][2];    // S of a tile (stream); the halves of its P
+  uint64_t ofull, join;
   uint32_t tmem, abort;
   uint32_t mask[kMasks];             // per tile, a bit per 8 positions: the page is in range
-  float m[kTile], l[kTile];          // stream 1's statistics for the merge
+  float2 ml[2][kTile];               // streams' (m, l) when they join
 };
-static_assert(sizeof(Ctl) <= 2048, "");
+struct CtlQ8 : Ctl {
+  float rowc[kTile];                 // two streams: the softmax's constant of each query row
+};
 
 template <int D, bool Q8>
-constexpr size_t smem_bytes() { return Layout<D, Q8>::kCtl + sizeof(Ctl) + 1024; }
+constexpr size_t smem_bytes() { return Layout<D, Q8>::kCtl + (Q8 ? sizeof(CtlQ8) : sizeof(Ctl)); }
 static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448 && smem_bytes<64, false>() <= 232448, "");
-static_assert(Layout<128, true>::kRawStages1 <= 8, "");
 
 // Waits for the phase of `bar` with this parity, at most kWaitNs; false once the block gives up.
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status) {
@@ -243,196 +259,272 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Ctl* ct
   return __all_sync(~0u, mbar_try(bar, parity) || mbar_wait_slow(bar, parity, ctl, status));
 }
 
-// What one block does.
-struct Item {
-  int s, kvh, split, nsplit;
-  int tok0, ntok;        // tokens of the unit within the sequence's new ones
-  int pos0;              // position of the unit's first token
-  int len;
-  int tile0, n;          // position tiles [tile0, tile0 + n)
-  bool two;              // two Q tiles (else two streams of one)
-};
-
-__device__ __forceinline__ bool find_item(const AttnParams& p, Item& it) {
-  const int b = blockIdx.x;
-  int lo = 0, hi = p.plan.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.plan.item0[mid] <= b) lo = mid;
-    else hi = mid;
-  }
-  it.s = p.plan.seq[lo];
-  it.nsplit = p.plan.nsplit[it.s];
-  it.len = p.seqs.len[it.s];
-  const int chunk = p.seqs.row0[it.s + 1] - p.seqs.row0[it.s];
-  const int UT = 2 * p.TT, nu = (chunk + UT - 1) / UT;
-  int rem = b - p.plan.item0[lo];
-  const int u = nu - 1 - rem / (p.Hkv * it.nsplit);
-  rem %= p.Hkv * it.nsplit;
-  it.kvh = rem / it.nsplit;
-  it.split = rem % it.nsplit;
-  it.tok0 = u * UT;
-  it.ntok = min(UT, chunk - it.tok0);
-  it.pos0 = it.len - chunk + it.tok0;
-  it.two = it.ntok > p.TT;
-  const int tiles = (it.pos0 + it.ntok - 1) / kTile + 1;
-  it.tile0 = it.split * p.plan.split_tiles;
-  it.n = it.nsplit == 1 ? tiles : min(p.plan.split_tiles, tiles - it.tile0);
-  return it.n > 0;       // (an early unit has fewer tiles than the sequence's last)
+// One arrival for the warp, after all its lanes' work so far.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// First float of the partials of (unit u, KV head, split) of a sequence: rows of D + 4 floats
-// (O, then m, l), `urows` of them per split.
-__device__ __forceinline__ size_t part_at(const AttnParams& p, int s, int u, int kvh, int split, int D) {
-  const int chunk = p.seqs.row0[s + 1] - p.seqs.row0[s];
-  const int urows = min(chunk, 2 * p.TT) * p.G;
-  return p.plan.part0[s] +
-         (static_cast<size_t>(u * p.Hkv + kvh) * p.plan.nsplit[s] + split) * urows * static_cast<size_t>(D + 4);
+// A ring position: entry and the parity of its current filling.
+template <int N>
+struct Ring {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// --------------------------------------------------------------------------- one row, plainly
+// Row r, query head h by one warp: 32 positions at a time, a lane per position for the scores,
+// D/32 dims per lane for the output; fp32, and no position beyond the row's own is touched.
+template <int D, bool Q8>
+__device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
+  const int lane = threadIdx.x & 31, kvh = h / p.plan.G, s = seq_of_row(p.seqs, r);
+  const int n = p.seqs.len[s] - p.seqs.row0[s + 1] + r + 1;
+  const uint16_t* q = p.q + static_cast<size_t>(r) * p.q_stride + static_cast<size_t>(h) * D;
+  const uint16_t* kv16 = reinterpret_cast<const uint16_t*>(p.kv);
+  const int8_t* codes = reinterpret_cast<const int8_t*>(p.kv);
+  const __half* scales = reinterpret_cast<const __half*>(p.kv + p.code_bytes);
+  const float c = 1.4426950408889634f * rsqrtf(static_cast<float>(D));
+  float m = -INFINITY, sum = 0.f, o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+  for (int t0 = 0; t0 < n; t0 += 32) {
+    const int t = t0 + lane;
+    int64_t line = -1;
+    float x = -INFINITY;
+    if (t < n) {
+      const int page = __ldg(p.bt + static_cast<size_t>(s) * p.maxpg + t / p.ps);
+      if (page >= 0 && page < p.P) {
+        line = (static_cast<int64_t>(page) * 2 * p.plan.Hkv + kvh) * p.ps + t % p.ps;
+        x = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; ++d) {
+          float k;
+          if constexpr (Q8) k = static_cast<float>(codes[line * D + d]) * __half2float(scales[line * (D / 32) + d / 32]);
+          else k = bf_lo(kv16[line * D + d]);
+          x = fmaf(bf_lo(__ldg(q + d)), k, x);
+        }
+        x *= c;
+      }
+    }
+    float mx = x;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
+    mx = fmaxf(mx, m);
+    // (a row whose scores so far are all -inf or NaN takes 0 as its reference; NaN goes on into w)
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float f = m == -INFINITY ? 0.f : ex2(m - ref), w = line >= 0 ? ex2(x - ref) : 0.f;
+    float ws = w;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) ws += __shfl_xor_sync(~0u, ws, k);
+    sum = (sum == 0.f ? 0.f : sum * f) + ws;
+    m = mx;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = o[i] == 0.f ? 0.f : o[i] * f;
+    for (int j = 0; j < 32; ++j) {
+      const int64_t lj = __shfl_sync(~0u, line, j);
+      const float wj = __shfl_sync(~0u, w, j);
+      if (lj < 0) continue;
+      const int64_t lv = lj + static_cast<int64_t>(p.plan.Hkv) * p.ps;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int d = 32 * i + lane;
+        float v;
+        if constexpr (Q8) v = static_cast<float>(codes[lv * D + d]) * __half2float(scales[lv * (D / 32) + i]);
+        else v = bf_lo(kv16[lv * D + d]);
+        o[i] = fmaf(wj, v, o[i]);
+      }
+    }
+  }
+  uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o[i] / sum));
 }
 
 // --------------------------------------------------------------------------- loads (warp 8)
 template <int D, bool Q8>
-__device__ __forceinline__ void produce(const AttnParams& p, const Item& it, uint32_t base, Ctl* ctl) {
+__device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl) {
   using L = Layout<D, Q8>;
   const int lane = threadIdx.x & 31;
-  const int r = p.box, nbox = (Q8 ? kRawPos : kTile) / r;     // copies of a stage
-  const int32_t* bt = p.bt + static_cast<size_t>(it.s) * p.maxpg;
-  // lane b looks up the page of the tile's b-th copy, one tile ahead
-  constexpr int kPerTile = Q8 ? 2 : 1;
-  auto lookup = [&](int j) {
-    const int pos = (it.tile0 + j) * kTile + lane * r;
-    return j < it.n && lane < nbox * kPerTile && pos < it.len ? __ldg(bt + pos / p.ps) : -1;
-  };
-  const uint32_t raw0 = base + (it.two ? L::kRaw : L::kTileBytes);
-  const int nraw = it.two ? L::kRawStages : L::kRawStages1;
-  int page_next = lookup(0);
-  int u = 0;                                                   // q8_0: raw stages filled
-  for (int j = 0; j < it.n; ++j) {
-    const int page = page_next;
-    page_next = lookup(j + 1);
-    const int pos = (it.tile0 + j) * kTile + lane * r;
-    const bool mine = lane < nbox * kPerTile;
-    const bool good = page >= 0 && page < p.P;
-    if (mine && pos < it.len && !good && p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
-    const int off = pos % p.ps;
-    // a bit per 8 positions
-    const uint32_t ok = __ballot_sync(~0u, mine && good);
-    const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
-    if (lane == 0) ctl->mask[j % kMasks] = mask;
-    if constexpr (!Q8) {
+  const int r = p.box, nbox = kTile / r;                       // copies of a tile
+  const bool mine = lane < nbox;
+  Ring<L::kStages> ring;
+  Ring<Q8 ? L::kRawStages : 1> raw;
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g;
+  uint32_t jg = 0;                                             // position tiles so far
+  while (walk.next(p.plan, p.seqs, g)) {
+    const int32_t* bt = p.bt + static_cast<size_t>(g.s) * p.maxpg;
+    // lane b looks up the page of the tile's b-th copy, one tile ahead
+    auto lookup = [&](int j) {
+      const int pos = (g.tile0 + j) * kTile + lane * r;
+      return j < g.n && mine && pos < g.len ? __ldg(bt + pos / p.ps) : -1;
+    };
+    int page_next = lookup(0);
+    for (int j = 0; j < g.n; ++j, ++jg) {
+      const int page = page_next;
+      page_next = lookup(j + 1);
+      const int pos = (g.tile0 + j) * kTile + lane * r, off = pos % p.ps;
+      const bool good = mine && page >= 0 && page < p.P;
+      if (mine && pos < g.len && !good && p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
+      // a bit per 8 positions
+      const uint32_t ok = __ballot_sync(~0u, good);
+      const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
+      if (lane == 0) ctl->mask[jg % kMasks] = mask;
       for (int which = 0; which < 2; ++which) {
-        const int c = 2 * j + which, st = c % L::kStages;
-        const uint32_t bar = smem_u32(&ctl->full[st]);
-        if (!mbar_wait(smem_u32(&ctl->empty[st]), ((c / L::kStages) & 1) ^ 1, ctl, p.status)) return;
-        if (lane == 0) mbar_expect(bar, L::kTileBytes);
-        __syncwarp();
-        // a copy out of the pool's range fills its positions with zeros
-        if (mine)
-          tma_5d(base + L::kKv + st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map, (it.kvh * p.ps + off) / 8,
-                 (good ? page : p.P) * 2 + which, bar);
-      }
-    } else {
-      for (int which = 0; which < 2; ++which)
-        for (int h = 0; h < 2; ++h, ++u) {
-          const int st = u % nraw;
-          const uint32_t bar = smem_u32(&ctl->raw_full[st]), dst = raw0 + st * kRawBytes;
-          if (!mbar_wait(smem_u32(&ctl->raw_empty[st]), ((u / nraw) & 1) ^ 1, ctl, p.status)) return;
-          const bool copy = mine && good && lane / nbox == h;
-          const int cnt = __popc(__ballot_sync(~0u, copy));
-          if (lane == 0) mbar_expect(bar, cnt * r * 136);
+        if constexpr (!Q8) {
+          const uint32_t bar = smem_u32(&ctl->full[ring.st]);
+          if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
+          if (lane == 0) mbar_expect(bar, L::kTileBytes);
           __syncwarp();
-          if (copy) {
-            const size_t line = (static_cast<size_t>(page) * 2 + which) * p.Hkv * p.ps +
-                                static_cast<size_t>(it.kvh) * p.ps + off;
-            const int b = lane - h * nbox;
-            bulk_g2s(dst + b * r * 128, p.kv + line * 128, r * 128, bar);
-            bulk_g2s(dst + kRawPos * 128 + b * r * 8, p.kv + p.code_bytes + line * 8, r * 8, bar);
+          // a copy out of the pool's range fills its positions with zeros
+          if (mine)
+            tma_5d(base + L::kKv + ring.st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map, (g.kvh * p.ps + off) / 8,
+                   (good ? page : p.P) * 2 + which, bar);
+          ring.step();
+        } else {
+          const uint32_t bar = smem_u32(&ctl->raw_full[raw.st]), dst = base + L::kRaw + raw.st * kRawBytes;
+          if (!mbar_wait(smem_u32(&ctl->raw_empty[raw.st]), raw.ph ^ 1u, ctl, p.status)) return;
+          if (lane == 0) mbar_expect(bar, __popc(ok) * r * 136);
+          __syncwarp();
+          if (good) {
+            const size_t line = (static_cast<size_t>(page) * 2 + which) * p.plan.Hkv * p.ps +
+                                static_cast<size_t>(g.kvh) * p.ps + off;
+            bulk_g2s(dst + lane * r * 128, p.kv + line * 128, r * 128, bar);
+            bulk_g2s(dst + kTile * 128 + lane * r * 8, p.kv + p.code_bytes + line * 8, r * 8, bar);
           }
+          raw.step();
         }
+      }
     }
   }
 }
 
+// Query tiles (warp 10): TT tokens x G heads x 64 dims a box, as soon as the last S of the segment
+// before has read the tiles -- under that segment's last softmax, values and epilogue.
+template <int D, bool Q8>
+__device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ctl* ctl) {
+  using L = Layout<D, Q8>;
+  const int lane = threadIdx.x & 31;
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g;
+  uint32_t k = 0;
+  while (walk.next(p.plan, p.seqs, g)) {
+    if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status)) return;
+    ++k;
+    if (lane == 0) {
+      for (int t = 0; t < (g.two ? 2 : 1); ++t) {
+        const uint32_t bar = smem_u32(&ctl->qraw[t]);
+        mbar_expect(bar, p.plan.TT * p.plan.G * D * 2);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tma_4d(base + t * L::kTileBytes + h * kTile * 128, &p.qmap, h, g.kvh * p.plan.G,
+                 p.seqs.row0[g.s] + g.tok0 + t * p.plan.TT, bar);
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // --------------------------------------------------------------------------- q8_0 (warps 12-15)
-// Codes to bf16 tiles in the operand layout.  A code becomes fp32 exactly (its byte with the sign
-// flipped is the low mantissa byte of 2^23 + 128 + code), times its f16 scale in fp32, rounded
-// once to bf16.  Positions of pages out of range or behind the sequence become zeros.
+// Codes to fp16 operand tiles.  With its sign bit flipped a code byte is code + 128, and as the low
+// byte of 0x64.. the fp16 1024 + 128 + code; less 1152 that is the code exactly, times the scale
+// rounded once.  Positions of pages out of range or behind the sequence become zeros, values of a
+// scale above 515 (127 * 515 is what fp16 holds) NaN.
 template <int D>
-__device__ __forceinline__ void decode(const AttnParams& p, const Item& it, uint32_t base, Ctl* ctl) {
+__device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* ctl) {
   using L = Layout<D, true>;
   const int tid = threadIdx.x & 127;
-  const uint32_t raw0 = base + (it.two ? L::kRaw : L::kTileBytes);
-  const int nraw = it.two ? L::kRawStages : L::kRawStages1;
-  const int piece = tid & 7, row0 = tid >> 3;       // 16 codes of rows row0 + 16 i
-  int u = 0;
-  for (int j = 0; j < it.n; ++j) {
-    const int p0 = (it.tile0 + j) * kTile;
-    for (int which = 0; which < 2; ++which) {
-      const int c = 2 * j + which, st = c % L::kStages;
-      if (!mbar_wait(smem_u32(&ctl->empty[st]), ((c / L::kStages) & 1) ^ 1, ctl, p.status)) return;
-      const uint32_t dst = base + L::kKv + st * L::kTileBytes + (piece >> 2) * 1024;
-      for (int h = 0; h < 2; ++h, ++u) {
-        const int rs = u % nraw;
-        const uint32_t src = raw0 + rs * kRawBytes;
-        if (!mbar_wait(smem_u32(&ctl->raw_full[rs]), (u / nraw) & 1, ctl, p.status)) return;
-        const uint32_t mask = ctl->mask[j % kMasks];
+  // A thread takes chunks x and x ^ 8 (8 codes, 16 bytes of operand each) of rows tid/8 + 16 i:
+  // odd rows begin with the upper half, which keeps 8-byte reads and 16-byte writes free of conflicts.
+  const int row0 = tid >> 3, x = (tid & 7) | (row0 & 1) << 3;
+  constexpr int NP = 4;
+  Ring<L::kStages> ring;
+  Ring<L::kRawStages> raw;
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g;
+  uint32_t jg = 0;
+  const __half2 bias = __half2half2(__float2half_rn(1152.f));
+  while (walk.next(p.plan, p.seqs, g)) {
+    for (int j = 0; j < g.n; ++j, ++jg) {
+      const int left = g.len - (g.tile0 + j) * kTile;
+      for (int which = 0; which < 2; ++which) {
+        if (!mbar_wait(smem_u32(&ctl->raw_full[raw.st]), raw.ph, ctl, p.status)) return;
+        if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
+        const uint32_t mask = ctl->mask[jg % kMasks];
+        // row0 + 16 i is in group 2 i + row0 / 8 of 8 rows, at row0 % 8 of it
+        const uint32_t src = base + L::kRaw + raw.st * kRawBytes + row0 * 128;
+        const uint32_t ssrc = base + L::kRaw + raw.st * kRawBytes + kTile * 128 + row0 * 8;
+        const uint32_t dst = base + L::kKv + ring.st * L::kTileBytes + (row0 >> 3) * L::kGroup + (row0 & 7) * 128 +
+                             (((x & 7) ^ (row0 & 7)) << 4);
+#pragma unroll 1
+        for (int q = 0; q < kTile / 16; q += NP) {
+          uint32_t w[NP][4];
+          uint16_t sc[NP][2];
 #pragma unroll
-        for (int i = 0; i < kRawPos / 16; ++i) {
-          const int row = row0 + 16 * i, n = h * kRawPos + row;
-          uint32_t w[4];
-          uint16_t sc;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(src + row * 128 + piece * 16));
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc) : "r"(src + kRawPos * 128 + row * 8 + (piece >> 1) * 2));
-          const float d = __half2float(__ushort_as_half(sc));
-          const bool live = ((mask >> (n >> 3)) & 1u) && p0 + n < it.len;
-          uint32_t o[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = w[k] ^ 0x80808080u;
-            float2 a, b;
-            a.x = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440));
-            a.y = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7441));
-            b.x = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7442));
-            b.y = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443));
-            const float2 off = make_float2(-8388736.f, -8388736.f), dd = make_float2(d, d);
-            a = mul2(add2(a, off), dd);
-            b = mul2(add2(b, off), dd);
-            o[2 * k] = live ? bf16x2(a.x, a.y) : 0u;
-            o[2 * k + 1] = live ? bf16x2(b.x, b.y) : 0u;
+          for (int i = 0; i < NP; ++i) {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(src + (q + i) * 2048 + x * 8));
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(src + (q + i) * 2048 + (x ^ 8) * 8));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc[i][0]) : "r"(ssrc + (q + i) * 128 + (x >> 2) * 2));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc[i][1]) : "r"(ssrc + (q + i) * 128 + ((x ^ 8) >> 2) * 2));
           }
-          const uint32_t at = dst + (n >> 3) * L::kGroup + (n & 7) * 128;
-          const uint32_t ch = (piece & 3) * 2;
-          sts16(at + ((ch ^ (n & 7)) << 4), o[0], o[1], o[2], o[3]);
-          sts16(at + (((ch + 1) ^ (n & 7)) << 4), o[4], o[5], o[6], o[7]);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const bool live = ((mask >> (2 * (q + i) + (row0 >> 3))) & 1u) && row0 + 16 * (q + i) < left;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t d = sc[i][c];
+              d = (d & 0x7fffu) > 0x6006u ? 0x7fffu : d;
+              d = live ? __byte_perm(d, 0, 0x1010) : 0u;
+              const __half2 dd = *reinterpret_cast<const __half2*>(&d);
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
+                uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
+                const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
+                const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
+                o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+                o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+              }
+              sts16(dst + (q + i) * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
+            }
+          }
         }
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(smem_u32(&ctl->raw_empty[rs]));
+        warp_arrive(smem_u32(&ctl->raw_empty[raw.st]));
+        fence_async_smem();
+        warp_arrive(smem_u32(&ctl->full[ring.st]));
+        raw.step();
+        ring.step();
       }
-      fence_async_smem();
-      __syncwarp();
-      if ((tid & 31) == 0) mbar_arrive(smem_u32(&ctl->full[st]));
     }
   }
 }
 
 // --------------------------------------------------------------------------- MMAs (warp 9)
 template <int D, bool Q8>
-__device__ __forceinline__ void issue(const AttnParams& p, const Item& it, uint32_t base, Ctl* ctl, uint32_t tm) {
+__device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* ctl, uint32_t tm) {
   using L = Layout<D, Q8>;
-  constexpr uint32_t kIdS = tc_idesc(kTile, kTile, false), kIdO = tc_idesc(kTile, D, true);
+  constexpr uint32_t kIdS = tc_idesc(!Q8, kTile, kTile, false), kIdO = tc_idesc(!Q8, kTile, D, true);
   const int lane = threadIdx.x & 31;
-  auto ring = [&](int c) { return c % L::kStages; };
-  auto wait_full = [&](int c) {
-    const bool ok = mbar_wait(smem_u32(&ctl->full[ring(c)]), (c / L::kStages) & 1, ctl, p.status);
+  uint32_t c0 = 0;                                 // ring entry of the segment's first K tile
+  uint32_t ps = 0, qs = 0;                         // phases of pfull and of the query tiles, a bit for each t
+  auto tile = [&](uint32_t c) { return base + L::kKv + c % L::kStages * L::kTileBytes; };
+  auto wait_full = [&](uint32_t c) {
+    const bool ok = mbar_wait(smem_u32(&ctl->full[c % L::kStages]), (c / L::kStages) & 1, ctl, p.status);
     tc_after();
     return ok;
   };
-  auto release = [&](int c) { tc_commit(smem_u32(&ctl->empty[ring(c)])); };
-  auto scores = [&](int t, int qt, int j) {        // S of tile (stream) t from Q tile qt and K tile j
-    const uint64_t a = tc_desc(base + qt * L::kTileBytes, 16, 1024);
-    const uint64_t b = tc_desc(base + L::kKv + ring(2 * j) * L::kTileBytes, 16, L::kGroup);
+  auto release = [&](uint32_t c) { tc_commit(smem_u32(&ctl->empty[c % L::kStages])); };
+  auto scores = [&](int t, int qt, uint32_t c) {   // S of tile (stream) t from Q tile qt and the K tile in entry c
+    const uint64_t a = tc_desc(base + qt * L::kTileBytes, 16, 1024), b = tc_desc(tile(c), 16, L::kGroup);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
       mma_ss(tm + t * kTile, a + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2, b + (k / 4) * (1024 >> 4) + (k % 4) * 2, kIdS,
@@ -440,280 +532,375 @@ __device__ __forceinline__ void issue(const AttnParams& p, const Item& it, uint3
     tc_commit(smem_u32(&ctl->sfull[t]));
     // the page mask travels with an ordinary arrival: the warp that wrote it arrived on `full`
     if (lane == 0) mbar_arrive(smem_u32(&ctl->sfull[t]));
-  };
-  auto values = [&](int t, int j, bool acc) {      // O of tile (stream) t += P V tile j
-    const uint64_t b = tc_desc(base + L::kKv + ring(2 * j + 1) * L::kTileBytes, 1024, L::kGroup);
-#pragma unroll
-    for (int k = 0; k < kTile / 16; ++k)
-      mma_ts(tm + 2 * kTile + t * D, tm + t * kTile + k * 8, b + k * (2 * L::kGroup >> 4), kIdO, acc || k > 0);
+    __syncwarp();
   };
   // bf16: what a page holds behind the sequence's last position must not meet a weight, not even
   // a zero one (0 * NaN): zeros instead.  (q8_0 tiles are zeroed as they are decoded.)
-  auto trim = [&](int j) {
-    const int first = it.len - (it.tile0 + j) * kTile;
+  auto trim = [&](int first, uint32_t c) {
     if (Q8 || first >= kTile) return;
     const int last = (first + p.box - 1) / p.box * p.box;      // copies behind are zeros already
-    const uint32_t v = base + L::kKv + ring(2 * j + 1) * L::kTileBytes;
+    const uint32_t v = tile(c);
     for (int n = first; n < last; ++n)
       if (lane < D / 8) sts16(v + (n >> 3) * L::kGroup + (lane >> 3) * 1024 + (n & 7) * 128 + (lane & 7) * 16, 0, 0, 0, 0);
     fence_async_smem();
     __syncwarp();
   };
-  auto wait_p = [&](int t, int i) {
-    const bool ok = mbar_wait(smem_u32(&ctl->pfull[t]), i & 1, ctl, p.status);
-    tc_after();
+  // O of tile (stream) t += P times the V tile in entry c, each half of P as it comes; `first` as in trim
+  auto values = [&](int t, uint32_t c, int first, bool acc) {
+    const uint64_t b = tc_desc(tile(c), 1024, L::kGroup);
+    const uint32_t ph = (ps >> t) & 1;
+    ps ^= 1u << t;
+    if (!wait_full(c)) return false;
+    trim(first, c);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!mbar_wait(smem_u32(&ctl->pfull[t][h]), ph, ctl, p.status)) return false;
+      tc_after();
+#pragma unroll
+      for (int k = 4 * h; k < 4 * h + 4; ++k)
+        mma_ts(tm + 2 * kTile + t * D, tm + t * kTile + k * 8, b + k * (2 * L::kGroup >> 4), kIdO, acc || k > 0);
+    }
+    return true;
+  };
+  auto wait_q = [&](int t) {
+    const bool ok = mbar_wait(smem_u32(Q8 ? &ctl->qbar[t] : &ctl->qraw[t]), (qs >> t) & 1, ctl, p.status);
+    qs ^= 1u << t;
     return ok;
   };
-  if (!mbar_wait(smem_u32(&ctl->qbar[0]), 0, ctl, p.status)) return;
-  if (it.two) {
-    if (!mbar_wait(smem_u32(&ctl->qbar[1]), 0, ctl, p.status)) return;
-    tc_after();
-    if (!wait_full(0)) return;
-    scores(0, 0, 0);
-    scores(1, 1, 0);
-    release(0);
-    for (int j = 0; j < it.n; ++j) {
-      const bool more = j + 1 < it.n;
-      if (!wait_p(0, j) || !wait_full(2 * j + 1)) return;
-      trim(j);
-      values(0, j, j > 0);
-      if (more) {
-        if (!wait_full(2 * j + 2)) return;
-        scores(0, 0, j + 1);
+  auto done_q = [&]() { tc_commit(smem_u32(&ctl->qfree)); };
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g;
+  while (walk.next(p.plan, p.seqs, g)) {
+    const uint32_t c = c0;
+    const int left = g.len - g.tile0 * kTile;
+    if (!wait_q(0)) return;
+    if (g.two) {
+      if (!wait_q(1) || !wait_full(c)) return;
+      scores(0, 0, c);
+      scores(1, 1, c);
+      release(c);
+      if (g.n == 1) done_q();
+      for (int j = 0; j < g.n; ++j) {
+        const bool more = j + 1 < g.n;
+        const uint32_t v = c + 2 * j + 1;
+        if (!values(0, v, left - j * kTile, j > 0)) return;
+        if (more) {
+          if (!wait_full(v + 1)) return;
+          scores(0, 0, v + 1);
+        }
+        if (!values(1, v, kTile, j > 0)) return;
+        release(v);
+        if (more) {
+          scores(1, 1, v + 1);
+          release(v + 1);
+          if (j + 2 == g.n) done_q();
+        }
       }
-      if (!wait_p(1, j)) return;
-      values(1, j, j > 0);
-      release(2 * j + 1);
-      if (more) {
-        scores(1, 1, j + 1);
-        release(2 * j + 2);
+    } else {
+      for (int j = 0; j < 2 && j < g.n; ++j) {
+        if (!wait_full(c + 2 * j)) return;
+        scores(j, 0, c + 2 * j);
+        release(c + 2 * j);
+      }
+      if (g.n <= 2) done_q();
+      for (int j = 0; j < g.n; ++j) {
+        const int t = j & 1;
+        const uint32_t v = c + 2 * j + 1;
+        if (!values(t, v, left - j * kTile, j > 1)) return;
+        release(v);
+        if (j + 2 < g.n) {
+          if (!wait_full(v + 3)) return;
+          scores(t, 0, v + 3);
+          release(v + 3);
+          if (j + 3 == g.n) done_q();
+        }
       }
     }
-  } else {
-    tc_after();
-    for (int j = 0; j < 2 && j < it.n; ++j) {
-      if (!wait_full(2 * j)) return;
-      scores(j, 0, j);
-      release(2 * j);
-    }
-    for (int j = 0; j < it.n; ++j) {
-      const int t = j & 1;
-      if (!wait_p(t, j >> 1) || !wait_full(2 * j + 1)) return;
-      trim(j);
-      values(t, j, j > 1);
-      release(2 * j + 1);
-      if (j + 2 < it.n) {
-        if (!wait_full(2 * j + 4)) return;
-        scores(t, 0, j + 2);
-        release(2 * j + 4);
-      }
-    }
+    tc_commit(smem_u32(&ctl->ofull));
+    c0 += 2 * g.n;
   }
-  tc_commit(smem_u32(&ctl->ofull));
 }
 
 // --------------------------------------------------------------------------- softmax (warps 0-7)
+// q8_0: a thread's landed query row over 2^e as fp16, in place, e the exponent of its largest
+// magnitude; returns 2^e.  (Rows of the tile behind the unit's hold anything.)
+template <int D>
+__device__ __forceinline__ float convert_q(uint32_t tile, int row) {
+  constexpr int CH = D / 8;
+  auto at = [&](int ch) { return tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
+  uint32_t w[CH][4];
+  float mx = 0.f;
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[ch][0]), "=r"(w[ch][1]), "=r"(w[ch][2]), "=r"(w[ch][3])
+                 : "r"(at(ch)));
+  }
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = max3(mx, fabsf(bf_lo(w[ch][k])), fabsf(bf_hi(w[ch][k])));
+  int e = static_cast<int>(__float_as_uint(mx) >> 23);
+  e = e == 0 || e == 255 ? 127 : e == 254 ? 253 : e;       // (zero rows; infinities end in exact_row)
+  const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = f16x2(bf_lo(w[ch][k]) * down, bf_hi(w[ch][k]) * down);
+    sts16(at(ch), o[0], o[1], o[2], o[3]);
+  }
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
 template <int D, bool Q8>
-__device__ __forceinline__ void softmax(const AttnParams& p, const Item& it, uint32_t base, uint8_t* smem, Ctl* ctl,
-                                        uint32_t tm) {
-  using L = Layout<D, Q8>;
+__device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl* ctl, uint32_t tm) {
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
-  const int urow0 = it.two ? t * p.TT * p.G : 0;    // first row of the tile within the unit
-  const int trows = p.TT * p.G;
-  const int rows = min(trows, it.ntok * p.G - urow0);
-  // the tile's query rows into the operand layout (K-major, 128-byte swizzle), zeros behind them
-  if (it.two || t == 0) {
-    const uint16_t* q = p.q + static_cast<size_t>(p.seqs.row0[it.s] + it.tok0 + (it.two ? t * p.TT : 0)) * p.q_stride +
-                        static_cast<size_t>(it.kvh) * p.G * D;
-    const uint32_t dst = base + t * L::kTileBytes;
-    constexpr int CH = D / 8;
-#pragma unroll 8
-    for (int i = 0; i < CH; ++i) {
-      const int x = i * 128 + row, rr = x / CH, ch = x % CH;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < rows) {
-        const int tok = rr / p.G;
-        w = __ldg(reinterpret_cast<const uint4*>(q + tok * p.q_stride + (rr - tok * p.G) * D) + ch);
-      }
-      sts16(dst + (ch >> 3) * (kTile * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), w.x, w.y, w.z, w.w);
-    }
-    fence_async_smem();
-    mbar_arrive(smem_u32(&ctl->qbar[t]));
-  }
-  const bool live = row < rows;
-  // rows behind the last see everything, so that they never ask for a mask
-  const int pos = live ? it.pos0 + (it.two ? t * p.TT : 0) + row / p.G : INT32_MAX;
-  const int mine = it.two ? it.n : (it.n - t + 1) / 2;
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t ts = tm + t * kTile + lane_base, to = tm + 2 * kTile + t * D + lane_base;
-  const float c = p.c, grow = 8.0f / c;
-  float m = -INFINITY, l = 0.f;
-  bool ok = true;
-  for (int i = 0; i < mine; ++i) {
-    const int j = it.two ? i : 2 * i + t;
-    ok = mbar_wait(smem_u32(&ctl->sfull[t]), i & 1, ctl, p.status);
-    if (!ok) break;
-    tc_after();
-    float s[kTile];
-#pragma unroll
-    for (int k = 0; k < kTile; k += 32) tc_ld32(ts + k, s + k);
-    tc_wait_ld();
-    const int limit = pos - (it.tile0 + j) * kTile;          // last column this row sees
-    const uint32_t mask = ctl->mask[j % kMasks];
-    if (__any_sync(~0u, limit < kTile - 1 || mask != 0xffffu)) {
-#pragma unroll
-      for (int k = 0; k < kTile; ++k)
-        if (k > limit || !((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
+  const uint32_t ts = tm + t * kTile + lane_base, to = tm + 2 * kTile + lane_base;
+  constexpr float kBias = Q8 ? 6.f : 0.f;          // weights carry 2^kBias
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g, next;
+  bool have = walk.next(p.plan, p.seqs, g);
+  uint32_t phase = 0, jg = 0, seg = 0;             // tiles of this stream, position tiles, segments so far
+  uint32_t qs = 0, qr = 0, joins = 0;              // phases of qbar[0], this warpgroup's qraw, and join
+  // both warpgroups: what either wrote before is the other's to read
+  auto join = [&]() {
+    warp_arrive(smem_u32(&ctl->join));
+    return mbar_wait(smem_u32(&ctl->join), joins++ & 1, ctl, p.status);
+  };
+  float cq = p.c;                                  // the row's constant
+  // q8_0: the next segment's rows of this warpgroup's tile
+  auto take_q = [&](const Segment& n) {
+    if constexpr (Q8) {
+      if (!n.two && t == 1) return true;
+      if (!mbar_wait(smem_u32(&ctl->qraw[t]), qr & 1, ctl, p.status)) return false;
+      ++qr;
+      cq = p.c * convert_q<D>(base + t * Layout<D, Q8>::kTileBytes, row);
+      if (!n.two) static_cast<CtlQ8*>(ctl)->rowc[row] = cq;
+      fence_async_smem();
+      warp_arrive(smem_u32(&ctl->qbar[t]));
     }
-    float mx[4] = {s[0], s[1], s[2], s[3]};
+    return true;
+  };
+  if (have && !take_q(g)) return;
+  while (have) {
+    const int trows = p.plan.TT * p.plan.G;
+    const int urow0 = g.two ? t * trows : 0;       // first row of the tile within the unit
+    const int rows = min(trows, g.ntok * p.plan.G - urow0);
+    const bool live = row < rows, any = warp * 32 < rows;
+    // rows behind the last see everything, so that they never ask for a mask
+    const int pos = live ? g.pos0 + ((urow0 + row) * p.plan.by_G >> 16) : INT32_MAX;
+    const int mine = g.two ? g.n : (g.n - t + 1) / 2;
+    float c = cq;
+    if constexpr (Q8) {
+      if (!g.two && t == 1 && mine > 0) {          // stream 1 takes the constants of stream 0's rows
+        if (!mbar_wait(smem_u32(&ctl->qbar[0]), qs & 1, ctl, p.status)) return;
+        c = static_cast<CtlQ8*>(ctl)->rowc[row];
+      }
+      ++qs;
+    }
+    const float grow = 8.0f / c;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < mine; ++i) {
+      const int j = g.two ? i : 2 * i + t;
+      if (!mbar_wait(smem_u32(&ctl->sfull[t]), phase & 1, ctl, p.status)) return;
+      ++phase;
+      if (any) {                                   // (warps without rows leave their lanes as they are)
+        tc_after();
+        float s[kTile];
 #pragma unroll
-    for (int k = 4; k < kTile; ++k) mx[k % 4] = fmaxf(mx[k % 4], s[k]);
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    // The reference moves only when the maximum outgrows it by 2^8: until then weights up to 2^8
-    // are as exact in bf16 and fp32 as weights up to 1, and O needs no rescaling.
-    if (i == 0) {
-      m = top;
-    } else {
-      const bool up = top > m + grow;
-      if (__any_sync(~0u, up)) {
-        const float mn = up ? top : m;
-        const float f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
-        l *= f;
-        m = mn;
-        // the previous P V is complete: S, issued after it, is
-        const float2 ff = make_float2(f, f);
+        for (int k = 0; k < kTile; k += 32) tc_ld32(ts + k, s + k);
+        tc_wait_ld();
+        const int limit = pos - (g.tile0 + j) * kTile;         // last column this row sees
+        const uint32_t mask = ctl->mask[(jg + j) % kMasks];
+        if (__any_sync(~0u, limit < kTile - 1 || mask != 0xffffu)) {
 #pragma unroll
-        for (int k = 0; k < D; k += 16) {
-          float o[16];
-          tc_ld16(to + k, o);
-          tc_wait_ld();
+          for (int k = 0; k < kTile; ++k)
+            if (k > limit || !((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float2 x = mul2(make_float2(o[e], o[e + 1]), ff);
-            o[e] = x.x;
-            o[e + 1] = x.y;
+        for (int k = 4; k < kTile - 4; k += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + e], s[k + 4 + e]);
+        }
+        const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], s[kTile - 4], s[kTile - 3]),
+                               fmaxf(s[kTile - 2], s[kTile - 1]));
+        // The reference moves only when the maximum outgrows it by 2^8: until then weights up to 2^8
+        // are as exact in the operands and in fp32 as weights up to 1, and O needs no rescaling.
+        if (i == 0) {
+          m = top;
+        } else {
+          const bool up = top > m + grow;
+          if (__any_sync(~0u, up)) {
+            const float mn = up ? top : m;
+            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+            l *= f;
+            m = mn;
+            // the previous P V is complete: S, issued after it, is
+            const float2 ff = make_float2(f, f);
+#pragma unroll
+            for (int k = 0; k < D; k += 16) {
+              float o[16];
+              tc_ld16(to + t * D + k, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const float2 x = mul2(make_float2(o[e], o[e + 1]), ff);
+                o[e] = x.x;
+                o[e + 1] = x.y;
+              }
+              tc_st16(to + t * D + k, o);
+            }
           }
-          tc_st16(to + k, o);
+        }
+        const float mb = m == -INFINITY ? 0.f : kBias - m * c;
+        const float2 cc = make_float2(c, c), mm = make_float2(mb, mb);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = h * 32 + 2 * k;
+            const float2 x = fma2(make_float2(s[e], s[e + 1]), cc, mm);
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            sum[k & 1] = add2(sum[k & 1], y);
+            w[k] = Q8 ? f16x2(y.x, y.y) : bf16x2(y.x, y.y);
+          }
+          tc_st16(ts + h * 16, w);
+          if (h & 1) {                             // half of P: its products start
+            tc_wait_st();
+            tc_before();
+            warp_arrive(smem_u32(&ctl->pfull[t][h / 2]));
+          }
+        }
+        const float2 sm = add2(sum[0], sum[1]);
+        l += sm.x + sm.y;
+      } else {
+        warp_arrive(smem_u32(&ctl->pfull[t][0]));
+        warp_arrive(smem_u32(&ctl->pfull[t][1]));
+      }
+    }
+    if (!mbar_wait(smem_u32(&ctl->ofull), seg & 1, ctl, p.status)) return;
+    tc_after();
+    jg += g.n;
+    // the next segment's rows, so that its first scores run under this one's epilogue
+    have = walk.next(p.plan, p.seqs, next);
+    if (have && !take_q(next)) return;
+
+    // m and l in powers of two; a row without a position has m = -inf and l = 0
+    m = m == -INFINITY ? m : m * c;
+    float f[2] = {g.two && t == 1 ? 0.f : 1.f, g.two && t == 1 ? 1.f : 0.f};
+    if (!g.two) {
+      // two streams of the same rows: both warpgroups read both outputs, each half of the columns
+      ctl->ml[t][row] = make_float2(m, l);
+      if (!join()) return;
+      const float2 a = ctl->ml[0][row], b = ctl->ml[1][row];
+      m = fmaxf(a.x, b.x);
+      f[0] = a.x == -INFINITY ? 0.f : ex2(a.x - m);
+      f[1] = b.x == -INFINITY ? 0.f : ex2(b.x - m);
+      l = a.y * f[0] + b.y * f[1];
+    }
+    if (any) {
+      const int urow = urow0 + row;
+      const int tok = urow * p.plan.by_G >> 16;
+      const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + urow - tok * p.plan.G;
+      float* part = p.part + (static_cast<size_t>(max(g.slot, 0)) * p.plan.urows + urow) * (D + 4);
+      uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      bool odd = false;
+      const int k0 = g.two ? 0 : t * (D / 2), k1 = g.two ? D : k0 + D / 2;
+#pragma unroll 1
+      for (int k = k0; k < k1; k += 32) {
+        float x[32];
+        tc_ld32(to + (g.two ? t * D : 0) + k, x);
+        tc_wait_ld();
+        if (!g.two) {
+          if (g.n > 1) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              float y[16];
+              tc_ld16(to + D + k + e, y);
+              tc_wait_ld();
+#pragma unroll
+              for (int z = 0; z < 16; ++z) x[e + z] = x[e + z] * f[0] + y[z] * f[1];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] *= f[0];
+          }
+        }
+        if (live && g.slot >= 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = bf16x2(x[e] * inv, x[e + 1] * inv);
+            w.y = bf16x2(x[e + 2] * inv, x[e + 3] * inv);
+            w.z = bf16x2(x[e + 4] * inv, x[e + 5] * inv);
+            w.w = bf16x2(x[e + 6] * inv, x[e + 7] * inv);
+            *reinterpret_cast<uint4*>(out + k + e) = w;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) odd |= !(fabsf(x[e] * inv) <= 3.3e38f);
+        }
+        __syncwarp();
+      }
+      if (live && g.slot >= 0 && (g.two || t == 0)) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
+      // rows that are not finite, again from the cache (each warpgroup those it saw; where both see
+      // one they write the same)
+      if (g.slot < 0) {
+        for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
+          const int who = __ffs(todo) - 1;
+          const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
+          __threadfence_block();
+          exact_row<D, Q8>(p, rr, hh);
         }
       }
     }
-    const float mb = m == -INFINITY ? 0.f : -m * c;
-    const float2 cc = make_float2(c, c), mm = make_float2(mb, mb);
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t w[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int e = h * 32 + 2 * k;
-        const float2 x = fma2(make_float2(s[e], s[e + 1]), cc, mm);
-        const float2 y = make_float2(ex2(x.x), ex2(x.y));
-        sum[k & 1] = add2(sum[k & 1], y);
-        w[k] = bf16x2(y.x, y.y);
-      }
-      tc_st16(ts + h * 16, w);
+    // neither stream's next values may overwrite an output that the other warpgroup still reads
+    if (!g.two) {
+      tc_before();
+      if (!join()) return;
     }
-    const float2 sm = add2(sum[0], sum[1]);
-    l += sm.x + sm.y;
-    tc_wait_st();
-    tc_before();
-    mbar_arrive(smem_u32(&ctl->pfull[t]));
+    ++seg;
+    g = next;
   }
-  if (ok) ok = mbar_wait(smem_u32(&ctl->ofull), 0, ctl, p.status);
-  tc_after();
-  // m and l in powers of two; a row without a position has m = -inf and l = 0
-  m = m == -INFINITY ? m : m * c;
-  float f0 = 1.f, f1 = 0.f;
-  float* other = reinterpret_cast<float*>(smem + L::kQ);   // stream 1's O, [D][128]: every MMA has read Q by now
-  const bool merge = !it.two;
-  if (merge) {
-    if (t == 1 && ok && warp * 32 < rows) {
-#pragma unroll 1
-      for (int k = 0; k < D; k += 32) {
-        float o[32];
-        if (mine > 0) {
-          tc_ld32(to + k, o);
-          tc_wait_ld();
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) other[(k + e) * 128 + row] = mine > 0 ? o[e] : 0.f;
-      }
-      ctl->m[row] = m;
-      ctl->l[row] = l;
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (t == 1) return;
-    const float m1 = ctl->m[row], l1 = ctl->l[row];
-    const float mt = fmaxf(m, m1);
-    if (mt != -INFINITY) {
-      f0 = ex2(m - mt);
-      f1 = ex2(m1 - mt);
-    }
-    l = l * f0 + l1 * f1;
-    m = mt;
-  }
-  if (!ok || warp * 32 >= rows) return;
-  const int urow = urow0 + row, tok = it.tok0 + urow / p.G, g = urow % p.G;
-  float* part = nullptr;
-  uint16_t* out = nullptr;
-  float inv = 1.f;
-  if (it.nsplit > 1) {
-    part = p.part + part_at(p, it.s, it.tok0 / (2 * p.TT), it.kvh, it.split, D) + static_cast<size_t>(urow) * (D + 4);
-  } else {
-    out = p.out + (static_cast<size_t>(p.seqs.row0[it.s] + tok) * p.Hq + it.kvh * p.G + g) * D;
-    inv = l == 0.f ? 0.f : 1.0f / l;
-  }
-#pragma unroll 1
-  for (int k = 0; k < D; k += 32) {
-    float x[32];
-    tc_ld32(to + k, x);
-    tc_wait_ld();
-    if (merge) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[e] = x[e] * f0 + other[(k + e) * 128 + row] * f1;
-    }
-    if (live && part != nullptr) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(part + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-    } else if (live) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint4 w;
-        w.x = bf16x2(x[e] * inv, x[e + 1] * inv);
-        w.y = bf16x2(x[e + 2] * inv, x[e + 3] * inv);
-        w.z = bf16x2(x[e + 4] * inv, x[e + 5] * inv);
-        w.w = bf16x2(x[e + 6] * inv, x[e + 7] * inv);
-        *reinterpret_cast<uint4*>(out + k + e) = w;
-      }
-    }
-    __syncwarp();
-  }
-  if (part != nullptr && live) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
 }
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using L = Layout<D, Q8>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::kCtl);
   const int warp = threadIdx.x >> 5;
-  Item it;
-  if (!find_item(p, it)) return;
+  if (base & 1023u) {                              // the operand layouts need it; dynamic shared memory starts so
+    if (p.status) *p.status = MK_ERR_UNSUPPORTED;
+    return;
+  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i) {                   // (q8_0: a K or V tile is the decode warps' work)
       mbar_init(smem_u32(&ctl->full[i]), Q8 ? 4 : 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
       mbar_init(smem_u32(&ctl->raw_full[i]), 1);
       mbar_init(smem_u32(&ctl->raw_empty[i]), 4);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&ctl->qbar[t]), 128);
+      mbar_init(smem_u32(&ctl->qraw[t]), 1);
+      mbar_init(smem_u32(&ctl->qbar[t]), 4);
       mbar_init(smem_u32(&ctl->sfull[t]), 2);
-      mbar_init(smem_u32(&ctl->pfull[t]), 128);
+      mbar_init(smem_u32(&ctl->pfull[t][0]), 4);
+      mbar_init(smem_u32(&ctl->pfull[t][1]), 4);
     }
+    mbar_init(smem_u32(&ctl->qfree), 1);
     mbar_init(smem_u32(&ctl->ofull), 1);
+    mbar_init(smem_u32(&ctl->join), 8);
     ctl->abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -725,19 +912,20 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
   __syncthreads();
   tc_after();
   const uint32_t tm = ctl->tmem;
-  // registers follow the work: a softmax thread holds a row of S (sum over the warpgroups within the launch's)
+  // registers follow the work: a softmax thread holds a row of S (the warpgroups' sum is the launch's)
   if (warp < 8) {
     if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    softmax<D, Q8>(p, it, base, smem, ctl, tm);
+    softmax<D, Q8>(p, base, ctl, tm);
   } else if (warp < 12) {
     if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) produce<D, Q8>(p, it, base, ctl);
-    if (warp == 9) issue<D, Q8>(p, it, base, ctl, tm);
+    if (warp == 8) produce<D, Q8>(p, base, ctl);
+    if (warp == 9) issue<D, Q8>(p, base, ctl, tm);
+    if (warp == 10) produce_q<D, Q8>(p, base, ctl);
   } else if constexpr (Q8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    decode<D>(p, it, base, ctl);
+    decode<D>(p, base, ctl);
   }
   __syncwarp();
   tc_before();
@@ -754,80 +942,59 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-// Merges the splits of split sequences, in split order: a warp per (row, query head).
-template <int D>
+// Merges the items that the ranges cut, in block order: blockIdx.x is the block that began one, a
+// warp takes a row.
+template <int D, bool Q8>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ AttnParams p) {
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (unit >= static_cast<int64_t>(p.seqs.row0[p.seqs.n]) * p.Hq) return;
-  const int r = static_cast<int>(unit / p.Hq), h = static_cast<int>(unit - static_cast<int64_t>(r) * p.Hq);
-  const int s = seq_of_row(p.seqs, r), ns = p.plan.nsplit[s];
-  if (ns == 1) return;
-  const int chunk = p.seqs.row0[s + 1] - p.seqs.row0[s], i = r - p.seqs.row0[s], UT = 2 * p.TT, u = i / UT;
-  const int last = p.seqs.len[s] - chunk + min(chunk, (u + 1) * UT) - 1;       // the unit's last position
-  const int n = (last / kTile) / p.plan.split_tiles + 1;                       // splits it has
-  const int urows = min(chunk, UT) * p.G, urow = (i - u * UT) * p.G + h % p.G;
-  const float* part = p.part + part_at(p, s, u, h / p.G, 0, D) + static_cast<size_t>(urow) * (D + 4);
-  const size_t step = static_cast<size_t>(urows) * (D + 4);
+  const AttnPlan& pl = p.plan;
+  const int b = blockIdx.x, lane = threadIdx.x & 31, urow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int item = pl.start[b + 1].item;
+  if (pl.start[b + 1].tile == 0 || (pl.start[b].item == item && pl.start[b].tile > 0)) return;
+  Segment g;
+  item_of(pl, p.seqs, item, g);
+  if (urow >= g.ntok * pl.G) return;
+  int n = 2;                                       // partials: the beginning, and each range that starts inside
+  while (b + n <= pl.blocks && pl.start[b + n].item == item) ++n;
+  const size_t row = static_cast<size_t>(pl.urows) * (D + 4);
+  auto at = [&](int k) { return p.part + static_cast<size_t>(2 * (b + k) + (k == 0 ? 1 : 0)) * row +
+                                static_cast<size_t>(urow) * (D + 4); };
   float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, part[k * step + D]);
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, at(k)[D]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
   constexpr int V = D / 32;
   float acc[V] = {}, L = 0.f;
-  if (M != -INFINITY)
-    for (int k = 0; k < n; ++k) {
-      const float* pk = part + k * step;
-      const float2 ml = *reinterpret_cast<const float2*>(pk + D);
-      const float f = ex2(ml.x - M);
-      L += f * ml.y;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float* pk = at(k);
+    const float2 ml = *reinterpret_cast<const float2*>(pk + D);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    L += f * ml.y;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, pk[lane * V + v], acc[v]);
-    }
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(f, pk[lane * V + v], acc[v]);
+  }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
+  const int r = p.seqs.row0[g.s] + g.tok0 + urow / pl.G, h = g.kvh * pl.G + urow % pl.G;
   uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D + lane * V;
+  bool odd = false;
 #pragma unroll
-  for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(out + v) = bf16x2(acc[v] * inv, acc[v + 1] * inv);
+  for (int v = 0; v < V; v += 2) {
+    *reinterpret_cast<uint32_t*>(out + v) = bf16x2(acc[v] * inv, acc[v + 1] * inv);
+    odd |= !(fabsf(acc[v] * inv) <= 3.3e38f) || !(fabsf(acc[v + 1] * inv) <= 3.3e38f);
+  }
+  if (__any_sync(~0u, odd)) exact_row<D, Q8>(p, r, h);
 }
 
 // --------------------------------------------------------------------------- host
-constexpr int kSms = 152;
-
-// Splits the positions so that the blocks come out even, where they would not by themselves.
-// Returns the number of blocks; *floats: the workspace.
-int64_t make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t* floats) {
-  const int G = c.num_q_heads / c.num_kv_heads, UT = 2 * (kTile / G);
-  pl->n = 0;
-  int64_t work = 0;
-  for (int s = 0; s < q.n; ++s) {
-    const int chunk = q.row0[s + 1] - q.row0[s];
-    pl->nsplit[s] = 1;
-    pl->part0[s] = 0;
-    if (chunk == 0) continue;
-    pl->seq[pl->n++] = s;
-    for (int64_t t0 = 0; t0 < chunk; t0 += UT)
-      work += int64_t(c.num_kv_heads) * ((q.len[s] - chunk + std::min<int64_t>(chunk, t0 + UT) - 1) / kTile + 1);
-  }
-  std::sort(pl->seq, pl->seq + pl->n, [&](int a, int b) { return q.len[a] != q.len[b] ? q.len[a] > q.len[b] : a < b; });
-  const int64_t even = (work + kSms - 1) / kSms;
-  pl->split_tiles = static_cast<int32_t>(std::max<int64_t>(even, 4));
-  int64_t items = 0;
-  size_t at = 0;
-  for (int i = 0; i < pl->n; ++i) {
-    const int s = pl->seq[i], chunk = q.row0[s + 1] - q.row0[s];
-    const int64_t units = (chunk + UT - 1) / UT, tiles = (q.len[s] - 1) / kTile + 1;
-    const int64_t ns = (tiles + pl->split_tiles - 1) / pl->split_tiles;
-    pl->nsplit[s] = static_cast<int32_t>(ns);
-    pl->item0[i] = static_cast<int32_t>(items);
-    items += units * c.num_kv_heads * ns;
-    if (ns > 1) {
-      pl->part0[s] = static_cast<int64_t>(at);
-      at += static_cast<size_t>(units * c.num_kv_heads * ns) * std::min(chunk, UT) * G * (c.head_dim + 4);
-    }
-  }
-  pl->item0[pl->n] = static_cast<int32_t>(items);
-  *floats = at;
-  return items;
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
+                                                                : nullptr;
+  }();
+  return encode;
 }
 
 // bf16 pages to TMA, innermost first: {64 dims, 8 positions, D/64 spans of dims, groups of 8
@@ -835,13 +1002,7 @@ int64_t make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, siz
 // 8-position groups a constant distance apart whatever the page size, which is what the operand
 // descriptors of both K (rows along dims) and V (rows along positions) need.
 int encode_pages(const mk_cache_shape& c, const void* kv, int box_pos, CUtensorMap* out) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
-                                                                : nullptr;
-  }();
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
   if (!encode) return chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t D = c.head_dim, ps = c.page_size, hkv = c.num_kv_heads;
   const cuuint64_t dims[5] = {64, 8, D / 64, hkv * ps / 8, static_cast<cuuint64_t>(c.num_pages) * 2};
@@ -854,17 +1015,32 @@ int encode_pages(const mk_cache_shape& c, const void* kv, int box_pos, CUtensorM
   return r == CUDA_SUCCESS ? MK_OK : chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
 }
 
+// Query rows to TMA: {64 dims, D/64 spans, heads, rows}; a box of TT rows x G heads lands as a tile's
+// [row][128 B], rows behind the call's as zeros.
+int encode_queries(const mk_cache_shape& c, const AttnPlan& pl, const void* q, int64_t stride, int rows, CUtensorMap* out) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
+  if (!encode) return chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t D = c.head_dim;
+  const cuuint64_t dims[4] = {64, D / 64, static_cast<cuuint64_t>(c.num_q_heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[3] = {128, D * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(pl.G), static_cast<cuuint32_t>(pl.TT)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MK_OK : chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", static_cast<int>(r));
+}
+
 template <int D, bool Q8>
-cudaError_t launch(const AttnParams& p, unsigned blocks, bool merge, cudaStream_t st) {
+cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   // (idempotent and cheap next to a launch; per device, so set on every call)
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem_bytes<D, Q8>()));
   if (e != cudaSuccess) return e;
-  attn_kernel<D, Q8><<<blocks, Layout<D, Q8>::kThreads, smem_bytes<D, Q8>(), st>>>(p);
+  attn_kernel<D, Q8><<<p.plan.blocks, Layout<D, Q8>::kThreads, smem_bytes<D, Q8>(), st>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !merge) return e;
-  const int64_t warps = static_cast<int64_t>(p.seqs.row0[p.seqs.n]) * p.Hq;
-  merge_kernel<D><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(p);
+  if (e != cudaSuccess || !p.plan.ranged) return e;
+  merge_kernel<D, Q8><<<dim3(p.plan.blocks, (p.plan.urows + 7) / 8), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -881,7 +1057,7 @@ extern "C" int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t
   if (!bytes_out) return chunk_fail(MK_ERR_INVALID_ARG, "bytes_out is NULL");
   AttnPlan plan;
   size_t floats = 0;
-  make_plan(*shape, seqs, &plan, &floats);
+  if (!make_plan(*shape, seqs, &plan, &floats)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
   *bytes_out = floats * sizeof(float);
   return MK_OK;
 }
@@ -896,6 +1072,7 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   const mk_cache_shape& c = *shape;
   if (q_stride < static_cast<int64_t>(c.num_q_heads) * c.head_dim || q_stride % 8)
     return chunk_fail(MK_ERR_INVALID_ARG, "q_stride must be a multiple of 8, at least num_q_heads*head_dim");
+  if (q_stride >= int64_t(1) << 38) return chunk_fail(MK_ERR_UNSUPPORTED, "q_stride above 2^38");
   const int rows = p.seqs.row0[num_seqs];
   if (rows > 0 && (!block_tables || !q || !kv_layer || !out))
     return chunk_fail(MK_ERR_INVALID_ARG, "a pointer argument is NULL");
@@ -903,8 +1080,7 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
       misaligned(workspace, 16))
     return chunk_fail(MK_ERR_INVALID_ARG, "pointers must be 16-byte aligned (block_tables 4-byte)");
   size_t floats = 0;
-  const int64_t items = make_plan(c, p.seqs, &p.plan, &floats);
-  if (items >= (int64_t(1) << 31)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
+  if (!make_plan(c, p.seqs, &p.plan, &floats)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
   if (workspace_bytes < floats * sizeof(float) || (floats > 0 && !workspace))
     return chunk_fail(MK_ERR_INVALID_ARG, "the workspace holds %zu bytes; these lengths need %zu", workspace_bytes,
                       floats * sizeof(float));
@@ -912,7 +1088,9 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   rc = clear_status(status_out, st);
   if (rc || rows == 0) return rc;
   const bool q8 = (c.flags & MK_FLAG_KV_Q8) != 0;
-  p.box = std::min(c.page_size & -c.page_size, q8 ? kRawPos : kTile);
+  p.box = std::min(c.page_size & -c.page_size, kTile);
+  rc = encode_queries(c, p.plan, q, q_stride, rows, &p.qmap);
+  if (rc) return rc;
   if (!q8) {
     rc = encode_pages(c, kv_layer, p.box, &p.map);
     if (rc) return rc;
@@ -926,16 +1104,10 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   p.part = static_cast<float*>(workspace);
   p.code_bytes = static_cast<size_t>(c.num_pages) * 2 * c.num_kv_heads * c.page_size * c.head_dim;
   p.Hq = c.num_q_heads;
-  p.Hkv = c.num_kv_heads;
-  p.G = c.num_q_heads / c.num_kv_heads;
-  p.TT = kTile / p.G;
   p.ps = c.page_size;
   p.P = c.num_pages;
   p.maxpg = c.max_pages_per_seq;
   p.c = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));
-  const unsigned blocks = static_cast<unsigned>(items);
-  const cudaError_t e = q8 ? launch<128, true>(p, blocks, floats > 0, st)
-                           : c.head_dim == 128 ? launch<128, false>(p, blocks, floats > 0, st)
-                                               : launch<64, false>(p, blocks, floats > 0, st);
+  const cudaError_t e = q8 ? launch<128, true>(p, st) : c.head_dim == 128 ? launch<128, false>(p, st) : launch<64, false>(p, st);
   return e == cudaSuccess ? MK_OK : chunk_fail(MK_ERR_CUDA, "chunk attention: %s", cudaGetErrorString(e));
 }

@@ -92,12 +92,13 @@ def head_norm(x, gain, eps):
 
 
 def attention(st: Setup, q, kv, drop=None):
-    """(out, weight, shift) in 64 bits for query rows q [rows][Hq][D]: the attention output;
-    sum_t p_t |v_t|, what a relative error of the weights scales with; and the largest
-    sum_d |q_d k_td| / sqrt(D) of a row, what a relative error of the keys shifts scores by.
+    """(out, weight, shift, total) in 64 bits for query rows q [rows][Hq][D]: the attention output;
+    sum_t p_t |v_t|, what a relative error of the weights scales with; the largest
+    sum_d |q_d k_td| / sqrt(D) of a row, what a relative error of the keys shifts scores by; and
+    sum_t |v_t|, what an absolute error of the weights scales with.
     ``drop``: bool [num_seqs][max length], positions whose page is out of range."""
     out = torch.zeros(st.rows, st.hq, st.d, dtype=torch.float64, device=q.device)
-    weight, shift = torch.zeros_like(out), torch.zeros(st.rows, st.hq, 1, dtype=torch.float64, device=q.device)
+    weight, total, shift = torch.zeros_like(out), torch.zeros_like(out), torch.zeros(st.rows, st.hq, 1, dtype=torch.float64, device=q.device)
     at = 0
     G = st.hq // st.hkv
     for s, (ln, n) in enumerate(zip(st.lens, st.news)):
@@ -115,21 +116,29 @@ def attention(st: Setup, q, kv, drop=None):
             p = torch.softmax(w, -1).nan_to_num(0.0)   # a row without a position: zeros
             out[at:at + n, h] = p @ v[h // G]
             weight[at:at + n, h] = p @ v[h // G].abs()
+            total[at:at + n, h] = (~hide).double() @ v[h // G].abs()
             shift[at:at + n, h, 0] = (x.abs() @ kk.abs().T / math.sqrt(st.d)).masked_fill(hide, 0).amax(-1)
         at += n
-    return out, weight, shift
+    return out, weight, shift, total
 
 
-def attention_bound(ref, weight, shift, q8):
-    """How far a correct kernel may be from the 64-bit attention, value by value.  Rounding to bf16
-    is off by at most 2^-8 of the value: the output, and each softmax weight (the sum uses the
-    unrounded ones); fp32 scores and sums add less than 2^-12 of the weighted values for the
-    lengths tested (D terms of 2^-24 each times a shift below 100).  Over a q8_0 cache the decoded
-    values round too: V by 2^-8, K by 2^-8 of sum |q k|, which moves every score by at most
-    ``shift * 2^-8`` and so every normalised weight by a factor within exp(+-2 of that)."""
+def attention_bound(ref, weight, shift, total, q8):
+    """How far a correct kernel may be from the 64-bit attention, value by value.  The output is
+    rounded to bf16 (off by at most 2^-8 of it), and so is each softmax weight over a bf16 cache
+    (the sum uses the unrounded ones); fp32 scores and sums add less than 2^-12 of the weighted
+    values for the lengths tested (D terms of 2^-24 each times a shift below 100).  Over a q8_0
+    cache the weights, V and K round to fp16, 2^-11 of each: K moves every score by at most
+    ``shift * 2^-11`` and so every normalised weight by a factor within exp(+-2 of that).  (A
+    query row's power of two is exact, and what fp16 loses of its values 2^-14 below the row's
+    largest is less than 2^-25 of that: 1 % more of the shift covers it.)  Small weights become
+    fp16 subnormals, spaced 2^-24 and so off by at most 2^-25 where the largest weight is 2^6 or
+    more (weights carry a factor 2^6 and are relative to a reference no larger than the row's
+    maximum): 2^-31 of each |v|."""
     h = 2.0 ** -8
     rel = h + 2.0 ** -12
+    tiny = total * 2.0 ** -31 if q8 else 0.0
     if q8:
-        rel = rel + h + (2 * shift * h).expm1()
+        e = 2.0 ** -11
+        rel = 2 * e + 2.0 ** -12 + (2 * 1.01 * shift * e).expm1()
     # an out value is rounded after it is off by the rest
-    return (weight * rel) * (1 + h) + ref.abs() * h + 1e-30
+    return (weight * rel + tiny) * (1 + h) + ref.abs() * h + 1e-30

@@ -142,3 +142,58 @@ def test_rope_frequencies():
                 dict(original_len=9, beta_slow=0.0)):
         with pytest.raises(mk.MkError):
             mk.rope_frequencies(128, 1e4, **bad)
+
+
+def check_plan(sh, cl, sl):
+    """Every position tile of every (sequence, unit, KV head) in exactly one segment, no segment empty,
+    the cut items' partials distinct and in block order; returns the blocks' tiles."""
+    seg = mk.plan_chunk_attention(sh, cl, sl)
+    G = sh.num_q_heads // sh.num_kv_heads
+    ut = 2 * (128 // G)
+    want = {}
+    for s, (c, n) in enumerate(zip(cl, sl)):
+        for u in range(-(-c // ut)):
+            for h in range(sh.num_kv_heads):
+                want[s, u, h] = (n - c + min(c, (u + 1) * ut) - 1) // 128 + 1
+    got, slots, load = {}, set(), {}
+    for b, s, u, h, t0, n, total, slot in seg.tolist():
+        assert n > 0 and want[s, u, h] == total and t0 + n <= total
+        assert got.get((s, u, h), 0) == t0       # segments of an item come in order, blocks ascending
+        got[s, u, h] = t0 + n
+        load[b] = load.get(b, 0) + n
+        if n == total:
+            assert slot == -1
+        else:
+            assert slot == 2 * b + (t0 == 0) and slot not in slots
+            slots.add(slot)
+    assert got == want
+    assert seg.size == 0 or (seg[:, 0].max() < 152 and np.all(np.diff(seg[:, 0]) >= 0))
+    bytes_ = mk.chunk_attention_workspace(sh, cl, sl)
+    rows = max([min(c, ut) for c in cl], default=0) * G
+    if slots:
+        assert bytes_ >= (max(slots) + 1) * rows * (sh.head_dim + 4) * 4
+    else:
+        assert bytes_ == 0
+    return load
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_plan_covers_every_tile_once(seed):
+    g = np.random.default_rng(seed)
+    hkv, G = int(g.choice([1, 2, 4, 8])), int(g.integers(1, 9))
+    sh = shape(num_q_heads=hkv * G, num_kv_heads=hkv, max_pages_per_seq=1 << 16, num_pages=1 << 10)
+    n = int(g.integers(1, 65))
+    sl = np.exp(g.uniform(0, np.log(g.choice([200, 5000, 200000])), n)).astype(int)
+    top = int(g.choice([1, 64, 3000]))
+    cl = [int(g.integers(0, min(x, top) + 1)) for x in sl]
+    check_plan(sh, cl, sl.tolist())
+
+
+@pytest.mark.parametrize("cl,sl", [([1], [131073]), ([1], [1]), ([8192], [8192]), ([2048], [32768]), ([1024], [16384]),
+                                   ([1] * 64, [32768] * 64), ([200000], [200000]), ([1], [1 << 20])])
+def test_plan_is_even(cl, sl):
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 16)
+    load = check_plan(sh, cl, sl)
+    total = sum(load.values())
+    if total > 152 * 8:      # enough to go round: the longest block within 15 % and a few tiles of even
+        assert max(load.values()) <= 1.15 * total / 152 + 4

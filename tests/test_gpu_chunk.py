@@ -187,9 +187,9 @@ def check_attention(st, std=1.5, drop=None, status_want=mk.MK_OK, q=None, extra_
     got = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, out=out, status=status)
     assert got is out and int(status) == status_want
     assert torch.all(out[st.rows:] == 7.0)
-    ref, weight, shift = R.attention(st, q, st.kv, drop)
+    ref, *scale = R.attention(st, q, st.kv, drop)
     far = (out[:st.rows].double() - ref).abs()
-    bound = R.attention_bound(ref, weight, shift, st.q8)
+    bound = R.attention_bound(ref, *scale, st.q8)
     assert torch.all(far <= bound), float((far / bound).max())
     return q, out
 
@@ -267,20 +267,50 @@ def test_attention_skips_pages_out_of_range(q8):
     out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, bad_bt, st.kv, status=status)
     assert int(status) == mk.MK_ERR_DEVICE_BOUNDS
     st.bt = ref_bt
-    ref, weight, shift = R.attention(st, q, st.kv, drop)
-    assert torch.all((out.double() - ref).abs() <= R.attention_bound(ref, weight, shift, q8))
+    ref, *scale = R.attention(st, q, st.kv, drop)
+    assert torch.all((out.double() - ref).abs() <= R.attention_bound(ref, *scale, q8))
     assert torch.all(out[:16] == 0) and torch.all(out[103:] == 0)
 
 
-def test_attention_nan_in_a_later_position_stays_there():
-    # a NaN value of the sequence reaches the rows that see it, and no other row of its chunk
-    st = R.Setup(4, 1, 64, 16, [90], [90], seed=15)
-    q = st.normal(90, 4, 64)
-    clean = mk.chunk_attention(st.shape(mk), q, [90], [90], st.bt, st.kv)
-    st.kv[st.bt[0, 80 // 16].long(), 0, 0, 80 % 16, 5] = float("nan")       # a key
-    out = mk.chunk_attention(st.shape(mk), q, [90], [90], st.bt, st.kv)
-    assert torch.isfinite(out[:80]).all() and torch.isnan(out[80:]).all()
-    assert torch.equal(out[:80], clean[:80])
+@pytest.mark.parametrize("hq,hkv,d,len_,new", [(4, 1, 64, 90, 90), (8, 1, 128, 5000, 90)])
+@pytest.mark.parametrize("which,value", [(0, "nan"), (1, "nan"), (1, "inf")])
+def test_attention_nan_in_a_later_position_stays_there(hq, hkv, d, len_, new, which, value):
+    # a NaN or infinity of the sequence reaches the rows that see it, and no other row of its tile
+    st = R.Setup(hq, hkv, d, 16, [len_], [new], seed=15)
+    q = st.normal(new, hq, d)
+    ref, *scale = R.attention(st, q, st.kv)
+    pos, row = len_ - 10, new - 10
+    st.kv[st.bt[0, pos // 16].long(), which, 0, pos % 16, 5] = float(value)
+    out = mk.chunk_attention(st.shape(mk), q, [new], [len_], st.bt, st.kv)
+    bound = R.attention_bound(ref, *scale, False)
+    assert torch.all((out[:row].double() - ref[:row]).abs() <= bound[:row])
+    hit = out[row:] if which == 0 else out[row:, :, 5]
+    assert torch.isnan(hit).all() if value == "nan" else torch.isinf(hit).all()
+
+
+@pytest.mark.parametrize("len_,new", [(90, 90), (5000, 2)])
+def test_attention_q8_values_beyond_fp16(len_, new):
+    # decoded values above 65504 (scales up to f16's largest) in a few positions, K and V
+    st = R.Setup(8, 2, 128, 16, [len_], [new], q8=True, seed=19)
+    codes, scales = st.planes()
+    for pos, which, sc in ((3, 1, 60000.0), (len_ - 5, 1, 3000.0), (len_ // 2, 0, 600.0), (len_ - 1, 0, 40000.0)):
+        page = st.bt[0, pos // 16].long()
+        scales[page, which, :, pos % 16, 1] = sc
+    check_attention(st, std=0.02)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_attention_queries_of_any_magnitude(q8):
+    # rows scaled by powers of two from 2^-100 to 2^100 against keys scaled the other way
+    st = R.Setup(8, 2, 128, 16, [200], [60], q8=q8, seed=20)
+    if q8:
+        q = st.normal(60, 8, 128)
+        e = torch.arange(60, device="cuda") * 3.0 - 100
+        q = (q.float() * torch.exp2(e.clamp(max=4.0))[:, None, None]).to(torch.bfloat16)
+    else:
+        st.kv[:, 0] = (st.kv[:, 0].float() * 2.0 ** -60).to(torch.bfloat16)
+        q = (st.normal(60, 8, 128).float() * 2.0 ** 60).to(torch.bfloat16)
+    check_attention(st, q=q)
 
 
 def test_attention_pool_beyond_32_bit_offsets():
@@ -366,8 +396,8 @@ def test_splitting_a_prompt_gives_the_same_cache_and_close_rows():
     assert torch.equal(bits(kv1), bits(kv2))
     o2 = torch.cat([o[:n] for o, n in got] + [got[1][0][1:]])
     st.kv = kv1
-    ref, weight, shift = R.attention(st, q1, kv1)
-    bound = R.attention_bound(ref, weight, shift, False)
+    ref, *scale = R.attention(st, q1, kv1)
+    bound = R.attention_bound(ref, *scale, False)
     assert torch.all((o1.double() - ref).abs() <= bound) and torch.all((o2.double() - ref).abs() <= bound)
 
 
