@@ -115,30 +115,31 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Shared-memory operand with the 128-byte swizzle: start address; lbo, sbo: bytes between the
-// 64-element spans of a row (used where rows run along the operand's K) and between 8-row groups.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory operand with the 128-byte swizzle, in two words: start address and lbo (bytes between
+// the 64-element spans of a row, used where rows run along the operand's K); sbo, bytes between
+// 8-row groups, and the constant fields.  Addresses advance in the low word alone.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo) { return sbo >> 4 | 1u << 14 | 2u << 29; }
 // bf16 (or fp16) operands, fp32 accumulator; b_mn: B is stored with its N dimension contiguous
 __device__ __forceinline__ constexpr uint32_t tc_idesc(bool bf16, int M, int N, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-// one elected lane of the converged warp issues
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One elected lane of the converged warp issues; the whole warp computes the operands, so that they
+// stay in uniform registers (issued from one thread's branch, an 8192-token prompt took 455 us
+// instead of 390: every operand moved across for every product).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t bhi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(bhi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -227,6 +228,7 @@ struct Ctl {
   uint64_t raw_full[8], raw_empty[8];
   uint64_t qraw[2], qbar[2], qfree;  // query tiles: landed, in the operand type (bf16: qraw itself), read by the last S
   uint64_t sfull[2], pfull[2][2];    // S of a tile (stream); the halves of its P
+  uint64_t landed, trim;             // a last V tile to be trimmed: landed, trimmed
   uint64_t ofull, join;
   uint32_t tmem, abort;
   uint32_t mask[kMasks];             // per tile, a bit per 8 positions: the page is in range
@@ -508,74 +510,101 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
   }
 }
 
-// --------------------------------------------------------------------------- MMAs (warp 9)
+// What a page holds behind the sequence's last position must not meet a weight, not even a zero one
+// (0 * NaN): warp 11 puts zeros there in a segment's last V tile.  (q8_0 tiles are zeroed as they are
+// decoded; whole copies behind the sequence are zeros already.)
+template <bool Q8>
+__device__ __forceinline__ bool trims(const Segment& g) { return !Q8 && (g.tile0 + g.n) * kTile > g.len; }
+
 template <int D, bool Q8>
-__device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* ctl, uint32_t tm) {
+__device__ __forceinline__ void trim(const AttnParams& p, uint32_t base, Ctl* ctl) {
+  using L = Layout<D, Q8>;
+  const int lane = threadIdx.x & 31;
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g;
+  uint32_t c0 = 0, k = 0;
+  while (walk.next(p.plan, p.seqs, g)) {
+    const uint32_t c = c0 + 2 * g.n - 1;
+    c0 += 2 * g.n;
+    if (!trims<Q8>(g)) continue;
+    // (told by the MMA thread, which keeps the entry until the trim: `full` itself may be phases away)
+    if (!mbar_wait(smem_u32(&ctl->landed), k & 1, ctl, p.status)) return;
+    ++k;
+    const int first = g.len - (g.tile0 + g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
+    const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
+    for (int n = first + lane / (D / 8); n < last; n += 256 / D) sts16(v + (n >> 3) * L::kGroup + (n & 7) * 128, 0, 0, 0, 0);
+    fence_async_smem();
+    warp_arrive(smem_u32(&ctl->trim));
+  }
+}
+
+// --------------------------------------------------------------------------- MMAs (warp 9)
+// A wait that gives up does not leave the loops (their bounds stay uniform that way): in an aborted block
+// every later wait returns at once and the products are of whatever is there.  All of tensor memory is the block's, from column 0: S (and P, over it) of tile (stream) t at column
+// t * 128, O at 256 + t * D.
+template <int D, bool Q8>
+__device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* ctl) {
   using L = Layout<D, Q8>;
   constexpr uint32_t kIdS = tc_idesc(!Q8, kTile, kTile, false), kIdO = tc_idesc(!Q8, kTile, D, true);
-  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kHiQ = desc_hi(1024), kHiKv = desc_hi(L::kGroup);
+  constexpr uint32_t kStep = L::kTileBytes >> 4;   // a tile in descriptor units
+  const uint32_t q_lo = desc_lo(base, 16), k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, 1024);
   uint32_t c0 = 0;                                 // ring entry of the segment's first K tile
-  uint32_t ps = 0, qs = 0;                         // phases of pfull and of the query tiles, a bit for each t
-  auto tile = [&](uint32_t c) { return base + L::kKv + c % L::kStages * L::kTileBytes; };
-  auto wait_full = [&](uint32_t c) {
-    const bool ok = mbar_wait(smem_u32(&ctl->full[c % L::kStages]), (c / L::kStages) & 1, ctl, p.status);
-    tc_after();
-    return ok;
+  uint32_t pp = 0, qq = 0, tr = 0;                 // phases of pfull and of the query tiles (a bit for each t), and trim
+  const int lane = threadIdx.x & 31;
+  auto wait = [&](const uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    if (!mbar_try(a, parity)) mbar_wait_slow(a, parity, ctl, p.status);
+    __syncwarp();
   };
+  auto wait_full = [&](uint32_t c) { wait(&ctl->full[c % L::kStages], (c / L::kStages) & 1); };
   auto release = [&](uint32_t c) { tc_commit(smem_u32(&ctl->empty[c % L::kStages])); };
   auto scores = [&](int t, int qt, uint32_t c) {   // S of tile (stream) t from Q tile qt and the K tile in entry c
-    const uint64_t a = tc_desc(base + qt * L::kTileBytes, 16, 1024), b = tc_desc(tile(c), 16, L::kGroup);
+    const uint32_t a = q_lo + qt * kStep, b = k_lo + c % L::kStages * kStep;
+    tc_after();
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
-      mma_ss(tm + t * kTile, a + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2, b + (k / 4) * (1024 >> 4) + (k % 4) * 2, kIdS,
-             k > 0);
+      mma_ss(t * kTile, a + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2, kHiQ, b + (k / 4) * (1024 >> 4) + (k % 4) * 2, kHiKv,
+             kIdS, k > 0);
     tc_commit(smem_u32(&ctl->sfull[t]));
     // the page mask travels with an ordinary arrival: the warp that wrote it arrived on `full`
     if (lane == 0) mbar_arrive(smem_u32(&ctl->sfull[t]));
     __syncwarp();
   };
-  // bf16: what a page holds behind the sequence's last position must not meet a weight, not even
-  // a zero one (0 * NaN): zeros instead.  (q8_0 tiles are zeroed as they are decoded.)
-  auto trim = [&](int first, uint32_t c) {
-    if (Q8 || first >= kTile) return;
-    const int last = (first + p.box - 1) / p.box * p.box;      // copies behind are zeros already
-    const uint32_t v = tile(c);
-    for (int n = first; n < last; ++n)
-      if (lane < D / 8) sts16(v + (n >> 3) * L::kGroup + (lane >> 3) * 1024 + (n & 7) * 128 + (lane & 7) * 16, 0, 0, 0, 0);
-    fence_async_smem();
-    __syncwarp();
-  };
-  // O of tile (stream) t += P times the V tile in entry c, each half of P as it comes; `first` as in trim
-  auto values = [&](int t, uint32_t c, int first, bool acc) {
-    const uint64_t b = tc_desc(tile(c), 1024, L::kGroup);
-    const uint32_t ph = (ps >> t) & 1;
-    ps ^= 1u << t;
-    if (!wait_full(c)) return false;
-    trim(first, c);
+  // O of tile (stream) t += P times the V tile in entry c, each half of P as it comes
+  auto values = [&](int t, uint32_t c, bool acc) {
+    const uint32_t b = v_lo + c % L::kStages * kStep, ph = (pp >> t) & 1;
+    pp ^= 1u << t;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!mbar_wait(smem_u32(&ctl->pfull[t][h]), ph, ctl, p.status)) return false;
+      wait(&ctl->pfull[t][h], ph);
       tc_after();
 #pragma unroll
       for (int k = 4 * h; k < 4 * h + 4; ++k)
-        mma_ts(tm + 2 * kTile + t * D, tm + t * kTile + k * 8, b + k * (2 * L::kGroup >> 4), kIdO, acc || k > 0);
+        mma_ts(2 * kTile + t * D, t * kTile + k * 8, b + k * (2 * L::kGroup >> 4), kHiKv, kIdO, acc || k > 0);
     }
-    return true;
   };
   auto wait_q = [&](int t) {
-    const bool ok = mbar_wait(smem_u32(Q8 ? &ctl->qbar[t] : &ctl->qraw[t]), (qs >> t) & 1, ctl, p.status);
-    qs ^= 1u << t;
-    return ok;
+    wait(Q8 ? &ctl->qbar[t] : &ctl->qraw[t], (qq >> t) & 1);
+    qq ^= 1u << t;
   };
   auto done_q = [&]() { tc_commit(smem_u32(&ctl->qfree)); };
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
   while (walk.next(p.plan, p.seqs, g)) {
     const uint32_t c = c0;
-    const int left = g.len - g.tile0 * kTile;
-    if (!wait_q(0)) return;
+    auto wait_v = [&](int j) {
+      wait_full(c + 2 * j + 1);
+      if (j + 1 == g.n && trims<Q8>(g)) {
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->landed));
+        wait(&ctl->trim, tr & 1);
+        ++tr;
+      }
+    };
+    wait_q(0);
     if (g.two) {
-      if (!wait_q(1) || !wait_full(c)) return;
+      wait_q(1);
+      wait_full(c);
       scores(0, 0, c);
       scores(1, 1, c);
       release(c);
@@ -583,12 +612,13 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
       for (int j = 0; j < g.n; ++j) {
         const bool more = j + 1 < g.n;
         const uint32_t v = c + 2 * j + 1;
-        if (!values(0, v, left - j * kTile, j > 0)) return;
+        wait_v(j);
+        values(0, v, j > 0);
         if (more) {
-          if (!wait_full(v + 1)) return;
+          wait_full(v + 1);
           scores(0, 0, v + 1);
         }
-        if (!values(1, v, kTile, j > 0)) return;
+        values(1, v, j > 0);
         release(v);
         if (more) {
           scores(1, 1, v + 1);
@@ -598,7 +628,7 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
       }
     } else {
       for (int j = 0; j < 2 && j < g.n; ++j) {
-        if (!wait_full(c + 2 * j)) return;
+        wait_full(c + 2 * j);
         scores(j, 0, c + 2 * j);
         release(c + 2 * j);
       }
@@ -606,10 +636,11 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
       for (int j = 0; j < g.n; ++j) {
         const int t = j & 1;
         const uint32_t v = c + 2 * j + 1;
-        if (!values(t, v, left - j * kTile, j > 1)) return;
+        wait_v(j);
+        values(t, v, j > 1);
         release(v);
         if (j + 2 < g.n) {
-          if (!wait_full(v + 3)) return;
+          wait_full(v + 3);
           scores(t, 0, v + 3);
           release(v + 3);
           if (j + 3 == g.n) done_q();
@@ -654,10 +685,10 @@ __device__ __forceinline__ float convert_q(uint32_t tile, int row) {
 }
 
 template <int D, bool Q8>
-__device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl* ctl, uint32_t tm) {
+__device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl* ctl) {
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t ts = tm + t * kTile + lane_base, to = tm + 2 * kTile + lane_base;
+  const uint32_t ts = t * kTile + lane_base, to = 2 * kTile + lane_base;
   constexpr float kBias = Q8 ? 6.f : 0.f;          // weights carry 2^kBias
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g, next;
@@ -714,10 +745,15 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
         tc_wait_ld();
         const int limit = pos - (g.tile0 + j) * kTile;         // last column this row sees
         const uint32_t mask = ctl->mask[(jg + j) % kMasks];
-        if (__any_sync(~0u, limit < kTile - 1 || mask != 0xffffu)) {
+        if (__any_sync(~0u, limit < kTile - 1)) {
 #pragma unroll
           for (int k = 0; k < kTile; ++k)
-            if (k > limit || !((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
+            if (k > limit) s[k] = -INFINITY;
+        }
+        if (mask != 0xffffu) {
+#pragma unroll
+          for (int k = 0; k < kTile; ++k)
+            if (!((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -807,8 +843,14 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
       const int urow = urow0 + row;
       const int tok = urow * p.plan.by_G >> 16;
       const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + urow - tok * p.plan.G;
-      float* part = p.part + (static_cast<size_t>(max(g.slot, 0)) * p.plan.urows + urow) * (D + 4);
-      uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D;
+      // a partial is [D/4][urows] of 4 columns, then [urows] of (m, l): a warp's rows lie side by side
+      float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(g.slot, 0)) * p.plan.urows * (D + 4));
+      // Stores to the output: the four lanes of a quad trade 16-byte pieces, so that each store
+      // covers 64 bytes of 8 rows instead of 16 bytes of 32.  The rows of the quad's lanes:
+      const int q4 = threadIdx.x & 3;
+      uint32_t row_off[4];                         // in heads, from the sequence's first row; ~0: none
+#pragma unroll
+      for (int e = 0; e < 4; ++e) row_off[e] = __shfl_sync(~0u, live ? static_cast<uint32_t>(r * p.Hq + h) : ~0u, e, 4);
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       bool odd = false;
       const int k0 = g.two ? 0 : t * (D / 2), k1 = g.two ? D : k0 + D / 2;
@@ -832,30 +874,50 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
             for (int e = 0; e < 32; ++e) x[e] *= f[0];
           }
         }
-        if (live && g.slot >= 0) {
+        if (g.slot >= 0) {
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        } else if (live) {
+            for (int e = 0; e < 32; e += 4)
+              part[static_cast<size_t>((k + e) / 4) * p.plan.urows + urow] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        } else {
+          uint32_t w[4][4];                        // piece e: columns k + 8 e
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = bf16x2(x[e] * inv, x[e + 1] * inv);
-            w.y = bf16x2(x[e + 2] * inv, x[e + 3] * inv);
-            w.z = bf16x2(x[e + 4] * inv, x[e + 5] * inv);
-            w.w = bf16x2(x[e + 6] * inv, x[e + 7] * inv);
-            *reinterpret_cast<uint4*>(out + k + e) = w;
+          for (int e = 0; e < 32; e += 2) {
+            const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
+            odd |= !(fabsf(y0) <= 3.3e38f) || !(fabsf(y1) <= 3.3e38f);
+            w[e / 8][e / 2 % 4] = bf16x2(y0, y1);
+          }
+          // piece e of lane i <-> piece i of lane e, a bit of the index at a time
+#pragma unroll
+          for (int bit = 1; bit < 4; bit <<= 1) {
+            const bool up = (q4 & bit) != 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (e & bit) continue;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t give = up ? w[e][z] : w[e | bit][z];
+                const uint32_t got = __shfl_xor_sync(~0u, give, bit);
+                if (up) w[e][z] = got;
+                else w[e | bit][z] = got;
+              }
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) odd |= !(fabsf(x[e] * inv) <= 3.3e38f);
+          for (int e = 0; e < 4; ++e)
+            if (row_off[e] != ~0u)
+              *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row_off[e]) * D + k + 8 * q4) =
+                  make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
         }
         __syncwarp();
       }
-      if (live && g.slot >= 0 && (g.two || t == 0)) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
+      if (live && g.slot >= 0 && (g.two || t == 0))
+        reinterpret_cast<float2*>(part + static_cast<size_t>(D / 4) * p.plan.urows)[urow] = make_float2(m, l);
       // rows that are not finite, again from the cache (each warpgroup those it saw; where both see
       // one they write the same)
       if (g.slot < 0) {
-        for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
+        for (uint32_t todo = __ballot_sync(~0u, odd && live); todo; todo &= todo - 1) {
           const int who = __ffs(todo) - 1;
           const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
           __threadfence_block();
@@ -899,6 +961,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
       mbar_init(smem_u32(&ctl->pfull[t][1]), 4);
     }
     mbar_init(smem_u32(&ctl->qfree), 1);
+    mbar_init(smem_u32(&ctl->landed), 1);
+    mbar_init(smem_u32(&ctl->trim), 1);
     mbar_init(smem_u32(&ctl->ofull), 1);
     mbar_init(smem_u32(&ctl->join), 8);
     ctl->abort = 0u;
@@ -911,18 +975,25 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
   tc_before();
   __syncthreads();
   tc_after();
+  // (all 512 columns: they begin at column 0, and the roles count on it)
   const uint32_t tm = ctl->tmem;
+  if (tm != 0u) {
+    if (p.status) *p.status = MK_ERR_UNSUPPORTED;
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+    return;
+  }
   // registers follow the work: a softmax thread holds a row of S (the warpgroups' sum is the launch's)
   if (warp < 8) {
     if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    softmax<D, Q8>(p, base, ctl, tm);
+    softmax<D, Q8>(p, base, ctl);
   } else if (warp < 12) {
     if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) produce<D, Q8>(p, base, ctl);
-    if (warp == 9) issue<D, Q8>(p, base, ctl, tm);
+    if (warp == 9) issue<D, Q8>(p, base, ctl);
     if (warp == 10) produce_q<D, Q8>(p, base, ctl);
+    if (!Q8 && warp == 11) trim<D, Q8>(p, base, ctl);
   } else if constexpr (Q8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     decode<D>(p, base, ctl);
@@ -942,47 +1013,57 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-// Merges the items that the ranges cut, in block order: blockIdx.x is the block that began one, a
-// warp takes a row.
+// Merges the items that the ranges cut, in block order: blockIdx.x is the block that began one.  A
+// block takes 8 rows, a thread 4 columns of one; a warp's 8 rows lie side by side in a partial.
 template <int D, bool Q8>
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ AttnParams p) {
   const AttnPlan& pl = p.plan;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, urow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int b = blockIdx.x, lane = threadIdx.x & 31, urow = blockIdx.y * 8 + (lane & 7);
+  const int chunk = (threadIdx.x >> 5) * 4 + (lane >> 3);
   const int item = pl.start[b + 1].item;
   if (pl.start[b + 1].tile == 0 || (pl.start[b].item == item && pl.start[b].tile > 0)) return;
   Segment g;
   item_of(pl, p.seqs, item, g);
-  if (urow >= g.ntok * pl.G) return;
+  const int rows = g.ntok * pl.G;
+  if (blockIdx.y * 8 >= rows) return;
+  const bool live = urow < rows;
   int n = 2;                                       // partials: the beginning, and each range that starts inside
   while (b + n <= pl.blocks && pl.start[b + n].item == item) ++n;
-  const size_t row = static_cast<size_t>(pl.urows) * (D + 4);
-  auto at = [&](int k) { return p.part + static_cast<size_t>(2 * (b + k) + (k == 0 ? 1 : 0)) * row +
-                                static_cast<size_t>(urow) * (D + 4); };
-  float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, at(k)[D]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-  constexpr int V = D / 32;
-  float acc[V] = {}, L = 0.f;
+  const size_t slot = static_cast<size_t>(pl.urows) * (D + 4);
+  const float* first = p.part + static_cast<size_t>(2 * b + 1) * slot;            // then slots 2(b+1), 2(b+2), ..
+  const size_t at_ml = static_cast<size_t>(pl.urows) * D + 2 * static_cast<size_t>(live ? urow : 0);
+  const size_t at_o = (static_cast<size_t>(chunk) * pl.urows + (live ? urow : 0)) * 4;
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int k = 0; k < n; ++k) {
-    const float* pk = at(k);
-    const float2 ml = *reinterpret_cast<const float2*>(pk + D);
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    L += f * ml.y;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(f, pk[lane * V + v], acc[v]);
+    const float* pk = k == 0 ? first : first + (2 * k - 1) * slot;
+    const float2 ml = *reinterpret_cast<const float2*>(pk + at_ml);
+    const float4 o = *reinterpret_cast<const float4*>(pk + at_o);
+    const float top = fmaxf(M, ml.x);
+    const float f = M == -INFINITY ? 0.f : ex2(M - top), fk = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    M = top;
+    L = L * f + ml.y * fk;
+    acc.x = acc.x * f + o.x * fk;
+    acc.y = acc.y * f + o.y * fk;
+    acc.z = acc.z * f + o.z * fk;
+    acc.w = acc.w * f + o.w * fk;
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
-  const int r = p.seqs.row0[g.s] + g.tok0 + urow / pl.G, h = g.kvh * pl.G + urow % pl.G;
-  uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D + lane * V;
-  bool odd = false;
-#pragma unroll
-  for (int v = 0; v < V; v += 2) {
-    *reinterpret_cast<uint32_t*>(out + v) = bf16x2(acc[v] * inv, acc[v + 1] * inv);
-    odd |= !(fabsf(acc[v] * inv) <= 3.3e38f) || !(fabsf(acc[v + 1] * inv) <= 3.3e38f);
+  const int tok = urow * pl.by_G >> 16;
+  const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * pl.G + urow - tok * pl.G;
+  acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (live)
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
+        make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+  const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
+  const bool odd = live && (!(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
+  for (uint32_t todo = __ballot_sync(~0u, odd), done = 0; todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1;
+    const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
+    if (!((done >> (who & 7)) & 1u)) exact_row<D, Q8>(p, rr, hh);
+    done |= 1u << (who & 7);
   }
-  if (__any_sync(~0u, odd)) exact_row<D, Q8>(p, r, h);
 }
 
 // --------------------------------------------------------------------------- host
@@ -1040,7 +1121,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   attn_kernel<D, Q8><<<p.plan.blocks, Layout<D, Q8>::kThreads, smem_bytes<D, Q8>(), st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.plan.ranged) return e;
-  merge_kernel<D, Q8><<<dim3(p.plan.blocks, (p.plan.urows + 7) / 8), 256, 0, st>>>(p);
+  merge_kernel<D, Q8><<<dim3(p.plan.blocks, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -9,10 +9,12 @@
 namespace mk {
 
 namespace {
-// Costs in position tiles: what an item adds besides its tiles (query rows in, the pipeline's
-// first scores, the epilogue), what a range's partials and the second kernel add, and the fewest
-// tiles a block is worth.
-constexpr int kItemCost = 2, kMergeCost = 5, kMinRange = 3;
+// Costs in tenths of a microsecond, as measured: a position tile and what an item adds to its tiles
+// (query rows, the pipeline's filling and emptying, the epilogue), for items of two tiles of rows and
+// of one; what the ranges' partials and the second kernel add (more where units of two tiles are cut:
+// an 8192-token prompt, even to 1 % as whole items, took 383 us so and 393 us in ranges).  (152 blocks streaming from HBM.)
+constexpr int kTileCost[2] = {14, 17}, kItemCost[2] = {40, 60}, kMergeCost[2] = {80, 250};
+constexpr int kMinRange = 3;                // position tiles a block is worth
 constexpr int kMaxWalk = 16 * kMaxBlocks;   // items beyond which whole ones are even enough
 }  // namespace
 
@@ -48,20 +50,21 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
   if (items == 0 || items > kMaxWalk) return true;
 
   // the slowest block of whole items, and the work altogether
-  int64_t load[kMaxBlocks] = {}, tiles = 0;
+  int64_t load[kMaxBlocks] = {}, tiles = 0, cost = 0;
   Segment g;
   for (int i = 0; i < pl->items; ++i) {
     item_of(*pl, q, i, g);
     tiles += g.tiles;
     const int round = i / pl->blocks, at = i % pl->blocks;
-    load[round & 1 ? pl->blocks - 1 - at : at] += g.tiles + kItemCost;
+    const int64_t x = g.tiles * kTileCost[g.two] + kItemCost[g.two];
+    load[round & 1 ? pl->blocks - 1 - at : at] += x;
+    cost += x;
   }
   const int64_t whole = *std::max_element(load, load + pl->blocks);
   const int nb = static_cast<int>(std::min<int64_t>(kMaxBlocks, (tiles + kMinRange - 1) / kMinRange));
-  const int64_t cost = tiles + items * kItemCost;
-  if (whole <= (cost + nb - 1) / nb + kMergeCost) return true;
+  if (whole <= (cost + nb - 1) / nb + kMergeCost[most > pl->TT]) return true;
 
-  // cut the line of items (each kItemCost, then its tiles) at equal cost
+  // cut the line of items (each its own cost, then its tiles') at equal cost
   pl->ranged = 1;
   pl->blocks = nb;
   int b = 1;
@@ -69,13 +72,13 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
   pl->start[0] = {0, 0};
   for (int i = 0; i < pl->items; ++i) {
     item_of(*pl, q, i, g);
-    const int64_t end = at + kItemCost + g.tiles;
+    const int64_t end = at + kItemCost[g.two] + g.tiles * kTileCost[g.two];
     for (; b < nb; ++b) {
       const int64_t x = cost * b / nb;
       if (x >= end) break;
-      const int64_t t = x - at - kItemCost;
-      if (t < 1) pl->start[b] = {i, 0};
-      else pl->start[b] = {i, static_cast<int32_t>(t)};   // 1 <= t < tiles
+      // (x below the item's own cost: the cut is before it; else after 0 <= t < tiles of its tiles)
+      const int64_t t = x < at + kItemCost[g.two] ? 0 : (x - at - kItemCost[g.two]) / kTileCost[g.two];
+      pl->start[b] = {i, static_cast<int32_t>(t)};
     }
     at = end;
   }
