@@ -11,7 +11,6 @@ and inspection).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import subprocess
@@ -149,6 +148,8 @@ _lock = threading.Lock()
 def lib():
     """The loaded CUDA library.  Raises if it has not been built: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -340,34 +341,42 @@ def _need(ok, what):
         raise MkError(MK_ERR_INVALID_ARG, what)
 
 
-def _chunk_args(shape, chunk_lens, seq_lens, block_tables, kv_layer):
-    """(chunk_lens, seq_lens as host int32, rows) after checks of what the C call cannot see."""
-    import torch
-    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
+# These calls are short next to their marshalling (a few microseconds on the device for a few tokens), so
+# it is kept lean: one comparison per argument, plain integers and bytes to ctypes, no context managers
+# unless the device or the stream is not the current one.
+def _lengths_arg(chunk_lens, seq_lens):
+    """Both as int32 bytes (ctypes passes their address), the number of sequences, the rows."""
+    cl, sl = np.asarray(chunk_lens, dtype=np.int32), np.asarray(seq_lens, dtype=np.int32)
     _need(cl.ndim == 1 and cl.shape == sl.shape, "chunk_lens and seq_lens: one length per sequence each")
     rows = sum(cl.tolist())
     _need(0 <= rows < 1 << 24, "chunk_lens: fewer than 2^24 rows")
-    _need(block_tables.is_cuda and block_tables.dtype is torch.int32 and block_tables.is_contiguous(),
-          "block_tables: contiguous int32 CUDA tensor")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] >= cl.size
-          and block_tables.shape[1] == shape.max_pages_per_seq, "block_tables: [num_seqs, max_pages_per_seq]")
-    q8 = shape.flags & FLAG_KV_Q8
+    return cl.tobytes(), sl.tobytes(), cl.size, rows
+
+
+def _cache_arg(shape, n_seqs, block_tables, kv_layer):
+    """The cache's device, after checks of what the C call cannot see."""
+    import torch
+    dev = kv_layer.device
+    bs = block_tables.shape
+    _need(dev.type == "cuda" and block_tables.device == dev and block_tables.dtype is torch.int32
+          and block_tables.is_contiguous() and len(bs) == 2 and bs[0] >= n_seqs and bs[1] == shape.max_pages_per_seq,
+          "block_tables: contiguous int32 [num_seqs, max_pages_per_seq] on the cache's CUDA device")
     n = shape.num_pages * 2 * shape.num_kv_heads * shape.page_size * shape.head_dim
-    _need(kv_layer.is_cuda and kv_layer.is_contiguous() and kv_layer.dtype is (torch.uint8 if q8 else torch.bfloat16)
-          and kv_layer.numel() == (n + n // 16 if q8 else n),
+    q8 = shape.flags & FLAG_KV_Q8
+    _need(kv_layer.dtype is (torch.uint8 if q8 else torch.bfloat16) and kv_layer.numel() == (n + n // 16 if q8 else n)
+          and kv_layer.is_contiguous(),
           "kv_layer: one layer of the shape's cache, contiguous CUDA tensor, bf16 (q8_0: uint8 codes, then f16 scales)")
-    _need(block_tables.device == kv_layer.device, "block_tables and kv_layer are on different devices")
-    return cl, sl, rows
+    return dev
 
 
 def _rows_arg(t, rows, heads, dim, device, what):
     """The row stride of t, bf16 rows of heads*dim contiguous values as [rows, heads*dim] or [rows, heads, dim]."""
     import torch
     shape, stride = t.shape, t.stride()
-    _need(t.is_cuda and t.device == device and t.dtype is torch.bfloat16 and shape[0] >= rows
+    _need(t.device == device and t.dtype is torch.bfloat16 and shape[0] >= rows
           and (shape[1:] == (heads * dim,) and stride[1] == 1
                or shape[1:] == (heads, dim) and stride[2] == 1 and (stride[1] == dim or heads == 1)),
-          f"{what}: bf16 CUDA rows of {heads} heads of {dim} contiguous values, at least {rows} rows")
+          f"{what}: bf16 rows of {heads} heads of {dim} contiguous values on the cache's device, at least {rows} rows")
     return stride[0] if shape[0] > 1 else heads * dim
 
 
@@ -375,32 +384,34 @@ def _out_arg(t, shape, device, what):
     import torch
     if t is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    _need(t.is_cuda and t.device == device and t.dtype is torch.bfloat16 and t.is_contiguous()
+    _need(t.device == device and t.dtype is torch.bfloat16 and t.is_contiguous()
           and t.shape[1:] == shape[1:] and t.shape[0] >= shape[0],
-          f"{what}: contiguous bf16 CUDA tensor of at least {list(shape)}")
+          f"{what}: contiguous bf16 tensor of at least {list(shape)} on the cache's device")
     return t
 
 
 def _status_arg(t, device):
     import torch
-    if t is not None:
-        _need(t.is_cuda and t.device == device and t.dtype is torch.int32 and t.numel() == 1,
-              "status: int32 CUDA tensor of one value")
-    return _ptr(t)
+    if t is None:
+        return None
+    _need(t.device == device and t.dtype is torch.int32 and t.numel() == 1,
+          "status: int32 tensor of one value on the cache's device")
+    return t.data_ptr()
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes ``device`` and ``stream`` (default: torch's current one of the device) current, so that new
-    outputs and workspaces belong to the stream that writes them; yields the stream as a C argument."""
+def _run(device, stream, call):
+    """``call(stream handle)`` with ``device`` and ``stream`` (default: torch's current one of the device)
+    current, so that new outputs and workspaces belong to the stream that writes them."""
     import torch
-    if stream is None:
-        with torch.cuda.device(device):
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    else:
+    if stream is not None:
         _need(stream.device == device, "stream is on another device than the tensors")
         with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
+            return call(stream.cuda_stream)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream(device).cuda_stream)
+    # (the handle alone: building a Stream object costs as much as the rest of the marshalling)
+    return call(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, rope: Rope | None = None,
@@ -414,29 +425,31 @@ def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_
     current one.  Returns the query rows, bf16 [rows, Hq, D] (``q_out`` or a new tensor).
     """
     import torch
-    cl, sl, rows = _chunk_args(shape, chunk_lens, seq_lens, block_tables, kv_layer)
-    dev, Hq, D = kv_layer.device, shape.num_q_heads, shape.head_dim
+    cl, sl, n, rows = _lengths_arg(chunk_lens, seq_lens)
+    dev, Hq, D = _cache_arg(shape, n, block_tables, kv_layer), shape.num_q_heads, shape.head_dim
     stride = _rows_arg(qkv, rows, Hq + 2 * shape.num_kv_heads, D, dev, "qkv")
     for t in (q_norm, k_norm):
-        _need(t is None or (t.is_cuda and t.device == dev and t.dtype is torch.bfloat16 and t.is_contiguous()
-                            and t.numel() == D), "q_norm / k_norm: contiguous bf16 CUDA [head_dim]")
-    with _on(dev, stream) as st:
-        q_out = _out_arg(q_out, (rows, Hq, D), dev, "q_out")
-        _check(lib().mk_append_chunk(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, _ptr(block_tables),
-                                     _ptr(qkv), stride, None if rope is None else ctypes.byref(rope.struct),
-                                     _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out), _ptr(kv_layer),
-                                     _status_arg(status, dev), st))
-    return q_out
+        _need(t is None or (t.device == dev and t.dtype is torch.bfloat16 and t.is_contiguous() and t.numel() == D),
+              "q_norm / k_norm: contiguous bf16 [head_dim] on the cache's device")
+    st = _status_arg(status, dev)
+
+    def call(handle):
+        out = _out_arg(q_out, (rows, Hq, D), dev, "q_out")
+        _check(lib().mk_append_chunk(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), qkv.data_ptr(), stride,
+                                     None if rope is None else ctypes.byref(rope.struct),
+                                     None if q_norm is None else q_norm.data_ptr(),
+                                     None if k_norm is None else k_norm.data_ptr(), eps, out.data_ptr(),
+                                     kv_layer.data_ptr(), st, handle))
+        return out
+    return _run(dev, stream, call)
 
 
 def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
     """Bytes of workspace :func:`chunk_attention` needs for these lengths (0: none)."""
-    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
-    _need(cl.ndim == 1 and cl.shape == sl.shape, "chunk_lens and seq_lens: one length per sequence each")
-    n = ctypes.c_size_t()
-    _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
-                                              ctypes.byref(n)))
-    return n.value
+    cl, sl, n, _ = _lengths_arg(chunk_lens, seq_lens)
+    need = ctypes.c_size_t()
+    _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), n, cl, sl, ctypes.byref(need)))
+    return need.value
 
 
 def plan_chunk_attention(shape: CacheShape, chunk_lens, seq_lens) -> np.ndarray:
@@ -458,36 +471,41 @@ def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv
     may be strided); workspace: CUDA tensor of at least :func:`chunk_attention_workspace` bytes, or
     None to take it from torch's allocator.  Returns bf16 [rows, Hq, D]."""
     import torch
-    cl, sl, rows = _chunk_args(shape, chunk_lens, seq_lens, block_tables, kv_layer)
-    dev, Hq, D = kv_layer.device, shape.num_q_heads, shape.head_dim
+    cl, sl, n, rows = _lengths_arg(chunk_lens, seq_lens)
+    dev, Hq, D = _cache_arg(shape, n, block_tables, kv_layer), shape.num_q_heads, shape.head_dim
     stride = _rows_arg(q, rows, Hq, D, dev, "q")
-    with _on(dev, stream) as st:
-        out = _out_arg(out, (rows, Hq, D), dev, "out")
-        if workspace is None:
-            need = chunk_attention_workspace(shape, cl, sl)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _need(workspace.is_cuda and workspace.device == dev and workspace.is_contiguous(),
-                  "workspace: contiguous CUDA tensor")
-        _check(lib().mk_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
-                                        _ptr(block_tables), _ptr(q), stride, _ptr(kv_layer), _ptr(out),
-                                        _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-                                        _status_arg(status, dev), st))
-    return out
+    st = _status_arg(status, dev)
+    _need(workspace is None or (workspace.device == dev and workspace.is_contiguous()),
+          "workspace: contiguous tensor on the cache's device")
+
+    def call(handle):
+        L, ws, need = lib(), workspace, ctypes.c_size_t()
+        o = _out_arg(out, (rows, Hq, D), dev, "out")
+        if ws is None:
+            _check(L.mk_chunk_attention_workspace(ctypes.byref(shape), n, cl, sl, ctypes.byref(need)))
+            if need.value:
+                ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _check(L.mk_chunk_attention(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), q.data_ptr(), stride,
+                                    kv_layer.data_ptr(), o.data_ptr(), None if ws is None else ws.data_ptr(),
+                                    0 if ws is None else ws.nbytes, st, handle))
+        return o
+    return _run(dev, stream, call)
 
 
 def read_cache(shape: CacheShape, counts, seq_lens, block_tables, kv_layer, k_out=None, v_out=None, status=None,
                stream=None):
     """The last ``counts[s]`` cached positions of every sequence as packed bf16 rows
     (``mk_read_cache``).  Returns (k, v), each [rows, Hkv, D]."""
-    cl, sl, rows = _chunk_args(shape, counts, seq_lens, block_tables, kv_layer)
-    dev, size = kv_layer.device, (rows, shape.num_kv_heads, shape.head_dim)
-    with _on(dev, stream) as st:
-        k_out, v_out = _out_arg(k_out, size, dev, "k_out"), _out_arg(v_out, size, dev, "v_out")
-        _check(lib().mk_read_cache(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, _ptr(block_tables),
-                                   _ptr(kv_layer), _ptr(k_out), _ptr(v_out), _status_arg(status, dev), st))
-    return k_out, v_out
+    cl, sl, n, rows = _lengths_arg(counts, seq_lens)
+    dev, size = _cache_arg(shape, n, block_tables, kv_layer), (rows, shape.num_kv_heads, shape.head_dim)
+    st = _status_arg(status, dev)
+
+    def call(handle):
+        k, v = _out_arg(k_out, size, dev, "k_out"), _out_arg(v_out, size, dev, "v_out")
+        _check(lib().mk_read_cache(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), kv_layer.data_ptr(),
+                                   k.data_ptr(), v.data_ptr(), st, handle))
+        return k, v
+    return _run(dev, stream, call)
 
 
 # ---------------------------------------------------------------- the engine

@@ -17,7 +17,7 @@
 // S, O, m and l, joined at the end.
 //
 // Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warp 8: loads.  Warp
-// 9: issues the MMAs.  Warp 10: query rows.  Over a q8_0 cache warps 12-15 decode codes into fp16 operand tiles.  Blocks
+// 9: issues the MMAs.  Warp 10: query rows.  Warp 11: trims V tails (q8_0: V loads).  Over a q8_0 cache warps 12-15 decode codes into fp16 operand tiles.  Blocks
 // are persistent (mk_chunk_plan.h): loads and scores of the next segment run under the epilogue of
 // this one.  Every wait is bounded: one that runs out raises the block's abort flag, every
 // role leaves its loop, copies in flight are let land and tensor memory is returned.
@@ -41,6 +41,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 namespace mk {
@@ -215,9 +216,9 @@ template <int D, bool Q8>
 struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;           // one operand tile
   static constexpr int kGroup = D / 64 * 1024;               // 8 positions of a K or V tile
-  static constexpr int kRawStages = Q8 ? 3 : 0;
+  static constexpr int kRawStages = Q8 ? 3 : 1;
   static constexpr int kRaw = 2 * kTileBytes;                // behind the two Q tiles
-  static constexpr int kKv = (kRaw + kRawStages * kRawBytes + 1023) / 1024 * 1024;
+  static constexpr int kKv = (kRaw + (Q8 ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
   static constexpr int kStages = Q8 ? 3 : D == 128 ? 5 : 8;
   static constexpr int kCtl = kKv + kStages * kTileBytes;
   static constexpr int kThreads = Q8 ? 512 : 384;
@@ -348,15 +349,18 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
     out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o[i] / sum));
 }
 
-// --------------------------------------------------------------------------- loads (warp 8)
+// --------------------------------------------------------------------------- loads (warp 8; q8_0: 8 K, 11 V)
+// A q8_0 tile of 16-position pages takes 16 copies, which one warp issues one by one: K and V have a
+// warp each (64 such tiles a block, one row: 126 us with one warp, 100 with two).  They share the ring
+// of raw stages: the decode warps release its entries strictly in order, so a warp that got entry e - 2
+// has seen e - 5 released, hence e - 6, and its wait for e - 3 cannot be a phase early.
 template <int D, bool Q8>
-__device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl) {
+__device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl, int only) {
   using L = Layout<D, Q8>;
   const int lane = threadIdx.x & 31;
   const int r = p.box, nbox = kTile / r;                       // copies of a tile
   const bool mine = lane < nbox;
   Ring<L::kStages> ring;
-  Ring<Q8 ? L::kRawStages : 1> raw;
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
   uint32_t jg = 0;                                             // position tiles so far
@@ -371,36 +375,38 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
     for (int j = 0; j < g.n; ++j, ++jg) {
       const int page = page_next;
       page_next = lookup(j + 1);
-      const int pos = (g.tile0 + j) * kTile + lane * r, off = pos % p.ps;
+      const int pos = (g.tile0 + j) * kTile + lane * r;
       const bool good = mine && page >= 0 && page < p.P;
       if (mine && pos < g.len && !good && p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
-      // a bit per 8 positions
       const uint32_t ok = __ballot_sync(~0u, good);
-      const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
-      if (lane == 0) ctl->mask[jg % kMasks] = mask;
-      for (int which = 0; which < 2; ++which) {
-        if constexpr (!Q8) {
+      if (!Q8 || only == 0) {
+        // a bit per 8 positions
+        const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
+        if (lane == 0) ctl->mask[jg % kMasks] = mask;
+      }
+      if constexpr (!Q8) {
+        for (int which = 0; which < 2; ++which) {
           const uint32_t bar = smem_u32(&ctl->full[ring.st]);
           if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
           if (lane == 0) mbar_expect(bar, L::kTileBytes);
           __syncwarp();
           // a copy out of the pool's range fills its positions with zeros
           if (mine)
-            tma_5d(base + L::kKv + ring.st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map, (g.kvh * p.ps + off) / 8,
-                   (good ? page : p.P) * 2 + which, bar);
+            tma_5d(base + L::kKv + ring.st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map,
+                   (g.kvh * p.ps + pos % p.ps) / 8, (good ? page : p.P) * 2 + which, bar);
           ring.step();
-        } else {
-          const uint32_t bar = smem_u32(&ctl->raw_full[raw.st]), dst = base + L::kRaw + raw.st * kRawBytes;
-          if (!mbar_wait(smem_u32(&ctl->raw_empty[raw.st]), raw.ph ^ 1u, ctl, p.status)) return;
-          if (lane == 0) mbar_expect(bar, __popc(ok) * r * 136);
-          __syncwarp();
-          if (good) {
-            const size_t line = (static_cast<size_t>(page) * 2 + which) * p.plan.Hkv * p.ps +
-                                static_cast<size_t>(g.kvh) * p.ps + off;
-            bulk_g2s(dst + lane * r * 128, p.kv + line * 128, r * 128, bar);
-            bulk_g2s(dst + kTile * 128 + lane * r * 8, p.kv + p.code_bytes + line * 8, r * 8, bar);
-          }
-          raw.step();
+        }
+      } else {
+        const uint32_t e = 2 * jg + only, rs = e % L::kRawStages;
+        const uint32_t bar = smem_u32(&ctl->raw_full[rs]), dst = base + L::kRaw + rs * kRawBytes;
+        if (!mbar_wait(smem_u32(&ctl->raw_empty[rs]), ((e / L::kRawStages) & 1u) ^ 1u, ctl, p.status)) return;
+        if (lane == 0) mbar_expect(bar, __popc(ok) * r * 136);
+        __syncwarp();
+        if (good) {
+          const size_t at = (static_cast<size_t>(page) * 2 + only) * p.plan.Hkv * p.ps +
+                            static_cast<size_t>(g.kvh) * p.ps + pos % p.ps;
+          bulk_g2s(dst + lane * r * 128, p.kv + at * 128, r * 128, bar);
+          bulk_g2s(dst + kTile * 128 + lane * r * 8, p.kv + p.code_bytes + at * 8, r * 8, bar);
         }
       }
     }
@@ -445,7 +451,9 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
   // A thread takes chunks x and x ^ 8 (8 codes, 16 bytes of operand each) of rows tid/8 + 16 i:
   // odd rows begin with the upper half, which keeps 8-byte reads and 16-byte writes free of conflicts.
   const int row0 = tid >> 3, x = (tid & 7) | (row0 & 1) << 3;
-  constexpr int NP = 4;
+  constexpr int NR = kTile / 16;                    // rows of a thread
+  // the four scales of a row to the pairs (d, d) of its chunks' blocks of 32: one permute each
+  const uint32_t b0 = x >> 2, pick0 = 0x1010u + b0 * 0x2222u, pick1 = 0x1010u + (b0 ^ 2u) * 0x2222u;
   Ring<L::kStages> ring;
   Ring<L::kRawStages> raw;
   SegmentWalk walk(p.plan, blockIdx.x);
@@ -464,40 +472,34 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
         const uint32_t ssrc = base + L::kRaw + raw.st * kRawBytes + kTile * 128 + row0 * 8;
         const uint32_t dst = base + L::kKv + ring.st * L::kTileBytes + (row0 >> 3) * L::kGroup + (row0 & 7) * 128 +
                              (((x & 7) ^ (row0 & 7)) << 4);
-#pragma unroll 1
-        for (int q = 0; q < kTile / 16; q += NP) {
-          uint32_t w[NP][4];
-          uint16_t sc[NP][2];
+        // every load before the first store: the stores are what a load would wait behind
+        uint32_t w[NR][4], sc[NR][2];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(src + (q + i) * 2048 + x * 8));
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(w[i][2]), "=r"(w[i][3])
-                         : "r"(src + (q + i) * 2048 + (x ^ 8) * 8));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc[i][0]) : "r"(ssrc + (q + i) * 128 + (x >> 2) * 2));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sc[i][1]) : "r"(ssrc + (q + i) * 128 + ((x ^ 8) >> 2) * 2));
-          }
+        for (int i = 0; i < NR; ++i) {
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(src + i * 2048 + x * 8));
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][2]), "=r"(w[i][3]) : "r"(src + i * 2048 + (x ^ 8) * 8));
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(sc[i][0]), "=r"(sc[i][1]) : "r"(ssrc + i * 128));
+        }
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const bool live = ((mask >> (2 * (q + i) + (row0 >> 3))) & 1u) && row0 + 16 * (q + i) < left;
+        for (int i = 0; i < NR; ++i) {
+          const bool live = ((mask >> (2 * i + (row0 >> 3))) & 1u) && row0 + 16 * i < left;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t d = sc[i][c];
-              d = (d & 0x7fffu) > 0x6006u ? 0x7fffu : d;
-              d = live ? __byte_perm(d, 0, 0x1010) : 0u;
-              const __half2 dd = *reinterpret_cast<const __half2*>(&d);
-              uint32_t o[4];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t d = __byte_perm(sc[i][0], sc[i][1], c == 0 ? pick0 : pick1);
+            d = (d & 0x7fffu) > 0x6006u ? 0x7fff7fffu : d;
+            d = live ? d : 0u;
+            const __half2 dd = *reinterpret_cast<const __half2*>(&d);
+            uint32_t o[4];
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
-                uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
-                const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
-                const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
-                o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
-                o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
-              }
-              sts16(dst + (q + i) * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
+              uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
+              const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
+              const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
+              o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+              o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
             }
+            sts16(dst + i * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
           }
         }
         warp_arrive(smem_u32(&ctl->raw_empty[raw.st]));
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
   } else if (warp < 12) {
     if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) produce<D, Q8>(p, base, ctl);
+    if (warp == 8 || (Q8 && warp == 11)) produce<D, Q8>(p, base, ctl, warp == 8 ? 0 : 1);
     if (warp == 9) issue<D, Q8>(p, base, ctl);
     if (warp == 10) produce_q<D, Q8>(p, base, ctl);
     if (!Q8 && warp == 11) trim<D, Q8>(p, base, ctl);
@@ -1114,10 +1116,18 @@ int encode_queries(const mk_cache_shape& c, const AttnPlan& pl, const void* q, i
 
 template <int D, bool Q8>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
-  // (idempotent and cheap next to a launch; per device, so set on every call)
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem_bytes<D, Q8>()));
+  // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<D, Q8>()));
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   attn_kernel<D, Q8><<<p.plan.blocks, Layout<D, Q8>::kThreads, smem_bytes<D, Q8>(), st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.plan.ranged) return e;

@@ -49,17 +49,32 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
   pl->blocks = static_cast<int32_t>(std::min<int64_t>(items, kMaxBlocks));
   if (items == 0 || items > kMaxWalk) return true;
 
+  // visits the items in order: (item, its position tiles, whether it has two tiles of rows)
+  auto each = [&](auto&& visit) {
+    int item = 0;
+    for (int i = 0; i < pl->n; ++i) {
+      const int s = pl->seq[i], chunk = q.row0[s + 1] - q.row0[s], before = q.len[s] - chunk;
+      for (int u = pl->units[i] - 1; u >= 0; --u) {
+        const int end = std::min(chunk, (u + 1) * UT), t = (before + end - 1) / kTile + 1;
+        const bool two = end - u * UT > pl->TT;
+        for (int h = 0; h < pl->Hkv; ++h) visit(item++, t, two);
+      }
+    }
+  };
   // the slowest block of whole items, and the work altogether
   int64_t load[kMaxBlocks] = {}, tiles = 0, cost = 0;
-  Segment g;
-  for (int i = 0; i < pl->items; ++i) {
-    item_of(*pl, q, i, g);
-    tiles += g.tiles;
-    const int round = i / pl->blocks, at = i % pl->blocks;
-    const int64_t x = g.tiles * kTileCost[g.two] + kItemCost[g.two];
-    load[round & 1 ? pl->blocks - 1 - at : at] += x;
+  int at_block = 0, step = 1;
+  each([&](int, int t, bool two) {
+    const int64_t x = t * kTileCost[two] + kItemCost[two];
+    tiles += t;
     cost += x;
-  }
+    load[at_block] += x;
+    at_block += step;                       // 0..B-1, then B-1..0
+    if (at_block == pl->blocks || at_block < 0) {
+      step = -step;
+      at_block += step;
+    }
+  });
   const int64_t whole = *std::max_element(load, load + pl->blocks);
   const int nb = static_cast<int>(std::min<int64_t>(kMaxBlocks, (tiles + kMinRange - 1) / kMinRange));
   if (whole <= (cost + nb - 1) / nb + kMergeCost[most > pl->TT]) return true;
@@ -70,18 +85,17 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
   int b = 1;
   int64_t at = 0;   // cost before item i
   pl->start[0] = {0, 0};
-  for (int i = 0; i < pl->items; ++i) {
-    item_of(*pl, q, i, g);
-    const int64_t end = at + kItemCost[g.two] + g.tiles * kTileCost[g.two];
+  each([&](int item, int t, bool two) {
+    const int64_t end = at + kItemCost[two] + t * kTileCost[two];
     for (; b < nb; ++b) {
       const int64_t x = cost * b / nb;
       if (x >= end) break;
-      // (x below the item's own cost: the cut is before it; else after 0 <= t < tiles of its tiles)
-      const int64_t t = x < at + kItemCost[g.two] ? 0 : (x - at - kItemCost[g.two]) / kTileCost[g.two];
-      pl->start[b] = {i, static_cast<int32_t>(t)};
+      // (x within the item's own cost: the cut is before it; else after 0 <= . < t of its tiles)
+      const int64_t cut = x < at + kItemCost[two] ? 0 : (x - at - kItemCost[two]) / kTileCost[two];
+      pl->start[b] = {item, static_cast<int32_t>(cut)};
     }
     at = end;
-  }
+  });
   for (; b <= nb; ++b) pl->start[b] = {pl->items, 0};
   *floats = static_cast<size_t>(2) * nb * pl->urows * (c.head_dim + 4);
   return true;
