@@ -81,8 +81,9 @@ int clear_status(int32_t* status_out, cudaStream_t s) {
 
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kMaxTile = 64;    // rows of a block
+constexpr int kBlock = 128;
+constexpr int kAppendRows = 4;  // rows of a block, at most
+constexpr int kMaxTile = 64;
 constexpr int kMaxPairs = 64;   // rotated pairs of a head
 
 struct Cache {
@@ -144,7 +145,8 @@ __device__ __forceinline__ void lane_chunks(int l, int R, bool half, int& ca, in
 // One block takes T rows.  The rows' cos and sin are computed once per (row, pair) and shared by
 // the row's heads; then D/16 lanes take a head: two 16-byte loads, the norm's sum by shuffles,
 // the rotation in registers, two 16-byte stores (q8_0: 8-byte codes and, per head, one 8-byte
-// store of its four scales).  Reads 2 B and writes 2 B (17/16 B) a value: HBM bound.
+// store of its four scales).  Reads 2 B and writes 2 B (17/16 B) a value: HBM bound.  A block takes
+// several rows where there are enough for two blocks an SM, few rows a block each.
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ ChunkSeqs seqs,
                                                         const __grid_constant__ Cache c,
@@ -154,11 +156,27 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
                                                         const uint16_t* k_norm, float eps,
                                                         uint16_t* __restrict__ q_out) {
   constexpr int LH = D / 16;   // lanes of a head
-  __shared__ float2 cs[4 * kMaxPairs];
-  __shared__ int32_t slot[kMaxTile];
+  __shared__ float2 cs[kAppendRows * kMaxPairs];
+  __shared__ int32_t slot[kAppendRows], at[kAppendRows];
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x * T, nr = min(T, seqs.row0[seqs.n] - r0);
-  __shared__ int32_t at[kMaxTile];
+  const int H = Hq + 2 * c.Hkv, l = tid % LH;
+  // a unit is a row's head; the next unit's loads are under way while this one is worked on, the
+  // first one's under the look-ups and angles
+  int row = 0, h = tid / LH;
+  while (h >= H) {
+    h -= H;
+    ++row;
+  }
+  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+  auto fetch = [&](int row, int h) {
+    int ca, cb;
+    lane_chunks(l, R, !interleaved && h < Hq + c.Hkv, ca, cb);
+    const uint16_t* src = qkv + static_cast<size_t>(r0 + row) * stride + static_cast<size_t>(h) * D;
+    wa = __ldg(reinterpret_cast<const uint4*>(src + 8 * ca));
+    wb = __ldg(reinterpret_cast<const uint4*>(src + 8 * cb));
+  };
+  if (row < nr) fetch(row, h);
   if (tid < nr) {
     int pos;
     slot[tid] = slot_of_row(seqs, c, r0 + tid, &pos);
@@ -174,16 +192,20 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
     cs[i] = make_float2(co * mscale, sn * mscale);
   }
   __syncthreads();
-  const int H = Hq + 2 * c.Hkv, l = tid % LH;
-  for (int u = tid / LH; u < nr * H; u += kBlock / LH) {
-    const int row = u / H, h = u - row * H;
+  while (row < nr) {
     const bool isq = h < Hq, isv = h >= Hq + c.Hkv;
     int ca, cb;
     lane_chunks(l, R, !interleaved && !isv, ca, cb);
-    const uint16_t* src = qkv + static_cast<size_t>(r0 + row) * stride + static_cast<size_t>(h) * D;
     float a[8], b[8];
-    unpack8(*reinterpret_cast<const uint4*>(src + 8 * ca), a);
-    unpack8(*reinterpret_cast<const uint4*>(src + 8 * cb), b);
+    unpack8(wa, a);
+    unpack8(wb, b);
+    const int crow = row, ch = h;
+    h += kBlock / LH;
+    while (h >= H) {
+      h -= H;
+      ++row;
+    }
+    if (row < nr) fetch(row, h);
     const uint16_t* gain = isq ? q_norm : k_norm;
     if (!isv) {
       // the lanes of a head are in one warp and agree on it (a warp's last heads may be missing:
@@ -206,7 +228,7 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
         }
       }
       if (l < R / 16) {
-        const float2* t = cs + row * half_r;
+        const float2* t = cs + crow * half_r;
         if (interleaved) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -229,14 +251,14 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
       }
     }
     if (isq) {
-      uint16_t* dst = q_out + (static_cast<size_t>(r0 + row) * Hq + h) * D;
+      uint16_t* dst = q_out + (static_cast<size_t>(r0 + crow) * Hq + ch) * D;
       *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8(a);
       *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8(b);
       continue;
     }
-    if (slot[row] < 0) continue;   // the whole row: its lanes agree
-    const int kvh = isv ? h - Hq - c.Hkv : h - Hq;
-    const size_t line = static_cast<size_t>(slot[row]) + static_cast<size_t>(isv ? c.Hkv + kvh : kvh) * c.ps;
+    if (slot[crow] < 0) continue;   // the whole row: its lanes agree
+    const int kvh = isv ? ch - Hq - c.Hkv : ch - Hq;
+    const size_t line = static_cast<size_t>(slot[crow]) + static_cast<size_t>(isv ? c.Hkv + kvh : kvh) * c.ps;
     if constexpr (!Q8) {
       uint16_t* dst = reinterpret_cast<uint16_t*>(c.kv) + line * D;
       *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8(a);
@@ -287,8 +309,10 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
   }
 }
 
-// One block takes T rows; a thread takes 8 values of one head's K or V row: 16 bytes in (q8_0: 8
-// codes and their block's scale), 16 bytes out, neighbouring threads the row's next values.
+// One block takes T rows; a thread takes 16 bytes of one head's K or V row (8 bf16 values, or 16
+// codes with their block's scale) and neighbouring threads the row's next, kUnroll of them at a
+// time so that their loads are in flight together.  Bytes in, bytes out: HBM bound.
+constexpr int kUnroll = 4, kReadUnits = 4;   // at a time; a thread's in all (16: 67 us where 4 take 59, 131072 q8_0 positions)
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kBlock) read_kernel(const __grid_constant__ ChunkSeqs seqs,
                                                       const __grid_constant__ Cache c, int T,
@@ -301,30 +325,56 @@ __global__ void __launch_bounds__(kBlock) read_kernel(const __grid_constant__ Ch
     slot[tid] = slot_of_row(seqs, c, r0 + tid, &pos);
   }
   __syncthreads();
-  constexpr int CH = D / 8;
-  const int per = 2 * c.Hkv * CH;   // units of a row: [K, V][head][chunk]
-  for (int u = tid; u < nr * per; u += kBlock) {
-    const int row = u / per, w = u - row * per, hh = w / CH, ch = w - hh * CH;
-    const bool isv = hh >= c.Hkv;
-    const int kvh = isv ? hh - c.Hkv : hh;
-    uint4 out = make_uint4(0u, 0u, 0u, 0u);
-    if (slot[row] >= 0) {
-      const size_t line = static_cast<size_t>(slot[row]) + static_cast<size_t>(hh) * c.ps;
-      if constexpr (!Q8) {
-        out = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(c.kv) + line * D) + ch);
-      } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(c.kv + line * D) + ch);
-        const float d = __half2float(__ushort_as_half(
-            __ldg(reinterpret_cast<const uint16_t*>(c.kv + c.code_bytes) + line * (D / 32) + ch / 4)));
-        float f[8];
+  constexpr int VAL = Q8 ? 16 : 8, CH = D / VAL;
+  const int heads = 2 * c.Hkv, ch = tid % CH;   // units: [row][K heads, V heads][chunk]
+  constexpr int kStep = kBlock / CH;            // heads between a thread's units
+  int row = 0, hh = tid / CH;
+  auto wrap = [&]() {
+    while (hh >= heads) {
+      hh -= heads;
+      ++row;
+    }
+  };
+  wrap();
+  while (row < nr) {
+    uint4 w[kUnroll];
+    uint16_t sc[kUnroll];
+    int urow[kUnroll], uh[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          f[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i % 4)))) * d;
-        out = pack8(f);
+    for (int i = 0; i < kUnroll; ++i) {
+      urow[i] = row;
+      uh[i] = hh;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      sc[i] = 0;
+      if (row < nr && slot[row] >= 0) {
+        const size_t line = static_cast<size_t>(slot[row]) + static_cast<size_t>(hh) * c.ps;
+        w[i] = __ldg(reinterpret_cast<const uint4*>(c.kv + line * D * (Q8 ? 1 : 2)) + ch);
+        if constexpr (Q8) sc[i] = __ldg(reinterpret_cast<const uint16_t*>(c.kv + c.code_bytes) + line * (D / 32) + ch / 2);
+      }
+      hh += kStep;
+      wrap();
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      if (urow[i] >= nr) break;
+      const bool isv = uh[i] >= c.Hkv;
+      uint16_t* dst = (isv ? v_out : k_out) +
+                      (static_cast<size_t>(r0 + urow[i]) * c.Hkv + (isv ? uh[i] - c.Hkv : uh[i])) * D + VAL * ch;
+      if constexpr (!Q8) {
+        *reinterpret_cast<uint4*>(dst) = w[i];
+      } else {
+        const float d = __half2float(__ushort_as_half(sc[i]));
+        const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            f[k] = static_cast<float>(static_cast<int8_t>(q[2 * half + k / 4] >> (8 * (k % 4)))) * d;
+          reinterpret_cast<uint4*>(dst)[half] = pack8(f);
+        }
       }
     }
-    uint16_t* dst = (isv ? v_out : k_out) + (static_cast<size_t>(r0 + row) * c.Hkv + kvh) * D;
-    *reinterpret_cast<uint4*>(dst + 8 * ch) = out;
   }
 }
 
@@ -424,7 +474,7 @@ extern "C" int mk_append_chunk(const mk_cache_shape* shape, int32_t num_seqs, co
   rc = clear_status(status_out, st);
   if (rc || rows == 0) return rc;
   const Cache cache = cache_of(c, block_tables, kv_layer, status_out);
-  const int T = rows >= 4 * 304 ? 4 : 1;
+  const int T = rows >= kAppendRows * 304 ? kAppendRows : rows >= 2 * 304 ? 2 : 1;
   const int grid = (rows + T - 1) / T;
   auto go = [&](auto kernel) {
     kernel<<<grid, kBlock, 0, st>>>(seqs, cache, turns, T, c.num_q_heads, static_cast<const uint16_t*>(qkv), qkv_stride,
@@ -453,9 +503,10 @@ extern "C" int mk_read_cache(const mk_cache_shape* shape, int32_t num_seqs, cons
   rc = clear_status(status_out, st);
   if (rc || rows == 0) return rc;
   const Cache cache = cache_of(c, block_tables, kv_layer, status_out);
-  const int per = 2 * c.num_kv_heads * c.head_dim / 8;
-  int T = 4 * kBlock / per;
+  const int per = 2 * c.num_kv_heads * c.head_dim / ((c.flags & MK_FLAG_KV_Q8) ? 16 : 8);   // units of a row
+  int T = kReadUnits * kBlock / per;
   T = T < 1 ? 1 : T > kMaxTile ? kMaxTile : T;
+  while (T > 1 && (rows + T - 1) / T < 304) T = (T + 1) / 2;                                 // two blocks an SM first
   const int grid = (rows + T - 1) / T;
   auto go = [&](auto kernel) {
     kernel<<<grid, kBlock, 0, st>>>(seqs, cache, T, static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out));
