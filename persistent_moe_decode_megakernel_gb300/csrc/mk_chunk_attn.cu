@@ -1015,43 +1015,83 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-// Merges the items that the ranges cut, in block order: blockIdx.x is the block that began one.  A
-// block takes 8 rows, a thread 4 columns of one; a warp's 8 rows lie side by side in a partial.
-template <int D, bool Q8>
+// Merges the items that the ranges cut, in block order; blockIdx.x is the item, 2 D threads a block.
+// Wide (units of few rows, cut into many parts): a block takes 128 / D rows, a warp every eighth
+// partial, whose loads are all on their way before the factors are known.  Else a block takes 8
+// rows, a thread 4 columns of one, a warp's 8 rows side by side in a partial; the parts are few.
+template <int D, bool Q8, bool WIDE>
 __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kWarps = 2 * D / 32, kLanes = D / 4, kRows = WIDE ? 32 / kLanes : 8;
+  constexpr int kMine = WIDE ? (kMaxBlocks + kWarps - 1) / kWarps : 1, kAtOnce = 8;
   const AttnPlan& pl = p.plan;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, urow = blockIdx.y * 8 + (lane & 7);
-  const int chunk = (threadIdx.x >> 5) * 4 + (lane >> 3);
-  const int item = pl.start[b + 1].item;
-  if (pl.start[b + 1].tile == 0 || (pl.start[b].item == item && pl.start[b].tile > 0)) return;
+  const int b = pl.cut_block[blockIdx.x], n = pl.cut_parts[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Segment g;
-  item_of(pl, p.seqs, item, g);
-  const int rows = g.ntok * pl.G;
-  if (blockIdx.y * 8 >= rows) return;
+  item_of(pl, p.seqs, pl.start[b + 1].item, g);
+  const int rows = g.ntok * pl.G, row0 = blockIdx.y * kRows;
+  if (row0 >= rows) return;
+  const int lrow = WIDE ? lane / kLanes : lane & 7, chunk = WIDE ? lane % kLanes : warp * 4 + (lane >> 3);
+  const int urow = row0 + lrow;
   const bool live = urow < rows;
-  int n = 2;                                       // partials: the beginning, and each range that starts inside
-  while (b + n <= pl.blocks && pl.start[b + n].item == item) ++n;
   const size_t slot = static_cast<size_t>(pl.urows) * (D + 4);
   const float* first = p.part + static_cast<size_t>(2 * b + 1) * slot;            // then slots 2(b+1), 2(b+2), ..
-  const size_t at_ml = static_cast<size_t>(pl.urows) * D + 2 * static_cast<size_t>(live ? urow : 0);
-  const size_t at_o = (static_cast<size_t>(chunk) * pl.urows + (live ? urow : 0)) * 4;
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* pk = k == 0 ? first : first + (2 * k - 1) * slot;
-    const float2 ml = *reinterpret_cast<const float2*>(pk + at_ml);
-    const float4 o = *reinterpret_cast<const float4*>(pk + at_o);
-    const float top = fmaxf(M, ml.x);
-    const float f = M == -INFINITY ? 0.f : ex2(M - top), fk = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    M = top;
-    L = L * f + ml.y * fk;
-    acc.x = acc.x * f + o.x * fk;
-    acc.y = acc.y * f + o.y * fk;
-    acc.z = acc.z * f + o.z * fk;
-    acc.w = acc.w * f + o.w * fk;
+  auto at = [&](int k) { return k == 0 ? first : first + (2 * k - 1) * slot; };
+  const size_t at_ml = static_cast<size_t>(pl.urows) * D, at_o = (static_cast<size_t>(chunk) * pl.urows + (live ? urow : 0)) * 4;
+  __shared__ float fac[kRows][kMaxBlocks], den[kRows];
+  __shared__ float4 sums[WIDE ? kWarps : 1][WIDE ? 32 : 1];
+  float4 held[kAtOnce];
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int k = warp + i * kWarps;
+      held[i] = k < n ? *reinterpret_cast<const float4*>(at(k) + at_o) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
-  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  // the factors of each row's partials: a warp a row (D = 64: WIDE's two rows, or two rows a warp in turn)
+  for (int r = warp; r < kRows; r += kWarps) {
+    const int row = min(row0 + r, rows - 1);
+    float M = -INFINITY, L = 0.f;
+    for (int k = lane; k < n; k += 32) {
+      const float m = at(k)[at_ml + 2 * row];
+      fac[r][k] = m;
+      M = fmaxf(M, m);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    for (int k = lane; k < n; k += 32) {
+      const float m = fac[r][k], f = m == -INFINITY ? 0.f : ex2(m - M);
+      fac[r][k] = f;
+      L += f * at(k)[at_ml + 2 * row + 1];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(~0u, L, o);
+    if (lane == 0) den[r] = L;
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4 o, float f) {
+    acc.x = fmaf(o.x, f, acc.x);
+    acc.y = fmaf(o.y, f, acc.y);
+    acc.z = fmaf(o.z, f, acc.z);
+    acc.w = fmaf(o.w, f, acc.w);
+  };
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (warp + i * kWarps < n) add(held[i], fac[lrow][warp + i * kWarps]);
+    for (int i = kAtOnce; i < kMine; ++i) {
+      const int k = warp + i * kWarps;
+      if (k < n) add(*reinterpret_cast<const float4*>(at(k) + at_o), fac[lrow][k]);
+    }
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < kWarps; ++w) add(sums[w][lane], 1.f);
+  } else {
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) add(*reinterpret_cast<const float4*>(at(k) + at_o), fac[lrow][k]);
+  }
+  const float L = den[lrow], inv = L == 0.f ? 0.f : 1.0f / L;
   const int tok = urow * pl.by_G >> 16;
   const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * pl.G + urow - tok * pl.G;
   acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -1060,11 +1100,12 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
         make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
   const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
   const bool odd = live && (!(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
-  for (uint32_t todo = __ballot_sync(~0u, odd), done = 0; todo; todo &= todo - 1) {
+  uint32_t done = 0;
+  for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1;
-    const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
-    if (!((done >> (who & 7)) & 1u)) exact_row<D, Q8>(p, rr, hh);
-    done |= 1u << (who & 7);
+    const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who), lr = __shfl_sync(~0u, lrow, who);
+    if (!((done >> lr) & 1u)) exact_row<D, Q8>(p, rr, hh);
+    done |= 1u << lr;
   }
 }
 
@@ -1130,8 +1171,14 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   }
   attn_kernel<D, Q8><<<p.plan.blocks, Layout<D, Q8>::kThreads, smem_bytes<D, Q8>(), st>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !p.plan.ranged) return e;
-  merge_kernel<D, Q8><<<dim3(p.plan.blocks, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
+  if (e != cudaSuccess || p.plan.cuts == 0) return e;
+  // (plans with units of two tiles cut an item in few parts)
+  if (p.plan.urows <= kTile / 2) {
+    constexpr int kRows = 128 / D;
+    merge_kernel<D, Q8, true><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
+  } else {
+    merge_kernel<D, Q8, false><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
+  }
   return cudaGetLastError();
 }
 

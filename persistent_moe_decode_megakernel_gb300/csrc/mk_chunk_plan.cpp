@@ -23,7 +23,7 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
   pl->G = c.num_q_heads / c.num_kv_heads;
   pl->TT = kTile / pl->G;
   pl->by_G = 65536 / pl->G + 1;   // exact below 2^9 rows
-  pl->n = pl->items = pl->blocks = pl->ranged = 0;
+  pl->n = pl->items = pl->blocks = pl->ranged = pl->cuts = 0;
   *floats = 0;
   const int UT = 2 * pl->TT;
   int most = 0;
@@ -97,6 +97,14 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
     at = end;
   });
   for (; b <= nb; ++b) pl->start[b] = {pl->items, 0};
+  for (b = 0; b < nb; ++b) {
+    const int item = pl->start[b + 1].item;
+    if (pl->start[b + 1].tile == 0 || (pl->start[b].item == item && pl->start[b].tile > 0)) continue;
+    int n = 2;
+    while (b + n <= nb && pl->start[b + n].item == item) ++n;
+    pl->cut_block[pl->cuts] = static_cast<uint8_t>(b);
+    pl->cut_parts[pl->cuts++] = static_cast<uint8_t>(n);
+  }
   *floats = static_cast<size_t>(2) * nb * pl->urows * (c.head_dim + 4);
   return true;
 }

@@ -30,6 +30,9 @@ struct AttnPlan {
   int32_t units[kMaxSeqs];           // of the i-th
   int32_t item0[kMaxSeqs + 1];       // first item of the i-th
   struct { int32_t item, tile; } start[kMaxBlocks + 1];   // ranged: where each block's range begins
+  int32_t cuts;                      // items that a cut falls into, and of each
+  uint8_t cut_block[kMaxBlocks];     // the block that runs its beginning,
+  uint8_t cut_parts[kMaxBlocks];     // and its partials: that block's and the next ones'
 };
 
 struct Segment {
