@@ -336,82 +336,84 @@ def rope_frequencies(rotary_dim: int, theta: float, factor: float = 1.0, origina
     return out
 
 
-def _need(ok, what):
-    if not ok:
-        raise MkError(MK_ERR_INVALID_ARG, what)
-
-
 # These calls are short next to their marshalling (a few microseconds on the device for a few tokens), so
-# it is kept lean: one comparison per argument, plain integers and bytes to ctypes, no context managers
-# unless the device or the stream is not the current one.
+# it is kept lean: torch is asked for as little as possible, messages are built only on failure, lengths go
+# to ctypes as bytes and pointers as integers, and no context manager is entered unless the device or the
+# stream is not the current one.
+def _bad(what):
+    raise MkError(MK_ERR_INVALID_ARG, what)
+
+
 def _lengths_arg(chunk_lens, seq_lens):
     """Both as int32 bytes (ctypes passes their address), the number of sequences, the rows."""
     cl, sl = np.asarray(chunk_lens, dtype=np.int32), np.asarray(seq_lens, dtype=np.int32)
-    _need(cl.ndim == 1 and cl.shape == sl.shape, "chunk_lens and seq_lens: one length per sequence each")
+    if cl.ndim != 1 or cl.shape != sl.shape:
+        _bad("chunk_lens and seq_lens: one length per sequence each")
     rows = sum(cl.tolist())
-    _need(0 <= rows < 1 << 24, "chunk_lens: fewer than 2^24 rows")
+    if not 0 <= rows < 1 << 24:
+        _bad("chunk_lens: fewer than 2^24 rows")
     return cl.tobytes(), sl.tobytes(), cl.size, rows
 
 
 def _cache_arg(shape, n_seqs, block_tables, kv_layer):
-    """The cache's device, after checks of what the C call cannot see."""
+    """The cache's device index, after checks of what the C call cannot see."""
     import torch
-    dev = kv_layer.device
-    bs = block_tables.shape
-    _need(dev.type == "cuda" and block_tables.device == dev and block_tables.dtype is torch.int32
-          and block_tables.is_contiguous() and len(bs) == 2 and bs[0] >= n_seqs and bs[1] == shape.max_pages_per_seq,
-          "block_tables: contiguous int32 [num_seqs, max_pages_per_seq] on the cache's CUDA device")
+    dev, bs, q8 = kv_layer.get_device(), block_tables.shape, shape.flags & FLAG_KV_Q8
+    if not (dev >= 0 and block_tables.get_device() == dev and block_tables.dtype is torch.int32 and len(bs) == 2
+            and bs[0] >= n_seqs and bs[1] == shape.max_pages_per_seq and block_tables.is_contiguous()):
+        _bad("block_tables: contiguous int32 [num_seqs, max_pages_per_seq] on the cache's CUDA device")
     n = shape.num_pages * 2 * shape.num_kv_heads * shape.page_size * shape.head_dim
-    q8 = shape.flags & FLAG_KV_Q8
-    _need(kv_layer.dtype is (torch.uint8 if q8 else torch.bfloat16) and kv_layer.numel() == (n + n // 16 if q8 else n)
-          and kv_layer.is_contiguous(),
-          "kv_layer: one layer of the shape's cache, contiguous CUDA tensor, bf16 (q8_0: uint8 codes, then f16 scales)")
+    if not (kv_layer.dtype is (torch.uint8 if q8 else torch.bfloat16) and kv_layer.numel() == (n + n // 16 if q8 else n)
+            and kv_layer.is_contiguous()):
+        _bad("kv_layer: one layer of the shape's cache, contiguous CUDA tensor, bf16 (q8_0: uint8 codes, then f16 scales)")
     return dev
 
 
-def _rows_arg(t, rows, heads, dim, device, what):
+def _rows_arg(t, rows, heads, dim, dev, what):
     """The row stride of t, bf16 rows of heads*dim contiguous values as [rows, heads*dim] or [rows, heads, dim]."""
     import torch
-    shape, stride = t.shape, t.stride()
-    _need(t.device == device and t.dtype is torch.bfloat16 and shape[0] >= rows
-          and (shape[1:] == (heads * dim,) and stride[1] == 1
-               or shape[1:] == (heads, dim) and stride[2] == 1 and (stride[1] == dim or heads == 1)),
-          f"{what}: bf16 rows of {heads} heads of {dim} contiguous values on the cache's device, at least {rows} rows")
-    return stride[0] if shape[0] > 1 else heads * dim
+    size, stride = t.shape, t.stride()
+    if not (t.get_device() == dev and t.dtype is torch.bfloat16 and size[0] >= rows
+            and (len(size) == 2 and size[1] == heads * dim and stride[1] == 1
+                 or len(size) == 3 and size[1] == heads and size[2] == dim and stride[2] == 1
+                 and (stride[1] == dim or heads == 1))):
+        _bad(f"{what}: bf16 rows of {heads} heads of {dim} contiguous values on the cache's device, at least {rows} rows")
+    return stride[0] if size[0] > 1 else heads * dim
 
 
-def _out_arg(t, shape, device, what):
+def _out_arg(t, size, dev, what, kv_layer):
     import torch
-    if t is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    _need(t.device == device and t.dtype is torch.bfloat16 and t.is_contiguous()
-          and t.shape[1:] == shape[1:] and t.shape[0] >= shape[0],
-          f"{what}: contiguous bf16 tensor of at least {list(shape)} on the cache's device")
+    if t is None:   # (a device object: an index costs torch a microsecond more)
+        return torch.empty(size, dtype=torch.bfloat16, device=kv_layer.device)
+    if not (t.get_device() == dev and t.dtype is torch.bfloat16 and t.is_contiguous() and t.shape[1:] == size[1:]
+            and t.shape[0] >= size[0]):
+        _bad(f"{what}: contiguous bf16 tensor of at least {list(size)} on the cache's device")
     return t
 
 
-def _status_arg(t, device):
+def _status_arg(t, dev):
     import torch
     if t is None:
         return None
-    _need(t.device == device and t.dtype is torch.int32 and t.numel() == 1,
-          "status: int32 tensor of one value on the cache's device")
+    if not (t.get_device() == dev and t.dtype is torch.int32 and t.numel() == 1):
+        _bad("status: int32 tensor of one value on the cache's device")
     return t.data_ptr()
 
 
-def _run(device, stream, call):
-    """``call(stream handle)`` with ``device`` and ``stream`` (default: torch's current one of the device)
-    current, so that new outputs and workspaces belong to the stream that writes them."""
+def _run(dev, stream, call, *args):
+    """``call(stream handle, *args)`` with device ``dev`` and ``stream`` (default: torch's current one of the
+    device) current, so that new outputs and workspaces belong to the stream that writes them."""
     import torch
-    if stream is not None:
-        _need(stream.device == device, "stream is on another device than the tensors")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return call(torch.cuda.current_stream(device).cuda_stream)
-    # (the handle alone: building a Stream object costs as much as the rest of the marshalling)
-    return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is None:
+        if torch._C._cuda_getDevice() == dev:
+            # (the handle alone: building a Stream object costs as much as the rest of the marshalling)
+            return call(torch._C._cuda_getCurrentRawStream(dev), *args)
+        with torch.cuda.device(dev):
+            return call(torch._C._cuda_getCurrentRawStream(dev), *args)
+    if stream.device.index != dev:
+        _bad("stream is on another device than the tensors")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream, *args)
 
 
 def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, rope: Rope | None = None,
@@ -429,18 +431,19 @@ def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_
     dev, Hq, D = _cache_arg(shape, n, block_tables, kv_layer), shape.num_q_heads, shape.head_dim
     stride = _rows_arg(qkv, rows, Hq + 2 * shape.num_kv_heads, D, dev, "qkv")
     for t in (q_norm, k_norm):
-        _need(t is None or (t.device == dev and t.dtype is torch.bfloat16 and t.is_contiguous() and t.numel() == D),
-              "q_norm / k_norm: contiguous bf16 [head_dim] on the cache's device")
+        if t is not None and not (t.get_device() == dev and t.dtype is torch.bfloat16 and t.is_contiguous()
+                                  and t.numel() == D):
+            _bad("q_norm / k_norm: contiguous bf16 [head_dim] on the cache's device")
     st = _status_arg(status, dev)
 
     def call(handle):
-        out = _out_arg(q_out, (rows, Hq, D), dev, "q_out")
-        _check(lib().mk_append_chunk(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), qkv.data_ptr(), stride,
-                                     None if rope is None else ctypes.byref(rope.struct),
-                                     None if q_norm is None else q_norm.data_ptr(),
-                                     None if k_norm is None else k_norm.data_ptr(), eps, out.data_ptr(),
-                                     kv_layer.data_ptr(), st, handle))
-        return out
+        out = _out_arg(q_out, (rows, Hq, D), dev, "q_out", kv_layer)
+        rc = lib().mk_append_chunk(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), qkv.data_ptr(), stride,
+                                   None if rope is None else ctypes.byref(rope.struct),
+                                   None if q_norm is None else q_norm.data_ptr(),
+                                   None if k_norm is None else k_norm.data_ptr(), eps, out.data_ptr(),
+                                   kv_layer.data_ptr(), st, handle)
+        return _check(rc) or out
     return _run(dev, stream, call)
 
 
@@ -475,16 +478,16 @@ def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv
     dev, Hq, D = _cache_arg(shape, n, block_tables, kv_layer), shape.num_q_heads, shape.head_dim
     stride = _rows_arg(q, rows, Hq, D, dev, "q")
     st = _status_arg(status, dev)
-    _need(workspace is None or (workspace.device == dev and workspace.is_contiguous()),
-          "workspace: contiguous tensor on the cache's device")
+    if workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
+        _bad("workspace: contiguous tensor on the cache's device")
 
     def call(handle):
         L, ws, need = lib(), workspace, ctypes.c_size_t()
-        o = _out_arg(out, (rows, Hq, D), dev, "out")
+        o = _out_arg(out, (rows, Hq, D), dev, "out", kv_layer)
         if ws is None:
             _check(L.mk_chunk_attention_workspace(ctypes.byref(shape), n, cl, sl, ctypes.byref(need)))
             if need.value:
-                ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+                ws = torch.empty(need.value, dtype=torch.uint8, device=kv_layer.device)
         _check(L.mk_chunk_attention(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), q.data_ptr(), stride,
                                     kv_layer.data_ptr(), o.data_ptr(), None if ws is None else ws.data_ptr(),
                                     0 if ws is None else ws.nbytes, st, handle))
@@ -501,7 +504,7 @@ def read_cache(shape: CacheShape, counts, seq_lens, block_tables, kv_layer, k_ou
     st = _status_arg(status, dev)
 
     def call(handle):
-        k, v = _out_arg(k_out, size, dev, "k_out"), _out_arg(v_out, size, dev, "v_out")
+        k, v = _out_arg(k_out, size, dev, "k_out", kv_layer), _out_arg(v_out, size, dev, "v_out", kv_layer)
         _check(lib().mk_read_cache(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), kv_layer.data_ptr(),
                                    k.data_ptr(), v.data_ptr(), st, handle))
         return k, v
