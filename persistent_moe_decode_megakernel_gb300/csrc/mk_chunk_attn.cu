@@ -16,8 +16,8 @@
 // tokens, as in decoding) runs two STREAMS instead: even and odd position tiles, each with its own
 // S, O, m and l, joined at the end.
 //
-// Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warp 8: loads.  Warp
-// 9: issues the MMAs.  Warp 10: query rows.  Warp 11: trims V tails (q8_0: V loads).  Over a q8_0 cache warps 12-15 decode codes into fp16 operand tiles.  Blocks
+// Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warps 8 and
+// 11: K and V loads.  Warp 9: issues the MMAs.  Warp 10: query rows and V tails.  Over a q8_0 cache warps 12-15 decode codes into fp16 operand tiles.  Blocks
 // are persistent (mk_chunk_plan.h): loads and scores of the next segment run under the epilogue of
 // this one.  Every wait is bounded: one that runs out raises the block's abort flag, every
 // role leaves its loop, copies in flight are let land and tensor memory is returned.
@@ -349,18 +349,22 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
     out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o[i] / sum));
 }
 
-// --------------------------------------------------------------------------- loads (warp 8; q8_0: 8 K, 11 V)
-// A q8_0 tile of 16-position pages takes 16 copies, which one warp issues one by one: K and V have a
-// warp each (64 such tiles a block, one row: 126 us with one warp, 100 with two).  They share the ring
-// of raw stages: the decode warps release its entries strictly in order, so a warp that got entry e - 2
-// has seen e - 5 released, hence e - 6, and its wait for e - 3 cannot be a phase early.
+// --------------------------------------------------------------------------- loads (warp 8: K, warp 11: V)
+// A tile of 16-position pages takes 8 copies (q8_0: 16), which a warp issues one by one, so K and V have a
+// warp each (64 position tiles a block, one row, the cache in L2: bf16 85 us with one warp, 59 with
+// two; q8_0 126 and 100).  They share a ring.  A warp waits for entry e - N's release (N stages) by its
+// parity, which is sound only if entry e - 2N is known to be released:
+//   bf16, N = 5: the warp got e - 2, so e - 7, the other operand's, was released; with e = K_j that is
+//     V_{j-4}, and the MMA warp releases K_{j-5} before it; with e = V_j it is K_{j-3}, and V_{j-5} goes
+//     before that (in units of one tile right before, in units of two earlier).  N = 8: e - 16 is the
+//     warp's own operand's, and it waited for it to get e - 8.
+//   q8_0, raw stages, N = 3: the decode warps release them strictly in order; e - 2 came after e - 5.
 template <int D, bool Q8>
 __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl, int only) {
   using L = Layout<D, Q8>;
   const int lane = threadIdx.x & 31;
   const int r = p.box, nbox = kTile / r;                       // copies of a tile
   const bool mine = lane < nbox;
-  Ring<L::kStages> ring;
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
   uint32_t jg = 0;                                             // position tiles so far
@@ -379,25 +383,23 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
       const bool good = mine && page >= 0 && page < p.P;
       if (mine && pos < g.len && !good && p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
       const uint32_t ok = __ballot_sync(~0u, good);
-      if (!Q8 || only == 0) {
+      if (only == 0) {
         // a bit per 8 positions
         const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
         if (lane == 0) ctl->mask[jg % kMasks] = mask;
       }
+      const uint32_t e = 2 * jg + only;                        // this tile's entry
       if constexpr (!Q8) {
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t bar = smem_u32(&ctl->full[ring.st]);
-          if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
-          if (lane == 0) mbar_expect(bar, L::kTileBytes);
-          __syncwarp();
-          // a copy out of the pool's range fills its positions with zeros
-          if (mine)
-            tma_5d(base + L::kKv + ring.st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map,
-                   (g.kvh * p.ps + pos % p.ps) / 8, (good ? page : p.P) * 2 + which, bar);
-          ring.step();
-        }
+        const uint32_t st = e % L::kStages, bar = smem_u32(&ctl->full[st]);
+        if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
+        if (lane == 0) mbar_expect(bar, L::kTileBytes);
+        __syncwarp();
+        // a copy out of the pool's range fills its positions with zeros
+        if (mine)
+          tma_5d(base + L::kKv + st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map,
+                 (g.kvh * p.ps + pos % p.ps) / 8, (good ? page : p.P) * 2 + only, bar);
       } else {
-        const uint32_t e = 2 * jg + only, rs = e % L::kRawStages;
+        const uint32_t rs = e % L::kRawStages;
         const uint32_t bar = smem_u32(&ctl->raw_full[rs]), dst = base + L::kRaw + rs * kRawBytes;
         if (!mbar_wait(smem_u32(&ctl->raw_empty[rs]), ((e / L::kRawStages) & 1u) ^ 1u, ctl, p.status)) return;
         if (lane == 0) mbar_expect(bar, __popc(ok) * r * 136);
@@ -413,15 +415,22 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
   }
 }
 
-// Query tiles (warp 10): TT tokens x G heads x 64 dims a box, as soon as the last S of the segment
-// before has read the tiles -- under that segment's last softmax, values and epilogue.
+// What a page holds behind the sequence's last position must not meet a weight, not even a zero one
+// (0 * NaN): zeros go there in a segment's last V tile.  (q8_0 tiles are zeroed as they are decoded;
+// whole copies behind the sequence are zeros already.)
+template <bool Q8>
+__device__ __forceinline__ bool trims(const Segment& g) { return !Q8 && (g.tile0 + g.n) * kTile > g.len; }
+
+// Warp 10.  Query tiles: TT tokens x G heads x 64 dims a box, as soon as the last S of the segment
+// before has read the tiles -- under that segment's last softmax, values and epilogue.  And the trim
+// of a segment's last V tile, when the MMA warp, which keeps the entry until then, says that it landed.
 template <int D, bool Q8>
 __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ctl* ctl) {
   using L = Layout<D, Q8>;
   const int lane = threadIdx.x & 31;
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
-  uint32_t k = 0;
+  uint32_t k = 0, trimmed = 0, c0 = 0;
   while (walk.next(p.plan, p.seqs, g)) {
     if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status)) return;
     ++k;
@@ -436,6 +445,17 @@ __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ct
       }
     }
     __syncwarp();
+    const uint32_t c = c0 + 2 * g.n - 1;
+    c0 += 2 * g.n;
+    if (trims<Q8>(g)) {
+      if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status)) return;
+      ++trimmed;
+      const int first = g.len - (g.tile0 + g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
+      const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
+      for (int n = first + lane / (D / 8); n < last; n += 256 / D) sts16(v + (n >> 3) * L::kGroup + (n & 7) * 128, 0, 0, 0, 0);
+      fence_async_smem();
+      warp_arrive(smem_u32(&ctl->trim));
+    }
   }
 }
 
@@ -509,34 +529,6 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
         ring.step();
       }
     }
-  }
-}
-
-// What a page holds behind the sequence's last position must not meet a weight, not even a zero one
-// (0 * NaN): warp 11 puts zeros there in a segment's last V tile.  (q8_0 tiles are zeroed as they are
-// decoded; whole copies behind the sequence are zeros already.)
-template <bool Q8>
-__device__ __forceinline__ bool trims(const Segment& g) { return !Q8 && (g.tile0 + g.n) * kTile > g.len; }
-
-template <int D, bool Q8>
-__device__ __forceinline__ void trim(const AttnParams& p, uint32_t base, Ctl* ctl) {
-  using L = Layout<D, Q8>;
-  const int lane = threadIdx.x & 31;
-  SegmentWalk walk(p.plan, blockIdx.x);
-  Segment g;
-  uint32_t c0 = 0, k = 0;
-  while (walk.next(p.plan, p.seqs, g)) {
-    const uint32_t c = c0 + 2 * g.n - 1;
-    c0 += 2 * g.n;
-    if (!trims<Q8>(g)) continue;
-    // (told by the MMA thread, which keeps the entry until the trim: `full` itself may be phases away)
-    if (!mbar_wait(smem_u32(&ctl->landed), k & 1, ctl, p.status)) return;
-    ++k;
-    const int first = g.len - (g.tile0 + g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
-    const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
-    for (int n = first + lane / (D / 8); n < last; n += 256 / D) sts16(v + (n >> 3) * L::kGroup + (n & 7) * 128, 0, 0, 0, 0);
-    fence_async_smem();
-    warp_arrive(smem_u32(&ctl->trim));
   }
 }
 
@@ -737,17 +729,18 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < mine; ++i) {
       const int j = g.two ? i : 2 * i + t;
+      const int limit = pos - (g.tile0 + j) * kTile;           // last column this row sees
+      const bool edge = __any_sync(~0u, limit < kTile - 1);
       if (!mbar_wait(smem_u32(&ctl->sfull[t]), phase & 1, ctl, p.status)) return;
       ++phase;
       if (any) {                                   // (warps without rows leave their lanes as they are)
         tc_after();
+        const uint32_t mask = ctl->mask[(jg + j) % kMasks];
         float s[kTile];
 #pragma unroll
         for (int k = 0; k < kTile; k += 32) tc_ld32(ts + k, s + k);
         tc_wait_ld();
-        const int limit = pos - (g.tile0 + j) * kTile;         // last column this row sees
-        const uint32_t mask = ctl->mask[(jg + j) % kMasks];
-        if (__any_sync(~0u, limit < kTile - 1)) {
+        if (edge) {
 #pragma unroll
           for (int k = 0; k < kTile; ++k)
             if (k > limit) s[k] = -INFINITY;
@@ -807,11 +800,18 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
             sum[k & 1] = add2(sum[k & 1], y);
             w[k] = Q8 ? f16x2(y.x, y.y) : bf16x2(y.x, y.y);
           }
-          tc_st16(ts + h * 16, w);
-          if (h & 1) {                             // half of P: its products start
+          // half of P stands when the third quarter is computed (and its own writing is still to come), the
+          // rest at the end: the products of the first half start under the second's exponentials
+          if (h == 2) {
             tc_wait_st();
             tc_before();
-            warp_arrive(smem_u32(&ctl->pfull[t][h / 2]));
+            warp_arrive(smem_u32(&ctl->pfull[t][0]));
+          }
+          tc_st16(ts + h * 16, w);
+          if (h == 3) {
+            tc_wait_st();
+            tc_before();
+            warp_arrive(smem_u32(&ctl->pfull[t][1]));
           }
         }
         const float2 sm = add2(sum[0], sum[1]);
@@ -992,10 +992,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
   } else if (warp < 12) {
     if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 || (Q8 && warp == 11)) produce<D, Q8>(p, base, ctl, warp == 8 ? 0 : 1);
+    if (warp == 8 || warp == 11) produce<D, Q8>(p, base, ctl, warp == 8 ? 0 : 1);
     if (warp == 9) issue<D, Q8>(p, base, ctl);
     if (warp == 10) produce_q<D, Q8>(p, base, ctl);
-    if (!Q8 && warp == 11) trim<D, Q8>(p, base, ctl);
   } else if constexpr (Q8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     decode<D>(p, base, ctl);
