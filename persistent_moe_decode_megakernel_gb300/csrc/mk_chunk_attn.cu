@@ -225,7 +225,7 @@ struct Layout {
 };
 
 struct Ctl {
-  uint64_t full[8], empty[8];        // K and V tiles: a block's j-th position tile is ring entries 2j (K), 2j+1 (V)
+  uint64_t full[8], empty[8];        // K and V tiles, a ring (see entry_of)
   uint64_t raw_full[8], raw_empty[8];
   uint64_t qraw[2], qbar[2], qfree;  // query tiles: landed, in the operand type (bf16: qraw itself), read by the last S
   uint64_t sfull[2], pfull[2][2];    // S of a tile (stream); the halves of its P
@@ -279,6 +279,24 @@ struct Ring {
     }
   }
 };
+
+// K and V tiles pass through a ring in the order in which the MMA warp needs and releases them.  A
+// segment's n position tiles are its 2 n entries: with two tiles of rows K0 V0 K1 V1 .., with two streams
+// K0 K1 V0 K2 V1 K3 .. V(n-2) V(n-1).  (Loaded as K0 V0 K1 V1 there too, V tiles waited in the ring for two
+// position tiles: one row, 64 tiles a block from HBM, 98.7 us instead of 96.6.)
+__device__ __forceinline__ int entry_of(const Segment& g, int v, int j) {
+  if (g.two) return 2 * j + v;
+  return v ? min(2 * j + 2, 2 * g.n - 1) : max(2 * j - 1, 0);
+}
+// and back: whether entry i is a V tile, and of which position tile
+__device__ __forceinline__ int tile_of(const Segment& g, int i, int& v) {
+  if (g.two) {
+    v = i & 1;
+    return i >> 1;
+  }
+  v = i == 2 * g.n - 1 || (i > 0 && !(i & 1));
+  return !v ? (i + 1) >> 1 : i == 2 * g.n - 1 ? g.n - 1 : (i - 2) >> 1;
+}
 
 // --------------------------------------------------------------------------- one row, plainly
 // Row r, query head h by one warp: 32 positions at a time, a lane per position for the scores,
@@ -352,13 +370,10 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
 // --------------------------------------------------------------------------- loads (warp 8: K, warp 11: V)
 // A tile of 16-position pages takes 8 copies (q8_0: 16), which a warp issues one by one, so K and V have a
 // warp each (64 position tiles a block, one row, the cache in L2: bf16 85 us with one warp, 59 with
-// two; q8_0 126 and 100).  They share a ring.  A warp waits for entry e - N's release (N stages) by its
-// parity, which is sound only if entry e - 2N is known to be released:
-//   bf16, N = 5: the warp got e - 2, so e - 7, the other operand's, was released; with e = K_j that is
-//     V_{j-4}, and the MMA warp releases K_{j-5} before it; with e = V_j it is K_{j-3}, and V_{j-5} goes
-//     before that (in units of one tile right before, in units of two earlier).  N = 8: e - 16 is the
-//     warp's own operand's, and it waited for it to get e - 8.
-//   q8_0, raw stages, N = 3: the decode warps release them strictly in order; e - 2 came after e - 5.
+// two; q8_0 126 and 100).  They share a ring of N stages.  A warp waits for entry e - N's release by its
+// parity, which is sound only if entry e - 2N is known to be released.  It is: entries are released in
+// order (by the MMA warp; raw stages by the decode warps), and the warp's own entry before e, which is
+// e - 3 at least, had to wait for one no earlier than e - 3 - N.
 template <int D, bool Q8>
 __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl, int only) {
   using L = Layout<D, Q8>;
@@ -367,8 +382,8 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
   const bool mine = lane < nbox;
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
-  uint32_t jg = 0;                                             // position tiles so far
-  while (walk.next(p.plan, p.seqs, g)) {
+  uint32_t jg = 0, c0 = 0;                                     // position tiles and ring entries so far
+  for (; walk.next(p.plan, p.seqs, g); c0 += 2 * g.n) {
     const int32_t* bt = p.bt + static_cast<size_t>(g.s) * p.maxpg;
     // lane b looks up the page of the tile's b-th copy, one tile ahead
     auto lookup = [&](int j) {
@@ -388,7 +403,7 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
         const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
         if (lane == 0) ctl->mask[jg % kMasks] = mask;
       }
-      const uint32_t e = 2 * jg + only;                        // this tile's entry
+      const uint32_t e = c0 + entry_of(g, only, j);
       if constexpr (!Q8) {
         const uint32_t st = e % L::kStages, bar = smem_u32(&ctl->full[st]);
         if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
@@ -480,13 +495,14 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
   Segment g;
   uint32_t jg = 0;
   const __half2 bias = __half2half2(__float2half_rn(1152.f));
-  while (walk.next(p.plan, p.seqs, g)) {
-    for (int j = 0; j < g.n; ++j, ++jg) {
-      const int left = g.len - (g.tile0 + j) * kTile;
-      for (int which = 0; which < 2; ++which) {
+  for (; walk.next(p.plan, p.seqs, g); jg += g.n) {
+    for (int i = 0; i < 2 * g.n; ++i) {
+      {
+        int v;
+        const int j = tile_of(g, i, v), left = g.len - (g.tile0 + j) * kTile;
         if (!mbar_wait(smem_u32(&ctl->raw_full[raw.st]), raw.ph, ctl, p.status)) return;
         if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
-        const uint32_t mask = ctl->mask[jg % kMasks];
+        const uint32_t mask = ctl->mask[(jg + j) % kMasks];
         // row0 + 16 i is in group 2 i + row0 / 8 of 8 rows, at row0 % 8 of it
         const uint32_t src = base + L::kRaw + raw.st * kRawBytes + row0 * 128;
         const uint32_t ssrc = base + L::kRaw + raw.st * kRawBytes + kTile * 128 + row0 * 8;
@@ -588,7 +604,7 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
   while (walk.next(p.plan, p.seqs, g)) {
     const uint32_t c = c0;
     auto wait_v = [&](int j) {
-      wait_full(c + 2 * j + 1);
+      wait_full(c + entry_of(g, 1, j));
       if (j + 1 == g.n && trims<Q8>(g)) {
         if (lane == 0) mbar_arrive(smem_u32(&ctl->landed));
         wait(&ctl->trim, tr & 1);
@@ -622,21 +638,21 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
       }
     } else {
       for (int j = 0; j < 2 && j < g.n; ++j) {
-        wait_full(c + 2 * j);
-        scores(j, 0, c + 2 * j);
-        release(c + 2 * j);
+        wait_full(c + j);
+        scores(j, 0, c + j);
+        release(c + j);
       }
       if (g.n <= 2) done_q();
       for (int j = 0; j < g.n; ++j) {
         const int t = j & 1;
-        const uint32_t v = c + 2 * j + 1;
+        const uint32_t v = c + entry_of(g, 1, j);
         wait_v(j);
         values(t, v, j > 1);
         release(v);
-        if (j + 2 < g.n) {
-          wait_full(v + 3);
-          scores(t, 0, v + 3);
-          release(v + 3);
+        if (j + 2 < g.n) {                         // the next entry: K of tile j + 2
+          wait_full(v + 1);
+          scores(t, 0, v + 1);
+          release(v + 1);
           if (j + 3 == g.n) done_q();
         }
       }
