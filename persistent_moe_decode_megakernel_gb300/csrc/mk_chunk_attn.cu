@@ -232,6 +232,7 @@ struct Ctl {
   uint64_t landed, trim;             // a last V tile to be trimmed: landed, trimmed
   uint64_t ofull, join;
   uint32_t tmem, abort;
+  uint32_t beat;                     // counts while a softmax warp works a row out plainly (exact_row)
   uint32_t mask[kMasks];             // per tile, a bit per 8 positions: the page is in range
   float2 ml[2][kTile];               // streams' (m, l) when they join
 };
@@ -243,12 +244,19 @@ template <int D, bool Q8>
 constexpr size_t smem_bytes() { return Layout<D, Q8>::kCtl + (Q8 ? sizeof(CtlQ8) : sizeof(Ctl)); }
 static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448 && smem_bytes<64, false>() <= 232448, "");
 
-// Waits for the phase of `bar` with this parity, at most kWaitNs; false once the block gives up.
+// Waits for the phase of `bar` with this parity, at most kWaitNs from the block's last sign of life in
+// exact_row; false once the block gives up.
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status) {
-  volatile uint32_t* abort = &ctl->abort;
-  const uint64_t t0 = globaltimer();
+  volatile uint32_t *abort = &ctl->abort, *beat = &ctl->beat;
+  uint64_t t0 = globaltimer();
+  uint32_t b0 = *beat;
   while (!mbar_try(bar, parity)) {
     if (*abort) return false;
+    const uint32_t b = *beat;
+    if (b != b0) {
+      b0 = b;
+      t0 = globaltimer();
+    }
     if (globaltimer() - t0 > kWaitNs) {
       *abort = 1u;
       if (status) *status = MK_ERR_TIMEOUT;
@@ -301,11 +309,12 @@ __device__ __forceinline__ int tile_of(const Segment& g, int i, int& v) {
 // --------------------------------------------------------------------------- one row, plainly
 // Row r, query head h by one warp: 32 positions at a time, a lane per position for the scores,
 // D/32 dims per lane for the output; fp32, and no position beyond the row's own is touched.
+// `beat`: counted every 1024 positions (the rest of the block may be waiting), or NULL.
 template <int D, bool Q8>
-__device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
+__device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volatile uint32_t* beat) {
   const int lane = threadIdx.x & 31, kvh = h / p.plan.G, s = seq_of_row(p.seqs, r);
   const int n = p.seqs.len[s] - p.seqs.row0[s + 1] + r + 1;
-  const uint16_t* q = p.q + static_cast<size_t>(r) * p.q_stride + static_cast<size_t>(h) * D;
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(r) * p.q_stride + static_cast<size_t>(h) * D);
   const uint16_t* kv16 = reinterpret_cast<const uint16_t*>(p.kv);
   const int8_t* codes = reinterpret_cast<const int8_t*>(p.kv);
   const __half* scales = reinterpret_cast<const __half*>(p.kv + p.code_bytes);
@@ -314,6 +323,7 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
   for (int t0 = 0; t0 < n; t0 += 32) {
+    if (beat != nullptr && lane == 0 && t0 % 1024 == 0) *beat = *beat + 1;
     const int t = t0 + lane;
     int64_t line = -1;
     float x = -INFINITY;
@@ -323,11 +333,23 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
         line = (static_cast<int64_t>(page) * 2 * p.plan.Hkv + kvh) * p.ps + t % p.ps;
         x = 0.f;
 #pragma unroll 4
-        for (int d = 0; d < D; ++d) {
-          float k;
-          if constexpr (Q8) k = static_cast<float>(codes[line * D + d]) * __half2float(scales[line * (D / 32) + d / 32]);
-          else k = bf_lo(kv16[line * D + d]);
-          x = fmaf(bf_lo(__ldg(q + d)), k, x);
+        for (int d = 0; d < D / 8; ++d) {            // 8 dims at a time
+          const uint4 a = __ldg(q + d);
+          const uint32_t qw[4] = {a.x, a.y, a.z, a.w};
+          float k[8];
+          if constexpr (Q8) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + line * D) + d);
+            const float sc = __half2float(scales[line * (D / 32) + d / 4]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) k[e] = static_cast<float>(static_cast<int8_t>((e < 4 ? w.x : w.y) >> (8 * (e % 4)))) * sc;
+          } else {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(kv16 + line * D) + d);
+            const uint32_t kw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) k[e] = e & 1 ? bf_hi(kw[e / 2]) : bf_lo(kw[e / 2]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x = fmaf(e & 1 ? bf_hi(qw[e / 2]) : bf_lo(qw[e / 2]), k[e], x);
         }
         x *= c;
       }
@@ -346,11 +368,10 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h) {
     m = mx;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = o[i] == 0.f ? 0.f : o[i] * f;
-    for (int j = 0; j < 32; ++j) {
-      const int64_t lj = __shfl_sync(~0u, line, j);
+    for (uint32_t in = __ballot_sync(~0u, line >= 0); in; in &= in - 1) {
+      const int j = __ffs(in) - 1;
+      const int64_t lv = __shfl_sync(~0u, line, j) + static_cast<int64_t>(p.plan.Hkv) * p.ps;
       const float wj = __shfl_sync(~0u, w, j);
-      if (lj < 0) continue;
-      const int64_t lv = lj + static_cast<int64_t>(p.plan.Hkv) * p.ps;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int d = 32 * i + lane;
@@ -939,7 +960,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
           const int who = __ffs(todo) - 1;
           const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
           __threadfence_block();
-          exact_row<D, Q8>(p, rr, hh);
+          exact_row<D, Q8>(p, rr, hh, &ctl->beat);
         }
       }
     }
@@ -984,6 +1005,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
     mbar_init(smem_u32(&ctl->ofull), 1);
     mbar_init(smem_u32(&ctl->join), 8);
     ctl->abort = 0u;
+    ctl->beat = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) {
@@ -1119,7 +1141,7 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
   for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1;
     const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who), lr = __shfl_sync(~0u, lrow, who);
-    if (!((done >> lr) & 1u)) exact_row<D, Q8>(p, rr, hh);
+    if (!((done >> lr) & 1u)) exact_row<D, Q8>(p, rr, hh, nullptr);
     done |= 1u << lr;
   }
 }

@@ -15,7 +15,7 @@ namespace {
 // an 8192-token prompt, even to 1 % as whole items, took 383 us so and 393 us in ranges).  (152 blocks streaming from HBM.)
 constexpr int kTileCost[2] = {14, 17}, kItemCost[2] = {40, 60}, kMergeCost[2] = {80, 250};
 constexpr int kMinRange = 3;                // position tiles a block is worth
-constexpr int kMaxWalk = 16 * kMaxBlocks;   // items beyond which whole ones are even enough
+constexpr int kMaxWalk = 1 << 17;            // items beyond which whole ones are even enough (and the walk long)
 }  // namespace
 
 bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t* floats) {

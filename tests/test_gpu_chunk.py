@@ -288,6 +288,20 @@ def test_attention_nan_in_a_later_position_stays_there(hq, hkv, d, len_, new, wh
     assert torch.isnan(hit).all() if value == "nan" else torch.isinf(hit).all()
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_attention_all_rows_poisoned(q8):
+    # a NaN at position 0 is every row's: each is worked out again, and none but NaN comes of it
+    st = R.Setup(16, 2, 128, 16, [3000, 40], [300, 7], q8=q8, seed=21)
+    q = st.normal(st.rows, 16, 128)
+    page = st.bt[0, 0].long()
+    if q8:
+        st.planes()[1][page, 0, :, 0] = float("nan")
+    else:
+        st.kv[page, 0, :, 0] = float("nan")
+    out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv)
+    assert torch.isnan(out[:300]).all() and torch.isfinite(out[300:]).all()
+
+
 @pytest.mark.parametrize("len_,new", [(90, 90), (5000, 2)])
 def test_attention_q8_values_beyond_fp16(len_, new):
     # decoded values above 65504 (scales up to f16's largest) in a few positions, K and V
@@ -377,6 +391,44 @@ def test_repeats_are_bit_identical_on_any_stream_and_in_graphs(q8):
         for a, b in zip(first, r):
             assert torch.equal(bits(a), bits(b))
     assert torch.equal(bits(st.kv), bits(kv2)) and torch.equal(bits(st.kv), bits(kv3))
+
+
+def test_no_rows_and_reused_outputs():
+    st = R.Setup(8, 2, 128, 16, [40, 5], [0, 0], seed=22)
+    status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((3, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert mk.chunk_attention(st.shape(mk), q, [0, 0], st.lens, st.bt, st.kv, out=out, status=status) is out
+    assert int(status) == mk.MK_OK and torch.all(out == 7.0)
+    assert mk.append_chunk(st.shape(mk), q.new_empty(0, 12 * 128), [0, 0], st.lens, st.bt, st.kv).shape == (0, 8, 128)
+    k, v = mk.read_cache(st.shape(mk), [0, 0], st.lens, st.bt, st.kv)
+    assert k.shape == v.shape == (0, 2, 128)
+
+
+def test_binding_refuses_wrong_tensors():
+    st = R.Setup(8, 2, 128, 16, [40, 5], [4, 5], seed=23)
+    sh, q = st.shape(mk), st.normal(9, 8, 128)
+    ok = dict(q=q, chunk_lens=st.news, seq_lens=st.lens, block_tables=st.bt, kv_layer=st.kv)
+    mk.chunk_attention(sh, **ok)
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for bad in (dict(q=q[:8]), dict(q=q.float()), dict(q=q.cpu()), dict(q=q.transpose(1, 2)), dict(q=q[:, :7]),
+                dict(block_tables=st.bt.long()), dict(block_tables=st.bt[:, :-1]), dict(block_tables=st.bt[:1]),
+                dict(block_tables=st.bt.cpu()), dict(kv_layer=st.kv[1:]), dict(kv_layer=st.kv.half()),
+                dict(chunk_lens=[4]), dict(chunk_lens=[4, 6]), dict(seq_lens=[3, 5]), dict(chunk_lens=[-1, 5]),
+                dict(out=torch.empty(8, 8, 128, dtype=torch.bfloat16, device="cuda")),
+                dict(out=torch.empty(9, 8, 128, device="cuda")), dict(status=torch.zeros(1, device="cuda")),
+                dict(status=torch.zeros(2, dtype=torch.int32, device="cuda")), dict(workspace=ws.cpu())):
+        with pytest.raises(mk.MkError) as e:
+            mk.chunk_attention(sh, **{**ok, **bad})
+        assert e.value.code == mk.MK_ERR_INVALID_ARG, bad
+    big = R.Setup(8, 2, 128, 16, [20000], [1], seed=24)
+    need = mk.chunk_attention_workspace(big.shape(mk), [1], [20000])
+    assert need > 16
+    with pytest.raises(mk.MkError) as e:    # too small a workspace
+        mk.chunk_attention(big.shape(mk), big.normal(1, 8, 128), [1], [20000], big.bt, big.kv, workspace=ws)
+    assert e.value.code == mk.MK_ERR_INVALID_ARG
+    with pytest.raises(mk.MkError):
+        mk.append_chunk(sh, st.normal(9, 12 * 128), st.news, st.lens, st.bt, st.kv, q_norm=st.normal(64))
 
 
 def test_splitting_a_prompt_gives_the_same_cache_and_close_rows():
