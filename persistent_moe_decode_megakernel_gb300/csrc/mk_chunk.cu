@@ -82,7 +82,6 @@ int clear_status(int32_t* status_out, cudaStream_t s) {
 namespace {
 
 constexpr int kBlock = 128;
-constexpr int kAppendRows = 4;  // rows of a block, at most
 constexpr int kMaxTile = 64;
 constexpr int kMaxPairs = 64;   // rotated pairs of a head
 
@@ -142,11 +141,13 @@ __device__ __forceinline__ void lane_chunks(int l, int R, bool half, int& ca, in
   cb = h ? l + R / 16 : 2 * l + 1;
 }
 
-// One block takes T rows.  The rows' cos and sin are computed once per (row, pair) and shared by
-// the row's heads; then D/16 lanes take a head: two 16-byte loads, the norm's sum by shuffles,
-// the rotation in registers, two 16-byte stores (q8_0: 8-byte codes and, per head, one 8-byte
-// store of its four scales).  Reads 2 B and writes 2 B (17/16 B) a value: HBM bound.  A block takes
-// several rows where there are enough for two blocks an SM, few rows a block each.
+// A warp takes a row, or a quarter or half of its heads where rows are few: it computes the row's
+// cos and sin (two pairs a lane) and passes them around once, so that each lane holds those of its 8
+// pairs for all the heads.  D/16 lanes take a head: two 16-byte loads, the norm's sum by shuffles, the
+// rotation in registers, two 16-byte stores (q8_0: 8-byte codes and, per head, one 8-byte store of its
+// four scales); the loads of the next kFly heads are in flight meanwhile.  Reads 2 B and writes 2 B
+// (17/16 B) a value: HBM bound.  (With the angles read from shared memory for every head, waiting for
+// those reads was the most frequent stall: 33.1 us for 8192 tokens of 32 + 2 * 4 heads, now 28.4, 5.9 TB/s.)
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ ChunkSeqs seqs,
                                                         const __grid_constant__ Cache c,
@@ -155,57 +156,56 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
                                                         int interleaved, float mscale, const uint16_t* q_norm,
                                                         const uint16_t* k_norm, float eps,
                                                         uint16_t* __restrict__ q_out) {
-  constexpr int LH = D / 16;   // lanes of a head
-  __shared__ float2 cs[kAppendRows * kMaxPairs];
-  __shared__ int32_t slot[kAppendRows], at[kAppendRows];
-  const int tid = threadIdx.x;
-  const int r0 = blockIdx.x * T, nr = min(T, seqs.row0[seqs.n] - r0);
-  const int H = Hq + 2 * c.Hkv, l = tid % LH;
-  // a unit is a row's head; the next unit's loads are under way while this one is worked on, the
-  // first one's under the look-ups and angles
-  int row = 0, h = tid / LH;
-  while (h >= H) {
-    h -= H;
-    ++row;
-  }
-  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
-  auto fetch = [&](int row, int h) {
+  constexpr int LH = D / 16, kWarps = kBlock / 32;   // lanes of a head
+  // loads in flight against registers (and with them warps): 8192 bf16 tokens of 40 heads of 128 took 31.7,
+  // 29.9, 28.4 us at 1, 2, 3; 16384 of 18 heads of 64 took 16.8, 16.4, 17.3; 4112 q8_0 tokens 17.6, 19.8, 20.0
+  constexpr int kFly = Q8 ? 1 : D == 128 ? 3 : 2;
+  __shared__ float2 cs[kWarps][kMaxPairs];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LH;
+  const int share = kWarps / T;                    // warps of a row
+  const int r = blockIdx.x * T + warp / share;
+  if (r >= seqs.row0[seqs.n]) return;
+  const int H = Hq + 2 * c.Hkv, step = share * (32 / LH);
+  const uint16_t* const src = qkv + static_cast<size_t>(r) * stride;
+  int h = (warp % share) * (32 / LH) + lane / LH;
+  uint4 wa[kFly], wb[kFly];
+  auto fetch = [&](int i, int h) {
+    if (h >= H) return;
     int ca, cb;
     lane_chunks(l, R, !interleaved && h < Hq + c.Hkv, ca, cb);
-    const uint16_t* src = qkv + static_cast<size_t>(r0 + row) * stride + static_cast<size_t>(h) * D;
-    wa = __ldg(reinterpret_cast<const uint4*>(src + 8 * ca));
-    wb = __ldg(reinterpret_cast<const uint4*>(src + 8 * cb));
+    wa[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(h) * D + 8 * ca));
+    wb[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(h) * D + 8 * cb));
   };
-  if (row < nr) fetch(row, h);
-  if (tid < nr) {
-    int pos;
-    slot[tid] = slot_of_row(seqs, c, r0 + tid, &pos);
-    at[tid] = pos;
+#pragma unroll
+  for (int i = 0; i < kFly; ++i) fetch(i, h + i * step);
+  int pos;
+  const int32_t slot = slot_of_row(seqs, c, r, &pos);
+  float2 tr[8];                                    // of the lane's pairs, in the order it meets them
+  if (R > 0) {
+    for (int p = lane; p < R / 2; p += 32) {
+      const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * turns.f[p]);    // [-1/2, 1/2) of a turn
+      float sn, co;
+      sincospif(static_cast<float>(turn) * 1.0842021724855044e-19f, &sn, &co);               // turn * 2^-63 half turns
+      cs[warp][p] = make_float2(co * mscale, sn * mscale);
+    }
+    __syncwarp();
+    if (l < R / 16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tr[i] = cs[warp][8 * l + i];   // both layouts: pairs 8 l .. 8 l + 7
+    }
   }
-  __syncthreads();
-  const int half_r = R / 2;
-  for (int i = tid; i < nr * half_r; i += kBlock) {
-    const int row = i / half_r, p = i - row * half_r;
-    const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(at[row]) * turns.f[p]);   // [-1/2, 1/2) of a turn
-    float sn, co;
-    sincospif(static_cast<float>(turn) * 1.0842021724855044e-19f, &sn, &co);                  // turn * 2^-63 half turns
-    cs[i] = make_float2(co * mscale, sn * mscale);
-  }
-  __syncthreads();
-  while (row < nr) {
-    const bool isq = h < Hq, isv = h >= Hq + c.Hkv;
+  for (; h < H; h += kFly * step) {
+#pragma unroll
+   for (int fly = 0; fly < kFly; ++fly) {
+    const int ch = h + fly * step;
+    if (ch >= H) break;                            // (the lanes of a head agree; the shuffles below are theirs)
+    const bool isq = ch < Hq, isv = ch >= Hq + c.Hkv;
     int ca, cb;
     lane_chunks(l, R, !interleaved && !isv, ca, cb);
     float a[8], b[8];
-    unpack8(wa, a);
-    unpack8(wb, b);
-    const int crow = row, ch = h;
-    h += kBlock / LH;
-    while (h >= H) {
-      h -= H;
-      ++row;
-    }
-    if (row < nr) fetch(row, h);
+    unpack8(wa[fly], a);
+    unpack8(wb[fly], b);
+    fetch(fly, ch + kFly * step);
     const uint16_t* gain = isq ? q_norm : k_norm;
     if (!isv) {
       // the lanes of a head are in one warp and agree on it (a warp's last heads may be missing:
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-        const uint32_t m = ((1u << LH) - 1u) << ((tid & 31) / LH * LH);
+        const uint32_t m = ((1u << LH) - 1u) << (lane / LH * LH);
 #pragma unroll
         for (int o = 1; o < LH; o <<= 1) ss += __shfl_xor_sync(m, ss, o);
         const float rs = rsqrtf(ss / D + eps);
@@ -228,11 +228,10 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
         }
       }
       if (l < R / 16) {
-        const float2* t = cs + crow * half_r;
         if (interleaved) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 x = t[4 * ca + i], y = t[4 * cb + i];
+            const float2 x = tr[i], y = tr[4 + i];
             const float a0 = a[2 * i], b0 = b[2 * i];
             a[2 * i] = a0 * x.x - a[2 * i + 1] * x.y;
             a[2 * i + 1] = a[2 * i + 1] * x.x + a0 * x.y;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 x = t[8 * ca + i];
+            const float2 x = tr[i];
             const float a0 = a[i];
             a[i] = a0 * x.x - b[i] * x.y;
             b[i] = b[i] * x.x + a0 * x.y;
@@ -251,14 +250,14 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
       }
     }
     if (isq) {
-      uint16_t* dst = q_out + (static_cast<size_t>(r0 + crow) * Hq + ch) * D;
+      uint16_t* dst = q_out + (static_cast<size_t>(r) * Hq + ch) * D;
       *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8(a);
       *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8(b);
       continue;
     }
-    if (slot[crow] < 0) continue;   // the whole row: its lanes agree
+    if (slot < 0) continue;                        // the whole row's
     const int kvh = isv ? ch - Hq - c.Hkv : ch - Hq;
-    const size_t line = static_cast<size_t>(slot[crow]) + static_cast<size_t>(isv ? c.Hkv + kvh : kvh) * c.ps;
+    const size_t line = static_cast<size_t>(slot) + static_cast<size_t>(isv ? c.Hkv + kvh : kvh) * c.ps;
     if constexpr (!Q8) {
       uint16_t* dst = reinterpret_cast<uint16_t*>(c.kv) + line * D;
       *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8(a);
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
         ma = fmaxf(ma, fabsf(a[i]));
         mb = fmaxf(mb, fabsf(b[i]));
       }
-      const uint32_t mask = ((1u << LH) - 1u) << ((tid & 31) / LH * LH);
+      const uint32_t mask = ((1u << LH) - 1u) << (lane / LH * LH);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         m[k] = fmaxf(ca / 4 == k ? ma : 0.f, cb / 4 == k ? mb : 0.f);
@@ -306,6 +305,7 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
     }
+  }
   }
 }
 
@@ -474,7 +474,7 @@ extern "C" int mk_append_chunk(const mk_cache_shape* shape, int32_t num_seqs, co
   rc = clear_status(status_out, st);
   if (rc || rows == 0) return rc;
   const Cache cache = cache_of(c, block_tables, kv_layer, status_out);
-  const int T = rows >= kAppendRows * 304 ? kAppendRows : rows >= 2 * 304 ? 2 : 1;
+  const int T = rows >= 4 * 304 ? 4 : rows >= 2 * 304 ? 2 : 1;   // two blocks an SM before a warp takes more heads
   const int grid = (rows + T - 1) / T;
   auto go = [&](auto kernel) {
     kernel<<<grid, kBlock, 0, st>>>(seqs, cache, turns, T, c.num_q_heads, static_cast<const uint16_t*>(qkv), qkv_stride,
