@@ -106,7 +106,9 @@ int mk_append_chunk(const mk_cache_shape* shape, int32_t num_seqs, const int32_t
 
 /*
  * Bytes of device workspace that mk_chunk_attention needs for these lengths (0 when it needs
- * none), written to bytes_out.  Host only.
+ * none), written to bytes_out.  Host only.  It holds the partial outputs of contexts split over
+ * blocks (at most 42 MB) and, for q8_0 sequences with many new tokens, their cache decoded to fp16
+ * (4 bytes a position, KV head and dim; at most 1 GiB in a call).
  */
 int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
                                  const int32_t* seq_lens, size_t* bytes_out);
@@ -119,9 +121,12 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  *   out:       device bf16 [rows][num_q_heads][head_dim]
  *   workspace: device, at least mk_chunk_attention_workspace bytes (NULL if 0), contents lost; a
  *              call owns it until its work is done
- * Products run on the tensor cores with bf16 operands (a q8_0 value is decoded to bf16, the
- * softmax weights are rounded to bf16); scores, softmax statistics and outputs are accumulated
- * in fp32 and rounded once.  Pages out of range are skipped: a row attends over its other
+ * Products run on the tensor cores: over a bf16 cache with bf16 operands (the softmax weights are
+ * rounded to bf16), over a q8_0 cache with fp16 ones (weights, decoded values and scaled query rows
+ * are rounded to fp16; rows that fp16 cannot hold are computed in fp32 instead).  Scores, softmax
+ * statistics and outputs are accumulated in fp32 and rounded once.  Rows never see later positions,
+ * whatever NaN or infinity these hold.  A device wait that runs out (a fault of the library) is
+ * reported as MK_ERR_TIMEOUT in status_out.  Pages out of range are skipped: a row attends over its other
  * positions, and one that has none gets zeros.  What lies in a page behind a sequence's last
  * position is never used, whatever its bits.
  */

@@ -139,8 +139,8 @@ int mk_num_ctas(mk_ctx* ctx);
 
 /*
  * The schedule mk_chunk_attention takes for these lengths (host only): *n_out segments, the first
- * max_segments of them written as 8 int32 each, block by block in the order a block runs them:
- * block, sequence, unit (up to two tiles of 128/G tokens), KV head, first position tile, position
+ * max_segments of them written as 9 int32 each, block by block in the order a block runs them:
+ * launch (0: from the pages; 1: q8_0 sequences decoded into the workspace first), block, sequence, unit (up to two tiles of 128/G tokens), KV head, first position tile, position
  * tiles, position tiles of the unit, partial written (-1: the segment is the whole unit).
  */
 int mk_plan_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,

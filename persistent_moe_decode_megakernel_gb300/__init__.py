@@ -456,12 +456,12 @@ def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
 
 
 def plan_chunk_attention(shape: CacheShape, chunk_lens, seq_lens) -> np.ndarray:
-    """The schedule of :func:`chunk_attention` (``mk_plan_chunk_attention``): int32 [segments, 8]."""
+    """The schedule of :func:`chunk_attention` (``mk_plan_chunk_attention``): int32 [segments, 9]."""
     cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
     n = ctypes.c_int32()
     _check(lib().mk_plan_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, None, 0,
                                          ctypes.byref(n)))
-    out = np.zeros((n.value, 8), dtype=np.int32)
+    out = np.zeros((n.value, 9), dtype=np.int32)
     _check(lib().mk_plan_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, out.ctypes.data,
                                          n.value, ctypes.byref(n)))
     return out

@@ -34,6 +34,7 @@
 // overflow fp16 (the decode makes them NaN) end there; a row that really holds a NaN stays one.
 
 #include "mk_chunk_plan.h"
+#include "mk_debug.h"
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -47,9 +48,19 @@
 namespace mk {
 namespace {
 
+// What the K and V operands come from: bf16 pages; q8_0 pages, decoded by the block; q8_0 pages that a
+// kernel before this one has decoded into the workspace (see stage_kernel).
+enum { kBf16, kQ8, kStaged };
+
 constexpr int kRawBytes = kTile * (128 + 8);   // q8_0: the codes and scales of a K or V tile
 constexpr int kMasks = 8;           // tiles whose page masks are kept (more than can be in flight)
 constexpr uint64_t kWaitNs = 2000000000ull;
+
+// The staged sequences and their tiles' numbers.
+struct StageTiles {
+  int32_t n;
+  int32_t seq[kMaxSeqs], first[kMaxSeqs + 1];
+};
 
 struct AttnParams {
   CUtensorMap map;                  // bf16 pages (see encode_pages)
@@ -64,6 +75,7 @@ struct AttnParams {
   uint16_t* out;
   float* part;
   size_t code_bytes;
+  int32_t stage0[kMaxSeqs];         // staged sequences: first tile in the workspace
   int32_t Hq, ps, P, maxpg;
   int32_t box;                      // positions of one copy: a power of two that divides ps
   float c;                          // log2(e) / sqrt(D)
@@ -212,16 +224,16 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
 }
 
 // --------------------------------------------------------------------------- shared memory
-template <int D, bool Q8>
+template <int D, int M>
 struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;           // one operand tile
   static constexpr int kGroup = D / 64 * 1024;               // 8 positions of a K or V tile
-  static constexpr int kRawStages = Q8 ? 3 : 1;
+  static constexpr int kRawStages = M == kQ8 ? 3 : 1;
   static constexpr int kRaw = 2 * kTileBytes;                // behind the two Q tiles
-  static constexpr int kKv = (kRaw + (Q8 ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
-  static constexpr int kStages = Q8 ? 3 : D == 128 ? 5 : 8;
+  static constexpr int kKv = (kRaw + (M == kQ8 ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
+  static constexpr int kStages = M == kQ8 ? 3 : D == 128 ? 5 : 8;
   static constexpr int kCtl = kKv + kStages * kTileBytes;
-  static constexpr int kThreads = Q8 ? 512 : 384;
+  static constexpr int kThreads = M == kQ8 ? 512 : 384;
 };
 
 struct Ctl {
@@ -240,9 +252,10 @@ struct CtlQ8 : Ctl {
   float rowc[kTile];                 // two streams: the softmax's constant of each query row
 };
 
-template <int D, bool Q8>
-constexpr size_t smem_bytes() { return Layout<D, Q8>::kCtl + (Q8 ? sizeof(CtlQ8) : sizeof(Ctl)); }
-static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448 && smem_bytes<64, false>() <= 232448, "");
+template <int D, int M>
+constexpr size_t smem_bytes() { return Layout<D, M>::kCtl + (M != kBf16 ? sizeof(CtlQ8) : sizeof(Ctl)); }
+static_assert(smem_bytes<128, kBf16>() <= 232448 && smem_bytes<128, kQ8>() <= 232448 && smem_bytes<128, kStaged>() <= 232448 &&
+              smem_bytes<64, kBf16>() <= 232448, "");
 
 // Waits for the phase of `bar` with this parity, at most kWaitNs from the block's last sign of life in
 // exact_row; false once the block gives up.
@@ -310,7 +323,7 @@ __device__ __forceinline__ int tile_of(const Segment& g, int i, int& v) {
 // Row r, query head h by one warp: 32 positions at a time, a lane per position for the scores,
 // D/32 dims per lane for the output; fp32, and no position beyond the row's own is touched.
 // `beat`: counted every 1024 positions (the rest of the block may be waiting), or NULL.
-template <int D, bool Q8>
+template <int D, int M>
 __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volatile uint32_t* beat) {
   const int lane = threadIdx.x & 31, kvh = h / p.plan.G, s = seq_of_row(p.seqs, r);
   const int n = p.seqs.len[s] - p.seqs.row0[s + 1] + r + 1;
@@ -337,7 +350,7 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
           const uint4 a = __ldg(q + d);
           const uint32_t qw[4] = {a.x, a.y, a.z, a.w};
           float k[8];
-          if constexpr (Q8) {
+          if constexpr (M != kBf16) {
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + line * D) + d);
             const float sc = __half2float(scales[line * (D / 32) + d / 4]);
 #pragma unroll
@@ -376,7 +389,7 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
       for (int i = 0; i < D / 32; ++i) {
         const int d = 32 * i + lane;
         float v;
-        if constexpr (Q8) v = static_cast<float>(codes[lv * D + d]) * __half2float(scales[lv * (D / 32) + i]);
+        if constexpr (M != kBf16) v = static_cast<float>(codes[lv * D + d]) * __half2float(scales[lv * (D / 32) + i]);
         else v = bf_lo(kv16[lv * D + d]);
         o[i] = fmaf(wj, v, o[i]);
       }
@@ -395,9 +408,9 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
 // parity, which is sound only if entry e - 2N is known to be released.  It is: entries are released in
 // order (by the MMA warp; raw stages by the decode warps), and the warp's own entry before e, which is
 // e - 3 at least, had to wait for one no earlier than e - 3 - N.
-template <int D, bool Q8>
+template <int D, int M>
 __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl, int only) {
-  using L = Layout<D, Q8>;
+  using L = Layout<D, M>;
   const int lane = threadIdx.x & 31;
   const int r = p.box, nbox = kTile / r;                       // copies of a tile
   const bool mine = lane < nbox;
@@ -425,7 +438,17 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
         if (lane == 0) ctl->mask[jg % kMasks] = mask;
       }
       const uint32_t e = c0 + entry_of(g, only, j);
-      if constexpr (!Q8) {
+      if constexpr (M == kStaged) {
+        // whole tiles of the workspace, their positions out of range or behind the sequence zeros already
+        const uint32_t st = e % L::kStages, bar = smem_u32(&ctl->full[st]);
+        if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
+        if (lane == 0) {
+          mbar_expect(bar, L::kTileBytes);
+          tma_5d(base + L::kKv + st * L::kTileBytes, &p.map, g.kvh * (kTile / 8),
+                 (p.stage0[g.s] + g.tile0 + j) * 2 + only, bar);
+        }
+        __syncwarp();
+      } else if constexpr (M == kBf16) {
         const uint32_t st = e % L::kStages, bar = smem_u32(&ctl->full[st]);
         if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
         if (lane == 0) mbar_expect(bar, L::kTileBytes);
@@ -454,15 +477,15 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
 // What a page holds behind the sequence's last position must not meet a weight, not even a zero one
 // (0 * NaN): zeros go there in a segment's last V tile.  (q8_0 tiles are zeroed as they are decoded;
 // whole copies behind the sequence are zeros already.)
-template <bool Q8>
-__device__ __forceinline__ bool trims(const Segment& g) { return !Q8 && (g.tile0 + g.n) * kTile > g.len; }
+template <int M>
+__device__ __forceinline__ bool trims(const Segment& g) { return M == kBf16 && (g.tile0 + g.n) * kTile > g.len; }
 
 // Warp 10.  Query tiles: TT tokens x G heads x 64 dims a box, as soon as the last S of the segment
 // before has read the tiles -- under that segment's last softmax, values and epilogue.  And the trim
 // of a segment's last V tile, when the MMA warp, which keeps the entry until then, says that it landed.
-template <int D, bool Q8>
+template <int D, int M>
 __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ctl* ctl) {
-  using L = Layout<D, Q8>;
+  using L = Layout<D, M>;
   const int lane = threadIdx.x & 31;
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
@@ -483,7 +506,7 @@ __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ct
     __syncwarp();
     const uint32_t c = c0 + 2 * g.n - 1;
     c0 += 2 * g.n;
-    if (trims<Q8>(g)) {
+    if (trims<M>(g)) {
       if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status)) return;
       ++trimmed;
       const int first = g.len - (g.tile0 + g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
@@ -502,7 +525,7 @@ __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ct
 // scale above 515 (127 * 515 is what fp16 holds) NaN.
 template <int D>
 __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* ctl) {
-  using L = Layout<D, true>;
+  using L = Layout<D, kQ8>;
   const int tid = threadIdx.x & 127;
   // A thread takes chunks x and x ^ 8 (8 codes, 16 bytes of operand each) of rows tid/8 + 16 i:
   // odd rows begin with the upper half, which keeps 8-byte reads and 16-byte writes free of conflicts.
@@ -573,10 +596,10 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
 // A wait that gives up does not leave the loops (their bounds stay uniform that way): in an aborted block
 // every later wait returns at once and the products are of whatever is there.  All of tensor memory is the block's, from column 0: S (and P, over it) of tile (stream) t at column
 // t * 128, O at 256 + t * D.
-template <int D, bool Q8>
+template <int D, int M>
 __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* ctl) {
-  using L = Layout<D, Q8>;
-  constexpr uint32_t kIdS = tc_idesc(!Q8, kTile, kTile, false), kIdO = tc_idesc(!Q8, kTile, D, true);
+  using L = Layout<D, M>;
+  constexpr uint32_t kIdS = tc_idesc(M == kBf16, kTile, kTile, false), kIdO = tc_idesc(M == kBf16, kTile, D, true);
   constexpr uint32_t kHiQ = desc_hi(1024), kHiKv = desc_hi(L::kGroup);
   constexpr uint32_t kStep = L::kTileBytes >> 4;   // a tile in descriptor units
   const uint32_t q_lo = desc_lo(base, 16), k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, 1024);
@@ -616,7 +639,7 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
     }
   };
   auto wait_q = [&](int t) {
-    wait(Q8 ? &ctl->qbar[t] : &ctl->qraw[t], (qq >> t) & 1);
+    wait(M != kBf16 ? &ctl->qbar[t] : &ctl->qraw[t], (qq >> t) & 1);
     qq ^= 1u << t;
   };
   auto done_q = [&]() { tc_commit(smem_u32(&ctl->qfree)); };
@@ -626,7 +649,7 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
     const uint32_t c = c0;
     auto wait_v = [&](int j) {
       wait_full(c + entry_of(g, 1, j));
-      if (j + 1 == g.n && trims<Q8>(g)) {
+      if (j + 1 == g.n && trims<M>(g)) {
         if (lane == 0) mbar_arrive(smem_u32(&ctl->landed));
         wait(&ctl->trim, tr & 1);
         ++tr;
@@ -715,12 +738,12 @@ __device__ __forceinline__ float convert_q(uint32_t tile, int row) {
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
-template <int D, bool Q8>
+template <int D, int M>
 __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl* ctl) {
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t ts = t * kTile + lane_base, to = 2 * kTile + lane_base;
-  constexpr float kBias = Q8 ? 6.f : 0.f;          // weights carry 2^kBias
+  constexpr float kBias = M != kBf16 ? 6.f : 0.f;          // weights carry 2^kBias
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g, next;
   bool have = walk.next(p.plan, p.seqs, g);
@@ -734,11 +757,11 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
   float cq = p.c;                                  // the row's constant
   // q8_0: the next segment's rows of this warpgroup's tile
   auto take_q = [&](const Segment& n) {
-    if constexpr (Q8) {
+    if constexpr (M != kBf16) {
       if (!n.two && t == 1) return true;
       if (!mbar_wait(smem_u32(&ctl->qraw[t]), qr & 1, ctl, p.status)) return false;
       ++qr;
-      cq = p.c * convert_q<D>(base + t * Layout<D, Q8>::kTileBytes, row);
+      cq = p.c * convert_q<D>(base + t * Layout<D, M>::kTileBytes, row);
       if (!n.two) static_cast<CtlQ8*>(ctl)->rowc[row] = cq;
       fence_async_smem();
       warp_arrive(smem_u32(&ctl->qbar[t]));
@@ -755,7 +778,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
     const int pos = live ? g.pos0 + ((urow0 + row) * p.plan.by_G >> 16) : INT32_MAX;
     const int mine = g.two ? g.n : (g.n - t + 1) / 2;
     float c = cq;
-    if constexpr (Q8) {
+    if constexpr (M != kBf16) {
       if (!g.two && t == 1 && mine > 0) {          // stream 1 takes the constants of stream 0's rows
         if (!mbar_wait(smem_u32(&ctl->qbar[0]), qs & 1, ctl, p.status)) return;
         c = static_cast<CtlQ8*>(ctl)->rowc[row];
@@ -835,7 +858,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
             const float2 x = fma2(make_float2(s[e], s[e + 1]), cc, mm);
             const float2 y = make_float2(ex2(x.x), ex2(x.y));
             sum[k & 1] = add2(sum[k & 1], y);
-            w[k] = Q8 ? f16x2(y.x, y.y) : bf16x2(y.x, y.y);
+            w[k] = M != kBf16 ? f16x2(y.x, y.y) : bf16x2(y.x, y.y);
           }
           // half of P stands when the third quarter is computed (and its own writing is still to come), the
           // rest at the end: the products of the first half start under the second's exponentials
@@ -960,7 +983,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
           const int who = __ffs(todo) - 1;
           const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
           __threadfence_block();
-          exact_row<D, Q8>(p, rr, hh, &ctl->beat);
+          exact_row<D, M>(p, rr, hh, &ctl->beat);
         }
       }
     }
@@ -974,9 +997,9 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
   }
 }
 
-template <int D, bool Q8>
-__global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
-  using L = Layout<D, Q8>;
+template <int D, int M>
+__global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using L = Layout<D, M>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + L::kCtl);
@@ -987,7 +1010,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {                   // (q8_0: a K or V tile is the decode warps' work)
-      mbar_init(smem_u32(&ctl->full[i]), Q8 ? 4 : 1);
+      mbar_init(smem_u32(&ctl->full[i]), M == kQ8 ? 4 : 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
       mbar_init(smem_u32(&ctl->raw_full[i]), 1);
       mbar_init(smem_u32(&ctl->raw_empty[i]), 4);
@@ -1024,16 +1047,16 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
   }
   // registers follow the work: a softmax thread holds a row of S (the warpgroups' sum is the launch's)
   if (warp < 8) {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (M == kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    softmax<D, Q8>(p, base, ctl);
+    softmax<D, M>(p, base, ctl);
   } else if (warp < 12) {
-    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (M == kQ8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 || warp == 11) produce<D, Q8>(p, base, ctl, warp == 8 ? 0 : 1);
-    if (warp == 9) issue<D, Q8>(p, base, ctl);
-    if (warp == 10) produce_q<D, Q8>(p, base, ctl);
-  } else if constexpr (Q8) {
+    if (warp == 8 || warp == 11) produce<D, M>(p, base, ctl, warp == 8 ? 0 : 1);
+    if (warp == 9) issue<D, M>(p, base, ctl);
+    if (warp == 10) produce_q<D, M>(p, base, ctl);
+  } else if constexpr (M == kQ8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     decode<D>(p, base, ctl);
   }
@@ -1056,7 +1079,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attn_kernel(const 
 // Wide (units of few rows, cut into many parts): a block takes 128 / D rows, a warp every eighth
 // partial, whose loads are all on their way before the factors are known.  Else a block takes 8
 // rows, a thread 4 columns of one, a warp's 8 rows side by side in a partial; the parts are few.
-template <int D, bool Q8, bool WIDE>
+template <int D, int M, bool WIDE>
 __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kWarps = 2 * D / 32, kLanes = D / 4, kRows = WIDE ? 32 / kLanes : 8;
   constexpr int kMine = WIDE ? (kMaxBlocks + kWarps - 1) / kWarps : 1, kAtOnce = 8;
@@ -1087,16 +1110,16 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
   // the factors of each row's partials: a warp a row (D = 64: WIDE's two rows, or two rows a warp in turn)
   for (int r = warp; r < kRows; r += kWarps) {
     const int row = min(row0 + r, rows - 1);
-    float M = -INFINITY, L = 0.f;
+    float top = -INFINITY, L = 0.f;
     for (int k = lane; k < n; k += 32) {
       const float m = at(k)[at_ml + 2 * row];
       fac[r][k] = m;
-      M = fmaxf(M, m);
+      top = fmaxf(top, m);
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     for (int k = lane; k < n; k += 32) {
-      const float m = fac[r][k], f = m == -INFINITY ? 0.f : ex2(m - M);
+      const float m = fac[r][k], f = m == -INFINITY ? 0.f : ex2(m - top);
       fac[r][k] = f;
       L += f * at(k)[at_ml + 2 * row + 1];
     }
@@ -1141,12 +1164,111 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
   for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1;
     const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who), lr = __shfl_sync(~0u, lrow, who);
-    if (!((done >> lr) & 1u)) exact_row<D, Q8>(p, rr, hh, nullptr);
+    if (!((done >> lr) & 1u)) exact_row<D, M>(p, rr, hh, nullptr);
     done |= 1u << lr;
   }
 }
 
+// --------------------------------------------------------------------------- staging
+// A q8_0 sequence with many units (of query rows) has its cache decoded once, into fp16 tiles in the
+// workspace, instead of by every unit's block: tile t of the staged ones is [K, V][KV head][128][D]
+// as a page of 128 positions would be.  What Decoder does to a value is done here: the product with
+// the scale rounded to fp16, NaN for scales above 515, zeros for positions out of range or behind the
+// sequence.  A thread takes 16 codes: 16 bytes and a scale in, 32 bytes out; HBM bound.
+constexpr int kStageThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_constant__ AttnParams p, __half* __restrict__ out,
+                                                              const __grid_constant__ StageTiles st) {
+  constexpr int CH = D / 16, kRows = kStageThreads / CH;       // chunks of a row, rows of a pass
+  const int tile = blockIdx.x, vh = blockIdx.y;                // vh: K heads, then V heads
+  int i = 0;
+  while (i + 1 < st.n && st.first[i + 1] <= tile) ++i;
+  const int s = st.seq[i], t = tile - st.first[i], len = p.seqs.len[s];
+  const int ch = threadIdx.x % CH;
+  const int32_t* bt = p.bt + static_cast<size_t>(s) * p.maxpg;
+  uint4 w[kTile / kRows];
+  uint16_t sc[kTile / kRows];
+#pragma unroll
+  for (int k = 0; k < kTile / kRows; ++k) {
+    const int pos = t * kTile + k * kRows + threadIdx.x / CH;
+    w[k] = make_uint4(0u, 0u, 0u, 0u);
+    sc[k] = 0;
+    if (pos >= len) continue;
+    const int page = __ldg(bt + pos / p.ps);
+    if (page < 0 || page >= p.P) {
+      if (p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
+      continue;
+    }
+    const size_t line = static_cast<size_t>(page) * 2 * p.plan.Hkv * p.ps + static_cast<size_t>(vh) * p.ps + pos % p.ps;
+    w[k] = __ldg(reinterpret_cast<const uint4*>(p.kv + line * D) + ch);
+    sc[k] = __ldg(reinterpret_cast<const uint16_t*>(p.kv + p.code_bytes) + line * (D / 32) + ch / 2);
+  }
+  const __half2 bias = __half2half2(__float2half_rn(1152.f));
+#pragma unroll
+  for (int k = 0; k < kTile / kRows; ++k) {
+    uint32_t d = sc[k];
+    if ((d & 0x7fffu) > 0x6006u) d = 0x7fffu;
+    const __half2 dd = __half2half2(__ushort_as_half(static_cast<uint16_t>(d)));
+    const uint32_t q[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = q[e] ^ 0x80808080u;
+      uint32_t lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
+      const __half2 hl = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&lo), bias), dd);
+      const __half2 hh = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&hi), bias), dd);
+      o[2 * e] = *reinterpret_cast<const uint32_t*>(&hl);
+      o[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&hh);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(
+        out + ((static_cast<size_t>(tile) * 2 * p.plan.Hkv + vh) * kTile + k * kRows + threadIdx.x / CH) * D + 16 * ch);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
 // --------------------------------------------------------------------------- host
+// Sequences whose cache is staged: from kStageUnits units on decoding once is less work than every unit's block
+// doing it (a tile staged costs its bytes, 0.017 us of the card a KV head; a unit's block that decodes
+// takes 0.8 us longer a tile, 0.005 us of the card); kStageBytes at most are staged in a call.
+constexpr int kStageUnits = 6;
+constexpr size_t kStageBytes = size_t(1) << 30;
+
+struct CallPlan {
+  AttnPlan direct, staged;           // the two launches' (q8_0 only: staged.items may be 0, as direct.items)
+  StageTiles tiles;
+  int32_t stage0[kMaxSeqs];
+  size_t stage_bytes, floats;        // workspace: staged tiles, then partials (the launches follow each other)
+  size_t bytes() const { return stage_bytes + floats * sizeof(float); }
+};
+
+bool plan_call(const mk_cache_shape& c, const ChunkSeqs& q, CallPlan* cp) {
+  bool direct[kMaxSeqs], staged[kMaxSeqs];
+  cp->stage_bytes = 0;
+  cp->tiles.n = 0;
+  cp->tiles.first[0] = 0;
+  const int UT = 2 * (kTile / (c.num_q_heads / c.num_kv_heads));
+  const size_t tile_bytes = static_cast<size_t>(2) * c.num_kv_heads * kTile * c.head_dim * 2;
+  for (int s = 0; s < q.n; ++s) {
+    const int chunk = q.row0[s + 1] - q.row0[s], tiles = (q.len[s] + kTile - 1) / kTile;
+    staged[s] = (c.flags & MK_FLAG_KV_Q8) && (chunk + UT - 1) / UT >= kStageUnits &&
+                cp->stage_bytes + tiles * tile_bytes <= kStageBytes;
+    direct[s] = !staged[s];
+    cp->stage0[s] = 0;
+    if (!staged[s]) continue;
+    StageTiles& t = cp->tiles;
+    cp->stage0[s] = t.first[t.n];
+    t.seq[t.n] = s;
+    t.first[t.n + 1] = t.first[t.n] + tiles;
+    ++t.n;
+    cp->stage_bytes += tiles * tile_bytes;
+  }
+  size_t a = 0, b = 0;
+  if (!make_plan(c, q, direct, &cp->direct, &a) || !make_plan(c, q, staged, &cp->staged, &b)) return false;
+  cp->floats = std::max(a, b);
+  return true;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
@@ -1158,19 +1280,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return encode;
 }
 
-// bf16 pages to TMA, innermost first: {64 dims, 8 positions, D/64 spans of dims, groups of 8
+// bf16 pages (or fp16 tiles of the workspace) to TMA, innermost first: {64 dims, 8 positions, D/64 spans of dims, groups of 8
 // positions over the KV heads, pages x (K, V)}.  A box lands as [group][span][8 positions][128 B]:
 // 8-position groups a constant distance apart whatever the page size, which is what the operand
 // descriptors of both K (rows along dims) and V (rows along positions) need.
-int encode_pages(const mk_cache_shape& c, const void* kv, int box_pos, CUtensorMap* out) {
+int encode_pages(int D_, int heads, int page_size, int pages, bool bf16, const void* kv, int box_pos, CUtensorMap* out) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
   if (!encode) return chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t D = c.head_dim, ps = c.page_size, hkv = c.num_kv_heads;
-  const cuuint64_t dims[5] = {64, 8, D / 64, hkv * ps / 8, static_cast<cuuint64_t>(c.num_pages) * 2};
+  const cuuint64_t D = D_, ps = page_size, hkv = heads;
+  const cuuint64_t dims[5] = {64, 8, D / 64, hkv * ps / 8, static_cast<cuuint64_t>(pages) * 2};
   const cuuint64_t strides[4] = {D * 2, 128, 8 * D * 2, hkv * ps * D * 2};
   const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(box_pos / 8), 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(kv), dims, strides, box, estr,
+  const CUresult r = encode(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(kv), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MK_OK : chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -1192,7 +1314,7 @@ int encode_queries(const mk_cache_shape& c, const AttnPlan& pl, const void* q, i
   return r == CUDA_SUCCESS ? MK_OK : chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", static_cast<int>(r));
 }
 
-template <int D, bool Q8>
+template <int D, int M>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
   static std::atomic<uint64_t> set{0};
@@ -1201,20 +1323,20 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(set.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem_bytes<D, Q8>()));
+    e = cudaFuncSetAttribute(attn_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<D, M>()));
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  attn_kernel<D, Q8><<<p.plan.blocks, Layout<D, Q8>::kThreads, smem_bytes<D, Q8>(), st>>>(p);
+  attn_kernel<D, M><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.plan.cuts == 0) return e;
   // (plans with units of two tiles cut an item in few parts)
   if (p.plan.urows <= kTile / 2) {
     constexpr int kRows = 128 / D;
-    merge_kernel<D, Q8, true><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
+    merge_kernel<D, M, true><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
   } else {
-    merge_kernel<D, Q8, false><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
+    merge_kernel<D, M, false><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
   }
   return cudaGetLastError();
 }
@@ -1230,10 +1352,9 @@ extern "C" int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t
   const int rc = check_chunk(shape, num_seqs, chunk_lens, seq_lens, &seqs);
   if (rc) return rc;
   if (!bytes_out) return chunk_fail(MK_ERR_INVALID_ARG, "bytes_out is NULL");
-  AttnPlan plan;
-  size_t floats = 0;
-  if (!make_plan(*shape, seqs, &plan, &floats)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
-  *bytes_out = floats * sizeof(float);
+  CallPlan plan;
+  if (!plan_call(*shape, seqs, &plan)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
+  *bytes_out = plan.bytes();
   return MK_OK;
 }
 
@@ -1254,35 +1375,77 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   if (misaligned(block_tables, 4) || misaligned(q, 16) || misaligned(kv_layer, 16) || misaligned(out, 16) ||
       misaligned(workspace, 16))
     return chunk_fail(MK_ERR_INVALID_ARG, "pointers must be 16-byte aligned (block_tables 4-byte)");
-  size_t floats = 0;
-  if (!make_plan(c, p.seqs, &p.plan, &floats)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
-  if (workspace_bytes < floats * sizeof(float) || (floats > 0 && !workspace))
+  CallPlan plan;
+  if (!plan_call(c, p.seqs, &plan)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
+  if (workspace_bytes < plan.bytes() || (plan.bytes() > 0 && !workspace))
     return chunk_fail(MK_ERR_INVALID_ARG, "the workspace holds %zu bytes; these lengths need %zu", workspace_bytes,
-                      floats * sizeof(float));
+                      plan.bytes());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = clear_status(status_out, st);
   if (rc || rows == 0) return rc;
   const bool q8 = (c.flags & MK_FLAG_KV_Q8) != 0;
   p.box = std::min(c.page_size & -c.page_size, kTile);
-  rc = encode_queries(c, p.plan, q, q_stride, rows, &p.qmap);
-  if (rc) return rc;
-  if (!q8) {
-    rc = encode_pages(c, kv_layer, p.box, &p.map);
-    if (rc) return rc;
-  }
   p.kv = static_cast<const uint8_t*>(kv_layer);
   p.bt = block_tables;
   p.status = status_out;
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_stride;
   p.out = static_cast<uint16_t*>(out);
-  p.part = static_cast<float*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.stage_bytes);
   p.code_bytes = static_cast<size_t>(c.num_pages) * 2 * c.num_kv_heads * c.page_size * c.head_dim;
+  std::copy(plan.stage0, plan.stage0 + kMaxSeqs, p.stage0);
   p.Hq = c.num_q_heads;
   p.ps = c.page_size;
   p.P = c.num_pages;
   p.maxpg = c.max_pages_per_seq;
   p.c = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));
-  const cudaError_t e = q8 ? launch<128, true>(p, st) : c.head_dim == 128 ? launch<128, false>(p, st) : launch<64, false>(p, st);
+  rc = encode_queries(c, plan.direct, q, q_stride, rows, &p.qmap);
+  if (rc) return rc;
+  cudaError_t e = cudaSuccess;
+  if (plan.direct.items > 0) {
+    p.plan = plan.direct;
+    if (!q8) {
+      rc = encode_pages(c.head_dim, c.num_kv_heads, c.page_size, c.num_pages, true, kv_layer, p.box, &p.map);
+      if (rc) return rc;
+    }
+    e = q8 ? launch<128, kQ8>(p, st) : c.head_dim == 128 ? launch<128, kBf16>(p, st) : launch<64, kBf16>(p, st);
+  }
+  if (e == cudaSuccess && plan.staged.items > 0) {
+    p.plan = plan.staged;
+    rc = encode_pages(128, c.num_kv_heads, kTile, plan.tiles.first[plan.tiles.n], false, workspace, kTile, &p.map);
+    if (rc) return rc;
+    stage_kernel<128><<<dim3(plan.tiles.first[plan.tiles.n], 2 * c.num_kv_heads), kStageThreads, 0, st>>>(
+        p, static_cast<__half*>(workspace), plan.tiles);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch<128, kStaged>(p, st);
+  }
   return e == cudaSuccess ? MK_OK : chunk_fail(MK_ERR_CUDA, "chunk attention: %s", cudaGetErrorString(e));
+}
+
+extern "C" int mk_plan_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                       const int32_t* seq_lens, int32_t* segments, int32_t max_segments,
+                                       int32_t* n_out) {
+  ChunkSeqs seqs;
+  const int rc = check_chunk(shape, num_seqs, chunk_lens, seq_lens, &seqs);
+  if (rc) return rc;
+  if (!n_out || (max_segments > 0 && !segments)) return chunk_fail(MK_ERR_INVALID_ARG, "NULL output");
+  CallPlan plan;
+  if (!plan_call(*shape, seqs, &plan)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
+  int32_t n = 0;
+  for (int launch = 0; launch < 2; ++launch) {
+    const AttnPlan& pl = launch ? plan.staged : plan.direct;
+    for (int b = 0; b < pl.blocks; ++b) {
+      SegmentWalk walk(pl, b);
+      Segment g;
+      while (walk.next(pl, seqs, g)) {
+        if (n < max_segments) {
+          const int32_t row[9] = {launch, b, g.s, g.unit, g.kvh, g.tile0, g.n, g.tiles, g.slot};
+          std::copy(row, row + 9, segments + 9 * static_cast<size_t>(n));
+        }
+        ++n;
+      }
+    }
+  }
+  *n_out = n;
+  return MK_OK;
 }

@@ -4,8 +4,6 @@
 
 #include <algorithm>
 
-#include "mk_debug.h"
-
 namespace mk {
 
 namespace {
@@ -18,7 +16,7 @@ constexpr int kMinRange = 3;                // position tiles a block is worth
 constexpr int kMaxWalk = 1 << 17;            // items beyond which whole ones are even enough (and the walk long)
 }  // namespace
 
-bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t* floats) {
+bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, const bool* use, AttnPlan* pl, size_t* floats) {
   pl->Hkv = c.num_kv_heads;
   pl->G = c.num_q_heads / c.num_kv_heads;
   pl->TT = kTile / pl->G;
@@ -29,7 +27,7 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
   int most = 0;
   for (int s = 0; s < q.n; ++s) {
     const int chunk = q.row0[s + 1] - q.row0[s];
-    if (chunk == 0) continue;
+    if (chunk == 0 || !use[s]) continue;
     pl->seq[pl->n++] = s;
     most = std::max(most, std::min(chunk, UT));
   }
@@ -110,31 +108,3 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t
 }
 
 }  // namespace mk
-
-using namespace mk;
-
-extern "C" int mk_plan_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
-                                       const int32_t* seq_lens, int32_t* segments, int32_t max_segments,
-                                       int32_t* n_out) {
-  ChunkSeqs seqs;
-  const int rc = check_chunk(shape, num_seqs, chunk_lens, seq_lens, &seqs);
-  if (rc) return rc;
-  if (!n_out || (max_segments > 0 && !segments)) return chunk_fail(MK_ERR_INVALID_ARG, "NULL output");
-  AttnPlan plan;
-  size_t floats = 0;
-  if (!make_plan(*shape, seqs, &plan, &floats)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
-  int32_t n = 0;
-  for (int b = 0; b < plan.blocks; ++b) {
-    SegmentWalk walk(plan, b);
-    Segment g;
-    while (walk.next(plan, seqs, g)) {
-      if (n < max_segments) {
-        const int32_t row[8] = {b, g.s, g.unit, g.kvh, g.tile0, g.n, g.tiles, g.slot};
-        std::copy(row, row + 8, segments + 8 * static_cast<size_t>(n));
-      }
-      ++n;
-    }
-  }
-  *n_out = n;
-  return MK_OK;
-}

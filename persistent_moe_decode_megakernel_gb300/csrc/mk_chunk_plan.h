@@ -97,8 +97,9 @@ struct SegmentWalk {
   }
 };
 
-// Fills the plan; *floats is the size of the partials (0: none).  False: more items than a call takes.
-bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, AttnPlan* pl, size_t* floats);
+// Fills the plan of the sequences that `use` marks; *floats is the size of the partials (0: none).  False: more items
+// than a call takes.
+bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, const bool* use, AttnPlan* pl, size_t* floats);
 
 }  // namespace mk
 

@@ -145,8 +145,9 @@ def test_rope_frequencies():
 
 
 def check_plan(sh, cl, sl):
-    """Every position tile of every (sequence, unit, KV head) in exactly one segment, no segment empty,
-    the cut items' partials distinct and in block order; returns the blocks' tiles."""
+    """Every position tile of every (sequence, unit, KV head) in exactly one segment, a sequence in one
+    launch, no segment empty, the cut items' partials distinct and in block order; returns the tiles of
+    each launch's blocks."""
     seg = mk.plan_chunk_attention(sh, cl, sl)
     G = sh.num_q_heads // sh.num_kv_heads
     ut = 2 * (128 // G)
@@ -155,25 +156,31 @@ def check_plan(sh, cl, sl):
         for u in range(-(-c // ut)):
             for h in range(sh.num_kv_heads):
                 want[s, u, h] = (n - c + min(c, (u + 1) * ut) - 1) // 128 + 1
-    got, slots, load = {}, set(), {}
-    for b, s, u, h, t0, n, total, slot in seg.tolist():
+    got, slots, load, where = {}, (set(), set()), ({}, {}), {}
+    for launch, b, s, u, h, t0, n, total, slot in seg.tolist():
+        assert where.setdefault(s, launch) == launch
         assert n > 0 and want[s, u, h] == total and t0 + n <= total
         assert got.get((s, u, h), 0) == t0       # segments of an item come in order, blocks ascending
         got[s, u, h] = t0 + n
-        load[b] = load.get(b, 0) + n
+        load[launch][b] = load[launch].get(b, 0) + n
         if n == total:
             assert slot == -1
         else:
-            assert slot == 2 * b + (t0 == 0) and slot not in slots
-            slots.add(slot)
+            assert slot == 2 * b + (t0 == 0) and slot not in slots[launch]
+            slots[launch].add(slot)
     assert got == want
-    assert seg.size == 0 or (seg[:, 0].max() < 152 and np.all(np.diff(seg[:, 0]) >= 0))
-    bytes_ = mk.chunk_attention_workspace(sh, cl, sl)
+    for launch in (0, 1):
+        blocks = seg[seg[:, 0] == launch][:, 1]
+        assert blocks.size == 0 or (blocks.max() < 152 and np.all(np.diff(blocks) >= 0))
+    # staged sequences are q8_0 ones of many units, and the workspace holds their tiles and the partials
+    staged = [s for s, launch in where.items() if launch == 1]
+    assert all(sh.flags == mk.FLAG_KV_Q8 and -(-cl[s] // ut) >= 6 for s in staged)
+    tiles = sum(-(-sl[s] // 128) for s in staged) * 2 * sh.num_kv_heads * 128 * sh.head_dim * 2
+    assert tiles <= 1 << 30
     rows = max([min(c, ut) for c in cl], default=0) * G
-    if slots:
-        assert bytes_ >= (max(slots) + 1) * rows * (sh.head_dim + 4) * 4
-    else:
-        assert bytes_ == 0
+    parts = (max(slots[0] | slots[1]) + 1) * (sh.head_dim + 4) * 4 if slots[0] | slots[1] else 0
+    bytes_ = mk.chunk_attention_workspace(sh, cl, sl)
+    assert bytes_ >= tiles and (bytes_ > tiles) == (parts > 0) and bytes_ <= tiles + 2 * 152 * rows * (sh.head_dim + 4) * 4
     return load
 
 
@@ -187,13 +194,27 @@ def test_plan_covers_every_tile_once(seed):
     top = int(g.choice([1, 64, 3000]))
     cl = [int(g.integers(0, min(x, top) + 1)) for x in sl]
     check_plan(sh, cl, sl.tolist())
+    sh.flags = mk.FLAG_KV_Q8
+    check_plan(sh, cl, sl.tolist())
 
 
 @pytest.mark.parametrize("cl,sl", [([1], [131073]), ([1], [1]), ([8192], [8192]), ([2048], [32768]), ([1024], [16384]),
                                    ([1] * 64, [32768] * 64), ([200000], [200000]), ([1], [1 << 20])])
 def test_plan_is_even(cl, sl):
     sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 16)
-    load = check_plan(sh, cl, sl)
+    load = check_plan(sh, cl, sl)[0]
     total = sum(load.values())
     if total > 152 * 8:      # enough to go round: the longest block within 15 % and a few tiles of even
         assert max(load.values()) <= 1.15 * total / 152 + 4
+
+
+def test_plan_stages_at_most_a_gigabyte():
+    # 8 KV heads: a tile of 128 positions is half a MiB staged
+    sh = shape(num_q_heads=64, num_kv_heads=8, max_pages_per_seq=1 << 16, flags=mk.FLAG_KV_Q8)
+    long, short = 2000 * 128, 100 * 128
+    seg = mk.plan_chunk_attention(sh, [400, 400, 400], [long, short, short])
+    launch = {s: k for k, s in zip(seg[:, 0].tolist(), seg[:, 2].tolist())}
+    assert launch == {0: 1, 1: 0, 2: 0}        # the second and third no longer fit
+    seg = mk.plan_chunk_attention(sh, [400, 400, 16], [2049 * 128, short, short])
+    launch = {s: k for k, s in zip(seg[:, 0].tolist(), seg[:, 2].tolist())}
+    assert launch == {0: 0, 1: 1, 2: 0}        # the first never fits, the last has too few rows

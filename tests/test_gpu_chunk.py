@@ -313,6 +313,30 @@ def test_attention_q8_values_beyond_fp16(len_, new):
     check_attention(st, std=0.02)
 
 
+def test_attention_q8_sequences_of_many_rows_and_of_few():
+    # those of many rows are decoded into the workspace first; pages out of range, values beyond fp16 and a
+    # tail inside a page on both sides
+    lens, news = [700, 300, 40, 513], [650, 2, 40, 300]
+    st = R.Setup(16, 2, 128, 24, lens, news, q8=True, seed=25)
+    assert set(mk.plan_chunk_attention(st.shape(mk), news, lens)[:, 0].tolist()) == {0, 1}
+    codes, scales = st.planes()
+    for s, pos, which, sc in ((0, 3, 1, 50000.0), (0, 600, 0, 700.0), (3, 511, 1, 65504.0), (1, 100, 1, 2000.0)):
+        scales[st.bt[s, pos // 24].long(), which, :, pos % 24, 2] = sc
+    drop = torch.zeros(4, 700, dtype=torch.bool, device="cuda")
+    good, bad = st.bt.clone(), st.bt.clone()
+    for s, p, v in ((0, 0, -1), (0, 7, st.P), (3, 20, 1 << 30), (1, 3, -9)):
+        drop[s, p * 24:p * 24 + 24] = True
+        bad[s, p] = v
+    q = st.normal(st.rows, 16, 128, std=0.02)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = mk.chunk_attention(st.shape(mk), q, news, lens, bad, st.kv, status=status)
+    assert int(status) == mk.MK_ERR_DEVICE_BOUNDS
+    st.bt = good
+    ref, *scale = R.attention(st, q, st.kv, drop)
+    far, bound = (out.double() - ref).abs(), R.attention_bound(ref, *scale, True)
+    assert torch.all(far <= bound), float((far / bound).max())
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_attention_queries_of_any_magnitude(q8):
     # rows scaled by powers of two from 2^-100 to 2^100 against keys scaled the other way
