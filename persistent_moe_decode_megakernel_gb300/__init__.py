@@ -12,8 +12,10 @@ and inspection).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import subprocess
+import sysconfig
 import threading
 from concurrent.futures import ThreadPoolExecutor
 
@@ -28,6 +30,8 @@ _INC = os.path.join(_ROOT, "include")
 TRACE = os.environ.get("MK_TRACE", "0") == "1"
 _BUILD = os.path.join(_HERE, "_build_trace" if TRACE else "_build")
 LIB_PATH = os.path.join(_BUILD, "libmk.so")
+_BIND = os.path.join(_HERE, "bind")
+BIND_PATH = os.path.join(_BUILD, "_mk_torch.so")   # marshalling of torch tensors for the chunk operators
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 MK_OK, MK_ERR_INVALID_ARG, MK_ERR_CUDA, MK_ERR_OOM = 0, -1, -2, -3
@@ -45,14 +49,18 @@ class MkError(RuntimeError):
 
 def _sources():
     return [os.path.join(_CSRC, f) for f in sorted(os.listdir(_CSRC)) if f.endswith((".cu", ".cuh", ".cpp", ".h"))] + [
-        os.path.join(_INC, f) for f in sorted(os.listdir(_INC)) if f.endswith(".h")]
+        os.path.join(_INC, f) for f in sorted(os.listdir(_INC)) if f.endswith(".h")] + [
+        os.path.join(_BIND, f) for f in sorted(os.listdir(_BIND)) if f.endswith(".cpp")]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile ``csrc/*.cu`` and ``csrc/*.cpp`` for sm_103a into ``_build/libmk.so``."""
+    """Compile ``csrc/*.cu`` and ``csrc/*.cpp`` for sm_103a into ``_build/libmk.so``, and
+    ``bind/mk_torch.cpp`` against torch into ``_build/_mk_torch.so`` (without torch, the library alone)."""
     os.makedirs(_BUILD, exist_ok=True)
-    srcs = _sources()
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= max(os.path.getmtime(s) for s in srcs):
+    newest = max(os.path.getmtime(s) for s in _sources())
+    have_torch = importlib.util.find_spec("torch") is not None
+    made = (LIB_PATH, BIND_PATH) if have_torch else (LIB_PATH,)
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in made):
         return LIB_PATH
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     nvcc = os.path.join(cuda, "bin", "nvcc")
@@ -70,6 +78,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", _INC, "-I", _CSRC, "-I",
                          os.path.join(cuda, "include"), "-DMK_TRACE=%d" % TRACE, "-c", src, "-o", obj])
 
+    if have_torch:
+        import torch
+        tdir = os.path.dirname(torch.__file__)
+        bind_obj = os.path.join(_BUILD, "mk_torch.o")
+        cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", _INC, "-isystem", os.path.join(tdir, "include"),
+                     "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"), "-isystem",
+                     os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], "-c",
+                     os.path.join(_BIND, "mk_torch.cpp"), "-o", bind_obj])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -83,6 +100,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     run([nvcc, ARCH, "-shared", "-o", tmp] + objs)
     os.replace(tmp, LIB_PATH)
+    if have_torch:
+        tmp = BIND_PATH + f".tmp{os.getpid()}"
+        run(["g++", "-shared", "-o", tmp, bind_obj, "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-lc10_cuda"])
+        os.replace(tmp, BIND_PATH)
     return LIB_PATH
 
 
@@ -336,84 +358,33 @@ def rope_frequencies(rotary_dim: int, theta: float, factor: float = 1.0, origina
     return out
 
 
-# These calls are short next to their marshalling (a few microseconds on the device for a few tokens), so
-# it is kept lean: torch is asked for as little as possible, messages are built only on failure, lengths go
-# to ctypes as bytes and pointers as integers, and no context manager is entered unless the device or the
-# stream is not the current one.
-def _bad(what):
-    raise MkError(MK_ERR_INVALID_ARG, what)
+_bind = None
 
 
-def _lengths_arg(chunk_lens, seq_lens):
-    """Both as int32 bytes (ctypes passes their address), the number of sequences, the rows."""
-    cl, sl = np.asarray(chunk_lens, dtype=np.int32), np.asarray(seq_lens, dtype=np.int32)
-    if cl.ndim != 1 or cl.shape != sl.shape:
-        _bad("chunk_lens and seq_lens: one length per sequence each")
-    rows = sum(cl.tolist())
-    if not 0 <= rows < 1 << 24:
-        _bad("chunk_lens: fewer than 2^24 rows")
-    return cl.tobytes(), sl.tobytes(), cl.size, rows
+def _native():
+    """The marshalling module.  Raises if it has not been built: there is no other path."""
+    global _bind
+    if _bind is None:
+        lib()
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"binding not built ({BIND_PATH} missing); call build() first")
+        spec = importlib.util.spec_from_file_location("_mk_torch", BIND_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.init(MkError, *(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in (
+            "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache", "mk_last_error")))
+        _bind = m
+    return _bind
 
 
-def _cache_arg(shape, n_seqs, block_tables, kv_layer):
-    """The cache's device index, after checks of what the C call cannot see."""
+def _on(stream, kv_layer, call, *args):
+    """``call`` with ``stream`` current, so that new outputs and workspaces belong to the stream that writes them."""
     import torch
-    dev, bs, q8 = kv_layer.get_device(), block_tables.shape, shape.flags & FLAG_KV_Q8
-    if not (dev >= 0 and block_tables.get_device() == dev and block_tables.dtype is torch.int32 and len(bs) == 2
-            and bs[0] >= n_seqs and bs[1] == shape.max_pages_per_seq and block_tables.is_contiguous()):
-        _bad("block_tables: contiguous int32 [num_seqs, max_pages_per_seq] on the cache's CUDA device")
-    n = shape.num_pages * 2 * shape.num_kv_heads * shape.page_size * shape.head_dim
-    if not (kv_layer.dtype is (torch.uint8 if q8 else torch.bfloat16) and kv_layer.numel() == (n + n // 16 if q8 else n)
-            and kv_layer.is_contiguous()):
-        _bad("kv_layer: one layer of the shape's cache, contiguous CUDA tensor, bf16 (q8_0: uint8 codes, then f16 scales)")
-    return dev
-
-
-def _rows_arg(t, rows, heads, dim, dev, what):
-    """The row stride of t, bf16 rows of heads*dim contiguous values as [rows, heads*dim] or [rows, heads, dim]."""
-    import torch
-    size, stride = t.shape, t.stride()
-    if not (t.get_device() == dev and t.dtype is torch.bfloat16 and size[0] >= rows
-            and (len(size) == 2 and size[1] == heads * dim and stride[1] == 1
-                 or len(size) == 3 and size[1] == heads and size[2] == dim and stride[2] == 1
-                 and (stride[1] == dim or heads == 1))):
-        _bad(f"{what}: bf16 rows of {heads} heads of {dim} contiguous values on the cache's device, at least {rows} rows")
-    return stride[0] if size[0] > 1 else heads * dim
-
-
-def _out_arg(t, size, dev, what, kv_layer):
-    import torch
-    if t is None:   # (a device object: an index costs torch a microsecond more)
-        return torch.empty(size, dtype=torch.bfloat16, device=kv_layer.device)
-    if not (t.get_device() == dev and t.dtype is torch.bfloat16 and t.is_contiguous() and t.shape[1:] == size[1:]
-            and t.shape[0] >= size[0]):
-        _bad(f"{what}: contiguous bf16 tensor of at least {list(size)} on the cache's device")
-    return t
-
-
-def _status_arg(t, dev):
-    import torch
-    if t is None:
-        return None
-    if not (t.get_device() == dev and t.dtype is torch.int32 and t.numel() == 1):
-        _bad("status: int32 tensor of one value on the cache's device")
-    return t.data_ptr()
-
-
-def _run(dev, stream, call, *args):
-    """``call(stream handle, *args)`` with device ``dev`` and ``stream`` (default: torch's current one of the
-    device) current, so that new outputs and workspaces belong to the stream that writes them."""
-    import torch
-    if stream is None:
-        if torch._C._cuda_getDevice() == dev:
-            # (the handle alone: building a Stream object costs as much as the rest of the marshalling)
-            return call(torch._C._cuda_getCurrentRawStream(dev), *args)
-        with torch.cuda.device(dev):
-            return call(torch._C._cuda_getCurrentRawStream(dev), *args)
-    if stream.device.index != dev:
-        _bad("stream is on another device than the tensors")
+    if stream.device != kv_layer.device:
+        raise MkError(MK_ERR_INVALID_ARG, "stream is on another device than the tensors")
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream, *args)
+        return call(*args)
 
 
 def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, rope: Rope | None = None,
@@ -426,32 +397,19 @@ def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_
     k_norm: bf16 CUDA [D] gains or None; status: int32 CUDA [1] or None; stream: default torch's
     current one.  Returns the query rows, bf16 [rows, Hq, D] (``q_out`` or a new tensor).
     """
-    import torch
-    cl, sl, n, rows = _lengths_arg(chunk_lens, seq_lens)
-    dev, Hq, D = _cache_arg(shape, n, block_tables, kv_layer), shape.num_q_heads, shape.head_dim
-    stride = _rows_arg(qkv, rows, Hq + 2 * shape.num_kv_heads, D, dev, "qkv")
-    for t in (q_norm, k_norm):
-        if t is not None and not (t.get_device() == dev and t.dtype is torch.bfloat16 and t.is_contiguous()
-                                  and t.numel() == D):
-            _bad("q_norm / k_norm: contiguous bf16 [head_dim] on the cache's device")
-    st = _status_arg(status, dev)
-
-    def call(handle):
-        out = _out_arg(q_out, (rows, Hq, D), dev, "q_out", kv_layer)
-        rc = lib().mk_append_chunk(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), qkv.data_ptr(), stride,
-                                   None if rope is None else ctypes.byref(rope.struct),
-                                   None if q_norm is None else q_norm.data_ptr(),
-                                   None if k_norm is None else k_norm.data_ptr(), eps, out.data_ptr(),
-                                   kv_layer.data_ptr(), st, handle)
-        return _check(rc) or out
-    return _run(dev, stream, call)
+    args = (shape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, None if rope is None else rope.struct, q_norm, k_norm,
+            eps, q_out, status)
+    return _native().append_chunk(*args) if stream is None else _on(stream, kv_layer, _native().append_chunk, *args)
 
 
 def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
     """Bytes of workspace :func:`chunk_attention` needs for these lengths (0: none)."""
-    cl, sl, n, _ = _lengths_arg(chunk_lens, seq_lens)
+    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
+    if cl.ndim != 1 or cl.shape != sl.shape:
+        raise MkError(MK_ERR_INVALID_ARG, "chunk_lens and seq_lens: one length per sequence each")
     need = ctypes.c_size_t()
-    _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), n, cl, sl, ctypes.byref(need)))
+    _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
+                                              ctypes.byref(need)))
     return need.value
 
 
@@ -473,42 +431,16 @@ def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv
     (``mk_chunk_attention``; arguments as :func:`append_chunk`).  q: bf16 CUDA [rows, Hq, D] (rows
     may be strided); workspace: CUDA tensor of at least :func:`chunk_attention_workspace` bytes, or
     None to take it from torch's allocator.  Returns bf16 [rows, Hq, D]."""
-    import torch
-    cl, sl, n, rows = _lengths_arg(chunk_lens, seq_lens)
-    dev, Hq, D = _cache_arg(shape, n, block_tables, kv_layer), shape.num_q_heads, shape.head_dim
-    stride = _rows_arg(q, rows, Hq, D, dev, "q")
-    st = _status_arg(status, dev)
-    if workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
-        _bad("workspace: contiguous tensor on the cache's device")
-
-    def call(handle):
-        L, ws, need = lib(), workspace, ctypes.c_size_t()
-        o = _out_arg(out, (rows, Hq, D), dev, "out", kv_layer)
-        if ws is None:
-            _check(L.mk_chunk_attention_workspace(ctypes.byref(shape), n, cl, sl, ctypes.byref(need)))
-            if need.value:
-                ws = torch.empty(need.value, dtype=torch.uint8, device=kv_layer.device)
-        _check(L.mk_chunk_attention(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), q.data_ptr(), stride,
-                                    kv_layer.data_ptr(), o.data_ptr(), None if ws is None else ws.data_ptr(),
-                                    0 if ws is None else ws.nbytes, st, handle))
-        return o
-    return _run(dev, stream, call)
+    args = (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status)
+    return _native().chunk_attention(*args) if stream is None else _on(stream, kv_layer, _native().chunk_attention, *args)
 
 
 def read_cache(shape: CacheShape, counts, seq_lens, block_tables, kv_layer, k_out=None, v_out=None, status=None,
                stream=None):
     """The last ``counts[s]`` cached positions of every sequence as packed bf16 rows
     (``mk_read_cache``).  Returns (k, v), each [rows, Hkv, D]."""
-    cl, sl, n, rows = _lengths_arg(counts, seq_lens)
-    dev, size = _cache_arg(shape, n, block_tables, kv_layer), (rows, shape.num_kv_heads, shape.head_dim)
-    st = _status_arg(status, dev)
-
-    def call(handle):
-        k, v = _out_arg(k_out, size, dev, "k_out", kv_layer), _out_arg(v_out, size, dev, "v_out", kv_layer)
-        _check(lib().mk_read_cache(ctypes.byref(shape), n, cl, sl, block_tables.data_ptr(), kv_layer.data_ptr(),
-                                   k.data_ptr(), v.data_ptr(), st, handle))
-        return k, v
-    return _run(dev, stream, call)
+    args = (shape, None, counts, seq_lens, block_tables, kv_layer, k_out, v_out, status)
+    return _native().read_cache(*args) if stream is None else _on(stream, kv_layer, _native().read_cache, *args)
 
 
 # ---------------------------------------------------------------- the engine

@@ -218,3 +218,29 @@ def test_plan_stages_at_most_a_gigabyte():
     seg = mk.plan_chunk_attention(sh, [400, 400, 16], [2049 * 128, short, short])
     launch = {s: k for k, s in zip(seg[:, 0].tolist(), seg[:, 2].tolist())}
     assert launch == {0: 0, 1: 1, 2: 0}        # the first never fits, the last has too few rows
+
+
+def test_binding_refuses_on_the_host():
+    # what is no tensor, no length or not on a CUDA device ends as MkError before anything is launched
+    torch = pytest.importorskip("torch")
+    sh = mk.CacheShape(8, 2, 128, 16, 8, 4, 0)
+    kv = torch.zeros(2 * 8 * 2 * 16 * 128, dtype=torch.bfloat16)
+    ok = dict(q=torch.zeros(3, 8, 128, dtype=torch.bfloat16), chunk_lens=[3], seq_lens=[5],
+              block_tables=torch.zeros(1, 4, dtype=torch.int32), kv_layer=kv)
+    two = np.array([3, 0, 3, 0])
+    for bad, word in ((dict(), "CUDA"), (dict(chunk_lens=np.array([3], np.int64)), "CUDA"), (dict(chunk_lens=two[:1]), "CUDA"),
+                      (dict(chunk_lens=torch.tensor([3])), "CUDA"), (dict(chunk_lens=two[::2], seq_lens=[5, 5]), "CUDA"),
+                      (dict(chunk_lens=[3.0]), "whole"), (dict(chunk_lens=np.array([3.0])), "whole"),
+                      (dict(chunk_lens="3"), "whole"), (dict(chunk_lens=None), "whole"), (dict(seq_lens=[1 << 31]), "whole"),
+                      (dict(seq_lens=np.array([1 << 40])), "32 bits"), (dict(seq_lens=[5, 5]), "one length"),
+                      (dict(chunk_lens=[1 << 23] * 2, seq_lens=[1 << 23] * 2), "rows"), (dict(chunk_lens=[-1]), "rows"),
+                      (dict(kv_layer=None), "kv_layer"), (dict(block_tables=[[0]]), "block_tables")):
+        with pytest.raises(mk.MkError) as e:
+            mk.chunk_attention(sh, **{**ok, **bad})
+        assert e.value.code == mk.MK_ERR_INVALID_ARG and word in str(e.value), (bad, str(e.value))
+    with pytest.raises(mk.MkError):
+        mk.chunk_attention(None, **ok)
+    with pytest.raises(mk.MkError):
+        mk.append_chunk(sh, ok["q"], [3], [5], ok["block_tables"], kv)
+    with pytest.raises(mk.MkError):
+        mk.read_cache(sh, [3], [5], ok["block_tables"], kv)
