@@ -16,11 +16,19 @@
 // tokens, as in decoding) runs two STREAMS instead: even and odd position tiles, each with its own
 // S, O, m and l, joined at the end.
 //
-// Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warps 8 and
-// 11: K and V loads.  Warp 9: issues the MMAs.  Warp 10: query rows and V tails.  Over a q8_0 cache warps 12-15 decode codes into fp16 operand tiles.  Blocks
-// are persistent (mk_chunk_plan.h): loads and scores of the next segment run under the epilogue of
-// this one.  Every wait is bounded: one that runs out raises the block's abort flag, every
-// role leaves its loop, copies in flight are let land and tensor memory is returned.
+// Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warps 8 and 11: K and V
+// loads.  Warp 9: issues the MMAs.  Warp 10: query rows and V tails.  Over a q8_0 cache warps 12-15
+// decode codes into fp16 operand tiles; sequences whose tiles many blocks would decode are decoded once
+// before (stage_kernel).  Blocks are persistent (mk_chunk_plan.h): loads and scores of the next segment
+// run under the epilogue of this one.  Every wait is bounded: one that runs out raises the block's abort
+// flag, every role leaves its loop, copies in flight are let land and tensor memory is returned.
+//
+// What bounds it.  Units of two tiles: 4 * 128^3 multiply-adds a position tile need 2048 tensor-core
+// cycles and as many of shared memory (192 KB of operands read, 64 KB written, at 128 B a cycle); about
+// 2800 are measured (8192-token prompt, 32 heads of 128: 342 us, 1.61 PFLOP/s; 2048 tokens behind
+// 30720: 635 us, 1.68).  Units of one tile: HBM, 160 KB of copies in flight a block (one token, 131072
+// positions: 49.5 us, 5.4 TB/s).  One-tile units over a q8_0 cache: the decode, 1300 cycles an
+// operand tile (one token, 262144 positions: 86 us).
 //
 // Operands.  bf16 cache: Q, K, V as they are, P rounded to bf16 (2^-8; its sum uses the unrounded
 // values).  q8_0 cache: fp16, whose 2^-11 keeps a decoded value three bits better than bf16 would
@@ -594,8 +602,8 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
 
 // --------------------------------------------------------------------------- MMAs (warp 9)
 // A wait that gives up does not leave the loops (their bounds stay uniform that way): in an aborted block
-// every later wait returns at once and the products are of whatever is there.  All of tensor memory is the block's, from column 0: S (and P, over it) of tile (stream) t at column
-// t * 128, O at 256 + t * D.
+// every later wait returns at once and the products are of whatever is there.  All of tensor memory is the
+// block's, from column 0: S (and P, over it) of tile (stream) t at column t * 128, O at 256 + t * D.
 template <int D, int M>
 __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* ctl) {
   using L = Layout<D, M>;
