@@ -57,8 +57,13 @@ namespace mk {
 namespace {
 
 // What the K and V operands come from: bf16 pages; q8_0 pages, decoded by the block; q8_0 pages that a
-// kernel before this one has decoded into the workspace (see stage_kernel).
-enum { kBf16, kQ8, kStaged };
+// kernel before this one has decoded into the workspace (see stage_kernel); q8_0 pages where every unit has
+// at most kFew rows (see softmax_few).
+enum { kBf16, kQ8, kStaged, kQ8Few };
+template <int M>
+constexpr bool kDecodes = M == kQ8 || M == kQ8Few;
+constexpr int kFew = 32;
+constexpr int kRawFew = 2;                     // raw stages of K and of V there
 
 constexpr int kRawBytes = kTile * (128 + 8);   // q8_0: the codes and scales of a K or V tile
 constexpr int kMasks = 8;           // tiles whose page masks are kept (more than can be in flight)
@@ -236,12 +241,12 @@ template <int D, int M>
 struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;           // one operand tile
   static constexpr int kGroup = D / 64 * 1024;               // 8 positions of a K or V tile
-  static constexpr int kRawStages = M == kQ8 ? 3 : 1;
-  static constexpr int kRaw = 2 * kTileBytes;                // behind the two Q tiles
-  static constexpr int kKv = (kRaw + (M == kQ8 ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
-  static constexpr int kStages = M == kQ8 ? 3 : D == 128 ? 5 : 8;
+  static constexpr int kRawStages = M == kQ8Few ? 2 * kRawFew : 3;
+  static constexpr int kRaw = (M == kQ8Few ? 1 : 2) * kTileBytes;   // behind the Q tiles
+  static constexpr int kKv = (kRaw + (kDecodes<M> ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
+  static constexpr int kStages = kDecodes<M> ? 3 : D == 128 ? 5 : 8;
   static constexpr int kCtl = kKv + kStages * kTileBytes;
-  static constexpr int kThreads = M == kQ8 ? 512 : 384;
+  static constexpr int kThreads = M == kQ8Few ? 640 : M == kQ8 ? 512 : 384;
 };
 
 struct Ctl {
@@ -259,11 +264,18 @@ struct Ctl {
 struct CtlQ8 : Ctl {
   float rowc[kTile];                 // two streams: the softmax's constant of each query row
 };
+struct CtlFew : CtlQ8 {
+  uint32_t raw_mask[2 * kRawFew];    // the page mask of a raw stage's tile
+  uint64_t shared[2];                // a warpgroup's parts of the output: written, read
+  float part[2][16][4][kFew];        // 16 columns of them: by column, warp and row
+};
 
 template <int D, int M>
-constexpr size_t smem_bytes() { return Layout<D, M>::kCtl + (M != kBf16 ? sizeof(CtlQ8) : sizeof(Ctl)); }
+constexpr size_t smem_bytes() {
+  return Layout<D, M>::kCtl + (M == kQ8Few ? sizeof(CtlFew) : M != kBf16 ? sizeof(CtlQ8) : sizeof(Ctl));
+}
 static_assert(smem_bytes<128, kBf16>() <= 232448 && smem_bytes<128, kQ8>() <= 232448 && smem_bytes<128, kStaged>() <= 232448 &&
-              smem_bytes<64, kBf16>() <= 232448, "");
+              smem_bytes<128, kQ8Few>() <= 232448 && smem_bytes<64, kBf16>() <= 232448, "");
 
 // Waits for the phase of `bar` with this parity, at most kWaitNs from the block's last sign of life in
 // exact_row; false once the block gives up.
@@ -440,11 +452,9 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
       const bool good = mine && page >= 0 && page < p.P;
       if (mine && pos < g.len && !good && p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
       const uint32_t ok = __ballot_sync(~0u, good);
-      if (only == 0) {
-        // a bit per 8 positions
-        const uint32_t mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
-        if (lane == 0) ctl->mask[jg % kMasks] = mask;
-      }
+      uint32_t mask = 0;                                       // a bit per 8 positions
+      if (only == 0 || M == kQ8Few) mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
+      if (only == 0 && lane == 0) ctl->mask[jg % kMasks] = mask;
       const uint32_t e = c0 + entry_of(g, only, j);
       if constexpr (M == kStaged) {
         // whole tiles of the workspace, their positions out of range or behind the sequence zeros already
@@ -466,16 +476,21 @@ __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl*
           tma_5d(base + L::kKv + st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map,
                  (g.kvh * p.ps + pos % p.ps) / 8, (good ? page : p.P) * 2 + only, bar);
       } else {
-        const uint32_t rs = e % L::kRawStages;
+        // one ring of raw stages by entries, or K's and V's by position tiles
+        const uint32_t ring = M == kQ8Few ? kRawFew : L::kRawStages, at = M == kQ8Few ? jg : e;
+        const uint32_t rs = at % ring + (M == kQ8Few ? only * kRawFew : 0);
         const uint32_t bar = smem_u32(&ctl->raw_full[rs]), dst = base + L::kRaw + rs * kRawBytes;
-        if (!mbar_wait(smem_u32(&ctl->raw_empty[rs]), ((e / L::kRawStages) & 1u) ^ 1u, ctl, p.status)) return;
-        if (lane == 0) mbar_expect(bar, __popc(ok) * r * 136);
+        if (!mbar_wait(smem_u32(&ctl->raw_empty[rs]), ((at / ring) & 1u) ^ 1u, ctl, p.status)) return;
+        if (lane == 0) {
+          if constexpr (M == kQ8Few) static_cast<CtlFew*>(ctl)->raw_mask[rs] = mask;
+          mbar_expect(bar, __popc(ok) * r * 136);
+        }
         __syncwarp();
         if (good) {
-          const size_t at = (static_cast<size_t>(page) * 2 + only) * p.plan.Hkv * p.ps +
+          const size_t line = (static_cast<size_t>(page) * 2 + only) * p.plan.Hkv * p.ps +
                             static_cast<size_t>(g.kvh) * p.ps + pos % p.ps;
-          bulk_g2s(dst + lane * r * 128, p.kv + at * 128, r * 128, bar);
-          bulk_g2s(dst + kTile * 128 + lane * r * 8, p.kv + p.code_bytes + at * 8, r * 8, bar);
+          bulk_g2s(dst + lane * r * 128, p.kv + line * 128, r * 128, bar);
+          bulk_g2s(dst + kTile * 128 + lane * r * 8, p.kv + p.code_bytes + line * 8, r * 8, bar);
         }
       }
     }
@@ -501,7 +516,13 @@ __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ct
   while (walk.next(p.plan, p.seqs, g)) {
     if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status)) return;
     ++k;
-    if (lane == 0) {
+    if (M == kQ8Few && lane == 0) {                // the rows four times, once for each warp of a warpgroup
+      const uint32_t bar = smem_u32(&ctl->qraw[0]), rows = kFew / p.plan.G * p.plan.G;
+      mbar_expect(bar, 4 * rows * D * 2);
+      for (int w = 0; w < 4; ++w)
+        for (int h = 0; h < D / 64; ++h)
+          tma_4d(base + h * kTile * 128 + w * kFew * 128, &p.qmap, h, g.kvh * p.plan.G, p.seqs.row0[g.s] + g.tok0, bar);
+    } else if (lane == 0) {
       for (int t = 0; t < (g.two ? 2 : 1); ++t) {
         const uint32_t bar = smem_u32(&ctl->qraw[t]);
         mbar_expect(bar, p.plan.TT * p.plan.G * D * 2);
@@ -531,9 +552,12 @@ __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ct
 // byte of 0x64.. the fp16 1024 + 128 + code; less 1152 that is the code exactly, times the scale
 // rounded once.  Positions of pages out of range or behind the sequence become zeros, values of a
 // scale above 515 (127 * 515 is what fp16 holds) NaN.
-template <int D>
-__device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* ctl) {
-  using L = Layout<D, kQ8>;
+//
+// kQ8Few has two groups of four warps: one decodes K tiles (group 0), one V tiles, each from raw stages of
+// its own.  They share the operand ring as the two loaders do over a bf16 cache, and by the same argument.
+template <int D, int M>
+__device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* ctl, int group) {
+  using L = Layout<D, M>;
   const int tid = threadIdx.x & 127;
   // A thread takes chunks x and x ^ 8 (8 codes, 16 bytes of operand each) of rows tid/8 + 16 i:
   // odd rows begin with the upper half, which keeps 8-byte reads and 16-byte writes free of conflicts.
@@ -541,60 +565,76 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
   constexpr int NR = kTile / 16;                    // rows of a thread
   // the four scales of a row to the pairs (d, d) of its chunks' blocks of 32: one permute each
   const uint32_t b0 = x >> 2, pick0 = 0x1010u + b0 * 0x2222u, pick1 = 0x1010u + (b0 ^ 2u) * 0x2222u;
-  Ring<L::kStages> ring;
-  Ring<L::kRawStages> raw;
+  const __half2 bias = __half2half2(__float2half_rn(1152.f));
+  // raw stage rs to operand stage st: a tile whose page mask is given and of which `left` positions are the sequence's
+  auto work = [&](uint32_t rs, uint32_t st, uint32_t mask, int left) {
+    // row0 + 16 i is in group 2 i + row0 / 8 of 8 rows, at row0 % 8 of it
+    const uint32_t src = base + L::kRaw + rs * kRawBytes + row0 * 128;
+    const uint32_t ssrc = base + L::kRaw + rs * kRawBytes + kTile * 128 + row0 * 8;
+    const uint32_t dst = base + L::kKv + st * L::kTileBytes + (row0 >> 3) * L::kGroup + (row0 & 7) * 128 +
+                         (((x & 7) ^ (row0 & 7)) << 4);
+    // every load before the first store: the stores are what a load would wait behind
+    uint32_t w[NR][4], sc[NR][2];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(src + i * 2048 + x * 8));
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][2]), "=r"(w[i][3]) : "r"(src + i * 2048 + (x ^ 8) * 8));
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(sc[i][0]), "=r"(sc[i][1]) : "r"(ssrc + i * 128));
+    }
+    // (kQ8Few: the loader may go on before the codes are worked on)
+    if constexpr (M == kQ8Few) warp_arrive(smem_u32(&ctl->raw_empty[rs]));
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const bool live = ((mask >> (2 * i + (row0 >> 3))) & 1u) && row0 + 16 * i < left;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t d = __byte_perm(sc[i][0], sc[i][1], c == 0 ? pick0 : pick1);
+        d = (d & 0x7fffu) > 0x6006u ? 0x7fff7fffu : d;
+        d = live ? d : 0u;
+        const __half2 dd = *reinterpret_cast<const __half2*>(&d);
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
+          uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
+          const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
+          const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
+          o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+          o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+        }
+        sts16(dst + i * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
+      }
+    }
+    if constexpr (M == kQ8) warp_arrive(smem_u32(&ctl->raw_empty[rs]));
+    fence_async_smem();
+    warp_arrive(smem_u32(&ctl->full[st]));
+  };
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
-  uint32_t jg = 0;
-  const __half2 bias = __half2half2(__float2half_rn(1152.f));
-  for (; walk.next(p.plan, p.seqs, g); jg += g.n) {
-    for (int i = 0; i < 2 * g.n; ++i) {
-      {
+  if constexpr (M == kQ8) {
+    Ring<L::kStages> ring;
+    Ring<L::kRawStages> raw;
+    uint32_t jg = 0;
+    for (; walk.next(p.plan, p.seqs, g); jg += g.n) {
+      for (int i = 0; i < 2 * g.n; ++i) {
         int v;
-        const int j = tile_of(g, i, v), left = g.len - (g.tile0 + j) * kTile;
+        const int j = tile_of(g, i, v);
         if (!mbar_wait(smem_u32(&ctl->raw_full[raw.st]), raw.ph, ctl, p.status)) return;
         if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
-        const uint32_t mask = ctl->mask[(jg + j) % kMasks];
-        // row0 + 16 i is in group 2 i + row0 / 8 of 8 rows, at row0 % 8 of it
-        const uint32_t src = base + L::kRaw + raw.st * kRawBytes + row0 * 128;
-        const uint32_t ssrc = base + L::kRaw + raw.st * kRawBytes + kTile * 128 + row0 * 8;
-        const uint32_t dst = base + L::kKv + ring.st * L::kTileBytes + (row0 >> 3) * L::kGroup + (row0 & 7) * 128 +
-                             (((x & 7) ^ (row0 & 7)) << 4);
-        // every load before the first store: the stores are what a load would wait behind
-        uint32_t w[NR][4], sc[NR][2];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(src + i * 2048 + x * 8));
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][2]), "=r"(w[i][3]) : "r"(src + i * 2048 + (x ^ 8) * 8));
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(sc[i][0]), "=r"(sc[i][1]) : "r"(ssrc + i * 128));
-        }
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const bool live = ((mask >> (2 * i + (row0 >> 3))) & 1u) && row0 + 16 * i < left;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t d = __byte_perm(sc[i][0], sc[i][1], c == 0 ? pick0 : pick1);
-            d = (d & 0x7fffu) > 0x6006u ? 0x7fff7fffu : d;
-            d = live ? d : 0u;
-            const __half2 dd = *reinterpret_cast<const __half2*>(&d);
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
-              uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
-              const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
-              const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
-              o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
-              o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
-            }
-            sts16(dst + i * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
-          }
-        }
-        warp_arrive(smem_u32(&ctl->raw_empty[raw.st]));
-        fence_async_smem();
-        warp_arrive(smem_u32(&ctl->full[ring.st]));
+        work(raw.st, ring.st, ctl->mask[(jg + j) % kMasks], g.len - (g.tile0 + j) * kTile);
         raw.step();
         ring.step();
+      }
+    }
+  } else {
+    Ring<kRawFew> raw;
+    for (uint32_t c0 = 0; walk.next(p.plan, p.seqs, g); c0 += 2 * g.n) {
+      for (int j = 0; j < g.n; ++j) {
+        const uint32_t e = c0 + entry_of(g, group, j), st = e % L::kStages, rs = raw.st + group * kRawFew;
+        if (!mbar_wait(smem_u32(&ctl->raw_full[rs]), raw.ph, ctl, p.status)) return;
+        if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
+        work(rs, st, static_cast<CtlFew*>(ctl)->raw_mask[rs], g.len - (g.tile0 + j) * kTile);
+        raw.step();
       }
     }
   }
@@ -717,31 +757,40 @@ __device__ __forceinline__ void issue(const AttnParams& p, uint32_t base, Ctl* c
 // --------------------------------------------------------------------------- softmax (warps 0-7)
 // q8_0: a thread's landed query row over 2^e as fp16, in place, e the exponent of its largest
 // magnitude; returns 2^e.  (Rows of the tile behind the unit's hold anything.)
-template <int D>
+template <int D, int B>
 __device__ __forceinline__ float convert_q(uint32_t tile, int row) {
   constexpr int CH = D / 8;
   auto at = [&](int ch) { return tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
-  uint32_t w[CH][4];
+  uint32_t w[B][4];                                // B chunks at a time (all of them, or read twice)
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int c = 0; c < B; ++c)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
+                   : "r"(at(c0 + c)));
+  };
   float mx = 0.f;
 #pragma unroll
-  for (int ch = 0; ch < CH; ++ch) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[ch][0]), "=r"(w[ch][1]), "=r"(w[ch][2]), "=r"(w[ch][3])
-                 : "r"(at(ch)));
+  for (int c0 = 0; c0 < CH; c0 += B) {
+    load(c0);
+#pragma unroll
+    for (int c = 0; c < B; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx = max3(mx, fabsf(bf_lo(w[c][k])), fabsf(bf_hi(w[c][k])));
   }
-#pragma unroll
-  for (int ch = 0; ch < CH; ++ch)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mx = max3(mx, fabsf(bf_lo(w[ch][k])), fabsf(bf_hi(w[ch][k])));
   int e = static_cast<int>(__float_as_uint(mx) >> 23);
   e = e == 0 || e == 255 ? 127 : e == 254 ? 253 : e;       // (zero rows; infinities end in exact_row)
   const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 #pragma unroll
-  for (int ch = 0; ch < CH; ++ch) {
-    uint32_t o[4];
+  for (int c0 = 0; c0 < CH; c0 += B) {
+    if (B < CH) load(c0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = f16x2(bf_lo(w[ch][k]) * down, bf_hi(w[ch][k]) * down);
-    sts16(at(ch), o[0], o[1], o[2], o[3]);
+    for (int c = 0; c < B; ++c) {
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = f16x2(bf_lo(w[c][k]) * down, bf_hi(w[c][k]) * down);
+      sts16(at(c0 + c), o[0], o[1], o[2], o[3]);
+    }
   }
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
@@ -769,7 +818,7 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
       if (!n.two && t == 1) return true;
       if (!mbar_wait(smem_u32(&ctl->qraw[t]), qr & 1, ctl, p.status)) return false;
       ++qr;
-      cq = p.c * convert_q<D>(base + t * Layout<D, M>::kTileBytes, row);
+      cq = p.c * convert_q<D, D / 8>(base + t * Layout<D, M>::kTileBytes, row);
       if (!n.two) static_cast<CtlQ8*>(ctl)->rowc[row] = cq;
       fence_async_smem();
       warp_arrive(smem_u32(&ctl->qbar[t]));
@@ -909,10 +958,11 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
       f[1] = b.x == -INFINITY ? 0.f : ex2(b.x - m);
       l = a.y * f[0] + b.y * f[1];
     }
+    const int urow = urow0 + row;
+    const int tok = urow * p.plan.by_G >> 16;
+    const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + urow - tok * p.plan.G;
+    bool odd = false;
     if (any) {
-      const int urow = urow0 + row;
-      const int tok = urow * p.plan.by_G >> 16;
-      const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + urow - tok * p.plan.G;
       // a partial is [D/4][urows] of 4 columns, then [urows] of (m, l): a warp's rows lie side by side
       float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(g.slot, 0)) * p.plan.urows * (D + 4));
       // Stores to the output: the four lanes of a quad trade 16-byte pieces, so that each store
@@ -922,7 +972,6 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
 #pragma unroll
       for (int e = 0; e < 4; ++e) row_off[e] = __shfl_sync(~0u, live ? static_cast<uint32_t>(r * p.Hq + h) : ~0u, e, 4);
       const float inv = l == 0.f ? 0.f : 1.0f / l;
-      bool odd = false;
       const int k0 = g.two ? 0 : t * (D / 2), k1 = g.two ? D : k0 + D / 2;
 #pragma unroll 1
       for (int k = k0; k < k1; k += 32) {
@@ -984,21 +1033,217 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
       }
       if (live && g.slot >= 0 && (g.two || t == 0))
         reinterpret_cast<float2*>(part + static_cast<size_t>(D / 4) * p.plan.urows)[urow] = make_float2(m, l);
-      // rows that are not finite, again from the cache (each warpgroup those it saw; where both see
-      // one they write the same)
-      if (g.slot < 0) {
-        for (uint32_t todo = __ballot_sync(~0u, odd && live); todo; todo &= todo - 1) {
-          const int who = __ffs(todo) - 1;
-          const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
-          __threadfence_block();
-          exact_row<D, M>(p, rr, hh, &ctl->beat);
-        }
-      }
     }
     // neither stream's next values may overwrite an output that the other warpgroup still reads
     if (!g.two) {
       tc_before();
       if (!join()) return;
+    }
+    // rows that are not finite, again from the cache, when both warpgroups' columns are written (where
+    // both see one they write the same)
+    if (g.slot < 0) {
+      for (uint32_t todo = __ballot_sync(~0u, odd && live); todo; todo &= todo - 1) {
+        const int who = __ffs(todo) - 1;
+        const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
+        __threadfence_block();
+        exact_row<D, M>(p, rr, hh, &ctl->beat);
+      }
+    }
+    ++seg;
+    g = next;
+  }
+}
+
+// Units of at most 32 rows over a q8_0 cache (single and speculative tokens).  A row's softmax is one warp's
+// work, and with rows in lanes 0-31 alone it is the same warp's, on the scheduler that the decode warps need
+// too: half of a position tile's time.  So the rows stand in all four warps' lanes, and warp w takes
+// positions 32 w .. 32 w + 31 of each tile: the others' weights are zeros in its lanes, whose O is the sum over its
+// own positions.  The eight parts of a row (two streams, four warps), each with its m and l, are
+// joined through shared memory.
+template <int D>
+__device__ __forceinline__ void softmax_few(const AttnParams& p, uint32_t base, Ctl* ctl) {
+  CtlFew* few = static_cast<CtlFew*>(ctl);
+  const int t = threadIdx.x >> 7, row = threadIdx.x & 127, lane = row & 31, warp = __shfl_sync(~0u, row >> 5, 0);
+  const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t ts = t * kTile + lane_base, to = 2 * kTile + lane_base;
+  constexpr float kBias = 6.f;                     // weights carry 2^kBias
+  SegmentWalk walk(p.plan, blockIdx.x);
+  Segment g, next;
+  bool have = walk.next(p.plan, p.seqs, g);
+  uint32_t phase = 0, jg = 0, seg = 0, joins = 0, meets = 0;
+  auto join = [&]() {                              // both warpgroups
+    warp_arrive(smem_u32(&ctl->join));
+    return mbar_wait(smem_u32(&ctl->join), joins++ & 1, ctl, p.status);
+  };
+  auto meet = [&]() {                              // this one
+    warp_arrive(smem_u32(&few->shared[t]));
+    return mbar_wait(smem_u32(&few->shared[t]), meets++ & 1, ctl, p.status);
+  };
+  uint32_t taken = 0;
+  float cq = p.c;                                  // the row's constant
+  auto take_q = [&]() {
+    if (!mbar_wait(smem_u32(&ctl->qraw[0]), taken++ & 1, ctl, p.status)) return false;
+    cq = p.c * convert_q<D, 4>(base, row);
+    few->rowc[row] = cq;
+    fence_async_smem();
+    warp_arrive(smem_u32(&ctl->qbar[0]));
+    return true;
+  };
+  if (have && t == 0 && !take_q()) return;
+  while (have) {
+    const int rows = g.ntok * p.plan.G, tok = lane * p.plan.by_G >> 16;
+    const bool live = lane < rows;
+    // rows behind the last see everything, so that they never ask for a mask
+    const int pos = live ? g.pos0 + tok : INT32_MAX;
+    const int mine = (g.n - t + 1) / 2;
+    float c = cq;
+    if (t == 1 && mine > 0) {                      // stream 1 takes the constants of stream 0's rows
+      if (!mbar_wait(smem_u32(&ctl->qbar[0]), seg & 1, ctl, p.status)) return;
+      c = few->rowc[row];
+    }
+    const float grow = 8.0f / c;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < mine; ++i) {
+      const int j = 2 * i + t;
+      const int limit = pos - (g.tile0 + j) * kTile - 32 * warp;   // last of its 32 columns this row sees
+      const bool edge = __any_sync(~0u, limit < 31);
+      if (!mbar_wait(smem_u32(&ctl->sfull[t]), phase & 1, ctl, p.status)) return;
+      ++phase;
+      tc_after();
+      const uint32_t mask = ctl->mask[(jg + j) % kMasks] >> (4 * warp) & 15u;
+      float s[32];
+      tc_ld32(ts + 32 * warp, s);
+      tc_wait_ld();
+      if (edge) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (k > limit) s[k] = -INFINITY;
+      }
+      if (mask != 15u) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (!((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int k = 4; k < 28; k += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[k + e], s[k + 4 + e]);
+      }
+      const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], s[28], s[29]), fmaxf(s[30], s[31]));
+      if (i == 0) {
+        m = top;
+      } else {
+        const bool up = top > m + grow;            // (as in softmax)
+        if (__any_sync(~0u, up)) {
+          const float mn = up ? top : m;
+          const float f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+          l *= f;
+          m = mn;
+          const float2 ff = make_float2(f, f);
+#pragma unroll 1
+          for (int k = 0; k < D; k += 16) {
+            float o[16];
+            tc_ld16(to + t * D + k, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 x = mul2(make_float2(o[e], o[e + 1]), ff);
+              o[e] = x.x;
+              o[e + 1] = x.y;
+            }
+            tc_st16(to + t * D + k, o);
+          }
+        }
+      }
+      const float mb = m == -INFINITY ? 0.f : kBias - m * c;
+      const float2 cc = make_float2(c, c), mm = make_float2(mb, mb);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t w[16], none[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float2 x = fma2(make_float2(s[2 * k], s[2 * k + 1]), cc, mm);
+        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+        sum[k & 1] = add2(sum[k & 1], y);
+        w[k] = f16x2(y.x, y.y);
+        none[k] = 0u;
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (h == warp) tc_st16(ts + h * 16, w);
+        else tc_st16(ts + h * 16, none);
+      }
+      tc_wait_st();
+      tc_before();
+      warp_arrive(smem_u32(&ctl->pfull[t][0]));
+      warp_arrive(smem_u32(&ctl->pfull[t][1]));
+      const float2 sm = add2(sum[0], sum[1]);
+      l += sm.x + sm.y;
+    }
+    if (!mbar_wait(smem_u32(&ctl->ofull), seg & 1, ctl, p.status)) return;
+    tc_after();
+    jg += g.n;
+    have = walk.next(p.plan, p.seqs, next);
+    if (have && t == 0 && !take_q()) return;
+
+    // m and l in powers of two; a part without a position has m = -inf and l = 0
+    ctl->ml[t][row] = make_float2(m == -INFINITY ? m : m * c, l);
+    if (!join()) return;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, ctl->ml[e >> 2][(e & 3) * 32 + lane].x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 a = ctl->ml[e >> 2][(e & 3) * 32 + lane];
+      l += a.x == -INFINITY ? 0.f : a.y * ex2(a.x - m);
+    }
+    const float m0 = ctl->ml[0][row].x, m1 = ctl->ml[1][row].x;
+    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+    const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + lane - tok * p.plan.G;
+    float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(g.slot, 0)) * p.plan.urows * (D + 4));
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    bool odd = false;
+    // each warpgroup half of the columns, 16 at a time, of which each warp sums up 4
+#pragma unroll 1
+    for (int k = t * (D / 2); k < (t + 1) * (D / 2); k += 16) {
+      float x[16], y[16];
+      tc_ld16(to + k, x);
+      if (g.n > 1) tc_ld16(to + D + k, y);
+      tc_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) few->part[t][e][warp][lane] = g.n > 1 ? x[e] * f0 + y[e] * f1 : x[e] * f0;
+      if (!meet()) return;
+      float o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float(*a)[kFew] = few->part[t][4 * warp + e];
+        o[e] = a[0][lane] + a[1][lane] + (a[2][lane] + a[3][lane]);
+      }
+      if (!meet()) return;
+      const int col = k + 4 * warp;
+      if (live && g.slot >= 0) {
+        part[static_cast<size_t>(col / 4) * p.plan.urows + lane] = make_float4(o[0], o[1], o[2], o[3]);
+      } else if (live) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e] *= inv;
+          odd |= !(fabsf(o[e]) <= 3.3e38f);
+        }
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + col) =
+            make_uint2(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]));
+      }
+    }
+    if (live && g.slot >= 0 && t == 0 && warp == 0)
+      reinterpret_cast<float2*>(part + static_cast<size_t>(D / 4) * p.plan.urows)[lane] = make_float2(m, l);
+    // neither stream's next values may overwrite an output that the other warpgroup still reads
+    tc_before();
+    __threadfence_block();
+    if (!join()) return;
+    // rows that are not finite, again from the cache (where two warps see one they write the same)
+    for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
+      const int who = __ffs(todo) - 1;
+      exact_row<D, kQ8Few>(p, __shfl_sync(~0u, r, who), __shfl_sync(~0u, h, who), &ctl->beat);
     }
     ++seg;
     g = next;
@@ -1018,7 +1263,7 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {                   // (q8_0: a K or V tile is the decode warps' work)
-      mbar_init(smem_u32(&ctl->full[i]), M == kQ8 ? 4 : 1);
+      mbar_init(smem_u32(&ctl->full[i]), kDecodes<M> ? 4 : 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
       mbar_init(smem_u32(&ctl->raw_full[i]), 1);
       mbar_init(smem_u32(&ctl->raw_empty[i]), 4);
@@ -1035,6 +1280,8 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
     mbar_init(smem_u32(&ctl->trim), 1);
     mbar_init(smem_u32(&ctl->ofull), 1);
     mbar_init(smem_u32(&ctl->join), 8);
+    if constexpr (M == kQ8Few)
+      for (int t = 0; t < 2; ++t) mbar_init(smem_u32(&static_cast<CtlFew*>(ctl)->shared[t]), 4);
     ctl->abort = 0u;
     ctl->beat = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1055,18 +1302,24 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
   }
   // registers follow the work: a softmax thread holds a row of S (the warpgroups' sum is the launch's)
   if (warp < 8) {
-    if constexpr (M == kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    softmax<D, M>(p, base, ctl);
+    if constexpr (M == kQ8Few) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+      softmax_few<D>(p, base, ctl);
+    } else {
+      if constexpr (M == kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      softmax<D, M>(p, base, ctl);
+    }
   } else if (warp < 12) {
-    if constexpr (M == kQ8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kDecodes<M>) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8 || warp == 11) produce<D, M>(p, base, ctl, warp == 8 ? 0 : 1);
     if (warp == 9) issue<D, M>(p, base, ctl);
     if (warp == 10) produce_q<D, M>(p, base, ctl);
-  } else if constexpr (M == kQ8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    decode<D>(p, base, ctl);
+  } else if constexpr (kDecodes<M>) {
+    if constexpr (M == kQ8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    decode<D, M>(p, base, ctl, (warp - 12) >> 2);
   }
   __syncwarp();
   tc_before();
@@ -1168,6 +1421,7 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
         make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
   const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
   const bool odd = live && (!(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
+  if constexpr (!WIDE) __syncthreads();            // (a row's columns are several warps')
   uint32_t done = 0;
   for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1;
@@ -1308,13 +1562,13 @@ int encode_pages(int D_, int heads, int page_size, int pages, bool bf16, const v
 
 // Query rows to TMA: {64 dims, D/64 spans, heads, rows}; a box of TT rows x G heads lands as a tile's
 // [row][128 B], rows behind the call's as zeros.
-int encode_queries(const mk_cache_shape& c, const AttnPlan& pl, const void* q, int64_t stride, int rows, CUtensorMap* out) {
+int encode_queries(const mk_cache_shape& c, int G, int tokens, const void* q, int64_t stride, int rows, CUtensorMap* out) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
   if (!encode) return chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t D = c.head_dim;
   const cuuint64_t dims[4] = {64, D / 64, static_cast<cuuint64_t>(c.num_q_heads), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[3] = {128, D * 2, static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(pl.G), static_cast<cuuint32_t>(pl.TT)};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1339,12 +1593,13 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   attn_kernel<D, M><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.plan.cuts == 0) return e;
+  constexpr int kMerge = M == kBf16 ? kBf16 : kQ8;
   // (plans with units of two tiles cut an item in few parts)
   if (p.plan.urows <= kTile / 2) {
     constexpr int kRows = 128 / D;
-    merge_kernel<D, M, true><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
+    merge_kernel<D, kMerge, true><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
   } else {
-    merge_kernel<D, M, false><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
+    merge_kernel<D, kMerge, false><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
   }
   return cudaGetLastError();
 }
@@ -1407,20 +1662,25 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   p.P = c.num_pages;
   p.maxpg = c.max_pages_per_seq;
   p.c = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));
-  rc = encode_queries(c, plan.direct, q, q_stride, rows, &p.qmap);
-  if (rc) return rc;
   cudaError_t e = cudaSuccess;
   if (plan.direct.items > 0) {
     p.plan = plan.direct;
+    const bool few = q8 && p.plan.urows <= kFew;
+    rc = encode_queries(c, p.plan.G, few ? kFew / p.plan.G : p.plan.TT, q, q_stride, rows, &p.qmap);
+    if (rc) return rc;
     if (!q8) {
       rc = encode_pages(c.head_dim, c.num_kv_heads, c.page_size, c.num_pages, true, kv_layer, p.box, &p.map);
       if (rc) return rc;
     }
-    e = q8 ? launch<128, kQ8>(p, st) : c.head_dim == 128 ? launch<128, kBf16>(p, st) : launch<64, kBf16>(p, st);
+    e = few                 ? launch<128, kQ8Few>(p, st)
+        : q8                ? launch<128, kQ8>(p, st)
+        : c.head_dim == 128 ? launch<128, kBf16>(p, st)
+                            : launch<64, kBf16>(p, st);
   }
   if (e == cudaSuccess && plan.staged.items > 0) {
     p.plan = plan.staged;
-    rc = encode_pages(128, c.num_kv_heads, kTile, plan.tiles.first[plan.tiles.n], false, workspace, kTile, &p.map);
+    rc = encode_queries(c, p.plan.G, p.plan.TT, q, q_stride, rows, &p.qmap);
+    if (!rc) rc = encode_pages(128, c.num_kv_heads, kTile, plan.tiles.first[plan.tiles.n], false, workspace, kTile, &p.map);
     if (rc) return rc;
     stage_kernel<128><<<dim3(plan.tiles.first[plan.tiles.n], 2 * c.num_kv_heads), kStageThreads, 0, st>>>(
         p, static_cast<__half*>(workspace), plan.tiles);
