@@ -27,8 +27,9 @@
 // cycles and as many of shared memory (192 KB of operands read, 64 KB written, at 128 B a cycle); about
 // 2800 are measured (8192-token prompt, 32 heads of 128: 342 us, 1.61 PFLOP/s; 2048 tokens behind
 // 30720: 635 us, 1.68).  Units of one tile: HBM, 160 KB of copies in flight a block (one token, 131072
-// positions: 49.5 us, 5.4 TB/s).  One-tile units over a q8_0 cache: the decode, 1300 cycles an
-// operand tile (one token, 262144 positions: 86 us).
+// positions: 49.5 us, 5.4 TB/s).  Few rows over a q8_0 cache: the decode, whose two products and byte
+// permute per two codes take the half-precision pipe as long as the copies take HBM (one token, 262144
+// positions: 71.9 us; without the two products 61, without any work 56).
 //
 // Operands.  bf16 cache: Q, K, V as they are, P rounded to bf16 (2^-8; its sum uses the unrounded
 // values).  q8_0 cache: fp16, whose 2^-11 keeps a decoded value three bits better than bf16 would
@@ -52,6 +53,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 namespace mk {
 namespace {
@@ -583,28 +585,45 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
     }
     // (kQ8Few: the loader may go on before the codes are worked on)
     if constexpr (M == kQ8Few) warp_arrive(smem_u32(&ctl->raw_empty[rs]));
+    // Most tiles need neither zeros nor NaN: every position is the sequence's, and no scale has the top bit of its
+    // exponent (is 2 or more).  A warp that sees so leaves the tests out, a third of its instructions (one
+    // token at 262144: 81.3 -> 71.9 us).  With units of more rows it is not the decode that they wait for.
+    auto convert = [&](auto all) {
+      constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const bool live = ((mask >> (2 * i + (row0 >> 3))) & 1u) && row0 + 16 * i < left;
+      for (int i = 0; i < NR; ++i) {
+        const bool live = ALL || (((mask >> (2 * i + (row0 >> 3))) & 1u) && row0 + 16 * i < left);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t d = __byte_perm(sc[i][0], sc[i][1], c == 0 ? pick0 : pick1);
-        d = (d & 0x7fffu) > 0x6006u ? 0x7fff7fffu : d;
-        d = live ? d : 0u;
-        const __half2 dd = *reinterpret_cast<const __half2*>(&d);
-        uint32_t o[4];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t d = __byte_perm(sc[i][0], sc[i][1], c == 0 ? pick0 : pick1);
+          if constexpr (!ALL) {
+            d = (d & 0x7fffu) > 0x6006u ? 0x7fff7fffu : d;
+            d = live ? d : 0u;
+          }
+          const __half2 dd = *reinterpret_cast<const __half2*>(&d);
+          uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
-          uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
-          const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
-          const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
-          o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
-          o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t v = w[i][2 * c + k] ^ 0x80808080u;
+            uint32_t a = __byte_perm(v, 0x64646464u, 0x4140), b = __byte_perm(v, 0x64646464u, 0x4342);
+            const __half2 ha = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), bias), dd);
+            const __half2 hb = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), bias), dd);
+            o[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+            o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+          }
+          sts16(dst + i * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
         }
-        sts16(dst + i * 2 * L::kGroup + (((x >> 3) ^ c) << 10), o[0], o[1], o[2], o[3]);
       }
+    };
+    bool plain = false;
+    if constexpr (M == kQ8Few) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) top |= sc[i][0] | sc[i][1];
+      plain = mask == 0xffffu && left >= kTile && !__any_sync(~0u, (top & 0x40004000u) != 0u);
     }
+    if (plain) convert(std::true_type());
+    else convert(std::false_type());
     if constexpr (M == kQ8) warp_arrive(smem_u32(&ctl->raw_empty[rs]));
     fence_async_smem();
     warp_arrive(smem_u32(&ctl->full[st]));
@@ -1059,7 +1078,8 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
 // too: half of a position tile's time.  So the rows stand in all four warps' lanes, and warp w takes
 // positions 32 w .. 32 w + 31 of each tile: the others' weights are zeros in its lanes, whose O is the sum over its
 // own positions.  The eight parts of a row (two streams, four warps), each with its m and l, are
-// joined through shared memory.
+// joined through shared memory.  (One token at 262144 positions, with the two groups of decode warps that the
+// saved registers pay for: 87.0 -> 81.3 us.)
 template <int D>
 __device__ __forceinline__ void softmax_few(const AttnParams& p, uint32_t base, Ctl* ctl) {
   CtlFew* few = static_cast<CtlFew*>(ctl);

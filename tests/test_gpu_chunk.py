@@ -337,6 +337,53 @@ def test_attention_q8_sequences_of_many_rows_and_of_few():
     assert torch.all(far <= bound), float((far / bound).max())
 
 
+# q8_0 units of at most 32 rows stand in each warp's lanes once: group sizes and tokens on both sides of that,
+# contexts on both sides of a tile's quarters, split over blocks and whole
+@pytest.mark.parametrize("hq,hkv,new", [(8, 1, 1), (8, 1, 4), (8, 1, 5), (3, 1, 10), (3, 1, 11), (10, 2, 6), (14, 2, 4), (2, 2, 32),
+                                        (2, 2, 33), (2, 1, 16), (24, 4, 5)])
+def test_attention_q8_few_rows(hq, hkv, new):
+    lens = [new, max(new, 31), max(new, 33), max(new, 97), 128, 129, 160 + new, 2000, 9000]
+    check_attention(R.Setup(hq, hkv, 128, 24, lens, [new] * len(lens), q8=True, seed=26), extra_rows=1)
+
+
+def test_attention_q8_few_rows_large_scales_and_lost_pages():
+    # scales on both sides of 2 and of what fp16 holds, in other quarters of other tiles; pages out of range, a whole
+    # quarter's (32 positions) and a whole tile's among them
+    lens, news = [1500, 130, 700], [2, 1, 3]
+    st = R.Setup(8, 2, 128, 16, lens, news, q8=True, seed=27)
+    codes, scales = st.planes()
+    for s, pos, which, sc in ((0, 40, 0, 1.9990), (0, 300, 0, 2.0), (0, 301, 1, 511.0), (0, 900, 1, 520.0), (0, 1499, 0, 65504.0),
+                              (1, 129, 1, 3.0), (2, 5, 0, 2.0)):
+        scales[st.bt[s, pos // 16].long(), which, :, pos % 16, 3] = sc
+    drop = torch.zeros(3, 1500, dtype=torch.bool, device="cuda")
+    good, bad = st.bt.clone(), st.bt.clone()
+    for s, p in [(0, 2), (0, 3), (0, 50), (1, 0), (1, 7)] + [(2, p) for p in range(8, 16)]:
+        drop[s, p * 16:p * 16 + 16] = True
+        bad[s, p] = st.P + p
+    q = st.normal(st.rows, 8, 128, std=0.02)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = mk.chunk_attention(st.shape(mk), q, news, lens, bad, st.kv, status=status)
+    assert int(status) == mk.MK_ERR_DEVICE_BOUNDS
+    st.bt = good
+    ref, *scale = R.attention(st, q, st.kv, drop)
+    far, bound = (out.double() - ref).abs(), R.attention_bound(ref, *scale, True)
+    assert torch.all(far <= bound), float((far / bound).max())
+
+
+def test_attention_q8_few_rows_rising_scores():
+    # every later key scores higher than all before: each quarter's maximum moves with every tile
+    st = R.Setup(8, 1, 128, 16, [2000], [3], q8=True, seed=28)
+    codes, scales = st.planes()
+    pos = torch.arange(2000, device="cuda")
+    page, off = st.bt[0, pos // 16].long(), pos % 16
+    codes[page, 0, 0, off] = 0
+    codes[page, 0, 0, off, 0] = 100
+    scales[page, 0, 0, off, 0] = (pos * 0.0008).to(torch.float16)
+    q = st.normal(3, 8, 128)
+    q[..., 0] = 4.0
+    check_attention(st, q=q)
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_attention_queries_of_any_magnitude(q8):
     # rows scaled by powers of two from 2^-100 to 2^100 against keys scaled the other way
