@@ -389,7 +389,8 @@ def _on(stream, kv_layer, call, *args):
 
 def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, rope: Rope | None = None,
                  q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, status=None, stream=None):
-    """Take the fused QKV rows of new tokens into the cache (``mk_append_chunk``).
+    """Take the fused QKV rows of new tokens into the cache (``mk_append_chunk``).  Forward only, as all
+    of these calls: nothing is recorded for autograd.
 
     qkv: bf16 CUDA [rows, (Hq + 2*Hkv)*D] (rows may be strided); chunk_lens / seq_lens: host int32
     [num_seqs], new tokens and length including them; block_tables: int32 CUDA [num_seqs,

@@ -3,7 +3,8 @@
 // outputs, takes the current stream of the cache's device and calls the C ABI; nothing else.
 //
 // These calls are short next to what Python spends on marshalling: for a few tokens the device needs
-// 3 to 8 us, and the same checks written in Python with ctypes took 12 us a call.
+// 3 to 8 us, and the same checks written in Python with ctypes took about 10 us more a call (attention of a
+// prompt of 65 tokens 17.9 us, now 8.4; 8 tokens appended 22.2, now 9.9).
 
 #define PY_SSIZE_T_CLEAN
 #include <ATen/ATen.h>
@@ -30,7 +31,8 @@ struct {
   decltype(&mk_last_error) last_error;
 } g_mk = {};
 
-// Other Python threads run while a call launches: a launch waits when the device's queue is full.
+// Other Python threads run while a call launches or allocates: a launch waits when the device's queue is
+// full, an allocation for the allocator's lock, whose holder may want the interpreter's.
 struct Unlocked {
   PyThreadState* s = PyEval_SaveThread();
   ~Unlocked() { PyEval_RestoreThread(s); }
@@ -180,11 +182,15 @@ struct Call {
          what);
     return t.size(0) > 1 ? t.stride(0) : heads * D;
   }
+  at::Tensor make(at::IntArrayRef size, at::ScalarType type) const {
+    Unlocked u;
+    return at::empty(size, kv.options().dtype(type));
+  }
   at::Tensor out(PyObject* o, int64_t heads, const char* what) const {
     const int64_t D = shape.head_dim;
     if (o == Py_None) {
       need(heads > 0 && D > 0 && heads <= (int64_t(1) << 20) && D <= 4096, "shape: heads or head_dim out of range");
-      return at::empty({rows, heads, D}, kv.options().dtype(at::kBFloat16));
+      return make({rows, heads, D}, at::kBFloat16);
     }
     const at::Tensor& t = tensor(o, what);
     need(bf16(t) && t.is_contiguous() && t.dim() == 3 && t.size(0) >= rows && t.size(1) == heads && t.size(2) == D, what);
@@ -266,7 +272,7 @@ PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       size_t bytes = 0;
       run([&] { return g_mk.workspace(&c.shape, c.n(), c.chunk.v, c.len.v, &bytes); });
-      if (bytes) ws = at::empty({static_cast<int64_t>(bytes)}, c.kv.options().dtype(at::kByte));
+      if (bytes) ws = c.make({static_cast<int64_t>(bytes)}, at::kByte);
     }
     const mk_stream_t on = c.stream();
     run([&] {

@@ -18,8 +18,8 @@
 //
 // Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warps 8 and 11: K and V
 // loads.  Warp 9: issues the MMAs.  Warp 10: query rows and V tails.  Over a q8_0 cache warps 12-15
-// decode codes into fp16 operand tiles; sequences whose tiles many blocks would decode are decoded once
-// before (stage_kernel).  Blocks are persistent (mk_chunk_plan.h): loads and scores of the next segment
+// decode codes into fp16 operand tiles (units of at most 32 rows: two groups, warps 12-15 K and 16-19 V);
+// sequences whose tiles many blocks would decode are decoded once before (stage_kernel).  Blocks are persistent (mk_chunk_plan.h): loads and scores of the next segment
 // run under the epilogue of this one.  Every wait is bounded: one that runs out raises the block's abort
 // flag, every role leaves its loop, copies in flight are let land and tensor memory is returned.
 //
