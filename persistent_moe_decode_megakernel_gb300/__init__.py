@@ -403,11 +403,19 @@ def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_
     return _native().append_chunk(*args) if stream is None else _on(stream, kv_layer, _native().append_chunk, *args)
 
 
+def _lengths(chunk_lens, seq_lens):
+    both = [np.asarray(x) for x in (chunk_lens, seq_lens)]
+    if both[0].ndim != 1 or both[0].shape != both[1].shape:
+        raise MkError(MK_ERR_INVALID_ARG, "chunk_lens and seq_lens: one length per sequence each")
+    i32 = np.iinfo(np.int32)
+    if any(x.size and (x.dtype.kind not in "iu" or x.min() < i32.min or x.max() > i32.max) for x in both):
+        raise MkError(MK_ERR_INVALID_ARG, "chunk_lens and seq_lens: whole numbers of 32 bits")
+    return [np.ascontiguousarray(x, dtype=np.int32) for x in both]
+
+
 def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
     """Bytes of workspace :func:`chunk_attention` needs for these lengths (0: none)."""
-    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
-    if cl.ndim != 1 or cl.shape != sl.shape:
-        raise MkError(MK_ERR_INVALID_ARG, "chunk_lens and seq_lens: one length per sequence each")
+    cl, sl = _lengths(chunk_lens, seq_lens)
     need = ctypes.c_size_t()
     _check(lib().mk_chunk_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
                                               ctypes.byref(need)))
@@ -416,7 +424,7 @@ def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
 
 def plan_chunk_attention(shape: CacheShape, chunk_lens, seq_lens) -> np.ndarray:
     """The schedule of :func:`chunk_attention` (``mk_plan_chunk_attention``): int32 [segments, 9]."""
-    cl, sl = np.ascontiguousarray(chunk_lens, dtype=np.int32), np.ascontiguousarray(seq_lens, dtype=np.int32)
+    cl, sl = _lengths(chunk_lens, seq_lens)
     n = ctypes.c_int32()
     _check(lib().mk_plan_chunk_attention(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, None, 0,
                                          ctypes.byref(n)))

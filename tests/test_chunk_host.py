@@ -244,3 +244,13 @@ def test_binding_refuses_on_the_host():
         mk.append_chunk(sh, ok["q"], [3], [5], ok["block_tables"], kv)
     with pytest.raises(mk.MkError):
         mk.read_cache(sh, [3], [5], ok["block_tables"], kv)
+
+
+@pytest.mark.parametrize("call", [mk.chunk_attention_workspace, mk.plan_chunk_attention])
+def test_plan_and_workspace_refuse_lengths(call):
+    sh = mk.CacheShape(8, 2, 128, 16, 8, 4, 0)
+    for cl, sl in (([3, 1], [5]), ([3], [5, 5]), ([[3]], [[5]]), ([3.0], [5]), ([3], [5.5]), ([3], [1 << 40]), ([], []), ([6], [5])):
+        with pytest.raises(mk.MkError) as e:
+            call(sh, cl, sl)
+        assert e.value.code == mk.MK_ERR_INVALID_ARG
+    call(sh, np.array([3, 0, 3, 0])[::2], (5, 5))
