@@ -464,6 +464,30 @@ def test_repeats_are_bit_identical_on_any_stream_and_in_graphs(q8):
     assert torch.equal(bits(st.kv), bits(kv2)) and torch.equal(bits(st.kv), bits(kv3))
 
 
+def test_calls_of_several_threads():
+    # each thread on a stream of its own, over its own cache type and rows, again and again: the first answers
+    import threading
+    cases = [R.Setup(8, 2, 128, 16, [3000, 129], [1, 1], q8=True, seed=30), R.Setup(8, 2, 128, 16, [3000, 129], [1, 1], seed=31),
+             R.Setup(8, 2, 128, 16, [700, 5], [300, 5], q8=True, seed=32), R.Setup(4, 2, 64, 16, [700, 5], [300, 5], seed=33)]
+    args = [(st.shape(mk), st.normal(st.rows, st.hq, st.d), st.news, st.lens, st.bt, st.kv) for st in cases]
+    want = [mk.chunk_attention(*a) for a in args]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        outs = [mk.chunk_attention(*args[i], stream=stream) for _ in range(20)]
+        stream.synchronize()
+        wrong.extend(i for o in outs if not torch.equal(o, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_no_rows_and_reused_outputs():
     st = R.Setup(8, 2, 128, 16, [40, 5], [0, 0], seed=22)
     status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
