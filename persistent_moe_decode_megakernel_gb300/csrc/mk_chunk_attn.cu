@@ -25,8 +25,8 @@
 //
 // What bounds it.  Units of two tiles: 4 * 128^3 multiply-adds a position tile need 2048 tensor-core
 // cycles and as many of shared memory (192 KB of operands read, 64 KB written, at 128 B a cycle); about
-// 2800 are measured (8192-token prompt, 32 heads of 128: 342 us, 1.61 PFLOP/s; 2048 tokens behind
-// 30720: 635 us, 1.68).  Units of one tile: HBM, 160 KB of copies in flight a block (one token, 131072
+// 2800 are measured (8192-token prompt, 32 heads of 128: 342 us, 1.61 PFLOP/s; the last 2048 of
+// 32768 tokens: 635 us, 1.68).  Units of one tile: HBM, 160 KB of copies in flight a block (one token, 131072
 // positions: 49.5 us, 5.4 TB/s).  Few rows over a q8_0 cache: the decode, whose two products and byte
 // permute per two codes take the half-precision pipe as long as the copies take HBM (one token, 262144
 // positions: 71.9 us; without the two products 61, without any work 56).
