@@ -94,8 +94,10 @@ int mk_rope_frequencies(int32_t rotary_dim, double theta, double factor, int32_t
  *                of q / of k, before the rotation
  *   q_out:       device bf16 [rows][num_q_heads][head_dim], the query rows mk_chunk_attention takes
  * k (normed and rotated) and v are written to their positions of kv_layer: as bf16, or quantized
- * from their fp32 values as MK_FLAG_KV_Q8 describes.  Everything is computed in fp32 (the angle
- * of far positions exactly reduced) and rounded once.  A row whose page is out of range writes
+ * from their fp32 values as MK_FLAG_KV_Q8 describes.  What is not finite stays so: a bf16 value as
+ * it is, a q8_0 block of 32 with a NaN or an infinity among its values gets a NaN or infinite scale, so
+ * that none of it reads back as finite (the step's own quantizer passes over a NaN).  Everything
+ * is computed in fp32 (the angle of far positions exactly reduced) and rounded once.  A row whose page is out of range writes
  * q_out but no k or v.  Two rows must not write one position (pages shared by two sequences
  * may be read, not appended to).  qkv, q_out and kv_layer must not overlap.
  */

@@ -108,6 +108,12 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
+// the larger one, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint32_t u[4];
 #pragma unroll
@@ -263,20 +269,21 @@ __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ 
       *reinterpret_cast<uint4*>(dst + 8 * ca) = pack8(a);
       *reinterpret_cast<uint4*>(dst + 8 * cb) = pack8(b);
     } else {
-      // the largest magnitude of each 32-value block over the head's lanes
+      // the largest magnitude of each 32-value block over the head's lanes; a NaN is the largest, and so the
+      // block's scale: all of it is then NaN, whatever the codes (under an infinite scale none is finite)
       float m[4] = {0.f, 0.f, 0.f, 0.f};
       float ma = 0.f, mb = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        ma = fmaxf(ma, fabsf(a[i]));
-        mb = fmaxf(mb, fabsf(b[i]));
+        ma = max_nan(ma, fabsf(a[i]));
+        mb = max_nan(mb, fabsf(b[i]));
       }
       const uint32_t mask = ((1u << LH) - 1u) << (lane / LH * LH);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        m[k] = fmaxf(ca / 4 == k ? ma : 0.f, cb / 4 == k ? mb : 0.f);
+        m[k] = max_nan(ca / 4 == k ? ma : 0.f, cb / 4 == k ? mb : 0.f);
 #pragma unroll
-        for (int o = 1; o < LH; o <<= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(mask, m[k], o));
+        for (int o = 1; o < LH; o <<= 1) m[k] = max_nan(m[k], __shfl_xor_sync(mask, m[k], o));
       }
       // the step's quantizer: d = max/127 in fp32, codes by its fp32 reciprocal (ties away from
       // zero), d stored as f16

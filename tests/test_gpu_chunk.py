@@ -595,3 +595,51 @@ def test_prefill_then_decode_step(q8):
     errs = check_rows(got, ref)
     print("prefill + step: rel L2", errs)
     eng.close()
+
+
+# ---------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("rot,norm", [(0, False), (128, False), (128, True)])
+def test_append_keeps_what_is_not_finite(rot, norm, value, q8):
+    # one value of one row's k, of another's v and of a third's q: no cached block of 32 (bf16: no value) that it
+    # is part of reads back as finite, and every other is what it is without it
+    st = R.Setup(4, 2, 128, 16, [70], [70], q8=q8, seed=34)
+    qkv, rope, _, gains = append_case(st, rot, False, norm)
+    sh = st.shape(mk)
+    args = dict(rope=rope, q_norm=gains[0], k_norm=gains[1])
+    q1 = mk.append_chunk(sh, qkv, [70], [70], st.bt, st.kv, **args)
+    k1, v1 = mk.read_cache(sh, [70], [70], st.bt, st.kv)
+    bad = qkv.clone()
+    bad[3, (4 + 1) * 128 + 37] = float(value)        # k head 1 of row 3
+    bad[20, (4 + 2) * 128 + 100] = float(value)      # v head 0 of row 20
+    bad[41, 2 * 128 + 64] = float(value)             # q head 2 of row 41
+    q2 = mk.append_chunk(sh, bad, [70], [70], st.bt, st.kv, **args)
+    k2, v2 = mk.read_cache(sh, [70], [70], st.bt, st.kv)
+    # dims that the value reaches: itself, with a rotation its pair, with a norm the head (an infinity: its own
+    # dim, inf * 0, and for the others x * 0)
+    reach = {37, 101} if rot else {37}
+    if norm:
+        reach = set(range(128)) if value == "nan" else reach
+    kblocks = sorted({d // 32 for d in reach})
+    hit = torch.zeros_like(k1, dtype=torch.bool)
+    for d in reach:
+        hit[3, 1, d] = True
+    if q8:
+        for b in kblocks:
+            hit[3, 1, 32 * b:32 * b + 32] = True
+    assert not torch.isfinite(k2[hit]).any()
+    if value == "nan" or q8:
+        assert torch.isnan(k2[hit]).any()
+    same = ~hit
+    if norm:
+        same[3, 1] = False                            # (the norm's sum is the head's)
+    assert torch.equal(bits(k2)[same], bits(k1)[same])
+    hit = torch.zeros_like(v1, dtype=torch.bool)
+    hit[20, 0, 96:128 if q8 else 101] = True
+    if not q8:
+        hit[20, 0, 96:100] = False
+    assert not torch.isfinite(v2[hit]).any() and torch.equal(bits(v2)[~hit], bits(v1)[~hit])
+    assert not torch.isfinite(q2[41, 2, 64])
+    rows = torch.arange(70, device="cuda") != 41
+    assert torch.equal(bits(q2)[rows], bits(q1)[rows])
