@@ -127,10 +127,11 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  * rounded to bf16), over a q8_0 cache with fp16 ones (weights, decoded values and scaled query rows
  * are rounded to fp16; rows that fp16 cannot hold are computed in fp32 instead).  Scores, softmax
  * statistics and outputs are accumulated in fp32 and rounded once.  Rows never see later positions,
- * whatever NaN or infinity these hold.  A device wait that runs out (a fault of the library) is
- * reported as MK_ERR_TIMEOUT in status_out.  Pages out of range are skipped: a row attends over its other
- * positions, and one that has none gets zeros.  What lies in a page behind a sequence's last
- * position is never used, whatever its bits.
+ * whatever NaN or infinity these hold.  Scores beyond fp32's range count as infinite: +inf makes its
+ * row NaN, -inf is no weight, and a row whose scores are all -inf is NaN.  A device wait that runs out
+ * (a fault of the library) is reported as MK_ERR_TIMEOUT in status_out.  Pages out of range are skipped:
+ * a row attends over its other positions, and one that has none gets zeros.  What lies in a page behind
+ * a sequence's last position is never used, whatever its bits.
  */
 int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
                        const int32_t* seq_lens, const int32_t* block_tables, const void* q, int64_t q_stride,

@@ -38,8 +38,8 @@
 // it fits; P carries a factor 2^6, so that small weights stay clear of fp16's subnormals.
 //
 // What a row does not see must not reach it, and what fp16 cannot hold must still come out right: a row
-// whose result is not finite is computed again from the cache in fp32, position by position
-// (exact_row).  A NaN or infinity among later V rows of the same tile (0 * NaN) and scales whose values
+// whose result is not finite, or whose weights are all zeros, is computed again from the cache in fp32,
+// position by position (exact_row).  A NaN or infinity among later V rows of the same tile (0 * NaN) and scales whose values
 // overflow fp16 (the decode makes them NaN) end there; a row that really holds a NaN stays one.
 
 #include "mk_chunk_plan.h"
@@ -355,6 +355,7 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
   const __half* scales = reinterpret_cast<const __half*>(p.kv + p.code_bytes);
   const float c = 1.4426950408889634f * rsqrtf(static_cast<float>(D));
   float m = -INFINITY, sum = 0.f, o[D / 32];
+  uint32_t seen = 0;                                 // positions whose page is in range
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
   for (int t0 = 0; t0 < n; t0 += 32) {
@@ -403,7 +404,9 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
     m = mx;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = o[i] == 0.f ? 0.f : o[i] * f;
-    for (uint32_t in = __ballot_sync(~0u, line >= 0); in; in &= in - 1) {
+    uint32_t in = __ballot_sync(~0u, line >= 0);
+    seen |= in;
+    for (; in; in &= in - 1) {
       const int j = __ffs(in) - 1;
       const int64_t lv = __shfl_sync(~0u, line, j) + static_cast<int64_t>(p.plan.Hkv) * p.ps;
       const float wj = __shfl_sync(~0u, w, j);
@@ -417,10 +420,11 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
       }
     }
   }
+  // (positions, but every score -inf: 0 / 0, the NaN that the formula has)
   uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
-    out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o[i] / sum));
+    out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(seen == 0u ? 0.f : o[i] / sum));
 }
 
 // --------------------------------------------------------------------------- loads (warp 8: K, warp 11: V)
@@ -980,7 +984,8 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
     const int urow = urow0 + row;
     const int tok = urow * p.plan.by_G >> 16;
     const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + urow - tok * p.plan.G;
-    bool odd = false;
+    // no weight at all: a row without a position, or one whose scores are all -inf or beyond fp32
+    bool odd = l == 0.f;
     if (any) {
       // a partial is [D/4][urows] of 4 columns, then [urows] of (m, l): a warp's rows lie side by side
       float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(g.slot, 0)) * p.plan.urows * (D + 4));
@@ -1058,8 +1063,8 @@ __device__ __forceinline__ void softmax(const AttnParams& p, uint32_t base, Ctl*
       tc_before();
       if (!join()) return;
     }
-    // rows that are not finite, again from the cache, when both warpgroups' columns are written (where
-    // both see one they write the same)
+    // rows that are not finite, or without a weight, again from the cache, when both warpgroups' columns are
+    // written (where both see one they write the same)
     if (g.slot < 0) {
       for (uint32_t todo = __ballot_sync(~0u, odd && live); todo; todo &= todo - 1) {
         const int who = __ffs(todo) - 1;
@@ -1223,7 +1228,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& p, uint32_t base, 
     const int r = p.seqs.row0[g.s] + g.tok0 + tok, h = g.kvh * p.plan.G + lane - tok * p.plan.G;
     float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(g.slot, 0)) * p.plan.urows * (D + 4));
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    bool odd = false;
+    bool odd = live && g.slot < 0 && l == 0.f;     // (as in softmax)
     // each warpgroup half of the columns, 16 at a time, of which each warp sums up 4
 #pragma unroll 1
     for (int k = t * (D / 2); k < (t + 1) * (D / 2); k += 16) {
@@ -1260,7 +1265,8 @@ __device__ __forceinline__ void softmax_few(const AttnParams& p, uint32_t base, 
     tc_before();
     __threadfence_block();
     if (!join()) return;
-    // rows that are not finite, again from the cache (where two warps see one they write the same)
+    // rows that are not finite, or without a weight, again from the cache (where several warps see one they write
+    // the same)
     for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
       const int who = __ffs(todo) - 1;
       exact_row<D, kQ8Few>(p, __shfl_sync(~0u, r, who), __shfl_sync(~0u, h, who), &ctl->beat);
@@ -1440,7 +1446,7 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
     *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
         make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
   const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
-  const bool odd = live && (!(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
+  const bool odd = live && (L == 0.f || !(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
   if constexpr (!WIDE) __syncthreads();            // (a row's columns are several warps')
   uint32_t done = 0;
   for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {

@@ -643,3 +643,42 @@ def test_append_keeps_what_is_not_finite(rot, norm, value, q8):
     assert not torch.isfinite(q2[41, 2, 64])
     rows = torch.arange(70, device="cuda") != 41
     assert torch.equal(bits(q2)[rows], bits(q1)[rows])
+
+
+SCORE_SHAPES = [(8, 1, 90, 90), (8, 1, 300, 3), (16, 2, 5000, 2), (8, 1, 9000, 40), (4, 1, 700, 700)]
+
+
+@pytest.mark.parametrize("hq,hkv,len_,new", SCORE_SHAPES)
+def test_attention_rows_whose_scores_are_all_minus_infinity(hq, hkv, len_, new):
+    # exp(-inf) / 0: a NaN, as softmax has it; zeros are what a row without a position gets.  Query heads of the
+    # other sign see scores of +inf, a NaN too; a second sequence is as it was
+    st = R.Setup(hq, hkv, 128, 16, [len_, 50], [new, 9], seed=35)
+    pos = torch.arange(len_, device="cuda")
+    page, off = st.bt[0, pos // 16].long(), pos % 16
+    q = st.normal(st.rows, hq, 128)
+    q[..., 0] = torch.where(torch.arange(hq, device="cuda") % 2 == 0, 1.0, -1.0).to(torch.bfloat16)
+    ref, *scale = R.attention(st, q, st.kv)
+    st.kv[page, 0, :, off, 0] = float("-inf")
+    out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv)
+    assert torch.isnan(out[:new]).all()
+    assert torch.all((out[new:].double() - ref[new:]).abs() <= R.attention_bound(ref, *scale, False)[new:])
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("hq,hkv,len_,new", SCORE_SHAPES)
+def test_attention_q8_scores_beyond_fp32(hq, hkv, len_, new, sign):
+    # every score of a row is beyond what fp32 holds although its key and its query row are well within fp16 and
+    # bf16: NaN, not zeros
+    st = R.Setup(hq, hkv, 128, 16, [len_, 50], [new, 9], q8=True, seed=36)
+    pos = torch.arange(len_, device="cuda")
+    page, off = st.bt[0, pos // 16].long(), pos % 16
+    codes, scales = st.planes()
+    q = st.normal(st.rows, hq, 128)
+    ref, *scale = R.attention(st, q, st.kv)
+    codes[page, 0, :, off] = 0
+    codes[page, 0, :, off, 0] = 127 * sign
+    scales[page, 0, :, off, 0] = 500.0
+    q[:new, :, 0] = 2.0 ** 120
+    out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv)
+    assert torch.isnan(out[:new]).all()
+    assert torch.all((out[new:].double() - ref[new:]).abs() <= R.attention_bound(ref, *scale, True)[new:])
