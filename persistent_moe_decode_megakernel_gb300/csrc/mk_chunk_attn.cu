@@ -557,10 +557,11 @@ __device__ __forceinline__ void produce_q(const AttnParams& p, uint32_t base, Ct
 // Codes to fp16 operand tiles.  With its sign bit flipped a code byte is code + 128, and as the low
 // byte of 0x64.. the fp16 1024 + 128 + code; less 1152 that is the code exactly, times the scale
 // rounded once.  Positions of pages out of range or behind the sequence become zeros, values of a
-// scale above 515 (127 * 515 is what fp16 holds) NaN.
+// scale of 512 or more NaN: 128 (a code may be -128) times the next smaller one, 511.75, is fp16's largest.
 //
 // kQ8Few has two groups of four warps: one decodes K tiles (group 0), one V tiles, each from raw stages of
 // its own.  They share the operand ring as the two loaders do over a bf16 cache, and by the same argument.
+constexpr uint32_t kMaxScale = 0x5fffu;            // 511.75, of which and below the values are decoded
 template <int D, int M>
 __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* ctl, int group) {
   using L = Layout<D, M>;
@@ -601,7 +602,7 @@ __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* 
         for (int c = 0; c < 2; ++c) {
           uint32_t d = __byte_perm(sc[i][0], sc[i][1], c == 0 ? pick0 : pick1);
           if constexpr (!ALL) {
-            d = (d & 0x7fffu) > 0x6006u ? 0x7fff7fffu : d;
+            d = (d & 0x7fffu) > kMaxScale ? 0x7fff7fffu : d;
             d = live ? d : 0u;
           }
           const __half2 dd = *reinterpret_cast<const __half2*>(&d);
@@ -1461,7 +1462,7 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ At
 // A q8_0 sequence with many units (of query rows) has its cache decoded once, into fp16 tiles in the
 // workspace, instead of by every unit's block: tile t of the staged ones is [K, V][KV head][128][D]
 // as a page of 128 positions would be.  What Decoder does to a value is done here: the product with
-// the scale rounded to fp16, NaN for scales above 515, zeros for positions out of range or behind the
+// the scale rounded to fp16, NaN for scales above kMaxScale, zeros for positions out of range or behind the
 // sequence.  A thread takes 16 codes: 16 bytes and a scale in, 32 bytes out; HBM bound.
 constexpr int kStageThreads = 256;
 template <int D>
@@ -1495,7 +1496,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
 #pragma unroll
   for (int k = 0; k < kTile / kRows; ++k) {
     uint32_t d = sc[k];
-    if ((d & 0x7fffu) > 0x6006u) d = 0x7fffu;
+    if ((d & 0x7fffu) > kMaxScale) d = 0x7fffu;
     const __half2 dd = __half2half2(__ushort_as_half(static_cast<uint16_t>(d)));
     const uint32_t q[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
     uint32_t o[8];

@@ -682,3 +682,20 @@ def test_attention_q8_scores_beyond_fp32(hq, hkv, len_, new, sign):
     out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv)
     assert torch.isnan(out[:new]).all()
     assert torch.all((out[new:].double() - ref[new:]).abs() <= R.attention_bound(ref, *scale, True)[new:])
+
+
+@pytest.mark.parametrize("len_,new", [(40, 1), (40, 9), (300, 200), (6000, 2)])
+def test_attention_q8_code_minus_128(len_, new):
+    # the one code that the quantizer does not make, under scales whose 127-fold fp16 still holds and whose 128-fold
+    # it does not: keys that a query row meets with a small value, so that the score is an ordinary one
+    st = R.Setup(8, 1, 128, 16, [len_], [new], q8=True, seed=37)
+    codes, scales = st.planes()
+    for p, sc in ((3, 514.0), (len_ // 2, 515.0), (len_ - new, 512.0), (len_ // 3, 511.5)):
+        page = st.bt[0, p // 16].long()
+        codes[page, :, :, p % 16, :32] = 0
+        codes[page, 0, :, p % 16, 7] = -128
+        scales[page, 0, :, p % 16, 0] = sc
+    q = st.normal(new, 8, 128, std=0.1)
+    q[..., :32] = 0
+    q[..., 7] = 2.0 ** -14
+    check_attention(st, q=q)
