@@ -128,7 +128,9 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  * are rounded to fp16; rows that fp16 cannot hold are computed in fp32 instead).  Scores, softmax
  * statistics and outputs are accumulated in fp32 and rounded once.  Rows never see later positions,
  * whatever NaN or infinity these hold.  Scores beyond fp32's range count as infinite: +inf makes its
- * row NaN, -inf is no weight, and a row whose scores are all -inf is NaN.  A device wait that runs out
+ * row NaN, -inf is no weight, and a row whose scores are all -inf is NaN.  Every row that NaN or
+ * infinity reaches, or fp16 cannot hold, costs an fp32 pass over its positions (up to its first NaN score): an
+ * 8192-token prompt may take a thousand times as long.  A device wait that runs out
  * (a fault of the library) is reported as MK_ERR_TIMEOUT in status_out.  Pages out of range are skipped:
  * a row attends over its other positions, and one that has none gets zeros.  What lies in a page behind
  * a sequence's last position is never used, whatever its bits.

@@ -40,7 +40,9 @@
 // What a row does not see must not reach it, and what fp16 cannot hold must still come out right: a row
 // whose result is not finite, or whose weights are all zeros, is computed again from the cache in fp32,
 // position by position (exact_row).  A NaN or infinity among later V rows of the same tile (0 * NaN) and scales whose values
-// overflow fp16 (the decode makes them NaN) end there; a row that really holds a NaN stays one.
+// overflow fp16 (the decode makes them NaN) end there; a row that really holds a NaN stays one.  A warp takes a
+// row and head at a time there: an 8192-token prompt of 32 heads takes 0.36 ms, 1.2 with a NaN in its second key,
+// 172 with one in its middle key, 292 with one in an early value (whose other dims go on to the end).
 
 #include "mk_chunk_plan.h"
 #include "mk_debug.h"
@@ -402,11 +404,13 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
     for (int k = 16; k; k >>= 1) ws += __shfl_xor_sync(~0u, ws, k);
     sum = (sum == 0.f ? 0.f : sum * f) + ws;
     m = mx;
+    seen |= __ballot_sync(~0u, line >= 0);
+    // A NaN in the sum (all lanes') stays, and makes every dim NaN: the rest of the row changes nothing.  (A NaN in
+    // an early key is every row's: a 4096-token prompt of 16 heads took 41 ms, now 0.31.)
+    if (sum != sum) break;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = o[i] == 0.f ? 0.f : o[i] * f;
-    uint32_t in = __ballot_sync(~0u, line >= 0);
-    seen |= in;
-    for (; in; in &= in - 1) {
+    for (uint32_t in = __ballot_sync(~0u, line >= 0); in; in &= in - 1) {
       const int j = __ffs(in) - 1;
       const int64_t lv = __shfl_sync(~0u, line, j) + static_cast<int64_t>(p.plan.Hkv) * p.ps;
       const float wj = __shfl_sync(~0u, w, j);

@@ -699,3 +699,29 @@ def test_attention_q8_code_minus_128(len_, new):
     q[..., :32] = 0
     q[..., 7] = 2.0 ** -14
     check_attention(st, q=q)
+
+
+def test_attention_a_poisoned_prompt_ends_soon():
+    # a NaN in an early key is every row's: each is worked out again only as far as that key.  (To the end it would be
+    # about a thousand times the prompt's time; a hundred times leave room for any clock.)
+    st = R.Setup(16, 2, 128, 16, [4096], [4096], seed=38)
+    q = st.normal(st.rows, 16, 128)
+    out = torch.empty_like(q)
+
+    def took():
+        best = None
+        for _ in range(3):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, out=out)
+            b.record()
+            b.synchronize()
+            best = a.elapsed_time(b) if best is None else min(best, a.elapsed_time(b))
+        return best
+
+    clean = took()
+    st.kv[st.bt[0, 0].long(), 0, :, 1, 9] = float("nan")
+    poisoned = took()
+    print("prompt of 4096:", clean, "ms, poisoned", poisoned, "ms")
+    assert torch.isfinite(out[0]).all() and torch.isnan(out[1:]).all()
+    assert poisoned < 100 * clean
