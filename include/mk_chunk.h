@@ -120,7 +120,7 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  * sequence, p the row's own position; the new tokens' k and v must be in the cache already.
  *   q:         device bf16 [rows][q_stride]: num_q_heads heads of head_dim; q_stride in elements, a
  *              multiple of 8 (num_q_heads*head_dim when contiguous)
- *   out:       device bf16 [rows][num_q_heads][head_dim]
+ *   out:       device bf16 [rows][num_q_heads][head_dim]; overlaps no row of q (MK_ERR_INVALID_ARG), nor kv_layer
  *   workspace: device, at least mk_chunk_attention_workspace bytes (NULL if 0), contents lost; a
  *              call owns it until its work is done
  * Products run on the tensor cores: over a bf16 cache with bf16 operands (the softmax weights are
@@ -143,7 +143,8 @@ int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int3
 /*
  * The last chunk_lens[s] positions of each sequence as contiguous rows: k_out and v_out, device
  * bf16 [rows][num_kv_heads][head_dim] (a q8_0 value is code * scale, rounded once).  With
- * chunk_lens == seq_lens that is every position.  Rows of pages out of range are zeros.
+ * chunk_lens == seq_lens that is every position.  Rows of pages out of range are zeros.  The outputs
+ * overlap neither each other nor kv_layer.
  */
 int mk_read_cache(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens, const int32_t* seq_lens,
                   const int32_t* block_tables, const void* kv_layer, void* k_out, void* v_out, int32_t* status_out,

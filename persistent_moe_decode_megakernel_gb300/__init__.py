@@ -438,8 +438,9 @@ def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv
                     status=None, stream=None):
     """Causal attention of the new tokens' query rows over their sequences' cached positions
     (``mk_chunk_attention``; arguments as :func:`append_chunk`).  q: bf16 CUDA [rows, Hq, D] (rows
-    may be strided); workspace: CUDA tensor of at least :func:`chunk_attention_workspace` bytes, or
-    None to take it from torch's allocator.  Returns bf16 [rows, Hq, D]."""
+    may be strided); out: another tensor than q's, or None for a new one; workspace: CUDA tensor of at
+    least :func:`chunk_attention_workspace` bytes, or None to take it from torch's allocator.  Returns
+    bf16 [rows, Hq, D]."""
     args = (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status)
     return _native().chunk_attention(*args) if stream is None else _on(stream, kv_layer, _native().chunk_attention, *args)
 

@@ -1607,6 +1607,14 @@ int encode_queries(const mk_cache_shape& c, int G, int tokens, const void* q, in
   return r == CUDA_SUCCESS ? MK_OK : chunk_fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", static_cast<int>(r));
 }
 
+// Whether n bytes at `out` share one with `rows` rows of n / rows bytes, `stride` apart, at `q`.  (A row that is
+// worked out again reads its query row when its first result is written already.)
+bool meets_rows(const void* out, const void* q, uint64_t rows, uint64_t stride, uint64_t n) {
+  const uint64_t o = reinterpret_cast<uintptr_t>(out), a = reinterpret_cast<uintptr_t>(q), width = n / rows;
+  const uint64_t r = o < a + width ? 0 : (o - a - width) / stride + 1;   // the first row that ends behind o
+  return r < rows && a + r * stride < o + n;
+}
+
 template <int D, int M>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
@@ -1669,6 +1677,9 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   if (misaligned(block_tables, 4) || misaligned(q, 16) || misaligned(kv_layer, 16) || misaligned(out, 16) ||
       misaligned(workspace, 16))
     return chunk_fail(MK_ERR_INVALID_ARG, "pointers must be 16-byte aligned (block_tables 4-byte)");
+  if (rows > 0 && meets_rows(out, q, rows, static_cast<uint64_t>(q_stride) * 2,
+                             static_cast<uint64_t>(rows) * c.num_q_heads * c.head_dim * 2))
+    return chunk_fail(MK_ERR_INVALID_ARG, "out overlaps q");
   CallPlan plan;
   if (!plan_call(c, p.seqs, &plan)) return chunk_fail(MK_ERR_UNSUPPORTED, "too many rows in one call");
   if (workspace_bytes < plan.bytes() || (plan.bytes() > 0 && !workspace))

@@ -254,3 +254,11 @@ def test_plan_and_workspace_refuse_lengths(call):
             call(sh, cl, sl)
         assert e.value.code == mk.MK_ERR_INVALID_ARG
     call(sh, np.array([3, 0, 3, 0])[::2], (5, 5))
+
+
+def test_attention_refuses_an_output_over_its_query_rows():
+    sh, row = shape(), 8 * 128 * 2                      # rows of 2048 bytes
+    for n, stride, at in ((3, 1024, 0), (3, 1024, 16), (3, 1024, 3 * row - 16), (3, 1024, -3 * row + 16), (1, 1024, 0),
+                          (3, 4096, 8192 - 3 * row + 16), (3, 4096, 2 * 8192 + row - 16), (2, 1 << 30, (1 << 31) + 16)):
+        assert attend(sh, (n,), (n,), stride=stride, out=PTR + (1 << 20) + at, q=PTR + (1 << 20)) == BAD, (n, stride, at)
+        assert "overlaps" in mk.lib().mk_last_error().decode()

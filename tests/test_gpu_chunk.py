@@ -725,3 +725,21 @@ def test_attention_a_poisoned_prompt_ends_soon():
     print("prompt of 4096:", clean, "ms, poisoned", poisoned, "ms")
     assert torch.isfinite(out[0]).all() and torch.isnan(out[1:]).all()
     assert poisoned < 100 * clean
+
+
+def test_attention_output_beside_strided_query_rows():
+    # an output that lies between the rows of q is no overlap; one that shares a value with a row is refused
+    st = R.Setup(2, 1, 128, 16, [20], [3], seed=39)
+    buf = st.normal(3, 8 * 256)
+    q = buf[:, :256].unflatten(1, (2, 128))
+    ref, *scale = R.attention(st, q, st.kv)
+    flat = buf.flatten()
+    out = flat[256:256 + 3 * 256].view(3, 2, 128)       # in the gap behind row 0
+    assert mk.chunk_attention(st.shape(mk), q, [3], [20], st.bt, st.kv, out=out) is out
+    assert torch.all((out.double() - ref).abs() <= R.attention_bound(ref, *scale, False))
+    before = flat.clone()
+    for at in (0, 8, 256 - 8, 8 * 256 - 2 * 256, 7 * 256 + 8, 16 * 256 + 248):
+        with pytest.raises(mk.MkError) as e:
+            mk.chunk_attention(st.shape(mk), q, [3], [20], st.bt, st.kv, out=flat[at:at + 768].view(3, 2, 128))
+        assert e.value.code == mk.MK_ERR_INVALID_ARG and "overlap" in str(e.value)
+    assert torch.equal(bits(flat), bits(before))
