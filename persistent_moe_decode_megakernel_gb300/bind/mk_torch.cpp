@@ -107,13 +107,16 @@ Lengths lengths(PyObject* o) {
   need(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "chunk_lens and seq_lens: in host memory");
   Py_buffer b;
   if (PyObject_CheckBuffer(o) && PyObject_GetBuffer(o, &b, PyBUF_FORMAT | PyBUF_ND) == 0) {
+    struct Release {                  // (a length that `add` refuses leaves by an exception)
+      Py_buffer* b;
+      ~Release() { PyBuffer_Release(b); }
+    } release{&b};
     const char f = b.format && b.format[0] && !b.format[1] ? b.format[0] : 0;
     const bool w4 = f == 'i' && b.itemsize == 4, w8 = (f == 'l' || f == 'q') && b.itemsize == 8;
     const bool ok = b.ndim == 1 && (w4 || w8);
     if (ok)
       for (Py_ssize_t i = 0; i < b.shape[0] && i <= kMaxSeqs; ++i)
         out.add(w4 ? static_cast<const int32_t*>(b.buf)[i] : static_cast<const int64_t*>(b.buf)[i]);
-    PyBuffer_Release(&b);
     if (ok) return out;
     out = Lengths();
   }

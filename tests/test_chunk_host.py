@@ -262,3 +262,19 @@ def test_attention_refuses_an_output_over_its_query_rows():
                           (3, 4096, 8192 - 3 * row + 16), (3, 4096, 2 * 8192 + row - 16), (2, 1 << 30, (1 << 31) + 16)):
         assert attend(sh, (n,), (n,), stride=stride, out=PTR + (1 << 20) + at, q=PTR + (1 << 20)) == BAD, (n, stride, at)
         assert "overlaps" in mk.lib().mk_last_error().decode()
+
+
+def test_refused_lengths_are_let_go():
+    # an array of lengths that is refused is not held afterwards
+    import sys
+    torch = pytest.importorskip("torch")
+    sh = mk.CacheShape(8, 2, 128, 16, 8, 4, 0)
+    args = (torch.zeros(2 * 8 * 2 * 16 * 128, dtype=torch.bfloat16), torch.zeros(1, 4, dtype=torch.int32))
+    for bad in (np.array([1 << 40]), np.array([-(1 << 40), 3]), np.array([1.5]), np.array([3, 4])):
+        before = sys.getrefcount(bad)
+        for call in (lambda: mk.chunk_attention(sh, args[0], bad, [5], args[1], args[0]),
+                     lambda: mk.append_chunk(sh, args[0], [3], bad, args[1], args[0]),
+                     lambda: mk.read_cache(sh, bad, bad, args[1], args[0])):
+            with pytest.raises(mk.MkError):
+                call()
+        assert sys.getrefcount(bad) == before
