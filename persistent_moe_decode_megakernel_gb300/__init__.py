@@ -364,17 +364,20 @@ _bind = None
 def _native():
     """The marshalling module.  Raises if it has not been built: there is no other path."""
     global _bind
-    if _bind is None:
-        lib()
-        import torch  # noqa: F401  (its libraries have to be loaded first)
-        if not os.path.exists(BIND_PATH):
-            raise RuntimeError(f"binding not built ({BIND_PATH} missing); call build() first")
-        spec = importlib.util.spec_from_file_location("_mk_torch", BIND_PATH)
-        m = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(m)
-        m.init(MkError, *(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in (
-            "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache", "mk_last_error")))
-        _bind = m
+    if _bind is not None:
+        return _bind
+    lib()
+    import torch  # noqa: F401  (its libraries have to be loaded first)
+    with _lock:
+        if _bind is None:
+            if not os.path.exists(BIND_PATH):
+                raise RuntimeError(f"binding not built ({BIND_PATH} missing); call build() first")
+            spec = importlib.util.spec_from_file_location("_mk_torch", BIND_PATH)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.init(MkError, *(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+                "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache", "mk_last_error")))
+            _bind = m
     return _bind
 
 

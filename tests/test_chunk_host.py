@@ -278,3 +278,33 @@ def test_refused_lengths_are_let_go():
             with pytest.raises(mk.MkError):
                 call()
         assert sys.getrefcount(bad) == before
+
+
+def test_binding_is_made_once(monkeypatch):
+    # threads whose first call it is load and initialise the module once between them
+    import importlib.util
+    import threading
+    import time
+    pytest.importorskip("torch")
+    mk.lib()
+    monkeypatch.setattr(mk, "_bind", None)
+    made, real = [], importlib.util.module_from_spec
+
+    def slow(spec):
+        made.append(spec.name)
+        time.sleep(0.2)
+        return real(spec)
+
+    monkeypatch.setattr(importlib.util, "module_from_spec", slow)
+    start, got = threading.Barrier(4), []
+
+    def call():
+        start.wait()
+        got.append(mk._native())
+
+    threads = [threading.Thread(target=call) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert made == ["_mk_torch"] and len(got) == 4 and all(m is mk._bind for m in got)
