@@ -342,11 +342,20 @@ class _RopeStruct(ctypes.Structure):
 class Rope:
     """Rotary positions of :func:`append_chunk`: ``inv_freq`` radians per position of each pair of
     the head's first ``2 * len(inv_freq)`` dims (float64, see :func:`rope_frequencies`); pair i is
-    dims (i, i + n) of the n pairs, or (2i, 2i + 1) with ``interleaved``."""
+    dims (i, i + n) of the n pairs, or (2i, 2i + 1) with ``interleaved``.  ``struct`` points into the
+    array, so an assignment to ``inv_freq`` writes into it (as many values as it has)."""
 
     def __init__(self, inv_freq, interleaved: bool = False, mscale: float = 1.0):
-        self.inv_freq = np.array(inv_freq, dtype=np.float64).reshape(-1)
-        self.struct = _RopeStruct(2 * self.inv_freq.size, int(interleaved), self.inv_freq.ctypes.data, float(mscale))
+        self._inv_freq = np.array(inv_freq, dtype=np.float64).reshape(-1)
+        self.struct = _RopeStruct(2 * self._inv_freq.size, int(interleaved), self._inv_freq.ctypes.data, float(mscale))
+
+    @property
+    def inv_freq(self):
+        return self._inv_freq
+
+    @inv_freq.setter
+    def inv_freq(self, values):
+        self._inv_freq[:] = values
 
 
 def rope_frequencies(rotary_dim: int, theta: float, factor: float = 1.0, original_len: int = 0,

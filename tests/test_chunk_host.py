@@ -308,3 +308,20 @@ def test_binding_is_made_once(monkeypatch):
     for t in threads:
         t.join()
     assert made == ["_mk_torch"] and len(got) == 4 and all(m is mk._bind for m in got)
+
+
+def test_rope_keeps_the_frequencies_that_its_calls_read():
+    # the C structure points into the array: an assignment writes there, and none leaves it behind
+    f = np.linspace(1.0, 0.1, 16)
+    r = mk.Rope(f)
+    f[:] = 7.0                                          # (a copy is kept)
+    seen = lambda: np.ctypeslib.as_array(ctypes.cast(r.struct.inv_freq, ctypes.POINTER(ctypes.c_double)), (16,)).copy()  # noqa: E731
+    want = np.linspace(1.0, 0.1, 16)
+    r.inv_freq[3] = want[3] = 0.25
+    assert np.array_equal(seen(), want) and r.struct.rotary_dim == 32
+    r.inv_freq *= 2
+    assert np.array_equal(seen(), 2 * want)
+    r.inv_freq = np.ones(16)
+    assert np.array_equal(seen(), np.ones(16)) and np.array_equal(r.inv_freq, np.ones(16))
+    with pytest.raises(ValueError):
+        r.inv_freq = np.ones(15)
