@@ -329,18 +329,49 @@ struct Ring {
 // segment's n position tiles are its 2 n entries: with two tiles of rows K0 V0 K1 V1 .., with two streams
 // K0 K1 V0 K2 V1 K3 .. V(n-2) V(n-1).  (Loaded as K0 V0 K1 V1 there too, V tiles waited in the ring for two
 // position tiles: one row, 64 tiles a block from HBM, 98.7 us instead of 96.6.)
-__device__ __forceinline__ int entry_of(const Segment& g, int v, int j) {
+__host__ __device__ __forceinline__ constexpr int entry_of(const Segment& g, int v, int j) {
   if (g.two) return 2 * j + v;
-  return v ? min(2 * j + 2, 2 * g.n - 1) : max(2 * j - 1, 0);
+  const int k = 2 * j - 1, w = 2 * j + 2, last = 2 * g.n - 1;
+  return v ? (w < last ? w : last) : k > 0 ? k : 0;
 }
 // and back: whether entry i is a V tile, and of which position tile
-__device__ __forceinline__ int tile_of(const Segment& g, int i, int& v) {
+__host__ __device__ __forceinline__ constexpr int tile_of(const Segment& g, int i, int& v) {
   if (g.two) {
     v = i & 1;
     return i >> 1;
   }
   v = i == 2 * g.n - 1 || (i > 0 && !(i & 1));
   return !v ? (i + 1) >> 1 : i == 2 * g.n - 1 ? g.n - 1 : (i - 2) >> 1;
+}
+
+// A ring of N stages filled by two producers, one of K and one of V tiles.  Each waits for the release of entry
+// e - N by its parity, which is sound only if entry e - 2N is known to be released.  It is, as long as entries are
+// released in order and a producer's own entry before e is e - N or later: it waited for that one's turn, e - 2N or
+// later.  (Released out of order, or with fewer stages, a producer could pass a phase early, fill a stage twice and
+// overflow its barrier.)  Whether these two orders keep to that, within segments and from one to the next:
+__host__ __device__ constexpr bool ring_holds(int N) {
+  for (int kinds = 0; kinds < 4; ++kinds)
+    for (int lens = 0; lens < 36; ++lens) {
+      int last[2] = {0, 0}, c0 = 0;
+      for (int k = 0; k < 2; ++k) {
+        Segment g = {};
+        g.two = (kinds >> k) & 1;
+        g.n = 1 + (k ? lens / 6 : lens % 6);
+        for (int i = 0; i < 2 * g.n; ++i) {
+          int v = 0;
+          const int j = tile_of(g, i, v);
+          if (j < 0 || j >= g.n || entry_of(g, v, j) != i) return false;
+        }
+        for (int v = 0; v < 2; ++v)
+          for (int j = 0; j < g.n; ++j) {
+            const int e = c0 + entry_of(g, v, j);
+            if (k + j > 0 && (e <= last[v] || e - last[v] > N)) return false;
+            last[v] = e;
+          }
+        c0 += 2 * g.n;
+      }
+    }
+  return true;
 }
 
 // --------------------------------------------------------------------------- one row, plainly
@@ -434,13 +465,12 @@ __device__ __noinline__ void exact_row(const AttnParams& p, int r, int h, volati
 // --------------------------------------------------------------------------- loads (warp 8: K, warp 11: V)
 // A tile of 16-position pages takes 8 copies (q8_0: 16), which a warp issues one by one, so K and V have a
 // warp each (64 position tiles a block, one row, the cache in L2: bf16 85 us with one warp, 59 with
-// two; q8_0 126 and 100).  They share a ring of N stages.  A warp waits for entry e - N's release by its
-// parity, which is sound only if entry e - 2N is known to be released.  It is: entries are released in
-// order (by the MMA warp; raw stages by the decode warps), and the warp's own entry before e, which is
-// e - 3 at least, had to wait for one no earlier than e - 3 - N.
+// two; q8_0 126 and 100).  They share a ring (see ring_holds), whose entries the MMA warp (raw stages: the
+// decode warps) releases in order.
 template <int D, int M>
 __device__ __forceinline__ void produce(const AttnParams& p, uint32_t base, Ctl* ctl, int only) {
   using L = Layout<D, M>;
+  static_assert(M == kQ8Few || ring_holds(M == kQ8 ? L::kRawStages : L::kStages), "");   // (kQ8Few: a raw ring each)
   const int lane = threadIdx.x & 31;
   const int r = p.box, nbox = kTile / r;                       // copies of a tile
   const bool mine = lane < nbox;
@@ -569,6 +599,7 @@ constexpr uint32_t kMaxScale = 0x5fffu;            // 511.75, of which and below
 template <int D, int M>
 __device__ __forceinline__ void decode(const AttnParams& p, uint32_t base, Ctl* ctl, int group) {
   using L = Layout<D, M>;
+  static_assert(M != kQ8Few || ring_holds(L::kStages), "");
   const int tid = threadIdx.x & 127;
   // A thread takes chunks x and x ^ 8 (8 codes, 16 bytes of operand each) of rows tid/8 + 16 i:
   // odd rows begin with the upper half, which keeps 8-byte reads and 16-byte writes free of conflicts.
