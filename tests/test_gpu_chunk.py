@@ -743,3 +743,57 @@ def test_attention_output_beside_strided_query_rows():
             mk.chunk_attention(st.shape(mk), q, [3], [20], st.bt, st.kv, out=flat[at:at + 768].view(3, 2, 128))
         assert e.value.code == mk.MK_ERR_INVALID_ARG and "overlap" in str(e.value)
     assert torch.equal(bits(flat), bits(before))
+
+
+# ---------------------------------------------------------------- blocks that run several segments
+def ragged(n, top, choices, seed=2):
+    g = np.random.default_rng(seed)
+    lens = [int(x) for x in np.exp(g.uniform(np.log(20), np.log(top), n))]
+    return lens, [min(ln, int(g.choice(choices))) for ln in lens]
+
+
+MIXED, FEW = ragged(64, 900, [1, 1, 3, 40, 140, 300]), ragged(64, 900, [1, 2, 3])
+STAGED = [300, 700, 513, 260, 900, 170, 400, 333, 220, 640], [200, 300, 170, 260, 180, 170, 210, 190, 220, 300]
+SEGMENTS = {
+    # name: hq, hkv, d, ps, q8, lens, news, launch, ranged, segments a block, pairs of (one or two tiles) in a row
+    "whole d128": (16, 8, 128, 16, False, *MIXED, 0, False, 5, {"11", "12", "21", "22"}),
+    "whole d64": (16, 8, 64, 24, False, *MIXED, 0, False, 5, {"11", "12", "21", "22"}),
+    "whole q8": (16, 8, 128, 16, True, *MIXED, 0, False, 5, {"11", "12", "21", "22"}),
+    "ranged d128": (8, 4, 128, 24, False, [9000] + MIXED[0][:40], [200] + MIXED[1][:40], 0, True, 4, {"11", "12", "21", "22"}),
+    "ranged d64": (8, 4, 64, 16, False, [9000] + MIXED[0][:40], [200] + MIXED[1][:40], 0, True, 4, {"11", "12", "21", "22"}),
+    "ranged q8": (8, 4, 128, 24, True, [9000] + MIXED[0][:40], [200] + MIXED[1][:40], 0, True, 4, {"11", "12", "21", "22"}),
+    "whole few rows": (64, 8, 128, 16, True, *FEW, 0, False, 4, {"11"}),
+    "ranged few rows": (64, 8, 128, 24, True, [6000] + FEW[0][:63], [3] + FEW[1][:63], 0, True, 5, {"11"}),
+    "whole staged": (64, 8, 128, 16, True, *STAGED, 1, False, 4, {"11", "12", "21", "22"}),
+    "ranged staged": (32, 4, 128, 16, True, [12000] + STAGED[0][:8], [170] + STAGED[1][:8], 1, True, 4, {"11", "12", "21", "22"}),
+}
+
+
+@pytest.mark.parametrize("name", SEGMENTS)
+def test_attention_blocks_of_several_segments(name):
+    # a persistent block's later segments: query tiles used again, phases and rings carried on, rows converted under
+    # the segment before, tails of V that are not the block's first, units of one tile behind units of two
+    hq, hkv, d, ps, q8, lens, news, launch, ranged, most, pairs = SEGMENTS[name]
+    st = R.Setup(hq, hkv, d, ps, lens, news, q8=q8, seed=40)
+    seg = mk.plan_chunk_attention(st.shape(mk), news, lens)
+    assert set(seg[:, 0].tolist()) == {launch} and bool((seg[:, 8] >= 0).any()) == ranged
+    TT = 128 // (hq // hkv)
+    assert (max(min(n, 2 * TT) for n in news) * (hq // hkv) <= 32) == ("few" in name)
+    count, seen, tails = {}, set(), 0
+    for a, b in zip(seg[:-1].tolist(), seg[1:].tolist()):
+        count[b[1]] = count.get(b[1], 1) + 1 if a[1] == b[1] else 1
+        if a[1] == b[1]:
+            seen.add("".join("12"[news[x[2]] - x[3] * 2 * TT > TT] for x in (a, b)))
+            tails += (b[5] + b[6]) * 128 > lens[b[2]]
+    assert max(count.values()) >= most and seen == pairs and tails >= 20
+    q, out = check_attention(st, extra_rows=1)
+    # the same with one sequence poisoned: its rows are worked out again between the block's segments
+    s = int(np.argmax(news))
+    page = st.bt[s, 0].long()
+    (st.planes()[1] if q8 else st.kv)[page, 0, :, 0] = float("nan")
+    got = mk.chunk_attention(st.shape(mk), q, news, lens, st.bt, st.kv)
+    at = sum(news[:s])
+    assert torch.isnan(got[at:at + news[s]]).all()
+    keep = torch.ones(st.rows, dtype=torch.bool, device="cuda")
+    keep[at:at + news[s]] = False
+    assert torch.equal(bits(got[:st.rows])[keep], bits(out[:st.rows])[keep])
