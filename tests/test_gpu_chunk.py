@@ -797,3 +797,34 @@ def test_attention_blocks_of_several_segments(name):
     keep = torch.ones(st.rows, dtype=torch.bool, device="cuda")
     keep[at:at + news[s]] = False
     assert torch.equal(bits(got[:st.rows])[keep], bits(out[:st.rows])[keep])
+
+
+def test_calls_of_several_threads_are_right():
+    # every thread's calls end, report no error and give the first answers, which are the reference's
+    from concurrent.futures import ThreadPoolExecutor
+    cases = [R.Setup(8, 2, 128, 16, [3000, 129], [1, 1], q8=True, seed=30), R.Setup(8, 2, 128, 16, [3000, 129], [1, 1], seed=31),
+             R.Setup(8, 2, 128, 16, [700, 5], [300, 5], q8=True, seed=32), R.Setup(4, 2, 64, 16, [700, 5], [300, 5], seed=33)]
+    checked = [check_attention(st) for st in cases]
+    torch.cuda.synchronize()
+
+    def work(i):
+        st, (q, want) = cases[i], checked[i]
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+        done = 0
+        for _ in range(20):
+            out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, status=status, stream=stream)
+            stream.synchronize()
+            assert int(status) == mk.MK_OK and torch.equal(out, want)
+            done += 1
+        return done
+
+    with ThreadPoolExecutor(4) as pool:
+        assert [f.result() for f in [pool.submit(work, i) for i in range(4)]] == [20] * 4
+
+
+def test_attention_q8_single_tokens_beside_a_few_rows_more():
+    # one sequence of 40 rows among single tokens: the launch takes the general form for all of them
+    lens, news = [700, 129, 33, 1, 260, 400, 2000, 6], [1, 1, 1, 1, 5, 1, 1, 1]
+    check_attention(R.Setup(16, 2, 128, 16, lens, news, q8=True, seed=41))
