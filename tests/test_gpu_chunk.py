@@ -828,3 +828,55 @@ def test_attention_q8_single_tokens_beside_a_few_rows_more():
     # one sequence of 40 rows among single tokens: the launch takes the general form for all of them
     lens, news = [700, 129, 33, 1, 260, 400, 2000, 6], [1, 1, 1, 1, 5, 1, 1, 1]
     check_attention(R.Setup(16, 2, 128, 16, lens, news, q8=True, seed=41))
+
+
+# ---------------------------------------------------------------- at the limits
+@pytest.mark.parametrize("hq,hkv,d,q8", [(1024, 1024, 64, False), (1024, 128, 128, False), (1024, 128, 128, True),
+                                         (1024, 1024, 128, True)])
+def test_most_heads(hq, hkv, d, q8):
+    st = R.Setup(hq, hkv, d, 8, [130, 3], [2, 3], q8=q8, seed=42)
+    check_append(st, d, False, True)
+    check_attention(st)
+    k, v = mk.read_cache(st.shape(mk), st.lens, st.lens, st.bt, st.kv)
+    want = torch.cat([st.cached(st.kv, s, ln) for s, ln in enumerate(st.lens)], 2).transpose(1, 2).float().to(torch.bfloat16)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("ps", [4096, 1000, 136])
+def test_large_and_odd_pages(ps, q8):
+    st = R.Setup(8, 2, 128, ps, [4500, 70, 1001], [3, 70, 170], q8=q8, seed=43)
+    check_append(st, 128, True, False)
+    check_attention(st)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_sequences_that_share_pages(q8):
+    # a common prefix lies in the pool once; one sequence is listed twice
+    st = R.Setup(8, 2, 128, 16, [500, 400, 500], [40, 7, 40], q8=q8, seed=44)
+    st.bt[1, :20] = st.bt[0, :20]
+    st.bt[2] = st.bt[0]
+    q = st.normal(st.rows, 8, 128)
+    q[47:] = q[:40]
+    _, out = check_attention(st, q=q)
+    assert torch.equal(out[:40], out[47:])
+    k, v = mk.read_cache(st.shape(mk), st.lens, st.lens, st.bt, st.kv)
+    assert torch.equal(k[:320], k[500:820]) and torch.equal(v[:500], v[900:])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_graph_follows_its_block_tables(q8):
+    # a replay reads the tables and the cache as they are then; lengths are the capture's
+    st = R.Setup(8, 2, 128, 16, [900, 40], [1, 40], q8=q8, seed=45)
+    q = st.normal(st.rows, 8, 128)
+    bt, kv = st.bt.clone(), st.kv.clone()
+    mk.chunk_attention(st.shape(mk), q, st.news, st.lens, bt, kv)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = mk.chunk_attention(st.shape(mk), q, st.news, st.lens, bt, kv)
+    other = R.Setup(8, 2, 128, 16, [900, 40], [1, 40], q8=q8, seed=46)
+    bt.copy_(other.bt)
+    kv.copy_(other.kv)
+    g.replay()
+    ref, *scale = R.attention(other, q, other.kv)
+    assert torch.all((out.double() - ref).abs() <= R.attention_bound(ref, *scale, q8))
