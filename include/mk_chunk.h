@@ -97,9 +97,9 @@ int mk_rope_frequencies(int32_t rotary_dim, double theta, double factor, int32_t
  * from their fp32 values as MK_FLAG_KV_Q8 describes.  What is not finite stays so: a bf16 value as
  * it is, a q8_0 block of 32 with a NaN or an infinity among its values gets a NaN or infinite scale, so
  * that none of it reads back as finite (the step's own quantizer passes over a NaN).  Everything
- * is computed in fp32 (the angle of far positions exactly reduced) and rounded once.  A row whose page is out of range writes
- * q_out but no k or v.  Two rows must not write one position (pages shared by two sequences
- * may be read, not appended to).  qkv, q_out and kv_layer must not overlap.
+ * is computed in fp32 (the angle of far positions exactly reduced) and rounded once.  A row whose
+ * page is out of range writes q_out but no k or v.  Two rows must not write one position (pages
+ * shared by two sequences may be read, not appended to).  qkv, q_out and kv_layer must not overlap.
  */
 int mk_append_chunk(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens, const int32_t* seq_lens,
                     const int32_t* block_tables, const void* qkv, int64_t qkv_stride, const mk_rope* rope,
@@ -126,14 +126,15 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  * Products run on the tensor cores: over a bf16 cache with bf16 operands (the softmax weights are
  * rounded to bf16), over a q8_0 cache with fp16 ones (weights, decoded values and scaled query rows
  * are rounded to fp16; rows that fp16 cannot hold are computed in fp32 instead).  Scores, softmax
- * statistics and outputs are accumulated in fp32 and rounded once.  Rows never see later positions,
- * whatever NaN or infinity these hold.  Scores beyond fp32's range count as infinite: +inf makes its
- * row NaN, -inf is no weight, and a row whose scores are all -inf is NaN.  Every row that NaN or
- * infinity reaches, or fp16 cannot hold, costs an fp32 pass over its positions (up to its first NaN score): an
- * 8192-token prompt may take a thousand times as long.  A device wait that runs out
- * (a fault of the library) is reported as MK_ERR_TIMEOUT in status_out.  Pages out of range are skipped:
- * a row attends over its other positions, and one that has none gets zeros.  What lies in a page behind
- * a sequence's last position is never used, whatever its bits.
+ * statistics and outputs are accumulated in fp32 and rounded once.
+ * Rows never see later positions, whatever NaN or infinity these hold.  Scores beyond fp32's range
+ * count as infinite: +inf makes its row NaN, -inf is no weight, and a row whose scores are all -inf is
+ * NaN.  Every row that NaN or infinity reaches, or fp16 cannot hold, costs an fp32 pass over its
+ * positions (up to its first NaN score): an 8192-token prompt may take a thousand times as long.
+ * Pages out of range are skipped: a row attends over its other positions, and one that has none gets
+ * zeros.  What lies in a page behind a sequence's last position is never used, whatever its bits.
+ * A device wait that runs out (a fault of the library) leaves outputs unfinished and is reported as
+ * MK_ERR_TIMEOUT in status_out.
  */
 int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
                        const int32_t* seq_lens, const int32_t* block_tables, const void* q, int64_t q_stride,

@@ -407,8 +407,8 @@ def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_
     qkv: bf16 CUDA [rows, (Hq + 2*Hkv)*D] (rows may be strided); chunk_lens / seq_lens: host int32
     [num_seqs], new tokens and length including them; block_tables: int32 CUDA [num_seqs,
     max_pages_per_seq]; kv_layer: the layer's cache, written; rope: rotation or None; q_norm /
-    k_norm: bf16 CUDA [D] gains or None; status: int32 CUDA [1] or None; stream: default torch's
-    current one.  Returns the query rows, bf16 [rows, Hq, D] (``q_out`` or a new tensor).
+    k_norm: bf16 CUDA [D] gains or None; status: int32 CUDA [1] or None (without it a page out of range,
+    or a device wait that ran out, is reported nowhere); stream: default torch's current one.  Returns the query rows, bf16 [rows, Hq, D] (``q_out`` or a new tensor).
     """
     args = (shape, qkv, chunk_lens, seq_lens, block_tables, kv_layer, None if rope is None else rope.struct, q_norm, k_norm,
             eps, q_out, status)

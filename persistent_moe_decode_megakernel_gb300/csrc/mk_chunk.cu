@@ -1,8 +1,9 @@
 // mk_chunk.cu -- a chunk of new tokens into the paged KV cache (mk_append_chunk), cached
 // positions back out of it (mk_read_cache), and the argument checks of the chunk operators.
 //
-// Both kernels move bytes and are bound by HBM: a row is read once and written once, 16 bytes
-// per thread and access, and everything between is in registers.
+// Both kernels move bytes: a row is read once and written once, 16 bytes per thread and access, and
+// everything between is in registers.  HBM bounds the bf16 append of 128-wide heads and the read; the q8_0 append
+// and heads of 64 are bound by their instructions (see append_kernel).
 
 #include "mk_chunk.h"
 
@@ -152,7 +153,9 @@ __device__ __forceinline__ void lane_chunks(int l, int R, bool half, int& ca, in
 // pairs for all the heads.  D/16 lanes take a head: two 16-byte loads, the norm's sum by shuffles, the
 // rotation in registers, two 16-byte stores (q8_0: 8-byte codes and, per head, one 8-byte store of its
 // four scales); the loads of the next kFly heads are in flight meanwhile.  Reads 2 B and writes 2 B
-// (17/16 B) a value: HBM bound.  (With the angles read from shared memory for every head, waiting for
+// (17/16 B) a value.  Over bf16 with heads of 128 that bounds it; over q8_0 it is the instructions, of which the
+// shuffles of norms and maxima wait longest (4112 tokens with norms, one wave of blocks: 20 us in the profiler, DRAM
+// at 27 %), and with heads of 64 too (16384 tokens of 18 heads: 18.5 us, 27 %).  (With the angles read from shared memory for every head, waiting for
 // those reads was the most frequent stall: 33.1 us for 8192 tokens of 32 + 2 * 4 heads, now 28.4, 5.9 TB/s.)
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kBlock) append_kernel(const __grid_constant__ ChunkSeqs seqs,
