@@ -7,6 +7,8 @@
  * one layer, the same ones the step, mk_kv_pool and mk_paged_attention_noalloc use:
  *   mk_append_chunk     per-head RMSNorm of q and k, rotary positions, the cache write
  *   mk_chunk_attention  causal attention of the new tokens over their sequences' positions
+ *   mk_window_attention the same over a window and the sequences' first positions
+ *   mk_prefix_attention the same for sequences that share their first pages, each shared page read once
  *   mk_read_cache       cached positions back as contiguous bf16 rows
  * A layer's prefill is: QKV product, mk_append_chunk, mk_chunk_attention, the rest of the
  * layer; the decode steps then go on from the same cache.
@@ -140,6 +142,46 @@ int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const int3
                        const int32_t* seq_lens, const int32_t* block_tables, const void* q, int64_t q_stride,
                        const void* kv_layer, void* out, void* workspace, size_t workspace_bytes, int32_t* status_out,
                        mk_stream_t stream);
+
+/*
+ * mk_chunk_attention where a row at position p sees the `window` positions p-window+1..p and the first `sinks`
+ * positions of its sequence (those of them up to p), and no others.  window >= 1 (beyond every length: all
+ * positions up to p), sinks >= 0.
+ * Block table entries of pages that hold no position that a row of the call sees are not read: such pages may
+ * have been given back, or be another sequence's by now.  What a row does not see never reaches it, whatever NaN or
+ * infinity it holds; the rest is as for mk_chunk_attention, of which every argument, limit, rounding and report
+ * keeps its meaning.  mk_window_attention_workspace gives the bytes of workspace (0: none).
+ */
+int mk_window_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                  const int32_t* seq_lens, int32_t window, int32_t sinks, size_t* bytes_out);
+int mk_window_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                        const int32_t* seq_lens, int32_t window, int32_t sinks, const int32_t* block_tables,
+                        const void* q, int64_t q_stride, const void* kv_layer, void* out, void* workspace,
+                        size_t workspace_bytes, int32_t* status_out, mk_stream_t stream);
+
+/*
+ * mk_chunk_attention of sequences that share pages: what it returns, with each shared position read for all rows
+ * of a group together where that is less work.
+ *   num_groups:  groups of the call, 1..num_seqs
+ *   group_seqs:  HOST int32 [num_groups]: sequences of each group, >= 1, num_seqs together; group 0 is the first
+ *                group_seqs[0] sequences, and so on
+ *   prefix_lens: HOST int32 [num_groups]: first positions that a group's sequences share, >= 0 and at most
+ *                seq_lens[s] - chunk_lens[s] of each of them (no new token is among them)
+ * The first prefix_len / page_size (rounded down) entries of a group's block tables must be the same pages, and
+ * are read in the table of any of its sequences; positions behind these pages are each sequence's own.  (Tables that
+ * differ there make the group's rows those of one or the other table; no page out of range is touched.)
+ * Every other argument, limit, rounding and report is as for mk_chunk_attention, of which the sums' order differs.
+ * mk_prefix_attention_workspace gives the bytes of workspace (0: none): beside what mk_chunk_attention's holds,
+ * two partial outputs for each row and query head of a group.
+ */
+int mk_prefix_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                  const int32_t* seq_lens, int32_t num_groups, const int32_t* group_seqs,
+                                  const int32_t* prefix_lens, size_t* bytes_out);
+int mk_prefix_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                        const int32_t* seq_lens, int32_t num_groups, const int32_t* group_seqs,
+                        const int32_t* prefix_lens, const int32_t* block_tables, const void* q, int64_t q_stride,
+                        const void* kv_layer, void* out, void* workspace, size_t workspace_bytes,
+                        int32_t* status_out, mk_stream_t stream);
 
 /*
  * The last chunk_lens[s] positions of each sequence as contiguous rows: k_out and v_out, device

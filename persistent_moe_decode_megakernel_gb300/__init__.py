@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 import subprocess
 import sysconfig
@@ -161,7 +162,8 @@ EXPORTS = ("mk_create", "mk_decode_step", "mk_decode_step_greedy", "mk_get_statu
            "mk_kv_pool_destroy", "mk_kv_admit", "mk_kv_reserve", "mk_kv_evict", "mk_kv_fill", "mk_kv_free_pages",
            "mk_kv_len", "mk_graph_create", "mk_graph_launch", "mk_graph_destroy", "mk_rope_frequencies",
            "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache",
-           "mk_plan_chunk_attention")
+           "mk_plan_chunk_attention", "mk_window_attention_workspace", "mk_window_attention",
+           "mk_prefix_attention_workspace", "mk_prefix_attention", "mk_plan_span_attention")
 
 _lib = None
 _lock = threading.Lock()
@@ -211,6 +213,11 @@ def lib():
             L.mk_chunk_attention_workspace.argtypes = [vp, i32, vp, vp, ctypes.POINTER(sz)]
             L.mk_chunk_attention.argtypes = [vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
             L.mk_plan_chunk_attention.argtypes = [vp, i32, vp, vp, vp, i32, ctypes.POINTER(i32)]
+            L.mk_window_attention_workspace.argtypes = [vp, i32, vp, vp, i32, i32, ctypes.POINTER(sz)]
+            L.mk_window_attention.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+            L.mk_prefix_attention_workspace.argtypes = [vp, i32, vp, vp, i32, vp, vp, ctypes.POINTER(sz)]
+            L.mk_prefix_attention.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+            L.mk_plan_span_attention.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, ctypes.POINTER(i32)]
             L.mk_read_cache.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
             L.mk_debug_trace.argtypes = [vp, i32, i32]
             L.mk_debug_trace_read.argtypes = [vp, vp, ctypes.c_size_t]
@@ -385,7 +392,9 @@ def _native():
             m = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(m)
             m.init(MkError, *(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
-                "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache", "mk_last_error")))
+                "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache", "mk_last_error",
+                "mk_window_attention_workspace", "mk_window_attention", "mk_prefix_attention_workspace",
+                "mk_prefix_attention")))
             _bind = m
     return _bind
 
@@ -415,14 +424,24 @@ def append_chunk(shape: CacheShape, qkv, chunk_lens, seq_lens, block_tables, kv_
     return _native().append_chunk(*args) if stream is None else _on(stream, kv_layer, _native().append_chunk, *args)
 
 
-def _lengths(chunk_lens, seq_lens):
-    both = [np.asarray(x) for x in (chunk_lens, seq_lens)]
+def _lengths(chunk_lens, seq_lens, names=("chunk_lens", "seq_lens"), per="sequence"):
+    both, what = [np.asarray(x) for x in (chunk_lens, seq_lens)], " and ".join(names)
     if both[0].ndim != 1 or both[0].shape != both[1].shape:
-        raise MkError(MK_ERR_INVALID_ARG, "chunk_lens and seq_lens: one length per sequence each")
+        raise MkError(MK_ERR_INVALID_ARG, f"{what}: one length per {per} each")
     i32 = np.iinfo(np.int32)
     if any(x.size and (x.dtype.kind not in "iu" or x.min() < i32.min or x.max() > i32.max) for x in both):
-        raise MkError(MK_ERR_INVALID_ARG, "chunk_lens and seq_lens: whole numbers of 32 bits")
+        raise MkError(MK_ERR_INVALID_ARG, f"{what}: whole numbers of 32 bits")
     return [np.ascontiguousarray(x, dtype=np.int32) for x in both]
+
+
+def _number(x, what):
+    try:
+        v = operator.index(x)
+    except TypeError:
+        v = 1 << 40
+    if not -(1 << 31) <= v < 1 << 31:
+        raise MkError(MK_ERR_INVALID_ARG, f"{what}: a whole number of 32 bits")
+    return v
 
 
 def chunk_attention_workspace(shape: CacheShape, chunk_lens, seq_lens) -> int:
@@ -455,6 +474,59 @@ def chunk_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv
     bf16 [rows, Hq, D]."""
     args = (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status)
     return _native().chunk_attention(*args) if stream is None else _on(stream, kv_layer, _native().chunk_attention, *args)
+
+
+def window_attention_workspace(shape: CacheShape, chunk_lens, seq_lens, window: int, sinks: int = 0) -> int:
+    """Bytes of workspace :func:`window_attention` needs for these lengths (0: none)."""
+    cl, sl = _lengths(chunk_lens, seq_lens)
+    need = ctypes.c_size_t()
+    _check(lib().mk_window_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data,
+                                               _number(window, "window"), _number(sinks, "sinks"), ctypes.byref(need)))
+    return need.value
+
+
+def prefix_attention_workspace(shape: CacheShape, chunk_lens, seq_lens, group_seqs, prefix_lens) -> int:
+    """Bytes of workspace :func:`prefix_attention` needs for these lengths (0: none)."""
+    cl, sl = _lengths(chunk_lens, seq_lens)
+    gs, pl = _lengths(group_seqs, prefix_lens, ("group_seqs", "prefix_lens"), "group")
+    need = ctypes.c_size_t()
+    _check(lib().mk_prefix_attention_workspace(ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, gs.size,
+                                               gs.ctypes.data, pl.ctypes.data, ctypes.byref(need)))
+    return need.value
+
+
+def plan_span_attention(shape: CacheShape, chunk_lens, seq_lens, window: int = 1, sinks: int = 0, group_seqs=(),
+                        prefix_lens=()) -> np.ndarray:
+    """The schedule of :func:`prefix_attention`, or without groups of :func:`window_attention`
+    (``mk_plan_span_attention``): int32 [segments, 18]."""
+    cl, sl = _lengths(chunk_lens, seq_lens)
+    gs, pl = (np.array(x, dtype=np.int32) for x in (group_seqs, prefix_lens))
+    n = ctypes.c_int32()
+    args = (ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, window, sinks, gs.size, gs.ctypes.data, pl.ctypes.data)
+    _check(lib().mk_plan_span_attention(*args, None, 0, ctypes.byref(n)))
+    out = np.zeros((n.value, 18), dtype=np.int32)
+    _check(lib().mk_plan_span_attention(*args, out.ctypes.data, n.value, ctypes.byref(n)))
+    return out
+
+
+def window_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv_layer, window: int, sinks: int = 0,
+                     out=None, workspace=None, status=None, stream=None):
+    """:func:`chunk_attention` in which a row at position p sees the ``window`` positions that end with p and the
+    first ``sinks`` positions of its sequence (``mk_window_attention``).  Block table entries of pages that no row
+    of the call sees are not read.  workspace: at least :func:`window_attention_workspace` bytes, or None."""
+    args = (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status, window, sinks)
+    return _native().window_attention(*args) if stream is None else _on(stream, kv_layer, _native().window_attention, *args)
+
+
+def prefix_attention(shape: CacheShape, q, chunk_lens, seq_lens, block_tables, kv_layer, group_seqs, prefix_lens,
+                     out=None, workspace=None, status=None, stream=None):
+    """:func:`chunk_attention` of sequences that share their first pages in groups, each shared page read for all
+    rows of its group together (``mk_prefix_attention``).  group_seqs / prefix_lens: host int32 [num_groups], the
+    number of (consecutive) sequences of each group and of the positions that these share; the first
+    ``prefix_len // page_size`` entries of a group's block tables are the same.  No new token is among the shared
+    positions.  workspace: at least :func:`prefix_attention_workspace` bytes, or None."""
+    args = (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status, group_seqs, prefix_lens)
+    return _native().prefix_attention(*args) if stream is None else _on(stream, kv_layer, _native().prefix_attention, *args)
 
 
 def read_cache(shape: CacheShape, counts, seq_lens, block_tables, kv_layer, k_out=None, v_out=None, status=None,

@@ -29,6 +29,10 @@ struct {
   decltype(&mk_chunk_attention) attention;
   decltype(&mk_read_cache) read;
   decltype(&mk_last_error) last_error;
+  decltype(&mk_window_attention_workspace) window_workspace;
+  decltype(&mk_window_attention) window;
+  decltype(&mk_prefix_attention_workspace) prefix_workspace;
+  decltype(&mk_prefix_attention) prefix;
 } g_mk = {};
 
 // Other Python threads run while a call launches or allocates: a launch waits when the device's queue is
@@ -101,10 +105,10 @@ struct Lengths {
   }
 };
 // Whole numbers: a buffer of 32- or 64-bit ones (numpy), or a sequence.
-Lengths lengths(PyObject* o) {
-  static const char* what = "chunk_lens and seq_lens: one whole number per sequence each";
+Lengths lengths(PyObject* o, const char* what = "chunk_lens and seq_lens: one whole number per sequence each",
+                const char* where = "chunk_lens and seq_lens: in host memory") {
   Lengths out;
-  need(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), "chunk_lens and seq_lens: in host memory");
+  need(!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda(), where);
   Py_buffer b;
   if (PyObject_CheckBuffer(o) && PyObject_GetBuffer(o, &b, PyBUF_FORMAT | PyBUF_ND) == 0) {
     struct Release {                  // (a length that `add` refuses leaves by an exception)
@@ -256,33 +260,91 @@ PyObject* append_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// chunk_attention(shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status)
+// The three attention calls: (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status, ..)
+// with what is their own behind that.  bytes(c, &n): the workspace's size; attend(c, q, stride, out, ws, bytes, status, on).
+template <class Bytes, class Attend>
+PyObject* attention(PyObject* const* a, const Call& c, Bytes&& need_bytes, Attend&& attend) {
+  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+  const at::Tensor& q = tensor(a[1], "q: a tensor");
+  const int64_t stride = c.rows_of(q, c.shape.num_q_heads,
+                                   "q: bf16 rows of num_q_heads heads of head_dim contiguous values on the cache's device, one "
+                                   "for each new token at least");
+  int32_t* status = c.status(a[8]);
+  const at::Tensor out = c.out(a[6], c.shape.num_q_heads, "out: contiguous bf16 [rows, num_q_heads, head_dim] on the cache's device");
+  at::Tensor ws;
+  if (a[7] != Py_None) {
+    ws = tensor(a[7], "workspace: a tensor or None");
+    need(ws.is_cuda() && ws.get_device() == c.dev && ws.is_contiguous(), "workspace: contiguous tensor on the cache's device");
+  } else {
+    size_t bytes = 0;
+    run([&] { return need_bytes(&bytes); });
+    if (bytes) ws = c.make({static_cast<int64_t>(bytes)}, at::kByte);
+  }
+  const mk_stream_t on = c.stream();
+  run([&] {
+    return attend(q.data_ptr(), stride, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
+                  status, on);
+  });
+  return keep(a[6], out);
+}
+
 PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 9)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Call c(a);
-    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
-    const at::Tensor& q = tensor(a[1], "q: a tensor");
-    const int64_t stride = c.rows_of(q, c.shape.num_q_heads,
-                                     "q: bf16 rows of num_q_heads heads of head_dim contiguous values on the cache's device, one "
-                                     "for each new token at least");
-    int32_t* status = c.status(a[8]);
-    const at::Tensor out = c.out(a[6], c.shape.num_q_heads, "out: contiguous bf16 [rows, num_q_heads, head_dim] on the cache's device");
-    at::Tensor ws;
-    if (a[7] != Py_None) {
-      ws = tensor(a[7], "workspace: a tensor or None");
-      need(ws.is_cuda() && ws.get_device() == c.dev && ws.is_contiguous(), "workspace: contiguous tensor on the cache's device");
-    } else {
-      size_t bytes = 0;
-      run([&] { return g_mk.workspace(&c.shape, c.n(), c.chunk.v, c.len.v, &bytes); });
-      if (bytes) ws = c.make({static_cast<int64_t>(bytes)}, at::kByte);
-    }
-    const mk_stream_t on = c.stream();
-    run([&] {
-      return g_mk.attention(&c.shape, c.n(), c.chunk.v, c.len.v, c.tables(), q.data_ptr(), stride, c.kv.data_ptr(),
-                            out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, status, on);
-    });
-    return keep(a[6], out);
+    return attention(
+        a, c, [&](size_t* bytes) { return g_mk.workspace(&c.shape, c.n(), c.chunk.v, c.len.v, bytes); },
+        [&](const void* q, int64_t stride, void* out, void* ws, size_t ws_bytes, int32_t* status, mk_stream_t on) {
+          return g_mk.attention(&c.shape, c.n(), c.chunk.v, c.len.v, c.tables(), q, stride, c.kv.data_ptr(), out, ws, ws_bytes,
+                                status, on);
+        });
+  });
+}
+
+int32_t number(PyObject* o, const char* what) {
+  PyObject* x = PyNumber_Index(o);
+  const long long v = x ? PyLong_AsLongLong(x) : -1;
+  Py_XDECREF(x);
+  if (PyErr_Occurred() || v < INT32_MIN || v > INT32_MAX) {
+    PyErr_Clear();
+    raise(MK_ERR_INVALID_ARG, what);
+  }
+  return static_cast<int32_t>(v);
+}
+
+// .., window, sinks)
+PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Call c(a);
+    const int32_t window = number(a[9], "window: a whole number of 32 bits"), sinks = number(a[10], "sinks: a whole number of 32 bits");
+    return attention(
+        a, c, [&](size_t* bytes) { return g_mk.window_workspace(&c.shape, c.n(), c.chunk.v, c.len.v, window, sinks, bytes); },
+        [&](const void* q, int64_t stride, void* out, void* ws, size_t ws_bytes, int32_t* status, mk_stream_t on) {
+          return g_mk.window(&c.shape, c.n(), c.chunk.v, c.len.v, window, sinks, c.tables(), q, stride, c.kv.data_ptr(), out, ws,
+                             ws_bytes, status, on);
+        });
+  });
+}
+
+// .., group_seqs, prefix_lens)
+PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Call c(a);
+    const char *what = "group_seqs and prefix_lens: one whole number per group each", *where = "group_seqs and prefix_lens: in host memory";
+    const Lengths seqs = lengths(a[9], what, where), shared = lengths(a[10], what, where);
+    need(seqs.n == shared.n, "group_seqs and prefix_lens: one number per group each");
+    const int groups = static_cast<int>(std::min<int64_t>(seqs.n, kMaxSeqs + 1));
+    return attention(
+        a, c,
+        [&](size_t* bytes) {
+          return g_mk.prefix_workspace(&c.shape, c.n(), c.chunk.v, c.len.v, groups, seqs.v, shared.v, bytes);
+        },
+        [&](const void* q, int64_t stride, void* out, void* ws, size_t ws_bytes, int32_t* status, mk_stream_t on) {
+          return g_mk.prefix(&c.shape, c.n(), c.chunk.v, c.len.v, groups, seqs.v, shared.v, c.tables(), q, stride, c.kv.data_ptr(),
+                             out, ws, ws_bytes, status, on);
+        });
   });
 }
 
@@ -307,13 +369,13 @@ PyObject* read_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(the exception class, called with (code, text); the addresses of the five calls in the order of g_mk)
+// init(the exception class, called with (code, text); the addresses of the nine calls in the order of g_mk)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 6)) return nullptr;
-  void* f[5];
-  for (int i = 0; i < 5; ++i) f[i] = PyLong_AsVoidPtr(a[1 + i]);
+  if (!count(n, 10)) return nullptr;
+  void* f[9];
+  for (int i = 0; i < 9; ++i) f[i] = PyLong_AsVoidPtr(a[1 + i]);
   if (PyErr_Occurred()) return nullptr;
-  static_assert(sizeof f == sizeof g_mk, "five calls");
+  static_assert(sizeof f == sizeof g_mk, "nine calls");
   std::memcpy(&g_mk, f, sizeof f);
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);
@@ -327,6 +389,8 @@ PyCFunction fast() {
 PyMethodDef methods[] = {
     {"append_chunk", fast<append_chunk>(), METH_FASTCALL, "mk_append_chunk on torch tensors"},
     {"chunk_attention", fast<chunk_attention>(), METH_FASTCALL, "mk_chunk_attention on torch tensors"},
+    {"window_attention", fast<window_attention>(), METH_FASTCALL, "mk_window_attention on torch tensors"},
+    {"prefix_attention", fast<prefix_attention>(), METH_FASTCALL, "mk_prefix_attention on torch tensors"},
     {"read_cache", fast<read_cache>(), METH_FASTCALL, "mk_read_cache on torch tensors"},
     {"init", fast<init>(), METH_FASTCALL, "the exception class and the C calls' addresses"},
     {nullptr, nullptr, 0, nullptr}};

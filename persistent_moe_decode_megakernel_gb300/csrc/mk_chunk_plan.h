@@ -21,6 +21,7 @@ constexpr int kTile = 128;           // positions of a tile, and rows of a tile
 constexpr int kMaxBlocks = 152;      // one block per SM
 
 struct AttnPlan {
+  static constexpr bool kSpans = false;
   int32_t n;                         // sequences with rows
   int32_t items, blocks, ranged;
   int32_t G, TT, Hkv;
@@ -42,6 +43,9 @@ struct Segment {
   int32_t tile0, n, tiles;           // position tiles [tile0, tile0 + n) of the item's `tiles`
   int32_t slot;                      // partial it writes, -1: it is the whole item and writes the output
   bool two;                          // two tiles of rows (else one)
+  // parts of the cache (mk_span_plan.h), where len, pos0 and tiles count places:
+  int32_t entry, row0;               // its entry; first packed row
+  int32_t head, gap;                 // place v is position v below `head`, v + gap from there on
 };
 
 __host__ __device__ inline void item_of(const AttnPlan& pl, const ChunkSeqs& q, int item, Segment& g) {
@@ -64,16 +68,18 @@ __host__ __device__ inline void item_of(const AttnPlan& pl, const ChunkSeqs& q, 
   g.tiles = (g.pos0 + g.ntok - 1) / kTile + 1;
 }
 
-// Walks one block's segments.
+// Walks one block's segments.  (Whole items' partials: see mk_span_plan.h.)
 struct SegmentWalk {
   int b, k, item, tile;
-  __host__ __device__ SegmentWalk(const AttnPlan& pl, int block) : b(block), k(0), item(0), tile(0) {
+  template <class Plan>
+  __host__ __device__ SegmentWalk(const Plan& pl, int block) : b(block), k(0), item(0), tile(0) {
     if (pl.ranged) {
       item = pl.start[b].item;
       tile = pl.start[b].tile;
     }
   }
-  __host__ __device__ bool next(const AttnPlan& pl, const ChunkSeqs& q, Segment& g) {
+  template <class Plan>
+  __host__ __device__ bool next(const Plan& pl, const ChunkSeqs& q, Segment& g) {
     if (!pl.ranged) {
       const int64_t i = static_cast<int64_t>(k) * pl.blocks + (k & 1 ? pl.blocks - 1 - b : b);
       ++k;
@@ -81,7 +87,7 @@ struct SegmentWalk {
       item_of(pl, q, static_cast<int>(i), g);
       g.tile0 = 0;
       g.n = g.tiles;
-      g.slot = -1;
+      g.slot = whole_slot(pl, g);
       return true;
     }
     const int ei = pl.start[b + 1].item, et = pl.start[b + 1].tile;
@@ -90,10 +96,15 @@ struct SegmentWalk {
     const int end = item == ei ? et : g.tiles;
     g.tile0 = tile;
     g.n = end - tile;
-    g.slot = tile == 0 && end == g.tiles ? -1 : 2 * b + (tile == 0 ? 1 : 0);
+    g.slot = tile == 0 && end == g.tiles ? whole_slot(pl, g) : 2 * b + (tile == 0 ? 1 : 0);
     ++item;
     tile = 0;
     return true;
+  }
+  template <class Plan>
+  __host__ __device__ static int whole_slot(const Plan& pl, const Segment& g) {
+    if constexpr (Plan::kSpans) return pl.e[g.entry].part0 >= 0 ? Plan::kWholeSlot : -1;
+    else return -1;
   }
 };
 

@@ -1,0 +1,238 @@
+// mk_span_plan.cpp -- the schedules of mk_window_attention and mk_prefix_attention (see mk_span_plan.h).  Host only.
+
+#include "mk_span_plan.h"
+
+#include <algorithm>
+
+#include "mk_schedule.h"
+
+namespace mk {
+
+namespace {
+
+// Launches are of one kind of operand each (SpanCall); a sequence's rows take
+//   kFewRows  over q8_0, where its units have at most 32 rows of a KV head,
+//   kStagedRows  over q8_0, where its units together decode each position kStageTimes or more often: decoding it once
+//             is less work (kStageBytes of decoded positions at most in a call),
+//   kPageRows  else.
+constexpr int kStageTimes = 4;
+constexpr size_t kStageBytes = size_t(1) << 30;
+
+struct Builder {
+  const mk_cache_shape& c;
+  SpanCall* call;
+  int G, UT;
+  Builder(const mk_cache_shape& c, SpanCall* call) : c(c), call(call), G(c.num_q_heads / c.num_kv_heads), UT(2 * (kTile / G)) {}
+
+  // adds an entry to the launch that suits it; returns where it is
+  EntryRef add(SpanEntry e) {
+    int kind = kPageRows;
+    e.units = (e.rows + UT - 1) / UT;
+    e.stage0 = e.stage_tile0 = e.stage_head = 0;
+    if (c.flags & MK_FLAG_KV_Q8) {
+      if (std::min(e.rows, UT) * G <= kFewUnit) kind = kFewRows;
+      else if (stage(&e)) kind = kStagedRows;
+    }
+    SpanPlan& pl = call->plan[kind];
+    EntryRef at = {static_cast<int8_t>(kind), static_cast<int8_t>(pl.n)};
+    if (kind == kStagedRows) call->tiles_entry[call->staged++] = at.entry;
+    pl.e[pl.n++] = e;
+    return at;
+  }
+
+  bool stage(SpanEntry* e) {
+    SpanPlan probe;
+    probe.G = G;
+    probe.TT = kTile / G;
+    probe.Hkv = c.num_kv_heads;
+    probe.window = call->plan[0].window;
+    probe.sinks = call->plan[0].sinks;
+    probe.box = call->plan[0].box;
+    probe.e[0] = *e;
+    Segment g;
+    unit_of(probe, 0, 0, 0, g);
+    const int head = (g.head + kTile - 1) / kTile;       // (the first unit reaches back furthest)
+    e->stage_tile0 = (g.head + g.gap) / kTile;
+    if (g.gap == 0) e->stage_tile0 = 0;
+    e->stage_head = std::min(head, e->stage_tile0);
+    const int own = e->stage_head + (e->len + kTile - 1) / kTile - e->stage_tile0;
+    int64_t times = 0;
+    for (int u = 0; u < e->units; ++u) {
+      unit_of(probe, 0, u, 0, g);
+      times += g.tiles;
+    }
+    const size_t bytes = static_cast<size_t>(own) * 2 * c.num_kv_heads * kTile * c.head_dim * 2;
+    if (times < static_cast<int64_t>(kStageTimes) * own || call->stage_bytes + bytes > kStageBytes) return false;
+    e->stage0 = call->stage_tiles;
+    call->stage_tiles += own;
+    call->stage_bytes += bytes;
+    return true;
+  }
+
+  bool finish() {
+    size_t at = 0;
+    for (int k = 0; k < kRowKinds; ++k) {
+      SpanPlan& pl = call->plan[k];
+      size_t floats = 0;
+      if (!make_plan(c, &pl, &floats)) return false;
+      call->part0[k] = at;
+      at += floats;
+    }
+    call->whole0 = at;
+    call->floats = at + static_cast<size_t>(call->whole_rows) * c.num_q_heads * (c.head_dim + 4);
+    return true;
+  }
+};
+
+void reset(const mk_cache_shape& c, int window, int sinks, SpanCall* call) {
+  for (SpanPlan& pl : call->plan) {
+    pl.n = 0;
+    pl.window = window;
+    pl.sinks = sinks;
+    pl.box = span_box(c);
+  }
+  call->staged = call->stage_tiles = call->joins = 0;
+  call->stage_bytes = 0;
+  call->whole_rows = 0;
+}
+
+// The sequences with rows, the longest first.
+int by_length(const ChunkSeqs& q, int* order) {
+  int n = 0;
+  for (int s = 0; s < q.n; ++s)
+    if (q.row0[s + 1] > q.row0[s]) order[n++] = s;
+  std::sort(order, order + n, [&](int a, int b) { return q.len[a] != q.len[b] ? q.len[a] > q.len[b] : a < b; });
+  return n;
+}
+
+SpanEntry entry_of(const ChunkSeqs& q, int s) {
+  SpanEntry e = {};
+  e.seq = s;
+  e.row0 = q.row0[s];
+  e.rows = q.row0[s + 1] - q.row0[s];
+  e.before = q.len[s] - e.rows;
+  e.len = q.len[s];
+  e.part0 = -1;
+  return e;
+}
+
+}  // namespace
+
+bool make_plan(const mk_cache_shape& c, SpanPlan* pl, size_t* floats) {
+  pl->Hkv = c.num_kv_heads;
+  pl->G = c.num_q_heads / c.num_kv_heads;
+  pl->TT = kTile / pl->G;
+  pl->by_G = 65536 / pl->G + 1;   // exact below 2^9 rows
+  pl->blocks = pl->ranged = pl->cuts = 0;
+  *floats = 0;
+  int most = 0;
+  int64_t items = 0;
+  for (int i = 0; i < pl->n; ++i) {
+    SpanEntry& e = pl->e[i];
+    most = std::max(most, std::min(e.rows, 2 * pl->TT));
+    e.item0 = static_cast<int32_t>(items);
+    items += static_cast<int64_t>(e.units) * pl->Hkv;
+    if (items >= (int64_t(1) << 31)) return false;
+  }
+  pl->urows = most * pl->G;
+  pl->items = static_cast<int32_t>(items);
+  auto each = [&](auto&& visit) {
+    int item = 0;
+    Segment g;
+    for (int i = 0; i < pl->n; ++i)
+      for (int u = pl->e[i].units - 1; u >= 0; --u) {
+        unit_of(*pl, i, u, 0, g);
+        for (int h = 0; h < pl->Hkv; ++h) visit(item++, g.tiles, g.two);
+      }
+  };
+  schedule(pl, most > pl->TT, c.head_dim, floats, each,
+           [&](int item) { return pl->e[entry_of_item(*pl, item)].part0 < 0; });
+  return true;
+}
+
+bool plan_window(const mk_cache_shape& c, const ChunkSeqs& q, int32_t window, int32_t sinks, SpanCall* call) {
+  reset(c, std::min(window, kNoWindow), std::min(sinks, kNoWindow), call);
+  Builder build(c, call);
+  int order[kMaxSeqs];
+  const int n = by_length(q, order);
+  for (int i = 0; i < n; ++i) build.add(entry_of(q, order[i]));
+  return build.finish();
+}
+
+bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups, const int32_t* group_seqs,
+                 const int32_t* prefix_lens, SpanCall* call) {
+  reset(c, kNoWindow, 0, call);
+  Builder build(c, call);
+  const int UT = build.UT;
+  // Whether a group's rows go over its shared positions together: where that saves its blocks more time (the costs of
+  // mk_schedule.h, over all blocks) than the second kernel takes with the partials of its rows.
+  bool shared[kMaxSeqs] = {};
+  int32_t common[kMaxSeqs];
+  for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++]) {
+    common[i] = prefix_lens[i] / c.page_size * c.page_size;
+    const int rows = q.row0[s0 + group_seqs[i]] - q.row0[s0], tiles = (common[i] + kTile - 1) / kTile;
+    auto cost = [&](int rows, int item) {
+      const int full = rows / UT, rest = rows % UT;
+      int64_t x = static_cast<int64_t>(full) * (tiles * kTileCost[0] + item * kItemCost[0]);
+      if (rest > UT / 2) x += tiles * kTileCost[0] + item * kItemCost[0];
+      else if (rest) x += tiles * kTileCost[1] + item * kItemCost[1];
+      return x;
+    };
+    int64_t apart = 0;
+    int with = 0;
+    for (int s = s0; s < s0 + group_seqs[i]; ++s) {
+      apart += cost(q.row0[s + 1] - q.row0[s], 0);
+      with += q.row0[s + 1] > q.row0[s];
+    }
+    const int64_t saved = (apart - cost(rows, 1)) * c.num_kv_heads / kMaxBlocks;
+    const int64_t bytes = static_cast<int64_t>(rows) * c.num_q_heads * (c.head_dim + 4) * 16;
+    shared[i] = with > 1 && tiles > 0 && saved > kJoinCost + bytes / kJoinBytes;
+  }
+  // entries in the order of SpanPlan: shared positions, sequences of their own, sequences of groups
+  EntryRef over[kMaxSeqs];
+  int order[kMaxSeqs];
+  for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++]) {
+    if (!shared[i]) continue;
+    SpanEntry e = {};
+    e.seq = s0;
+    e.row0 = q.row0[s0];
+    e.rows = q.row0[s0 + group_seqs[i]] - e.row0;
+    e.before = e.len = common[i];
+    e.part0 = call->whole_rows;
+    call->whole_rows += e.rows;
+    over[i] = build.add(e);
+  }
+  for (int pass = 0; pass < 2; ++pass) {
+    int group_of[kMaxSeqs] = {};
+    for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++])
+      for (int s = s0; s < s0 + group_seqs[i]; ++s) group_of[s] = i;
+    const int n = by_length(q, order);
+    for (int k = 0; k < n; ++k) {
+      const int s = order[k], i = group_of[s];
+      if (shared[i] != (pass == 1)) continue;
+      SpanEntry e = entry_of(q, s);
+      if (pass == 0) {
+        build.add(e);
+        continue;
+      }
+      e.from = common[i];
+      e.part0 = call->whole_rows;
+      call->whole_rows += e.rows;
+      JoinSeq& j = call->join[call->joins++];
+      j.own = build.add(e);
+      j.over = over[i];
+    }
+  }
+  if (!build.finish()) return false;
+  // each unit and KV head of a joined sequence is a block's work of the second kernel
+  int64_t jobs = 0;
+  for (int k = 0; k < call->joins; ++k) {
+    call->join[k].job0 = static_cast<int32_t>(jobs);
+    const SpanEntry& e = call->plan[call->join[k].own.kind].e[call->join[k].own.entry];
+    jobs += static_cast<int64_t>(e.units) * c.num_kv_heads;
+  }
+  call->jobs = static_cast<int32_t>(jobs);
+  return jobs < (int64_t(1) << 31);
+}
+
+}  // namespace mk

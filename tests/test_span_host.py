@@ -1,0 +1,278 @@
+"""Host tests of attention over parts of the cache (mk_window_attention, mk_prefix_attention): what they refuse before
+anything is launched, and their schedules.  No GPU needed."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import persistent_moe_decode_megakernel_gb300 as mk
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    mk.build()
+
+
+def i32(*v):
+    return np.array(v, dtype=np.int32)
+
+
+def shape(**over):
+    s = mk.CacheShape(8, 2, 128, 16, 32, 8, 0)
+    for k, v in over.items():
+        setattr(s, k, v)
+    return s
+
+
+PTR = 1 << 20    # an aligned address that no refused call reads
+BAD, NO = mk.MK_ERR_INVALID_ARG, mk.MK_ERR_UNSUPPORTED
+
+
+def window(sh, cl=(3,), sl=(5,), n=None, w=4, sinks=1, stride=None, q=PTR, kv=PTR, bt=PTR, out=PTR, ws=None, ws_bytes=0,
+           status=None):
+    cl, sl = i32(*cl), i32(*sl)
+    stride = sh.num_q_heads * sh.head_dim if stride is None else stride
+    return mk.lib().mk_window_attention(ctypes.byref(sh), len(cl) if n is None else n, cl.ctypes.data, sl.ctypes.data, w, sinks,
+                                        bt, q, stride, kv, out, ws, ws_bytes, status, None)
+
+
+def prefix(sh, cl=(3,), sl=(5,), n=None, groups=None, shared=None, ngroups=None, stride=None, q=PTR, kv=PTR, bt=PTR, out=PTR,
+           ws=None, ws_bytes=0, status=None):
+    groups, shared = i32(*((len(cl),) if groups is None else groups)), i32(*((0,) if shared is None else shared))
+    cl, sl = i32(*cl), i32(*sl)
+    stride = sh.num_q_heads * sh.head_dim if stride is None else stride
+    return mk.lib().mk_prefix_attention(ctypes.byref(sh), len(cl) if n is None else n, cl.ctypes.data, sl.ctypes.data,
+                                        len(groups) if ngroups is None else ngroups, groups.ctypes.data, shared.ctypes.data, bt,
+                                        q, stride, kv, out, ws, ws_bytes, status, None)
+
+
+@pytest.mark.parametrize("call", [window, prefix])
+@pytest.mark.parametrize("over,code", [
+    (dict(num_q_heads=0), BAD), (dict(page_size=-1), BAD), (dict(num_q_heads=9), BAD), (dict(flags=4), BAD),
+    (dict(head_dim=96), NO), (dict(num_q_heads=18), NO), (dict(page_size=12), NO), (dict(flags=2, head_dim=64), NO),
+    (dict(page_size=1 << 28, max_pages_per_seq=8), NO), (dict(num_pages=1 << 30), NO)])
+def test_refuses_shapes(call, over, code):
+    assert call(shape(**over)) == code
+    assert mk.lib().mk_last_error().decode() != ""
+
+
+@pytest.mark.parametrize("call", [window, prefix])
+@pytest.mark.parametrize("cl,sl,n,code", [
+    ((-1,), (5,), None, BAD), ((6,), (5,), None, BAD), ((1,), (129,), None, BAD), ((3,), (5,), 0, BAD),
+    ((1,) * 65, (1,) * 65, None, BAD), ((1, 2, 9), (1, 2, 8), None, BAD)])
+def test_refuses_lengths(call, cl, sl, n, code):
+    assert call(shape(), cl, sl, n) == code
+
+
+@pytest.mark.parametrize("call", [window, prefix])
+def test_refuses_pointers_strides_and_workspaces(call):
+    sh = shape()
+    for k in ("q", "kv", "out"):
+        assert call(sh, **{k: None}) == BAD and call(sh, **{k: PTR + 8}) == BAD
+    far = 1 << 30
+    assert call(sh, out=far, bt=None) == BAD and call(sh, out=far, bt=PTR + 2) == BAD
+    assert call(sh, out=far, stride=8 * 128 - 8) == BAD and call(sh, out=far, stride=8 * 128 + 2) == BAD
+    assert call(sh, out=far, stride=1 << 38) == NO
+    assert call(sh, out=far, ws=PTR + 4) == BAD and call(sh, out=far, status=PTR + 1) == BAD
+    assert call(sh, out=PTR + 16) == BAD and "overlaps" in mk.lib().mk_last_error().decode()
+    big = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 16)
+    kw = dict(w=1 << 20) if call is window else {}
+    assert call(big, (1,), (100000,), out=far, **kw) == BAD and "workspace" in mk.lib().mk_last_error().decode()
+    assert call(shape(max_pages_per_seq=1 << 26), (1 << 24,), (1 << 24,), out=far) == NO
+
+
+def test_refuses_windows():
+    for w, sinks in ((0, 0), (-1, 0), (1, -1), (-(1 << 31), 0), (1, -(1 << 31))):
+        assert window(shape(), w=w, sinks=sinks) == BAD
+        with pytest.raises(mk.MkError):
+            mk.window_attention_workspace(shape(), [3], [5], w, sinks)
+    for w, sinks in ((1 << 31, 0), (2.5, 0), ("3", 0), (None, 0), (3, 1 << 40), (3, 0.0)):
+        with pytest.raises(mk.MkError) as e:
+            mk.window_attention_workspace(shape(), [3], [5], w, sinks)
+        assert e.value.code == BAD and "whole number" in str(e.value)
+
+
+def test_refuses_groups():
+    sh, cl, sl = shape(), (1, 2, 0, 1), (50, 40, 33, 60)
+    for groups, shared, n in (((4,), (39,), None), ((4,), (34,), None), ((4,), (-1,), None), ((3,), (0,), None),
+                              ((5,), (0,), None), ((2, 1), (0, 0), None), ((2, 3), (0, 0), None), ((4, 0), (0, 0), None),
+                              ((0, 4), (0, 0), None), ((1,) * 5, (0,) * 5, None), ((4,), (0,), 0), ((4,), (0,), -1),
+                              ((1 << 31) - 1, 5, None)):
+        groups, shared = (groups, shared) if isinstance(groups, tuple) else ((groups, shared), (0, 0))
+        assert prefix(sh, cl, sl, groups=groups, shared=shared, ngroups=n) == BAD, (groups, shared, n)
+        if n is None:
+            with pytest.raises(mk.MkError):
+                mk.prefix_attention_workspace(sh, cl, sl, groups, shared)
+    for groups, shared in (([4], [33]), ([2, 2], [38, 33]), ([1, 1, 1, 1], [49, 38, 33, 59]), ([3, 1], [0, 0])):
+        mk.prefix_attention_workspace(sh, cl, sl, groups, shared)
+    a = i32(1)
+    for g, p in ((None, a.ctypes.data), (a.ctypes.data, None)):
+        assert mk.lib().mk_prefix_attention(ctypes.byref(sh), 1, a.ctypes.data, i32(5).ctypes.data, 1, g, p, PTR, PTR, 1024, PTR,
+                                            1 << 30, None, 0, None, None) == BAD
+    for bad in (([4], [0, 0]), ([4.0], [0]), ([[4]], [[0]]), ([4], [1 << 40])):
+        with pytest.raises(mk.MkError) as e:
+            mk.prefix_attention_workspace(sh, cl, sl, *bad)
+        assert e.value.code == BAD and "group_seqs" in str(e.value)
+
+
+def test_no_rows_is_no_work():
+    # nothing is launched, so no device is needed and pointers may be NULL
+    for call in (window, prefix):
+        assert call(shape(), (0, 0), (5, 0)) == mk.MK_OK
+        assert call(shape(), (0,), (0,), q=None, kv=None, bt=None, out=None) == mk.MK_OK
+    assert mk.window_attention_workspace(shape(), [0], [0], 1) == 0
+    assert mk.prefix_attention_workspace(shape(), [0, 0], [0, 9], [2], [0]) == 0
+
+
+def test_binding_refuses_on_the_host():
+    torch = pytest.importorskip("torch")
+    sh = mk.CacheShape(8, 2, 128, 16, 8, 4, 0)
+    kv = torch.zeros(2 * 8 * 2 * 16 * 128, dtype=torch.bfloat16)
+    args = (sh, torch.zeros(3, 8, 128, dtype=torch.bfloat16), [3], [5], torch.zeros(1, 4, dtype=torch.int32), kv)
+    for call in (lambda *a: mk.window_attention(*a, 4), lambda *a: mk.prefix_attention(*a, [1], [0])):
+        with pytest.raises(mk.MkError) as e:
+            call(*args)
+        assert e.value.code == BAD and "CUDA" in str(e.value)
+        for i, bad, word in ((2, [3.0], "whole"), (3, [5, 5], "one length"), (3, [1 << 31], "whole"), (5, None, "kv_layer"),
+                             (4, [[0]], "block_tables"), (0, None, "shape"), (2, [-1], "rows")):
+            with pytest.raises(mk.MkError) as e:
+                call(*args[:i], bad, *args[i + 1:])
+            assert e.value.code == BAD and word in str(e.value), (i, bad, str(e.value))
+
+
+# ---------------------------------------------------------------- schedules
+COLS = ("launch", "block", "entry", "table", "row0", "ntok", "kvh", "head", "gap", "pos0", "len", "tile0", "n", "tiles", "slot",
+        "stage0", "stage_tile0", "stage_head")
+WHOLE = 304
+
+
+def segments(sh, cl, sl, **kw):
+    return [dict(zip(COLS, row)) for row in mk.plan_span_attention(sh, cl, sl, **kw).tolist()]
+
+
+def check_plan(sh, cl, sl, window=None, sinks=0, groups=(), shared=()):
+    """Every position that a row sees is one place of one segment of each KV head, and no other place is seen; no copy
+    reads a page that the call's rows do not see; copies stay within pages; partials are distinct."""
+    G, Hkv, ps = sh.num_q_heads // sh.num_kv_heads, sh.num_kv_heads, sh.page_size
+    box, TT = min(ps & -ps, 128), 128 // G
+    kw = dict(group_seqs=groups, prefix_lens=shared) if len(groups) else dict(window=window, sinks=sinks)
+    segs = segments(sh, cl, sl, **kw)
+    w = window if window is not None else 1 << 30
+    row0 = np.concatenate([[0], np.cumsum(cl)])
+    seq_of = np.repeat(np.arange(len(cl)), cl)
+    group_of = np.repeat(np.arange(len(groups)), groups) if len(groups) else np.arange(len(cl))
+    count = [np.zeros((Hkv, c, n), dtype=np.int32) for c, n in zip(cl, sl)]
+    visible = []
+    for c, n in zip(cl, sl):
+        row, pos = np.arange(n - c, n)[:, None], np.arange(n)[None, :]
+        visible.append((pos <= row) & ((pos > row - w) | (pos < sinks)))
+    slots, floats, staged = {0: set(), 1: set(), 2: set()}, {}, {}
+    for g in segs:
+        assert 0 < g["n"] and 0 <= g["tile0"] and g["tile0"] + g["n"] <= g["tiles"] and 0 < g["ntok"] <= 2 * TT
+        assert g["head"] % box == 0 and g["gap"] % box == 0 and 0 <= g["block"] < 152
+        v = np.arange(g["tile0"] * 128, min((g["tile0"] + g["n"]) * 128, g["len"]))
+        pos = np.where(v < g["head"], v, v + g["gap"])
+        for p in pos[v % box == 0]:                              # a copy's first position
+            assert p % box == 0
+            page = slice(p // ps * ps, p // ps * ps + ps)
+            if window is not None:
+                assert visible[g["table"]][:, page].any(), (p, g)
+        if g["launch"] == 1:
+            for t in np.unique(pos // 128):
+                at = g["stage0"] + (t if t < g["stage_head"] else t - g["stage_tile0"] + g["stage_head"])
+                assert (t < g["stage_head"] or t >= g["stage_tile0"]) and staged.setdefault(at, (g["entry"], t)) == (g["entry"], t)
+        for i in range(g["ntok"]):
+            r = g["row0"] + i
+            s = seq_of[r]
+            p0 = g["pos0"] + i
+            seen = (v <= p0) & ((v < sinks) | (v > p0 - w))
+            own = s == g["table"]
+            if not own:                                          # another sequence's table: shared whole pages only
+                assert group_of[s] == group_of[g["table"]]
+                assert np.all(pos[seen] < shared[group_of[s]] // ps * ps)
+            count[s][g["kvh"], r - row0[s], pos[seen]] += 1
+        if 0 <= g["slot"] < WHOLE:
+            assert g["slot"] == 2 * g["block"] + (g["tile0"] == 0) and g["slot"] not in slots[g["launch"]]
+            slots[g["launch"]].add(g["slot"])
+            assert g["n"] < g["tiles"]
+        else:
+            assert g["n"] == g["tiles"]
+        if sh.flags == mk.FLAG_KV_Q8:
+            assert (g["launch"] == 2) <= (g["ntok"] * G <= 32)
+        else:
+            assert g["launch"] == 0
+    for s, c in enumerate(count):
+        assert np.array_equal(c, np.broadcast_to(visible[s][None], c.shape)), s
+    # who writes the output: a row that one entry has does so by itself, of two neither
+    entries = {}
+    for g in segs:
+        for r in range(g["row0"], g["row0"] + g["ntok"]):
+            entries.setdefault((r, g["kvh"]), set()).add((g["launch"], g["entry"]))
+    for g in segs:
+        many = {len(entries[r, g["kvh"]]) for r in range(g["row0"], g["row0"] + g["ntok"])}
+        assert many in ({1}, {2})
+        if g["n"] == g["tiles"]:
+            assert g["slot"] == (-1 if many == {1} else WHOLE)
+    return segs
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_window_plan_covers_what_rows_see(seed):
+    g = np.random.default_rng(seed)
+    hkv, G = int(g.choice([1, 2, 4])), int(g.integers(1, 9))
+    sh = shape(num_q_heads=hkv * G, num_kv_heads=hkv, page_size=int(g.choice([8, 16, 24, 64, 128, 40, 256])), max_pages_per_seq=512,
+               num_pages=64, flags=int(g.choice([0, 2])))
+    n = int(g.integers(1, 9))
+    sl = np.exp(g.uniform(0, np.log(g.choice([50, 1500])), n)).astype(int)
+    top = int(g.choice([1, 40, 700]))
+    cl = [int(g.integers(0, min(x, top) + 1)) for x in sl]
+    w, sinks = int(np.exp(g.uniform(0, np.log(2000)))), int(g.choice([0, 1, 4, 17, 128, 300, 5000]))
+    check_plan(sh, cl, sl.tolist(), w, sinks)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_prefix_plan_covers_what_rows_see(seed):
+    g = np.random.default_rng(1000 + seed)
+    hkv, G = int(g.choice([1, 2, 4])), int(g.integers(1, 9))
+    sh = shape(num_q_heads=hkv * G, num_kv_heads=hkv, page_size=int(g.choice([8, 16, 24, 64])), max_pages_per_seq=4096,
+               num_pages=64, flags=int(g.choice([0, 2])))
+    groups = [int(x) for x in g.integers(1, 20, int(g.integers(1, 4)))]
+    shared = [int(np.exp(g.uniform(0, np.log(4000)))) for _ in groups]
+    top = int(g.choice([1, 1, 5, 60]))
+    cl = [int(g.integers(0, top + 1)) for _ in range(sum(groups))]
+    sl = [c + int(g.integers(0, 200)) + p for c, p in zip(cl, np.repeat(shared, groups))]
+    check_plan(sh, cl, sl, groups=groups, shared=shared)
+
+
+def test_a_long_shared_prefix_is_read_once():
+    # 64 sequences of one token behind 32768 shared positions: every shared tile is in the schedule for the group's
+    # rows (two units of a KV head), not for each sequence
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 12)
+    segs = segments(sh, [1] * 64, [32768 + 100] * 64, group_seqs=[64], prefix_lens=[32768])
+    assert sum(g["n"] for g in segs) == 4 * 2 * 256 + 64 * 4
+    # of two sequences over a few positions each takes its own way
+    segs = segments(sh, [1] * 2, [200] * 2, group_seqs=[2], prefix_lens=[128])
+    assert all(g["slot"] == -1 and g["len"] == 200 for g in segs)
+
+
+def test_window_plan_skips_the_hidden_middle():
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 14)
+    segs = segments(sh, [1], [131073], window=1000, sinks=4)
+    # positions 130073..131072, from a multiple of 16 on: 1009 places, and 16 of the sinks' copy
+    assert [(g["head"], g["len"], g["tiles"]) for g in segs if g["tile0"] == 0] == [(16, 1025, 9)] * 4
+    assert sum(g["n"] for g in segs) == 4 * 9
+    segs = segments(sh, [8192], [8192], window=1024, sinks=4)
+    assert max(g["tiles"] for g in segs) == 9
+
+
+def test_plans_of_the_largest_calls():
+    # 2^20 rows, a sequence of 2^30 positions: planned in little time, and nothing overflows
+    sh = shape(max_pages_per_seq=1 << 26)
+    assert mk.window_attention_workspace(sh, [1 << 20], [1 << 30], 1 << 30, 1 << 30) >= 0
+    segs = segments(sh, [1], [1 << 30], window=(1 << 31) - 1, sinks=(1 << 31) - 1)
+    assert sum(g["n"] for g in segs) == 2 * (1 << 23)
+    segs = segments(sh, [2], [1 << 30], window=5, sinks=16)
+    assert [(g["head"], g["gap"], g["len"]) for g in segs] == [(16, (1 << 30) - 32, 32)] * 2
+    segs = segments(sh, [1, 1], [1 << 30, 1 << 30], group_seqs=[2], prefix_lens=[(1 << 30) - 1])
+    # 2^30 - 16 shared positions, and 16 of each sequence's own
+    assert sum(g["n"] for g in segs) == 2 * (1 << 23) + 2 * 2
