@@ -1484,7 +1484,7 @@ template <int D, int M, bool WIDE, class Plan>
 __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ Params<Plan> p) {
   constexpr int kWarps = 2 * D / 32, kLanes = D / 4, kRows = WIDE ? 32 / kLanes : 8;
   constexpr int kMine = WIDE ? (kMaxBlocks + kWarps - 1) / kWarps : 1, kAtOnce = 8;
-  const AttnPlan& pl = p.plan;
+  const Plan& pl = p.plan;
   const int b = pl.cut_block[blockIdx.x], n = pl.cut_parts[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Segment g;
