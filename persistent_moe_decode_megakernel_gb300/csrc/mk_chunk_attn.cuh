@@ -113,15 +113,25 @@ struct Params {
     if constexpr (Plan::kSpans) return place < g.head ? place : place + g.gap;
     else return place;
   }
-  // a segment's partial: [D/4][stride] of 4 columns, then [stride] of (m, l)
+  // the position tile of a segment's j-th step, and its KV head
+  __device__ __forceinline__ int tile_at(const Segment& g, int j) const {
+    if constexpr (Plan::kSpans) return g.tile0 + (g.pair ? j >> 1 : j);
+    else return g.tile0 + j;
+  }
+  __device__ __forceinline__ int head_at(const Segment& g, int j) const {
+    if constexpr (Plan::kSpans) return g.kvh + (g.pair ? j & 1 : 0);
+    else return g.kvh;
+  }
+  // a segment's partial (of a pair, tile t's head): [D/4][stride] of 4 columns, then [stride] of (m, l)
   template <int D>
-  __device__ __forceinline__ float4* partial(const Segment& g, int& stride) const {
+  __device__ __forceinline__ float4* partial(const Segment& g, int t, int& stride, int& row) const {
     if constexpr (Plan::kSpans) {
       if (g.slot == Plan::kWholeSlot) {
         stride = g.ntok * plan.G;
-        const size_t row = static_cast<size_t>(plan.e[g.entry].part0 + g.tok0) * Hq + static_cast<size_t>(g.kvh) * stride;
-        return reinterpret_cast<float4*>(whole + row * (D + 4));
+        const size_t before = static_cast<size_t>(plan.e[g.entry].part0 + g.tok0) * Hq + static_cast<size_t>(head_at(g, t)) * stride;
+        return reinterpret_cast<float4*>(whole + before * (D + 4));
       }
+      if (g.pair) row += t * g.ntok * plan.G;
     }
     stride = plan.urows;
     return reinterpret_cast<float4*>(part + static_cast<size_t>(max(g.slot, 0)) * plan.urows * (D + 4));
@@ -518,14 +528,14 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
     const int32_t* bt = p.bt + static_cast<size_t>(g.s) * p.maxpg;
     // lane b looks up the page of the tile's b-th copy, one tile ahead
     auto lookup = [&](int j) {
-      const int at = (g.tile0 + j) * kTile + lane * r;
+      const int at = p.tile_at(g, j) * kTile + lane * r;
       return j < g.n && mine && at < g.len ? __ldg(bt + p.position(g, at) / p.ps) : -1;
     };
     int page_next = lookup(0);
     for (int j = 0; j < g.n; ++j, ++jg) {
       const int page = page_next;
       page_next = lookup(j + 1);
-      const int at = (g.tile0 + j) * kTile + lane * r, pos = p.position(g, at);
+      const int at = p.tile_at(g, j) * kTile + lane * r, pos = p.position(g, at), kvh = p.head_at(g, j);
       const bool good = mine && page >= 0 && page < p.P;
       if (mine && at < g.len && !good && p.status) *p.status = MK_ERR_DEVICE_BOUNDS;
       const uint32_t ok = __ballot_sync(~0u, good);
@@ -545,7 +555,7 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
           // (behind the entry's last position: out of the map's range, which fills with zeros)
           const int page = at < g.len ? n.stage0 + (tile < n.stage_head ? tile : tile - from) : 1 << 29;
           tma_5d(base + L::kKv + st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map,
-                 (g.kvh * kTile + pos % kTile) / 8, page * 2 + only, bar);
+                 (kvh * kTile + pos % kTile) / 8, page * 2 + only, bar);
         }
       } else if constexpr (M == kStaged) {
         // whole tiles of the workspace, their positions out of range or behind the sequence zeros already
@@ -553,7 +563,7 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
         if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
         if (lane == 0) {
           mbar_expect(bar, L::kTileBytes);
-          tma_5d(base + L::kKv + st * L::kTileBytes, &p.map, g.kvh * (kTile / 8),
+          tma_5d(base + L::kKv + st * L::kTileBytes, &p.map, kvh * (kTile / 8),
                  (p.stage0[g.s] + g.tile0 + j) * 2 + only, bar);
         }
         __syncwarp();
@@ -565,7 +575,7 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
         // a copy out of the pool's range fills its positions with zeros
         if (mine)
           tma_5d(base + L::kKv + st * L::kTileBytes + lane * (r / 8) * L::kGroup, &p.map,
-                 (g.kvh * p.ps + pos % p.ps) / 8, (good ? page : p.P) * 2 + only, bar);
+                 (kvh * p.ps + pos % p.ps) / 8, (good ? page : p.P) * 2 + only, bar);
       } else {
         // one ring of raw stages by entries, or K's and V's by position tiles
         const uint32_t ring = M == kQ8Few ? kRawFew : L::kRawStages, at = M == kQ8Few ? jg : e;
@@ -579,7 +589,7 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
         __syncwarp();
         if (good) {
           const size_t line = (static_cast<size_t>(page) * 2 + only) * p.plan.Hkv * p.ps +
-                            static_cast<size_t>(g.kvh) * p.ps + pos % p.ps;
+                            static_cast<size_t>(kvh) * p.ps + pos % p.ps;
           bulk_g2s(dst + lane * r * 128, p.kv + line * 128, r * 128, bar);
           bulk_g2s(dst + kTile * 128 + lane * r * 8, p.kv + p.code_bytes + line * 8, r * 8, bar);
         }
@@ -591,8 +601,16 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
 // What a page holds behind the sequence's last position must not meet a weight, not even a zero one
 // (0 * NaN): zeros go there in a segment's last V tile.  (q8_0 tiles are zeroed as they are decoded;
 // whole copies behind the sequence are zeros already.)
-template <int M>
-__device__ __forceinline__ bool trims(const Segment& g) { return M == kBf16 && (g.tile0 + g.n) * kTile > g.len; }
+template <int M, class Plan>
+__device__ __forceinline__ bool trims(const Params<Plan>& p, const Segment& g) {
+  return M == kBf16 && (p.tile_at(g, g.n - 1) + 1) * kTile > g.len;
+}
+// Pairs of KV heads, as units of two tiles, have a query tile and an output a stream.
+template <class Plan>
+__device__ __forceinline__ bool pairs(const Segment& g) {
+  if constexpr (Plan::kSpans) return g.pair;
+  else return false;
+}
 
 // Warp 10.  Query tiles: TT tokens x G heads x 64 dims a box, as soon as the last S of the segment
 // before has read the tiles -- under that segment's last softmax, values and epilogue.  And the trim
@@ -614,27 +632,29 @@ __device__ __forceinline__ void produce_q(const Params<Plan>& p, uint32_t base, 
         for (int h = 0; h < D / 64; ++h)
           tma_4d(base + h * kTile * 128 + w * kFew * 128, &p.qmap, h, g.kvh * p.plan.G, p.first_row(g), bar);
     } else if (lane == 0) {
-      for (int t = 0; t < (g.two ? 2 : 1); ++t) {
+      for (int t = 0; t < (g.two || pairs<Plan>(g) ? 2 : 1); ++t) {
         const uint32_t bar = smem_u32(&ctl->qraw[t]);
         mbar_expect(bar, p.plan.TT * p.plan.G * D * 2);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
-          tma_4d(base + t * L::kTileBytes + h * kTile * 128, &p.qmap, h, g.kvh * p.plan.G,
-                 p.first_row(g) + t * p.plan.TT, bar);
+          tma_4d(base + t * L::kTileBytes + h * kTile * 128, &p.qmap, h, p.head_at(g, t) * p.plan.G,
+                 p.first_row(g) + (g.two ? t * p.plan.TT : 0), bar);
       }
     }
     __syncwarp();
-    const uint32_t c = c0 + 2 * g.n - 1;
-    c0 += 2 * g.n;
-    if (trims<M>(g)) {
-      if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status)) return;
-      ++trimmed;
-      const int first = g.len - (g.tile0 + g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
-      const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
-      for (int n = first + lane / (D / 8); n < last; n += 256 / D) sts16(v + (n >> 3) * L::kGroup + (n & 7) * 128, 0, 0, 0, 0);
-      fence_async_smem();
-      warp_arrive(smem_u32(&ctl->trim));
+    if (trims<M>(p, g)) {
+      for (int k = pairs<Plan>(g) ? 1 : 0; k >= 0; --k) {
+        const uint32_t c = c0 + entry_of(g, 1, g.n - 1 - k);
+        if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status)) return;
+        ++trimmed;
+        const int first = g.len - p.tile_at(g, g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
+        const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
+        for (int n = first + lane / (D / 8); n < last; n += 256 / D) sts16(v + (n >> 3) * L::kGroup + (n & 7) * 128, 0, 0, 0, 0);
+        fence_async_smem();
+        warp_arrive(smem_u32(&ctl->trim));
+      }
     }
+    c0 += 2 * g.n;
   }
 }
 
@@ -731,7 +751,7 @@ __device__ __forceinline__ void decode(const Params<Plan>& p, uint32_t base, Ctl
         const int j = tile_of(g, i, v);
         if (!mbar_wait(smem_u32(&ctl->raw_full[raw.st]), raw.ph, ctl, p.status)) return;
         if (!mbar_wait(smem_u32(&ctl->empty[ring.st]), ring.ph ^ 1u, ctl, p.status)) return;
-        work(raw.st, ring.st, ctl->mask[(jg + j) % kMasks], g.len - (g.tile0 + j) * kTile);
+        work(raw.st, ring.st, ctl->mask[(jg + j) % kMasks], g.len - p.tile_at(g, j) * kTile);
         raw.step();
         ring.step();
       }
@@ -743,7 +763,7 @@ __device__ __forceinline__ void decode(const Params<Plan>& p, uint32_t base, Ctl
         const uint32_t e = c0 + entry_of(g, group, j), st = e % L::kStages, rs = raw.st + group * kRawFew;
         if (!mbar_wait(smem_u32(&ctl->raw_full[rs]), raw.ph, ctl, p.status)) return;
         if (!mbar_wait(smem_u32(&ctl->empty[st]), ((e / L::kStages) & 1u) ^ 1u, ctl, p.status)) return;
-        work(rs, st, static_cast<CtlFew*>(ctl)->raw_mask[rs], g.len - (g.tile0 + j) * kTile);
+        work(rs, st, static_cast<CtlFew*>(ctl)->raw_mask[rs], g.len - p.tile_at(g, j) * kTile);
         raw.step();
       }
     }
@@ -807,15 +827,16 @@ __device__ __forceinline__ void issue(const Params<Plan>& p, uint32_t base, Ctl*
     const uint32_t c = c0;
     auto wait_v = [&](int j) {
       wait_full(c + entry_of(g, 1, j));
-      if (j + 1 == g.n && trims<M>(g)) {
+      if ((j + 1 == g.n || (pairs<Plan>(g) && j + 2 == g.n)) && trims<M>(p, g)) {
         if (lane == 0) mbar_arrive(smem_u32(&ctl->landed));
         wait(&ctl->trim, tr & 1);
         ++tr;
       }
     };
     wait_q(0);
+    const int q1 = pairs<Plan>(g) ? 1 : 0;         // the query tile of stream 1
+    if (g.two || q1) wait_q(1);
     if (g.two) {
-      wait_q(1);
       wait_full(c);
       scores(0, 0, c);
       scores(1, 1, c);
@@ -841,7 +862,7 @@ __device__ __forceinline__ void issue(const Params<Plan>& p, uint32_t base, Ctl*
     } else {
       for (int j = 0; j < 2 && j < g.n; ++j) {
         wait_full(c + j);
-        scores(j, 0, c + j);
+        scores(j, j & q1, c + j);
         release(c + j);
       }
       if (g.n <= 2) done_q();
@@ -853,7 +874,7 @@ __device__ __forceinline__ void issue(const Params<Plan>& p, uint32_t base, Ctl*
         release(v);
         if (j + 2 < g.n) {                         // the next entry: K of tile j + 2
           wait_full(v + 1);
-          scores(t, 0, v + 1);
+          scores(t, t & q1, v + 1);
           release(v + 1);
           if (j + 3 == g.n) done_q();
         }
@@ -925,11 +946,11 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
   // q8_0: the next segment's rows of this warpgroup's tile
   auto take_q = [&](const Segment& n) {
     if constexpr (M != kBf16) {
-      if (!n.two && t == 1) return true;
+      if (!n.two && !pairs<Plan>(n) && t == 1) return true;
       if (!mbar_wait(smem_u32(&ctl->qraw[t]), qr & 1, ctl, p.status)) return false;
       ++qr;
       cq = p.c * convert_q<D, D / 8>(base + t * Layout<D, M>::kTileBytes, row);
-      if (!n.two) static_cast<CtlQ8*>(ctl)->rowc[row] = cq;
+      if (!n.two && !pairs<Plan>(n)) static_cast<CtlQ8*>(ctl)->rowc[row] = cq;
       fence_async_smem();
       warp_arrive(smem_u32(&ctl->qbar[t]));
     }
@@ -938,6 +959,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
   if (have && !take_q(g)) return;
   while (have) {
     const int trows = p.plan.TT * p.plan.G;
+    const bool solo = g.two || pairs<Plan>(g);     // an output of its own, not half of the streams'
     const int urow0 = g.two ? t * trows : 0;       // first row of the tile within the unit
     const int rows = min(trows, g.ntok * p.plan.G - urow0);
     const bool live = row < rows, any = warp * 32 < rows;
@@ -946,7 +968,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
     const int mine = g.two ? g.n : (g.n - t + 1) / 2;
     float c = cq;
     if constexpr (M != kBf16) {
-      if (!g.two && t == 1 && mine > 0) {          // stream 1 takes the constants of stream 0's rows
+      if (!solo && t == 1 && mine > 0) {           // stream 1 takes the constants of stream 0's rows
         if (!mbar_wait(smem_u32(&ctl->qbar[0]), qs & 1, ctl, p.status)) return;
         c = static_cast<CtlQ8*>(ctl)->rowc[row];
       }
@@ -956,14 +978,14 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < mine; ++i) {
       const int j = g.two ? i : 2 * i + t;
-      const int limit = pos - (g.tile0 + j) * kTile;           // last column this row sees
+      const int limit = pos - p.tile_at(g, j) * kTile;           // last column this row sees
       const bool edge = __any_sync(~0u, limit < kTile - 1);
       // parts of the cache: of this tile's columns the row does not see those from `sinks` to `below`
       int below = -1, sinks = 0;
       bool lower = false;
       if constexpr (Plan::kSpans) {
         below = live ? limit - p.plan.window : -1;
-        sinks = p.plan.sinks - (g.tile0 + j) * kTile;
+        sinks = p.plan.sinks - p.tile_at(g, j) * kTile;
         lower = __any_sync(~0u, below >= max(sinks, 0));
       }
       if (!mbar_wait(smem_u32(&ctl->sfull[t]), phase & 1, ctl, p.status)) return;
@@ -1070,8 +1092,8 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
 
     // m and l in powers of two; a row without a position has m = -inf and l = 0
     m = m == -INFINITY ? m : m * c;
-    float f[2] = {g.two && t == 1 ? 0.f : 1.f, g.two && t == 1 ? 1.f : 0.f};
-    if (!g.two) {
+    float f[2] = {solo && t == 1 ? 0.f : 1.f, solo && t == 1 ? 1.f : 0.f};
+    if (!solo) {
       // two streams of the same rows: both warpgroups read both outputs, each half of the columns
       ctl->ml[t][row] = make_float2(m, l);
       if (!join()) return;
@@ -1083,13 +1105,13 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
     }
     const int urow = urow0 + row;
     const int tok = urow * p.plan.by_G >> 16;
-    const int r = p.first_row(g) + tok, h = g.kvh * p.plan.G + urow - tok * p.plan.G;
+    const int r = p.first_row(g) + tok, h = p.head_at(g, t) * p.plan.G + urow - tok * p.plan.G;
     // no weight at all: a row without a position, or one whose scores are all -inf or beyond fp32
     bool odd = l == 0.f;
     if (any) {
       // (a warp's rows lie side by side)
-      int stride;
-      float4* part = p.template partial<D>(g, stride);
+      int stride, prow = urow;
+      float4* part = p.template partial<D>(g, t, stride, prow);
       // Stores to the output: the four lanes of a quad trade 16-byte pieces, so that each store
       // covers 64 bytes of 8 rows instead of 16 bytes of 32.  The rows of the quad's lanes:
       const int q4 = threadIdx.x & 3;
@@ -1097,13 +1119,13 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
 #pragma unroll
       for (int e = 0; e < 4; ++e) row_off[e] = __shfl_sync(~0u, live ? static_cast<uint32_t>(r * p.Hq + h) : ~0u, e, 4);
       const float inv = l == 0.f ? 0.f : 1.0f / l;
-      const int k0 = g.two ? 0 : t * (D / 2), k1 = g.two ? D : k0 + D / 2;
+      const int k0 = solo ? 0 : t * (D / 2), k1 = solo ? D : k0 + D / 2;
 #pragma unroll 1
       for (int k = k0; k < k1; k += 32) {
         float x[32];
-        tc_ld32(to + (g.two ? t * D : 0) + k, x);
+        tc_ld32(to + (solo ? t * D : 0) + k, x);
         tc_wait_ld();
-        if (!g.two) {
+        if (!solo) {
           if (g.n > 1) {
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
@@ -1122,7 +1144,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
           if (live) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              part[static_cast<size_t>((k + e) / 4) * stride + urow] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+              part[static_cast<size_t>((k + e) / 4) * stride + prow] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
         } else {
           uint32_t w[4][4];                        // piece e: columns k + 8 e
@@ -1156,11 +1178,11 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
         }
         __syncwarp();
       }
-      if (live && g.slot >= 0 && (g.two || t == 0))
-        reinterpret_cast<float2*>(part + static_cast<size_t>(D / 4) * stride)[urow] = make_float2(m, l);
+      if (live && g.slot >= 0 && (solo || t == 0))
+        reinterpret_cast<float2*>(part + static_cast<size_t>(D / 4) * stride)[prow] = make_float2(m, l);
     }
     // neither stream's next values may overwrite an output that the other warpgroup still reads
-    if (!g.two) {
+    if (!solo) {
       tc_before();
       if (!join()) return;
     }
@@ -1339,8 +1361,8 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
     const float m0 = ctl->ml[0][row].x, m1 = ctl->ml[1][row].x;
     const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
     const int r = p.first_row(g) + tok, h = g.kvh * p.plan.G + lane - tok * p.plan.G;
-    int stride;
-    float4* part = p.template partial<D>(g, stride);
+    int stride, prow = lane;                       // (no pairs: its row is its lane)
+    float4* part = p.template partial<D>(g, 0, stride, prow);
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     bool odd = live && g.slot < 0 && l == 0.f;     // (as in softmax)
     // each warpgroup half of the columns, 16 at a time, of which each warp sums up 4
@@ -1489,7 +1511,7 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ Pa
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Segment g;
   item_of(pl, p.seqs, pl.start[b + 1].item, g);
-  const int rows = g.ntok * pl.G, row0 = blockIdx.y * kRows;
+  const int hrows = g.ntok * pl.G, rows = pairs<Plan>(g) ? 2 * hrows : hrows, row0 = blockIdx.y * kRows;
   if (row0 >= rows) return;
   const int lrow = WIDE ? lane / kLanes : lane & 7, chunk = WIDE ? lane % kLanes : warp * 4 + (lane >> 3);
   const int urow = row0 + lrow;
@@ -1553,8 +1575,9 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ Pa
     for (int k = 0; k < n; ++k) add(*reinterpret_cast<const float4*>(at(k) + at_o), fac[lrow][k]);
   }
   const float L = den[lrow], inv = L == 0.f ? 0.f : 1.0f / L;
-  const int tok = urow * pl.by_G >> 16;
-  const int r = p.first_row(g) + tok, h = g.kvh * pl.G + urow - tok * pl.G;
+  const int second = pairs<Plan>(g) && urow >= hrows ? 1 : 0, hrow = urow - second * hrows;
+  const int tok = hrow * pl.by_G >> 16;
+  const int r = p.first_row(g) + tok, h = (g.kvh + second) * pl.G + hrow - tok * pl.G;
   acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   if (live)
     *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =

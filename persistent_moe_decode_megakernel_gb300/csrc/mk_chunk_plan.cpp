@@ -36,15 +36,15 @@ bool make_plan(const mk_cache_shape& c, const ChunkSeqs& q, const bool* use, Att
   }
   pl->item0[pl->n] = static_cast<int32_t>(items);
   pl->items = static_cast<int32_t>(items);
-  // visits the items in order: (item, its position tiles, whether it has two tiles of rows)
+  // visits the items in order: (item, its position tiles, its kind)
   auto each = [&](auto&& visit) {
     int item = 0;
     for (int i = 0; i < pl->n; ++i) {
       const int s = pl->seq[i], chunk = q.row0[s + 1] - q.row0[s], before = q.len[s] - chunk;
       for (int u = pl->units[i] - 1; u >= 0; --u) {
         const int end = std::min(chunk, (u + 1) * UT), t = (before + end - 1) / kTile + 1;
-        const bool two = end - u * UT > pl->TT;
-        for (int h = 0; h < pl->Hkv; ++h) visit(item++, t, two);
+        const int kind = end - u * UT > pl->TT ? kTwoTiles : kOneTile;
+        for (int h = 0; h < pl->Hkv; ++h) visit(item++, t, kind);
       }
     }
   };

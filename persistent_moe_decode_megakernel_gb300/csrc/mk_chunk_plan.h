@@ -46,6 +46,7 @@ struct Segment {
   // parts of the cache (mk_span_plan.h), where len, pos0 and tiles count places:
   int32_t entry, row0;               // its entry; first packed row
   int32_t head, gap;                 // place v is position v below `head`, v + gap from there on
+  bool pair;                         // KV heads kvh and kvh + 1: n counts both heads' tiles, in turn
 };
 
 __host__ __device__ inline void item_of(const AttnPlan& pl, const ChunkSeqs& q, int item, Segment& g) {
@@ -86,7 +87,7 @@ struct SegmentWalk {
       if (i >= pl.items) return false;   // (the last round may skip a block; no later round has items)
       item_of(pl, q, static_cast<int>(i), g);
       g.tile0 = 0;
-      g.n = g.tiles;
+      g.n = steps(pl, g, g.tiles);
       g.slot = whole_slot(pl, g);
       return true;
     }
@@ -95,11 +96,16 @@ struct SegmentWalk {
     item_of(pl, q, item, g);
     const int end = item == ei ? et : g.tiles;
     g.tile0 = tile;
-    g.n = end - tile;
+    g.n = steps(pl, g, end - tile);
     g.slot = tile == 0 && end == g.tiles ? whole_slot(pl, g) : 2 * b + (tile == 0 ? 1 : 0);
     ++item;
     tile = 0;
     return true;
+  }
+  template <class Plan>
+  __host__ __device__ static int steps(const Plan&, const Segment& g, int tiles) {
+    if constexpr (Plan::kSpans) return g.pair ? 2 * tiles : tiles;
+    else return tiles;
   }
   template <class Plan>
   __host__ __device__ static int whole_slot(const Plan& pl, const Segment& g) {

@@ -10,14 +10,16 @@
 namespace mk {
 
 // Costs in tenths of a microsecond, as measured: a position tile and what an item adds to its tiles
-// (query rows, the pipeline's filling and emptying, the epilogue), for items of two tiles of rows and
-// of one; what the ranges' partials and the second kernel add (more where units of two tiles are cut:
+// (query rows, the pipeline's filling and emptying, the epilogue), for items of one tile of rows and, second, of
+// two; what the ranges' partials and the second kernel add (more where units of two tiles are cut:
 // an 8192-token prompt, even to 1 % as whole items, took 383 us so and 393 us in ranges).  (152 blocks streaming from HBM.)
-constexpr int kTileCost[2] = {14, 17}, kItemCost[2] = {40, 60}, kMergeCost[2] = {80, 250};
+// Third, items of two KV heads: both heads' tiles.
+enum { kOneTile, kTwoTiles, kTwoHeads };
+constexpr int kTileCost[3] = {14, 17, 28}, kItemCost[3] = {40, 60, 40}, kMergeCost[2] = {80, 250};
 constexpr int kMinRange = 3;                // position tiles a block is worth
 constexpr int kMaxWalk = 1 << 17;            // items beyond which whole ones are even enough (and the walk long)
 
-// `each` visits the plan's items in order: (item, its position tiles, whether it has two tiles of rows).  Fills
+// `each` visits the plan's items in order: (item, its position tiles, which of the three kinds it is).  Fills
 // ranged, blocks, start and the cut items of which `joined` (item) is true; *floats is the size of their partials.
 template <class Plan, class Each, class Joined>
 void schedule(Plan* pl, bool any_two, int head_dim, size_t* floats, Each&& each, Joined&& joined) {
@@ -26,8 +28,8 @@ void schedule(Plan* pl, bool any_two, int head_dim, size_t* floats, Each&& each,
   // the slowest block of whole items, and the work altogether
   int64_t load[kMaxBlocks] = {}, tiles = 0, cost = 0;
   int at_block = 0, step = 1;
-  each([&](int, int t, bool two) {
-    const int64_t x = t * kTileCost[two] + kItemCost[two];
+  each([&](int, int t, int kind) {
+    const int64_t x = t * kTileCost[kind] + kItemCost[kind];
     tiles += t;
     cost += x;
     load[at_block] += x;
@@ -47,13 +49,13 @@ void schedule(Plan* pl, bool any_two, int head_dim, size_t* floats, Each&& each,
   int b = 1;
   int64_t at = 0;   // cost before item i
   pl->start[0] = {0, 0};
-  each([&](int item, int t, bool two) {
-    const int64_t end = at + kItemCost[two] + t * kTileCost[two];
+  each([&](int item, int t, int kind) {
+    const int64_t end = at + kItemCost[kind] + t * kTileCost[kind];
     for (; b < nb; ++b) {
       const int64_t x = cost * b / nb;
       if (x >= end) break;
       // (x within the item's own cost: the cut is before it; else after 0 <= . < t of its tiles)
-      const int64_t cut = x < at + kItemCost[two] ? 0 : (x - at - kItemCost[two]) / kTileCost[two];
+      const int64_t cut = x < at + kItemCost[kind] ? 0 : (x - at - kItemCost[kind]) / kTileCost[kind];
       pl->start[b] = {item, static_cast<int32_t>(cut)};
     }
     at = end;

@@ -9,130 +9,129 @@ namespace mk {
 namespace {
 
 // The rows of groups: each has the partials of its own sequence's positions and of the shared ones, in one piece or cut
-// over blocks.  A block takes 8 rows of a unit of the sequence's, a thread 4 columns of one; a warp's 8 rows lie side by
-// side in a partial.  Sums go over the partials of the sequence, then over those of the group, each in block order.
+// over blocks.  A warp takes 8 rows of a unit of the sequence's and 16 columns of each, a lane 4 columns of one: the
+// rows lie side by side in a partial.  It reads every (m, l) of its rows itself and has its first columns on their way
+// before it knows the factors, so that no warp waits for another.  Sums go over the partials of the sequence, then over
+// those of the group, each in block order.
+//
+// What it takes is latency, so the launch brings just what is looked up, and a block copies it into shared memory at once
+// (walked where it lies, in the constant bank, each step of a search was a miss of its own).
+struct JoinEntry {
+  int32_t kind, row0, rows, units, item0, part0, pair, pad;
+};
 template <int KINDS>
 struct Joins {
-  SpanPlan plan[KINDS];
+  // of each launch: where its blocks' ranges begin, item * 2 + whether inside the item (whole items: no block)
+  int32_t start[KINDS][kMaxBlocks + 1], blocks[KINDS], urows[KINDS];
   const float* part[KINDS];
-  int32_t n;
-  JoinSeq join[kMaxSeqs];
+  const float* whole;
+  int32_t n, Hkv, G, UT;
+  struct { JoinEntry own, over; int32_t job0, pad; } join[kMaxSeqs];
 };
 struct PartSet {                     // the partials of one row: `first`, then next, next + step, ..
   const float *first, *next;
   size_t step;
   int32_t n, stride, row;
   __device__ __forceinline__ const float* at(int k) const { return k == 0 ? first : next + (k - 1) * step; }
+  template <int D>
+  __device__ __forceinline__ float2 ml(int k) const {
+    return reinterpret_cast<const float2*>(at(k) + static_cast<size_t>(stride) * D)[row];
+  }
+  __device__ __forceinline__ float4 columns(int k, int chunk) const {
+    return reinterpret_cast<const float4*>(at(k))[static_cast<size_t>(chunk) * stride + row];
+  }
 };
-template <int D>
-__device__ __forceinline__ PartSet parts_of(const Params<SpanPlan>& p, const SpanPlan& pl, const float* part, int entry, int unit,
-                                            int kvh, int row) {
-  const SpanEntry& e = pl.e[entry];
-  const int item = e.item0 + (e.units - 1 - unit) * pl.Hkv + kvh, tok0 = unit * 2 * pl.TT;
+template <int D, int KINDS>
+__device__ __forceinline__ PartSet parts_of(const Joins<KINDS>& a, const JoinEntry& e, int unit, int kvh, int row) {
+  const int item = e.item0 + (e.units - 1 - unit) * (a.Hkv >> e.pair) + (kvh >> e.pair), tok0 = unit * a.UT, blocks = a.blocks[e.kind];
+  const int32_t* start = a.start[e.kind];
   PartSet s;
   s.row = row;
   s.n = 1;
   int b = 0;
-  if (pl.ranged) {
+  if (blocks > 0) {
     // the first block whose range ends behind the item's beginning, and those whose ranges end inside it
-    int lo = 0, hi = pl.blocks - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      const auto end = pl.start[mid + 1];
-      if (end.item > item || (end.item == item && end.tile > 0)) hi = mid;
-      else lo = mid + 1;
+    int hi = blocks - 1;
+    while (b < hi) {
+      const int mid = (b + hi) >> 1;
+      if (start[mid + 1] > 2 * item) hi = mid;
+      else b = mid + 1;
     }
-    b = lo;
-    while (b + s.n <= pl.blocks && pl.start[b + s.n].item == item) ++s.n;
+    while (b + s.n <= blocks && start[b + s.n] == 2 * item + 1) ++s.n;
   }
   if (s.n == 1) {
-    s.stride = min(e.rows - tok0, 2 * pl.TT) * pl.G;
-    s.first = s.next = p.whole + (static_cast<size_t>(e.part0 + tok0) * p.Hq + static_cast<size_t>(kvh) * s.stride) * (D + 4);
+    s.stride = min(e.rows - tok0, a.UT) * a.G;
+    s.first = s.next = a.whole + (static_cast<size_t>(e.part0 + tok0) * a.G * a.Hkv + static_cast<size_t>(kvh) * s.stride) * (D + 4);
     s.step = 0;
   } else {
-    const size_t slot = static_cast<size_t>(pl.urows) * (D + 4);
-    s.stride = pl.urows;
-    s.first = part + (2 * static_cast<size_t>(b) + 1) * slot;
-    s.next = part + 2 * (static_cast<size_t>(b) + 1) * slot;
+    const size_t slot = static_cast<size_t>(a.urows[e.kind]) * (D + 4);
+    s.row += (kvh & e.pair) * min(e.rows - tok0, a.UT) * a.G;
+    s.stride = a.urows[e.kind];
+    s.first = a.part[e.kind] + (2 * static_cast<size_t>(b) + 1) * slot;
+    s.next = a.part[e.kind] + 2 * (static_cast<size_t>(b) + 1) * slot;
     s.step = 2 * slot;
   }
   return s;
 }
 
 template <int D, int M, int KINDS>
-__global__ void __launch_bounds__(2 * D) join_kernel(const __grid_constant__ Params<SpanPlan> p,
-                                                     const __grid_constant__ Joins<KINDS> a) {
-  constexpr int kRows = 8, kWarps = 2 * D / 32, kMost = 2 * kMaxBlocks;
-  __shared__ PartSet sets[kRows][2];
-  __shared__ float fac[kRows][kMost], den[kRows];
+__global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) join_kernel(const __grid_constant__ Params<AttnPlan> p,
+                                                                     const __grid_constant__ Joins<KINDS> given) {
+  constexpr int kAhead = 3;          // partials of each set whose columns are read before the factors are known
+  __shared__ Joins<KINDS> a;
+  for (unsigned i = threadIdx.x; i < sizeof a / 8; i += 2 * D) {
+    uint2 w;                         // (by their generic address: constant reads would go one lane at a time)
+    asm volatile("ld.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(reinterpret_cast<const uint2*>(&given) + i));
+    reinterpret_cast<uint2*>(&a)[i] = w;
+  }
+  __syncthreads();
   int lo = 0, hi = a.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (a.join[mid].job0 <= static_cast<int>(blockIdx.x)) lo = mid;
     else hi = mid;
   }
-  const JoinSeq& j = a.join[lo];
-  const SpanPlan &own = a.plan[j.own.kind], &over = a.plan[j.over.kind];
-  const SpanEntry &e = own.e[j.own.entry], &o = over.e[j.over.entry];
-  const int G = own.G, UT = 2 * own.TT, rem = blockIdx.x - j.job0, unit = rem / own.Hkv, kvh = rem - unit * own.Hkv;
-  const int rows = min(e.rows - unit * UT, UT) * G, row0 = blockIdx.y * kRows;
+  const JoinEntry &e = a.join[lo].own, &o = a.join[lo].over;
+  const int G = a.G, UT = a.UT, rem = blockIdx.x - a.join[lo].job0, unit = rem / a.Hkv, kvh = rem - unit * a.Hkv;
+  const int rows = min(e.rows - unit * UT, UT) * G, row0 = blockIdx.y * 8;
   if (row0 >= rows) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = warp; r < kRows; r += kWarps) {
-    const int row = min(row0 + r, rows - 1);
-    if (lane < 2) {
-      if (lane == 0) {
-        sets[r][0] = parts_of<D>(p, own, a.part[j.own.kind], j.own.entry, unit, kvh, row);
-      } else {
-        const int tok = e.row0 + unit * UT + row / G - o.row0, ou = tok / UT;
-        sets[r][1] = parts_of<D>(p, over, a.part[j.over.kind], j.over.entry, ou, kvh, (tok - ou * UT) * G + row % G);
-      }
-    }
-    __syncwarp();
-    const int n0 = sets[r][0].n, n = n0 + sets[r][1].n;
-    auto ml = [&](int k) {
-      const PartSet& s = sets[r][k >= n0];
-      return reinterpret_cast<const float2*>(s.at(k >= n0 ? k - n0 : k) + static_cast<size_t>(s.stride) * D)[s.row];
-    };
-    float top = -INFINITY, L = 0.f;
-    for (int k = lane; k < n; k += 32) {
-      const float m = ml(k).x;
-      fac[r][k] = m;
-      top = fmaxf(top, m);
-    }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunk = warp * 4 + (lane >> 3);
+  const bool live = row0 + (lane & 7) < rows;
+  const int row = min(row0 + (lane & 7), rows - 1), tok = row / G, r = e.row0 + unit * UT + tok;
+  const int ou = (r - o.row0) / UT;
+  const PartSet set[2] = {parts_of<D>(a, e, unit, kvh, row),
+                          parts_of<D>(a, o, ou, kvh, (r - o.row0 - ou * UT) * G + row - tok * G)};
+  float4 held[2][kAhead];
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-    for (int k = lane; k < n; k += 32) {
-      const float m = fac[r][k], f = m == -INFINITY ? 0.f : ex2(m - top);
-      fac[r][k] = f;
-      L += f * ml(k).y;
-    }
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) L += __shfl_xor_sync(~0u, L, w);
-    if (lane == 0) den[r] = L;
-  }
-  __syncthreads();
-  const int lrow = lane & 7, chunk = warp * 4 + (lane >> 3), urow = row0 + lrow;
-  const bool live = urow < rows;
+    for (int k = 0; k < kAhead; ++k)
+      held[i][k] = k < set[i].n ? set[i].columns(k, chunk) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll 8
+    for (int k = 0; k < set[i].n; ++k) top = fmaxf(top, set[i].template ml<D>(k).x);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  int k0 = 0;
+  float L = 0.f;
+  auto add = [&](const float4 x, const float2 ml) {
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    L = fmaf(ml.y, f, L);
+    acc.x = fmaf(x.x, f, acc.x);
+    acc.y = fmaf(x.y, f, acc.y);
+    acc.z = fmaf(x.z, f, acc.z);
+    acc.w = fmaf(x.w, f, acc.w);
+  };
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const PartSet s = sets[lrow][i];
-    const size_t off = (static_cast<size_t>(chunk) * s.stride + s.row) * 4;
-#pragma unroll 8
-    for (int k = 0; k < s.n; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(s.at(k) + off);
-      const float f = fac[lrow][k0 + k];
-      acc.x = fmaf(x.x, f, acc.x);
-      acc.y = fmaf(x.y, f, acc.y);
-      acc.z = fmaf(x.z, f, acc.z);
-      acc.w = fmaf(x.w, f, acc.w);
-    }
-    k0 += s.n;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (k < set[i].n) add(held[i][k], set[i].template ml<D>(k));
+#pragma unroll 4
+    for (int k = kAhead; k < set[i].n; ++k) add(set[i].columns(k, chunk), set[i].template ml<D>(k));
   }
-  const float L = den[lrow], inv = L == 0.f ? 0.f : 1.0f / L;
-  const int tok = urow / G, r = e.row0 + unit * UT + tok, h = kvh * G + urow - tok * G;
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  const int h = kvh * G + row - tok * G;
   acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   if (live)
     *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
@@ -140,29 +139,43 @@ __global__ void __launch_bounds__(2 * D) join_kernel(const __grid_constant__ Par
   // (as in merge_kernel)
   const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
   const bool odd = live && (L == 0.f || !(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
-  __syncthreads();
+  __syncthreads();                   // (a row's columns are several warps')
   uint32_t done = 0;
   for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
-    const int who = __ffs(todo) - 1;
-    const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who), lr = __shfl_sync(~0u, lrow, who);
+    const int who = __ffs(todo) - 1, lr = who & 7;
+    const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
     if (!((done >> lr) & 1u)) exact_row<D, M>(p, rr, hh, nullptr);
     done |= 1u << lr;
   }
 }
 
+// `p`: a call's parameters without a plan (the rows that are worked out again see all their positions)
 template <int D, int M, int KINDS>
-cudaError_t join(const SpanCall& call, const Params<SpanPlan>& p, const float* const* part, cudaStream_t st) {
+cudaError_t join(const SpanCall& call, const Params<AttnPlan>& p, const float* const* part, const float* whole, cudaStream_t st) {
   Joins<KINDS> a;
+  static_assert(sizeof a % 8 == 0, "");
+  const int UT = 2 * call.plan[0].TT, G = call.plan[0].G;
   int most = 0;
   for (int k = 0; k < KINDS; ++k) {
-    a.plan[k] = call.plan[k];
+    const SpanPlan& pl = call.plan[k];
+    a.blocks[k] = pl.items > 0 && pl.ranged ? pl.blocks : 0;
+    for (int b = 0; b <= kMaxBlocks; ++b)
+      a.start[k][b] = b <= a.blocks[k] && a.blocks[k] ? 2 * pl.start[b].item + (pl.start[b].tile > 0) : 0;
+    a.urows[k] = pl.urows;
     a.part[k] = part[k];
   }
+  a.whole = whole;
   a.n = call.joins;
-  std::copy(call.join, call.join + call.joins, a.join);
+  a.Hkv = call.plan[0].Hkv;
+  a.G = G;
+  a.UT = UT;
+  auto entry = [&](const EntryRef& r) {
+    const SpanEntry& e = call.plan[r.kind].e[r.entry];
+    return JoinEntry{r.kind, e.row0, e.rows, e.units, e.item0, e.part0, e.pair, 0};
+  };
   for (int k = 0; k < call.joins; ++k) {
-    const SpanPlan& pl = call.plan[call.join[k].own.kind];
-    most = std::max(most, std::min(pl.e[call.join[k].own.entry].rows, 2 * pl.TT) * pl.G);
+    a.join[k] = {entry(call.join[k].own), entry(call.join[k].over), call.join[k].job0, 0};
+    most = std::max(most, std::min(a.join[k].own.rows, UT) * G);
   }
   join_kernel<D, M, KINDS><<<dim3(call.jobs, (most + 7) / 8), 2 * D, 0, st>>>(p, a);
   return cudaGetLastError();
@@ -212,10 +225,16 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
                               : launch<64, kBf16>(p, st);
     }
   }
-  if (e == cudaSuccess && call.joins > 0)
-    e = q8                  ? join<128, kQ8, kRowKinds>(call, p, part, st)
-        : c.head_dim == 128 ? join<128, kBf16, 1>(call, p, part, st)
-                            : join<64, kBf16, 1>(call, p, part, st);
+  if (e == cudaSuccess && call.joins > 0) {
+    Params<AttnPlan> all = {};
+    all.seqs = p.seqs;
+    fill_params(c, block_tables, q, q_stride, kv_layer, out, status_out, &all);
+    all.plan.G = p.plan.G;
+    all.plan.Hkv = p.plan.Hkv;
+    e = q8                  ? join<128, kQ8, kRowKinds>(call, all, part, p.whole, st)
+        : c.head_dim == 128 ? join<128, kBf16, 1>(call, all, part, p.whole, st)
+                            : join<64, kBf16, 1>(call, all, part, p.whole, st);
+  }
   return e == cudaSuccess ? MK_OK : chunk_fail(MK_ERR_CUDA, "attention over parts of the cache: %s", cudaGetErrorString(e));
 }
 
@@ -325,9 +344,9 @@ extern "C" int mk_plan_span_attention(const mk_cache_shape* shape, int32_t num_s
       while (walk.next(pl, seqs, g)) {
         if (n < max_segments) {
           const SpanEntry& e = pl.e[g.entry];
-          const int32_t row[18] = {k,     b,       g.entry, g.s,  g.row0,  g.ntok, g.kvh,    g.head,         g.gap,
-                                   g.pos0, g.len,  g.tile0, g.n,  g.tiles, g.slot, e.stage0, e.stage_tile0, e.stage_head};
-          std::copy(row, row + 18, segments + 18 * static_cast<size_t>(n));
+          const int32_t row[19] = {k,     b,       g.entry, g.s,  g.row0,  g.ntok, g.kvh,    g.head,         g.gap,
+                                   g.pos0, g.len,  g.tile0, g.pair ? g.n / 2 : g.n,  g.tiles, g.slot, e.stage0, e.stage_tile0, e.stage_head, g.pair};
+          std::copy(row, row + 19, segments + 19 * static_cast<size_t>(n));
         }
         ++n;
       }

@@ -17,6 +17,7 @@ namespace {
 //   kPageRows  else.
 constexpr int kStageTimes = 4;
 constexpr size_t kStageBytes = size_t(1) << 30;
+constexpr int kPairTiles = 4;
 
 struct Builder {
   const mk_cache_shape& c;
@@ -28,7 +29,7 @@ struct Builder {
   EntryRef add(SpanEntry e) {
     int kind = kPageRows;
     e.units = (e.rows + UT - 1) / UT;
-    e.stage0 = e.stage_tile0 = e.stage_head = 0;
+    e.pair = e.stage0 = e.stage_tile0 = e.stage_head = 0;
     if (c.flags & MK_FLAG_KV_Q8) {
       if (std::min(e.rows, UT) * G <= kFewUnit) kind = kFewRows;
       else if (stage(&e)) kind = kStagedRows;
@@ -40,11 +41,16 @@ struct Builder {
     return at;
   }
 
+  void fill(SpanPlan* pl) {
+    pl->Hkv = c.num_kv_heads;
+    pl->G = G;
+    pl->TT = kTile / G;
+    pl->by_G = 65536 / G + 1;   // exact below 2^9 rows
+  }
+
   bool stage(SpanEntry* e) {
     SpanPlan probe;
-    probe.G = G;
-    probe.TT = kTile / G;
-    probe.Hkv = c.num_kv_heads;
+    fill(&probe);
     probe.window = call->plan[0].window;
     probe.sinks = call->plan[0].sinks;
     probe.box = call->plan[0].box;
@@ -71,8 +77,22 @@ struct Builder {
 
   bool finish() {
     size_t at = 0;
+    // Two KV heads an item, where there are more items than blocks without that, or kPairTiles position tiles a block.
+    // (Few rows over q8_0 stand in all lanes of a block's, so that both streams are one head's.)
+    SpanPlan& pages = call->plan[kPageRows];
+    fill(&pages);
+    int64_t items = 0, tiles = 0;
+    Segment g;
+    for (int i = 0; i < pages.n; ++i) {
+      unit_of(pages, i, pages.e[i].units - 1, 0, g);     // (its longest)
+      items += static_cast<int64_t>(pages.e[i].units) * c.num_kv_heads;
+      tiles += static_cast<int64_t>(pages.e[i].units) * c.num_kv_heads * g.tiles;
+    }
+    const bool pair = c.num_kv_heads % 2 == 0 && (items > kMaxBlocks || tiles > kPairTiles * kMaxBlocks);
+    for (int i = 0; i < pages.n; ++i) pages.e[i].pair = pair && pages.e[i].rows <= kTile / G;
     for (int k = 0; k < kRowKinds; ++k) {
       SpanPlan& pl = call->plan[k];
+      fill(&pl);
       size_t floats = 0;
       if (!make_plan(c, &pl, &floats)) return false;
       call->part0[k] = at;
@@ -119,19 +139,17 @@ SpanEntry entry_of(const ChunkSeqs& q, int s) {
 }  // namespace
 
 bool make_plan(const mk_cache_shape& c, SpanPlan* pl, size_t* floats) {
-  pl->Hkv = c.num_kv_heads;
-  pl->G = c.num_q_heads / c.num_kv_heads;
-  pl->TT = kTile / pl->G;
-  pl->by_G = 65536 / pl->G + 1;   // exact below 2^9 rows
   pl->blocks = pl->ranged = pl->cuts = 0;
   *floats = 0;
   int most = 0;
+  bool any_two = false;
   int64_t items = 0;
   for (int i = 0; i < pl->n; ++i) {
     SpanEntry& e = pl->e[i];
-    most = std::max(most, std::min(e.rows, 2 * pl->TT));
+    most = std::max(most, std::min(e.rows, 2 * pl->TT) << e.pair);
+    any_two |= e.rows > pl->TT;
     e.item0 = static_cast<int32_t>(items);
-    items += static_cast<int64_t>(e.units) * pl->Hkv;
+    items += static_cast<int64_t>(e.units) * (pl->Hkv >> e.pair);
     if (items >= (int64_t(1) << 31)) return false;
   }
   pl->urows = most * pl->G;
@@ -142,10 +160,11 @@ bool make_plan(const mk_cache_shape& c, SpanPlan* pl, size_t* floats) {
     for (int i = 0; i < pl->n; ++i)
       for (int u = pl->e[i].units - 1; u >= 0; --u) {
         unit_of(*pl, i, u, 0, g);
-        for (int h = 0; h < pl->Hkv; ++h) visit(item++, g.tiles, g.two);
+        const int kind = g.two ? kTwoTiles : g.pair ? kTwoHeads : kOneTile;
+        for (int h = 0; h < pl->Hkv >> pl->e[i].pair; ++h) visit(item++, g.tiles, kind);
       }
   };
-  schedule(pl, most > pl->TT, c.head_dim, floats, each,
+  schedule(pl, any_two, c.head_dim, floats, each,
            [&](int item) { return pl->e[entry_of_item(*pl, item)].part0 < 0; });
   return true;
 }
@@ -164,63 +183,67 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
   reset(c, kNoWindow, 0, call);
   Builder build(c, call);
   const int UT = build.UT;
-  // Whether a group's rows go over its shared positions together: where that saves its blocks more time (the costs of
+  // Runs of a group's sequences whose rows do not fill a unit of their own (with others', they share one), between those
+  // that do.  A run's rows go over the shared positions together where that saves its blocks more time (the costs of
   // mk_schedule.h, over all blocks) than the second kernel takes with the partials of its rows.
-  bool shared[kMaxSeqs] = {};
-  int32_t common[kMaxSeqs];
-  for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++]) {
-    common[i] = prefix_lens[i] / c.page_size * c.page_size;
-    const int rows = q.row0[s0 + group_seqs[i]] - q.row0[s0], tiles = (common[i] + kTile - 1) / kTile;
-    auto cost = [&](int rows, int item) {
-      const int full = rows / UT, rest = rows % UT;
-      int64_t x = static_cast<int64_t>(full) * (tiles * kTileCost[0] + item * kItemCost[0]);
-      if (rest > UT / 2) x += tiles * kTileCost[0] + item * kItemCost[0];
-      else if (rest) x += tiles * kTileCost[1] + item * kItemCost[1];
-      return x;
-    };
-    int64_t apart = 0;
-    int with = 0;
-    for (int s = s0; s < s0 + group_seqs[i]; ++s) {
-      apart += cost(q.row0[s + 1] - q.row0[s], 0);
-      with += q.row0[s + 1] > q.row0[s];
-    }
-    const int64_t saved = (apart - cost(rows, 1)) * c.num_kv_heads / kMaxBlocks;
-    const int64_t bytes = static_cast<int64_t>(rows) * c.num_q_heads * (c.head_dim + 4) * 16;
-    shared[i] = with > 1 && tiles > 0 && saved > kJoinCost + bytes / kJoinBytes;
-  }
-  // entries in the order of SpanPlan: shared positions, sequences of their own, sequences of groups
+  int32_t common[kMaxSeqs];                              // whole pages that a sequence's run goes over together, or 0
   EntryRef over[kMaxSeqs];
-  int order[kMaxSeqs];
   for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++]) {
-    if (!shared[i]) continue;
-    SpanEntry e = {};
-    e.seq = s0;
-    e.row0 = q.row0[s0];
-    e.rows = q.row0[s0 + group_seqs[i]] - e.row0;
-    e.before = e.len = common[i];
-    e.part0 = call->whole_rows;
-    call->whole_rows += e.rows;
-    over[i] = build.add(e);
+    const int positions = prefix_lens[i] / c.page_size * c.page_size, tiles = (positions + kTile - 1) / kTile;
+    auto cost = [&](int rows, int item) {                // (a unit of more than half its rows has two tiles)
+      const int full = rows / UT + (rows % UT > UT / 2), rest = rows % UT > 0 && rows % UT <= UT / 2;
+      return static_cast<int64_t>(full) * (tiles * kTileCost[kTwoTiles] + item * kItemCost[kTwoTiles]) +
+             rest * (tiles * kTileCost[kOneTile] + item * kItemCost[kOneTile]);
+    };
+    for (int s = s0, end = s0 + group_seqs[i]; s < end;) {
+      const int first = s;
+      int with = 0;
+      int64_t apart = 0;
+      for (; s < end && q.row0[s + 1] - q.row0[s] < UT; ++s) {
+        apart += cost(q.row0[s + 1] - q.row0[s], 0);
+        with += q.row0[s + 1] > q.row0[s];
+        common[s] = 0;
+      }
+      const int rows = q.row0[s] - q.row0[first];
+      if (with > 1 && tiles > 0) {
+        const int64_t saved = (apart - cost(rows, 1)) * c.num_kv_heads / kMaxBlocks;
+        const int64_t bytes = static_cast<int64_t>(rows) * c.num_q_heads * (c.head_dim + 4) * 16;
+        if (saved > kJoinCost + bytes / kJoinBytes) {
+          SpanEntry e = {};
+          e.seq = first;
+          e.row0 = q.row0[first];
+          e.rows = rows;
+          e.before = e.len = positions;
+          e.part0 = call->whole_rows;
+          call->whole_rows += rows;
+          const EntryRef at = build.add(e);
+          for (int k = first; k < s; ++k) {
+            common[k] = positions;
+            over[k] = at;
+          }
+        }
+      }
+      if (s < end && s == first) common[s++] = 0;         // fills units of its own
+    }
   }
+  // after the shared positions, sequences that write the output and then those of runs (the order of SpanPlan)
+  int order[kMaxSeqs];
+  const int n = by_length(q, order);
   for (int pass = 0; pass < 2; ++pass) {
-    int group_of[kMaxSeqs] = {};
-    for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++])
-      for (int s = s0; s < s0 + group_seqs[i]; ++s) group_of[s] = i;
-    const int n = by_length(q, order);
     for (int k = 0; k < n; ++k) {
-      const int s = order[k], i = group_of[s];
-      if (shared[i] != (pass == 1)) continue;
+      const int s = order[k];
+      if ((common[s] > 0) != (pass == 1)) continue;
       SpanEntry e = entry_of(q, s);
       if (pass == 0) {
         build.add(e);
         continue;
       }
-      e.from = common[i];
+      e.from = common[s];
       e.part0 = call->whole_rows;
       call->whole_rows += e.rows;
       JoinSeq& j = call->join[call->joins++];
       j.own = build.add(e);
-      j.over = over[i];
+      j.over = over[s];
     }
   }
   if (!build.finish()) return false;

@@ -9,6 +9,10 @@
 // of a copy's positions.  A window's tiles begin where its first row's does, not at a multiple of 128, and the sinks
 // take the room of a copy or two instead of a tile of their own.
 //
+// An entry of one tile of rows (a few tokens, as in decoding) takes two KV heads at a time where their number is even: the
+// block's two streams, which are even and odd position tiles of an item otherwise, are the heads then, so that short items
+// are half as many and end without a join of the streams.
+//
 // Rows of a group have two items' worth of weights, the shared positions' and their own sequence's: such segments
 // write a partial (m, l, O) each, which a second kernel joins.
 #ifndef MK_SPAN_PLAN_H
@@ -28,6 +32,7 @@ struct SpanEntry {
   int32_t before;                    // position of its first row (shared positions: their number, so that all are before)
   int32_t from, len;                 // positions [from, len); from is a multiple of a copy's
   int32_t units, item0;
+  int32_t pair;                      // 1: an item is two KV heads
   int32_t part0;                     // rows of partials before its own, -1: it writes the output
   int32_t stage0, stage_tile0, stage_head;   // q8_0 staged: its first tile in the workspace; the position tile that
                                              // follows the first stage_head ones there
@@ -65,6 +70,7 @@ __host__ __device__ inline void unit_of(const SpanPlan& pl, int i, int unit, int
   g.entry = i;
   g.unit = unit;
   g.kvh = kvh;
+  g.pair = e.pair != 0;
   g.tok0 = unit * UT;
   g.row0 = e.row0 + g.tok0;
   g.ntok = e.rows - g.tok0 < UT ? e.rows - g.tok0 : UT;
@@ -82,11 +88,11 @@ __host__ __device__ inline void unit_of(const SpanPlan& pl, int i, int unit, int
 }
 
 __host__ __device__ inline void item_of(const SpanPlan& pl, const ChunkSeqs&, int item, Segment& g) {
-  const int i = entry_of_item(pl, item), rem = item - pl.e[i].item0, back = rem / pl.Hkv;
-  unit_of(pl, i, pl.e[i].units - 1 - back, rem - back * pl.Hkv, g);
+  const int i = entry_of_item(pl, item), rem = item - pl.e[i].item0, heads = pl.Hkv >> pl.e[i].pair, back = rem / heads;
+  unit_of(pl, i, pl.e[i].units - 1 - back, (rem - back * heads) << pl.e[i].pair, g);
 }
 
-// Fills items and schedule of pl (whose n, e without item0, window, sinks and box are given); *floats is the size of
+// Fills items and schedule of pl (all else of which is given); *floats is the size of
 // the cut items' partials.  False: more items than a call takes.
 bool make_plan(const mk_cache_shape& c, SpanPlan* pl, size_t* floats);
 

@@ -142,8 +142,13 @@ def test_binding_refuses_on_the_host():
 
 # ---------------------------------------------------------------- schedules
 COLS = ("launch", "block", "entry", "table", "row0", "ntok", "kvh", "head", "gap", "pos0", "len", "tile0", "n", "tiles", "slot",
-        "stage0", "stage_tile0", "stage_head")
+        "stage0", "stage_tile0", "stage_head", "pair")
 WHOLE = 304
+
+
+def heads(segs):
+    """Position tiles over all KV heads."""
+    return sum(g["n"] * (1 + g["pair"]) for g in segs)
 
 
 def segments(sh, cl, sl, **kw):
@@ -190,7 +195,8 @@ def check_plan(sh, cl, sl, window=None, sinks=0, groups=(), shared=()):
             if not own:                                          # another sequence's table: shared whole pages only
                 assert group_of[s] == group_of[g["table"]]
                 assert np.all(pos[seen] < shared[group_of[s]] // ps * ps)
-            count[s][g["kvh"], r - row0[s], pos[seen]] += 1
+            for h in range(g["kvh"], g["kvh"] + 1 + g["pair"]):
+                count[s][h, r - row0[s], pos[seen]] += 1
         if 0 <= g["slot"] < WHOLE:
             assert g["slot"] == 2 * g["block"] + (g["tile0"] == 0) and g["slot"] not in slots[g["launch"]]
             slots[g["launch"]].add(g["slot"])
@@ -204,10 +210,16 @@ def check_plan(sh, cl, sl, window=None, sinks=0, groups=(), shared=()):
     for s, c in enumerate(count):
         assert np.array_equal(c, np.broadcast_to(visible[s][None], c.shape)), s
     # who writes the output: a row that one entry has does so by itself, of two neither
-    entries = {}
+    entries, hkv_even = {}, Hkv % 2 == 0
+    units = {}
+    for g in segs:
+        units.setdefault((g["launch"], g["entry"]), set()).add(g["row0"])
+    units = {k: len(v) for k, v in units.items()}
     for g in segs:
         for r in range(g["row0"], g["row0"] + g["ntok"]):
-            entries.setdefault((r, g["kvh"]), set()).add((g["launch"], g["entry"]))
+            assert not g["pair"] or (hkv_even and g["ntok"] <= TT and g["launch"] == 0 and units[g["launch"], g["entry"]] == 1)
+            for h in range(g["kvh"], g["kvh"] + 1 + g["pair"]):
+                entries.setdefault((r, h), set()).add((g["launch"], g["entry"]))
     for g in segs:
         many = {len(entries[r, g["kvh"]]) for r in range(g["row0"], g["row0"] + g["ntok"])}
         assert many in ({1}, {2})
@@ -249,7 +261,7 @@ def test_a_long_shared_prefix_is_read_once():
     # rows (two units of a KV head), not for each sequence
     sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 12)
     segs = segments(sh, [1] * 64, [32768 + 100] * 64, group_seqs=[64], prefix_lens=[32768])
-    assert sum(g["n"] for g in segs) == 4 * 2 * 256 + 64 * 4
+    assert heads(segs) == 4 * 2 * 256 + 64 * 4
     # of two sequences over a few positions each takes its own way
     segs = segments(sh, [1] * 2, [200] * 2, group_seqs=[2], prefix_lens=[128])
     assert all(g["slot"] == -1 and g["len"] == 200 for g in segs)
@@ -259,10 +271,21 @@ def test_window_plan_skips_the_hidden_middle():
     sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 14)
     segs = segments(sh, [1], [131073], window=1000, sinks=4)
     # positions 130073..131072, from a multiple of 16 on: 1009 places, and 16 of the sinks' copy
-    assert [(g["head"], g["len"], g["tiles"]) for g in segs if g["tile0"] == 0] == [(16, 1025, 9)] * 4
-    assert sum(g["n"] for g in segs) == 4 * 9
+    assert [(g["head"], g["len"], g["tiles"], g["pair"]) for g in segs if g["tile0"] == 0] == [(16, 1025, 9, 0)] * 4
+    assert heads(segs) == 4 * 9
     segs = segments(sh, [8192], [8192], window=1024, sinks=4)
     assert max(g["tiles"] for g in segs) == 9
+
+
+def test_window_plan_pairs_heads_of_many_tokens():
+    # a block's two streams are two KV heads where there are more items than blocks without that, or four tiles a block
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 14)
+    for n, ln, tiles, pair in ((64, 5000, 9, 1), (17, 5000, 9, 1), (16, 5000, 9, 0), (1, 5000, 9, 0), (39, 100, 1, 1),
+                               (38, 100, 1, 0)):
+        segs = segments(sh, [1] * n, [ln] * n, window=1024, sinks=4)
+        assert {g["pair"] for g in segs} == {pair} and heads(segs) == n * 4 * tiles, (n, ln)
+    sh.num_q_heads, sh.num_kv_heads = 24, 3
+    assert {g["pair"] for g in segments(sh, [1] * 64, [5000] * 64, window=1024)} == {0}
 
 
 def test_plans_of_the_largest_calls():
@@ -270,9 +293,9 @@ def test_plans_of_the_largest_calls():
     sh = shape(max_pages_per_seq=1 << 26)
     assert mk.window_attention_workspace(sh, [1 << 20], [1 << 30], 1 << 30, 1 << 30) >= 0
     segs = segments(sh, [1], [1 << 30], window=(1 << 31) - 1, sinks=(1 << 31) - 1)
-    assert sum(g["n"] for g in segs) == 2 * (1 << 23)
+    assert heads(segs) == 2 * (1 << 23)
     segs = segments(sh, [2], [1 << 30], window=5, sinks=16)
     assert [(g["head"], g["gap"], g["len"]) for g in segs] == [(16, (1 << 30) - 32, 32)] * 2
     segs = segments(sh, [1, 1], [1 << 30, 1 << 30], group_seqs=[2], prefix_lens=[(1 << 30) - 1])
     # 2^30 - 16 shared positions, and 16 of each sequence's own
-    assert sum(g["n"] for g in segs) == 2 * (1 << 23) + 2 * 2
+    assert heads(segs) == 2 * (1 << 23) + 2 * 2
