@@ -97,10 +97,10 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
       rc = encode_pages(c.head_dim, c.num_kv_heads, c.page_size, c.num_pages, true, kv_layer, p.box, &p.map);
       if (rc) return rc;
     }
-    e = few                 ? launch<128, kQ8Few>(p, st)
-        : q8                ? launch<128, kQ8>(p, st)
-        : c.head_dim == 128 ? launch<128, kBf16>(p, st)
-                            : launch<64, kBf16>(p, st);
+    e = few                 ? launch_merged<128, kQ8Few>(p, st)
+        : q8                ? launch_merged<128, kQ8>(p, st)
+        : c.head_dim == 128 ? launch_merged<128, kBf16>(p, st)
+                            : launch_merged<64, kBf16>(p, st);
   }
   if (e == cudaSuccess && plan.staged.items > 0) {
     p.plan = plan.staged;
@@ -110,7 +110,7 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
     stage_kernel<128><<<dim3(plan.tiles.first[plan.tiles.n], 2 * c.num_kv_heads), kStageThreads, 0, st>>>(
         p, static_cast<__half*>(workspace), plan.tiles);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch<128, kStaged>(p, st);
+    if (e == cudaSuccess) e = launch_merged<128, kStaged>(p, st);
   }
   return e == cudaSuccess ? MK_OK : chunk_fail(MK_ERR_CUDA, "chunk attention: %s", cudaGetErrorString(e));
 }

@@ -83,23 +83,26 @@ struct StageTiles {
   int32_t seq[kMaxSeqs], first[kMaxSeqs + 1];   // (parts of the cache: entries)
 };
 
-template <class Plan>
-struct Params {
-  CUtensorMap map;                  // bf16 pages (see encode_pages)
-  CUtensorMap qmap;                 // query rows (see encode_queries)
+// What a call's kernels share.
+struct CallParams {
   ChunkSeqs seqs;
-  Plan plan;
   const uint8_t* kv;
   const int32_t* bt;
   int32_t* status;
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* out;
+  size_t code_bytes;
+  int32_t Hq, ps, P, maxpg;
+};
+template <class Plan>
+struct Params : CallParams {
+  CUtensorMap map;                  // bf16 pages (see encode_pages)
+  CUtensorMap qmap;                 // query rows (see encode_queries)
+  Plan plan;
   float* part;                      // partials of cut items, two slots a block
   float* whole;                     // and (parts of the cache) of whole items that are joined with another
-  size_t code_bytes;
   int32_t stage0[Plan::kSpans ? 1 : kMaxSeqs];   // staged sequences: first tile in the workspace (entries hold their own)
-  int32_t Hq, ps, P, maxpg;
   int32_t box;                      // positions of one copy: a power of two that divides ps
   float c;                          // log2(e) / sqrt(D)
 
@@ -299,7 +302,7 @@ struct Ctl {
   uint64_t qraw[2], qbar[2], qfree;  // query tiles: landed, in the operand type (bf16: qraw itself), read by the last S
   uint64_t sfull[2], pfull[2][2];    // S of a tile (stream); the halves of its P
   uint64_t landed, trim;             // a last V tile to be trimmed: landed, trimmed
-  uint64_t ofull, join;
+  uint64_t ofull[2], join;           // O of a tile (stream) is complete
   uint32_t tmem, abort;
   uint32_t beat;                     // counts while a softmax warp works a row out plainly (exact_row)
   uint32_t mask[kMasks];             // per tile, a bit per 8 positions: the page is in range
@@ -345,6 +348,13 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ct
 // The whole warp waits and agrees on the outcome (and is converged for what follows).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status) {
   return __all_sync(~0u, mbar_try(bar, parity) || mbar_wait_slow(bar, parity, ctl, status));
+}
+
+// The block is in its last epilogue: a kernel behind this one that waits for it itself may be launched meanwhile.
+// (Launched from the beginning on, it cost kernels of many short segments more than it saved: 57.3 -> 60.9 us.)
+template <class Plan>
+__device__ __forceinline__ void let_next_start() {
+  if constexpr (Plan::kSpans) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // One arrival for the warp, after all its lanes' work so far.
@@ -418,11 +428,11 @@ __host__ __device__ constexpr bool ring_holds(int N) {
 // Row r, query head h by one warp: 32 positions at a time, a lane per position for the scores,
 // D/32 dims per lane for the output; fp32, and no position beyond the row's own is touched.
 // `beat`: counted every 1024 positions (the rest of the block may be waiting), or NULL.
-template <int D, int M, class Plan>
-__device__ __noinline__ void exact_row(const Params<Plan>& p, int r, int h, volatile uint32_t* beat) {
+template <int D, int M, class P>
+__device__ __noinline__ void exact_row(const P& p, int r, int h, volatile uint32_t* beat) {
   const int lane = threadIdx.x & 31, kvh = h / p.plan.G, s = seq_of_row(p.seqs, r);
   int n = p.seqs.len[s] - p.seqs.row0[s + 1] + r + 1, first = 0, skip = 0;
-  if constexpr (Plan::kSpans) {                      // the first positions, and those of the window
+  if constexpr (decltype(p.plan)::kSpans) {                      // the first positions, and those of the window
     skip = max(n - p.plan.window, 0);
     first = min(p.plan.sinks, skip);
     skip -= first;
@@ -443,7 +453,7 @@ __device__ __noinline__ void exact_row(const Params<Plan>& p, int r, int h, vola
     int64_t line = -1;
     float x = -INFINITY;
     if (t < n) {
-      const int pos = Plan::kSpans && t >= first ? t + skip : t;
+      const int pos = decltype(p.plan)::kSpans && t >= first ? t + skip : t;
       const int page = __ldg(p.bt + static_cast<size_t>(s) * p.maxpg + pos / p.ps);
       if (page >= 0 && page < p.P) {
         line = (static_cast<int64_t>(page) * 2 * p.plan.Hkv + kvh) * p.ps + pos % p.ps;
@@ -847,6 +857,7 @@ __device__ __forceinline__ void issue(const Params<Plan>& p, uint32_t base, Ctl*
         const uint32_t v = c + 2 * j + 1;
         wait_v(j);
         values(0, v, j > 0);
+        if (!more) tc_commit(smem_u32(&ctl->ofull[0]));
         if (more) {
           wait_full(v + 1);
           scores(0, 0, v + 1);
@@ -871,6 +882,7 @@ __device__ __forceinline__ void issue(const Params<Plan>& p, uint32_t base, Ctl*
         const uint32_t v = c + entry_of(g, 1, j);
         wait_v(j);
         values(t, v, j > 1);
+        if (q1 && j + 2 == g.n) tc_commit(smem_u32(&ctl->ofull[0]));
         release(v);
         if (j + 2 < g.n) {                         // the next entry: K of tile j + 2
           wait_full(v + 1);
@@ -880,7 +892,8 @@ __device__ __forceinline__ void issue(const Params<Plan>& p, uint32_t base, Ctl*
         }
       }
     }
-    tc_commit(smem_u32(&ctl->ofull));
+    if (!g.two && !q1) tc_commit(smem_u32(&ctl->ofull[0]));   // (both streams' rows are both warpgroups')
+    tc_commit(smem_u32(&ctl->ofull[1]));
     c0 += 2 * g.n;
   }
 }
@@ -924,6 +937,23 @@ __device__ __forceinline__ float convert_q(uint32_t tile, int row) {
     }
   }
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
+// The columns of 32 that a row sees, a bit each: those up to `limit`, without those from `sinks` to `below`, of pages
+// in range (a bit of `mask` for 8 columns).
+__device__ __forceinline__ uint32_t first_bits(int n) {       // n <= 0: none; n >= 32: all
+  uint32_t x;
+  asm("shl.b32 %0, 1, %1;" : "=r"(x) : "r"(max(n, 0)));      // (shifts of 32 and more give 0)
+  return x - 1u;
+}
+__device__ __forceinline__ uint32_t seen32(int limit, int below, int sinks, uint32_t mask) {
+  const uint32_t pages = (((mask & 15u) * 0x00204081u) & 0x01010101u) * 0xffu;
+  return first_bits(min(limit, 31) + 1) & ~(first_bits(min(below, 31) + 1) & ~first_bits(sinks)) & pages;
+}
+__device__ __forceinline__ void hide32(float* s, uint32_t seen) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!((seen >> k) & 1u)) s[k] = -INFINITY;
 }
 
 template <int D, int M, class Plan>
@@ -997,20 +1027,14 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
 #pragma unroll
         for (int k = 0; k < kTile; k += 32) tc_ld32(ts + k, s + k);
         tc_wait_ld();
-        if (edge) {
+        if (edge || lower || mask != 0xffffu) {
+          // 32 columns at a time, those that some row of the warp does not see whole (a comparison or three for every
+          // column of the tile instead cost an 8192-token prompt through a window of 1024 11 us of 126)
 #pragma unroll
-          for (int k = 0; k < kTile; ++k)
-            if (k > limit) s[k] = -INFINITY;
-        }
-        if (lower) {
-#pragma unroll
-          for (int k = 0; k < kTile; ++k)
-            if (k <= below && k >= sinks) s[k] = -INFINITY;
-        }
-        if (mask != 0xffffu) {
-#pragma unroll
-          for (int k = 0; k < kTile; ++k)
-            if (!((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
+          for (int k = 0; k < kTile; k += 32) {
+            const uint32_t m = seen32(limit - k, below - k, sinks - k, mask >> (k >> 3));
+            if (__any_sync(~0u, m != ~0u)) hide32(s + k, m);
+          }
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -1083,11 +1107,12 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
         warp_arrive(smem_u32(&ctl->pfull[t][1]));
       }
     }
-    if (!mbar_wait(smem_u32(&ctl->ofull), seg & 1, ctl, p.status)) return;
+    have = walk.next(p.plan, p.seqs, next);        // (under the last products)
+    if (!mbar_wait(smem_u32(&ctl->ofull[t]), seg & 1, ctl, p.status)) return;
     tc_after();
     jg += g.n;
+    if (!have) let_next_start<Plan>();
     // the next segment's rows, so that its first scores run under this one's epilogue
-    have = walk.next(p.plan, p.seqs, next);
     if (have && !take_q(next)) return;
 
     // m and l in powers of two; a row without a position has m = -inf and l = 0
@@ -1269,21 +1294,7 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
       float s[32];
       tc_ld32(ts + 32 * warp, s);
       tc_wait_ld();
-      if (edge) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (k > limit) s[k] = -INFINITY;
-      }
-      if (lower) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (k <= below && k >= sinks) s[k] = -INFINITY;
-      }
-      if (mask != 15u) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (!((mask >> (k >> 3)) & 1u)) s[k] = -INFINITY;
-      }
+      if (edge || lower || mask != 15u) hide32(s, seen32(limit, below, sinks, mask));
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
       for (int k = 4; k < 28; k += 8) {
@@ -1340,10 +1351,11 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
       const float2 sm = add2(sum[0], sum[1]);
       l += sm.x + sm.y;
     }
-    if (!mbar_wait(smem_u32(&ctl->ofull), seg & 1, ctl, p.status)) return;
+    if (!mbar_wait(smem_u32(&ctl->ofull[t]), seg & 1, ctl, p.status)) return;
     tc_after();
     jg += g.n;
     have = walk.next(p.plan, p.seqs, next);
+    if (!have) let_next_start<Plan>();
     if (have && t == 0 && !take_q()) return;
 
     // m and l in powers of two; a part without a position has m = -inf and l = 0
@@ -1440,13 +1452,18 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
     mbar_init(smem_u32(&ctl->qfree), 1);
     mbar_init(smem_u32(&ctl->landed), 1);
     mbar_init(smem_u32(&ctl->trim), 1);
-    mbar_init(smem_u32(&ctl->ofull), 1);
+    mbar_init(smem_u32(&ctl->ofull[0]), 1);
+    mbar_init(smem_u32(&ctl->ofull[1]), 1);
     mbar_init(smem_u32(&ctl->join), 8);
     if constexpr (M == kQ8Few)
       for (int t = 0; t < 2; ++t) mbar_init(smem_u32(&static_cast<CtlFew*>(ctl)->shared[t]), 4);
     ctl->abort = 0u;
     ctl->beat = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if constexpr (Plan::kSpans) {
+    if (threadIdx.x == 320) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.qmap));
+    if (threadIdx.x == 256) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.map));
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
@@ -1502,16 +1519,16 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
 // Wide (units of few rows, cut into many parts): a block takes 128 / D rows, a warp every eighth
 // partial, whose loads are all on their way before the factors are known.  Else a block takes 8
 // rows, a thread 4 columns of one, a warp's 8 rows side by side in a partial; the parts are few.
-template <int D, int M, bool WIDE, class Plan>
-__global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ Params<Plan> p) {
+template <int D, int M, bool WIDE>
+__global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ Params<AttnPlan> p) {
   constexpr int kWarps = 2 * D / 32, kLanes = D / 4, kRows = WIDE ? 32 / kLanes : 8;
   constexpr int kMine = WIDE ? (kMaxBlocks + kWarps - 1) / kWarps : 1, kAtOnce = 8;
-  const Plan& pl = p.plan;
+  const AttnPlan& pl = p.plan;
   const int b = pl.cut_block[blockIdx.x], n = pl.cut_parts[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Segment g;
   item_of(pl, p.seqs, pl.start[b + 1].item, g);
-  const int hrows = g.ntok * pl.G, rows = pairs<Plan>(g) ? 2 * hrows : hrows, row0 = blockIdx.y * kRows;
+  const int rows = g.ntok * pl.G, row0 = blockIdx.y * kRows;
   if (row0 >= rows) return;
   const int lrow = WIDE ? lane / kLanes : lane & 7, chunk = WIDE ? lane % kLanes : warp * 4 + (lane >> 3);
   const int urow = row0 + lrow;
@@ -1575,9 +1592,8 @@ __global__ void __launch_bounds__(2 * D) merge_kernel(const __grid_constant__ Pa
     for (int k = 0; k < n; ++k) add(*reinterpret_cast<const float4*>(at(k) + at_o), fac[lrow][k]);
   }
   const float L = den[lrow], inv = L == 0.f ? 0.f : 1.0f / L;
-  const int second = pairs<Plan>(g) && urow >= hrows ? 1 : 0, hrow = urow - second * hrows;
-  const int tok = hrow * pl.by_G >> 16;
-  const int r = p.first_row(g) + tok, h = (g.kvh + second) * pl.G + hrow - tok * pl.G;
+  const int tok = urow * pl.by_G >> 16;
+  const int r = p.first_row(g) + tok, h = g.kvh * pl.G + urow - tok * pl.G;
   acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   if (live)
     *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
@@ -1753,6 +1769,22 @@ void fill_params(const mk_cache_shape& c, const int32_t* block_tables, const voi
   p->c = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.head_dim)));
 }
 
+// A kernel that may be launched while the one before it on the stream still runs, for which it waits itself.
+template <class... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D, int M, class Plan>
 cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
   // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
@@ -1768,15 +1800,21 @@ cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   attn_kernel<D, M, Plan><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
-  e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+// And the kernel that merges what its ranges cut.
+template <int D, int M>
+cudaError_t launch_merged(const Params<AttnPlan>& p, cudaStream_t st) {
+  const cudaError_t e = launch<D, M>(p, st);
   if (e != cudaSuccess || p.plan.cuts == 0) return e;
   constexpr int kMerge = M == kBf16 ? kBf16 : kQ8;
   // (plans with units of two tiles cut an item in few parts)
   if (p.plan.urows <= kTile / 2) {
     constexpr int kRows = 128 / D;
-    merge_kernel<D, kMerge, true, Plan><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
+    merge_kernel<D, kMerge, true><<<dim3(p.plan.cuts, (p.plan.urows + kRows - 1) / kRows), 2 * D, 0, st>>>(p);
   } else {
-    merge_kernel<D, kMerge, false, Plan><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
+    merge_kernel<D, kMerge, false><<<dim3(p.plan.cuts, (p.plan.urows + 7) / 8), 2 * D, 0, st>>>(p);
   }
   return cudaGetLastError();
 }

@@ -71,9 +71,10 @@ __host__ __device__ inline void item_of(const AttnPlan& pl, const ChunkSeqs& q, 
 
 // Walks one block's segments.  (Whole items' partials: see mk_span_plan.h.)
 struct SegmentWalk {
-  int b, k, item, tile;
+  int b, k, item, tile, entry;
   template <class Plan>
-  __host__ __device__ SegmentWalk(const Plan& pl, int block) : b(block), k(0), item(0), tile(0) {
+  __host__ __device__ SegmentWalk(const Plan& pl, int block) : b(block), k(0), item(0), tile(0), entry(0) {
+    if constexpr (Plan::kSpans) entry = pl.start[b].entry;
     if (pl.ranged) {
       item = pl.start[b].item;
       tile = pl.start[b].tile;
@@ -85,7 +86,7 @@ struct SegmentWalk {
       const int64_t i = static_cast<int64_t>(k) * pl.blocks + (k & 1 ? pl.blocks - 1 - b : b);
       ++k;
       if (i >= pl.items) return false;   // (the last round may skip a block; no later round has items)
-      item_of(pl, q, static_cast<int>(i), g);
+      look(pl, q, static_cast<int>(i), g);
       g.tile0 = 0;
       g.n = steps(pl, g, g.tiles);
       g.slot = whole_slot(pl, g);
@@ -93,7 +94,7 @@ struct SegmentWalk {
     }
     const int ei = pl.start[b + 1].item, et = pl.start[b + 1].tile;
     if (item > ei || (item == ei && tile >= et)) return false;
-    item_of(pl, q, item, g);
+    look(pl, q, item, g);
     const int end = item == ei ? et : g.tiles;
     g.tile0 = tile;
     g.n = steps(pl, g, end - tile);
@@ -101,6 +102,16 @@ struct SegmentWalk {
     ++item;
     tile = 0;
     return true;
+  }
+  // (items rise: an entry is looked for from the last one's on)
+  template <class Plan>
+  __host__ __device__ void look(const Plan& pl, const ChunkSeqs& q, int i, Segment& g) {
+    if constexpr (Plan::kSpans) {
+      while (entry + 1 < pl.n && pl.e[entry + 1].item0 <= i) ++entry;
+      item_of_entry(pl, entry, i, g);
+    } else {
+      item_of(pl, q, i, g);
+    }
   }
   template <class Plan>
   __host__ __device__ static int steps(const Plan&, const Segment& g, int tiles) {

@@ -8,16 +8,27 @@
 namespace mk {
 namespace {
 
-// The rows of groups: each has the partials of its own sequence's positions and of the shared ones, in one piece or cut
-// over blocks.  A warp takes 8 rows of a unit of the sequence's and 16 columns of each, a lane 4 columns of one: the
-// rows lie side by side in a partial.  It reads every (m, l) of its rows itself and has its first columns on their way
-// before it knows the factors, so that no warp waits for another.  Sums go over the partials of the sequence, then over
-// those of the group, each in block order.
+// Joins partials: of a cut item's rows (in block order), and of the rows of groups, which have those of their own
+// sequence's positions and then those of the shared ones, each in one piece or cut.
 //
-// What it takes is latency, so the launch brings just what is looked up, and a block copies it into shared memory at once
-// (walked where it lies, in the constant bank, each step of a search was a miss of its own).
+// 8 rows lie side by side in a partial, so 8 lanes read 128 bytes of one.  Few rows (kSplit): the warp's other lanes
+// take every fourth partial each, a warp has 4 columns, a block half of all, and every read is on its way before any is waited for: what it
+// takes is the latency of one.  Many rows: they take other columns, and a block goes over several groups of 8 rows.
+//
+// The launch brings just what is looked up, and a block copies it into shared memory at once, before it waits for the
+// kernel that writes the partials (walked where it lies, in the constant bank, each step of a search was a miss of its
+// own).
+struct Sight {
+  static constexpr bool kSpans = true;
+  int32_t G, Hkv, window, sinks;
+};
+struct JoinParams : CallParams {     // what the rows that are worked out again need
+  Sight plan;
+};
 struct JoinEntry {
-  int32_t kind, row0, rows, units, item0, part0, pair, pad;
+  int32_t row0, rows, units, item0, part0;
+  int8_t kind, pair;
+  int16_t pad;
 };
 template <int KINDS>
 struct Joins {
@@ -25,8 +36,9 @@ struct Joins {
   int32_t start[KINDS][kMaxBlocks + 1], blocks[KINDS], urows[KINDS];
   const float* part[KINDS];
   const float* whole;
-  int32_t n, Hkv, G, UT;
-  struct { JoinEntry own, over; int32_t job0, pad; } join[kMaxSeqs];
+  int32_t cuts, n, Hkv, G, UT, pad;
+  struct { JoinEntry own, over; int32_t job0, pad; } join[kMaxSeqs];   // sequences of groups
+  struct { int32_t row0; int16_t rows, kvh; uint8_t kind, pair, block, parts; } cut[KINDS * kMaxBlocks];   // cut items
 };
 struct PartSet {                     // the partials of one row: `first`, then next, next + step, ..
   const float *first, *next;
@@ -41,14 +53,25 @@ struct PartSet {                     // the partials of one row: `first`, then n
     return reinterpret_cast<const float4*>(at(k))[static_cast<size_t>(chunk) * stride + row];
   }
 };
+// of a cut item that block b begins
+template <int D, int KINDS>
+__device__ __forceinline__ PartSet cut_parts(const Joins<KINDS>& a, int kind, int b, int n, int row) {
+  const size_t slot = static_cast<size_t>(a.urows[kind]) * (D + 4);
+  PartSet s;
+  s.n = n;
+  s.row = row;
+  s.stride = a.urows[kind];
+  s.first = a.part[kind] + (2 * static_cast<size_t>(b) + 1) * slot;
+  s.next = a.part[kind] + 2 * (static_cast<size_t>(b) + 1) * slot;
+  s.step = 2 * slot;
+  return s;
+}
 template <int D, int KINDS>
 __device__ __forceinline__ PartSet parts_of(const Joins<KINDS>& a, const JoinEntry& e, int unit, int kvh, int row) {
-  const int item = e.item0 + (e.units - 1 - unit) * (a.Hkv >> e.pair) + (kvh >> e.pair), tok0 = unit * a.UT, blocks = a.blocks[e.kind];
+  const int item = e.item0 + (e.units - 1 - unit) * (a.Hkv >> e.pair) + (kvh >> e.pair), tok0 = unit * a.UT;
+  const int blocks = a.blocks[e.kind], rows = min(e.rows - tok0, a.UT) * a.G;
   const int32_t* start = a.start[e.kind];
-  PartSet s;
-  s.row = row;
-  s.n = 1;
-  int b = 0;
+  int n = 1, b = 0;
   if (blocks > 0) {
     // the first block whose range ends behind the item's beginning, and those whose ranges end inside it
     int hi = blocks - 1;
@@ -57,105 +80,159 @@ __device__ __forceinline__ PartSet parts_of(const Joins<KINDS>& a, const JoinEnt
       if (start[mid + 1] > 2 * item) hi = mid;
       else b = mid + 1;
     }
-    while (b + s.n <= blocks && start[b + s.n] == 2 * item + 1) ++s.n;
+    while (b + n <= blocks && start[b + n] == 2 * item + 1) ++n;
   }
-  if (s.n == 1) {
-    s.stride = min(e.rows - tok0, a.UT) * a.G;
-    s.first = s.next = a.whole + (static_cast<size_t>(e.part0 + tok0) * a.G * a.Hkv + static_cast<size_t>(kvh) * s.stride) * (D + 4);
-    s.step = 0;
-  } else {
-    const size_t slot = static_cast<size_t>(a.urows[e.kind]) * (D + 4);
-    s.row += (kvh & e.pair) * min(e.rows - tok0, a.UT) * a.G;
-    s.stride = a.urows[e.kind];
-    s.first = a.part[e.kind] + (2 * static_cast<size_t>(b) + 1) * slot;
-    s.next = a.part[e.kind] + 2 * (static_cast<size_t>(b) + 1) * slot;
-    s.step = 2 * slot;
-  }
+  if (n > 1) return cut_parts<D>(a, e.kind, b, n, row + (kvh & e.pair) * rows);
+  PartSet s;
+  s.n = 1;
+  s.row = row;
+  s.stride = rows;
+  s.first = s.next = a.whole + (static_cast<size_t>(e.part0 + tok0) * a.G * a.Hkv + static_cast<size_t>(kvh) * rows) * (D + 4);
+  s.step = 0;
   return s;
 }
 
-template <int D, int M, int KINDS>
-__global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) join_kernel(const __grid_constant__ Params<AttnPlan> p,
-                                                                     const __grid_constant__ Joins<KINDS> given) {
-  constexpr int kAhead = 3;          // partials of each set whose columns are read before the factors are known
+template <int D, int M, int KINDS, bool kSplit>
+__global__ void __launch_bounds__(kSplit ? 4 * D : 2 * D, kSplit ? 256 / D : 512 / D)
+    join_kernel(const __grid_constant__ JoinParams p, const __grid_constant__ Joins<KINDS> given) {
+  constexpr int kThreads = kSplit ? 4 * D : 2 * D, kEvery = kSplit ? 4 : 1;   // a lane takes every kEvery-th partial,
+  constexpr int kAhead = kSplit ? 5 : 3;                                      // that many at once
   __shared__ Joins<KINDS> a;
-  for (unsigned i = threadIdx.x; i < sizeof a / 8; i += 2 * D) {
+  __shared__ PartSet sets[2][8][2];
+  for (unsigned i = threadIdx.x; i < sizeof a / 8; i += kThreads) {
     uint2 w;                         // (by their generic address: constant reads would go one lane at a time)
     asm volatile("ld.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(reinterpret_cast<const uint2*>(&given) + i));
     reinterpret_cast<uint2*>(&a)[i] = w;
   }
   __syncthreads();
-  int lo = 0, hi = a.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.join[mid].job0 <= static_cast<int>(blockIdx.x)) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, UT = a.UT;
+  const int chunk = kSplit ? static_cast<int>(blockIdx.z) * (D / 8) + warp : warp * 4 + (lane >> 3), mine = kSplit ? lane >> 3 : 0;
+  const bool cut = static_cast<int>(blockIdx.x) < a.cuts;
+  int lo = 0, unit = 0, kvh, hrows, rows, r0;
+  if (cut) {
+    const auto& c = a.cut[blockIdx.x];
+    kvh = c.kvh;
+    hrows = c.rows * G;
+    rows = hrows << c.pair;
+    r0 = c.row0;
+  } else {
+    const int job = blockIdx.x - a.cuts;
+    int hi = a.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.join[mid].job0 <= job) lo = mid;
+      else hi = mid;
+    }
+    const JoinEntry& e = a.join[lo].own;
+    const int rem = job - a.join[lo].job0;
+    unit = rem / a.Hkv;
+    kvh = rem - unit * a.Hkv;
+    hrows = rows = min(e.rows - unit * UT, UT) * G;
+    r0 = e.row0 + unit * UT;
   }
-  const JoinEntry &e = a.join[lo].own, &o = a.join[lo].over;
-  const int G = a.G, UT = a.UT, rem = blockIdx.x - a.join[lo].job0, unit = rem / a.Hkv, kvh = rem - unit * a.Hkv;
-  const int rows = min(e.rows - unit * UT, UT) * G, row0 = blockIdx.y * 8;
-  if (row0 >= rows) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunk = warp * 4 + (lane >> 3);
-  const bool live = row0 + (lane & 7) < rows;
-  const int row = min(row0 + (lane & 7), rows - 1), tok = row / G, r = e.row0 + unit * UT + tok;
-  const int ou = (r - o.row0) / UT;
-  const PartSet set[2] = {parts_of<D>(a, e, unit, kvh, row),
-                          parts_of<D>(a, o, ou, kvh, (r - o.row0 - ou * UT) * G + row - tok * G)};
-  float4 held[2][kAhead];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      held[i][k] = k < set[i].n ? set[i].columns(k, chunk) : make_float4(0.f, 0.f, 0.f, 0.f);
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll 8
-    for (int k = 0; k < set[i].n; ++k) top = fmaxf(top, set[i].template ml<D>(k).x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-  auto add = [&](const float4 x, const float2 ml) {
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    L = fmaf(ml.y, f, L);
-    acc.x = fmaf(x.x, f, acc.x);
-    acc.y = fmaf(x.y, f, acc.y);
-    acc.z = fmaf(x.z, f, acc.z);
-    acc.w = fmaf(x.w, f, acc.w);
+  // where a group of 8 rows finds its partials: 16 lanes of one warp look it up, a group ahead
+  auto find = [&](int row0, int into) {
+    if (warp != 0 || lane >= 16) return;
+    const int row = min(row0 + (lane & 7), rows - 1), over = lane >> 3;
+    if (cut) {
+      const auto& c = a.cut[blockIdx.x];
+      sets[into][lane & 7][over] = cut_parts<D>(a, c.kind, c.block, c.parts, row);
+      if (over) sets[into][lane & 7][over].n = 0;
+    } else {
+      const JoinEntry& o = a.join[lo].over;
+      const int tok = row / G, ot = r0 + tok - o.row0, ou = ot / UT;
+      sets[into][lane & 7][over] = over ? parts_of<D>(a, o, ou, kvh, (ot - ou * UT) * G + row - tok * G)
+                                        : parts_of<D>(a, a.join[lo].own, unit, kvh, row);
+    }
   };
+  int row0 = blockIdx.y * 8, turn = 0;
+  if (row0 >= rows) return;
+  find(row0, 0);
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (; row0 < rows; row0 += gridDim.y * 8, turn ^= 1) {
+    const bool live = row0 + (lane & 7) < rows;
+    const int row = min(row0 + (lane & 7), rows - 1), second = row >= hrows ? 1 : 0, hrow = row - second * hrows;
+    const int tok = hrow / G, r = r0 + tok, h = (kvh + second) * G + hrow - tok * G;
+    const PartSet &own = sets[turn][lane & 7][0], &over = sets[turn][lane & 7][1];
+    const int n = own.n + over.n;    // partials, the own ones first
+    auto ml = [&](int k) { return k < own.n ? own.template ml<D>(k) : over.template ml<D>(k - own.n); };
+    auto columns = [&](int k) { return k < own.n ? own.columns(k, chunk) : over.columns(k - own.n, chunk); };
+    float4 held[kAhead];
+    float2 held_ml[kAhead];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = mine + i * kEvery;
+      held_ml[i] = k < n ? ml(k) : make_float2(-INFINITY, 0.f);
+      held[i] = k < n ? columns(k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    find(row0 + gridDim.y * 8, turn ^ 1);
+    float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (k < set[i].n) add(held[i][k], set[i].template ml<D>(k));
+    for (int i = 0; i < kAhead; ++i) top = fmaxf(top, held_ml[i].x);
 #pragma unroll 4
-    for (int k = kAhead; k < set[i].n; ++k) add(set[i].columns(k, chunk), set[i].template ml<D>(k));
-  }
-  const float inv = L == 0.f ? 0.f : 1.0f / L;
-  const int h = kvh * G + row - tok * G;
-  acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (live)
-    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
-        make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
-  // (as in merge_kernel)
-  const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
-  const bool odd = live && (L == 0.f || !(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
-  __syncthreads();                   // (a row's columns are several warps')
-  uint32_t done = 0;
-  for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
-    const int who = __ffs(todo) - 1, lr = who & 7;
-    const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
-    if (!((done >> lr) & 1u)) exact_row<D, M>(p, rr, hh, nullptr);
-    done |= 1u << lr;
+    for (int k = mine + kAhead * kEvery; k < n; k += kEvery) top = fmaxf(top, ml(k).x);
+    if constexpr (kSplit) {
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    auto add = [&](const float4 x, const float2 ml) {
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      L = fmaf(ml.y, f, L);
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z);
+      acc.w = fmaf(x.w, f, acc.w);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) add(held[i], held_ml[i]);
+#pragma unroll 4
+    for (int k = mine + kAhead * kEvery; k < n; k += kEvery) add(columns(k), ml(k));
+    if constexpr (kSplit) {
+#pragma unroll
+      for (int w = 8; w < 32; w <<= 1) {
+        L += __shfl_xor_sync(~0u, L, w);
+        acc.x += __shfl_xor_sync(~0u, acc.x, w);
+        acc.y += __shfl_xor_sync(~0u, acc.y, w);
+        acc.z += __shfl_xor_sync(~0u, acc.z, w);
+        acc.w += __shfl_xor_sync(~0u, acc.w, w);
+      }
+    }
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (live && mine == 0)
+      *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
+          make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+    // (as in merge_kernel; a row's columns are several warps')
+    const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
+    const bool odd = live && (L == 0.f || !(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
+    if (__syncthreads_or(odd)) {
+      uint32_t done = 0;
+      for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
+        const int who = __ffs(todo) - 1, lr = who & 7;
+        const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
+        if (!((done >> lr) & 1u)) exact_row<D, M>(p, rr, hh, nullptr);
+        done |= 1u << lr;
+      }
+    }
   }
 }
-
-// `p`: a call's parameters without a plan (the rows that are worked out again see all their positions)
 template <int D, int M, int KINDS>
-cudaError_t join(const SpanCall& call, const Params<AttnPlan>& p, const float* const* part, const float* whole, cudaStream_t st) {
+cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const float* const* part, cudaStream_t st) {
   Joins<KINDS> a;
   static_assert(sizeof a % 8 == 0, "");
   const int UT = 2 * call.plan[0].TT, G = call.plan[0].G;
+  JoinParams p;                         // what the rows that are worked out again need
+  static_cast<CallParams&>(p) = given;
+  p.plan.G = G;
+  p.plan.Hkv = call.plan[0].Hkv;
+  p.plan.window = call.plan[0].window;
+  p.plan.sinks = call.plan[0].sinks;
   int most = 0;
+  int64_t groups = 0;                // of 8 rows
+  a.cuts = 0;
   for (int k = 0; k < KINDS; ++k) {
     const SpanPlan& pl = call.plan[k];
     a.blocks[k] = pl.items > 0 && pl.ranged ? pl.blocks : 0;
@@ -163,22 +240,45 @@ cudaError_t join(const SpanCall& call, const Params<AttnPlan>& p, const float* c
       a.start[k][b] = b <= a.blocks[k] && a.blocks[k] ? 2 * pl.start[b].item + (pl.start[b].tile > 0) : 0;
     a.urows[k] = pl.urows;
     a.part[k] = part[k];
+    for (int i = 0; i < (pl.items > 0 ? pl.cuts : 0); ++i) {
+      Segment g;
+      const int item = pl.start[pl.cut_block[i] + 1].item;
+      item_of_entry(pl, entry_of_item(pl, item), item, g);
+      auto& x = a.cut[a.cuts++];
+      x.row0 = g.row0;
+      x.rows = static_cast<int16_t>(g.ntok);
+      x.kvh = static_cast<int16_t>(g.kvh);
+      x.kind = static_cast<uint8_t>(k);
+      x.pair = g.pair;
+      x.block = pl.cut_block[i];
+      x.parts = pl.cut_parts[i];
+      const int rows = g.ntok * G << x.pair;
+      most = std::max(most, rows);
+      groups += (rows + 7) / 8;
+    }
   }
-  a.whole = whole;
+  a.whole = given.whole;
   a.n = call.joins;
   a.Hkv = call.plan[0].Hkv;
   a.G = G;
   a.UT = UT;
   auto entry = [&](const EntryRef& r) {
     const SpanEntry& e = call.plan[r.kind].e[r.entry];
-    return JoinEntry{r.kind, e.row0, e.rows, e.units, e.item0, e.part0, e.pair, 0};
+    return JoinEntry{e.row0, e.rows, e.units, e.item0, e.part0, r.kind, static_cast<int8_t>(e.pair), 0};
   };
   for (int k = 0; k < call.joins; ++k) {
     a.join[k] = {entry(call.join[k].own), entry(call.join[k].over), call.join[k].job0, 0};
-    most = std::max(most, std::min(a.join[k].own.rows, UT) * G);
+    const int rows = std::min(a.join[k].own.rows, UT) * G;
+    most = std::max(most, rows);
+    groups += static_cast<int64_t>(a.join[k].own.units) * a.Hkv * ((rows + 7) / 8);
   }
-  join_kernel<D, M, KINDS><<<dim3(call.jobs, (most + 7) / 8), 2 * D, 0, st>>>(p, a);
-  return cudaGetLastError();
+  const int jobs = a.cuts + call.jobs;
+  if (jobs == 0) return cudaSuccess;
+  // few: blocks of half the columns, all at once or nearly; many: some ten blocks an SM, each over several groups of rows
+  if (groups <= kMaxBlocks * (256 / D))
+    return launch_after(join_kernel<D, M, KINDS, true>, dim3(jobs, (most + 7) / 8, 2), 4 * D, 0, st, p, a);
+  const int y = std::max(1, std::min((most + 7) / 8, (10 * kMaxBlocks + jobs - 1) / jobs));
+  return launch_after(join_kernel<D, M, KINDS, false>, dim3(jobs, y), 2 * D, 0, st, p, a);
 }
 
 int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, const int32_t* block_tables, const void* q,
@@ -225,16 +325,10 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
                               : launch<64, kBf16>(p, st);
     }
   }
-  if (e == cudaSuccess && call.joins > 0) {
-    Params<AttnPlan> all = {};
-    all.seqs = p.seqs;
-    fill_params(c, block_tables, q, q_stride, kv_layer, out, status_out, &all);
-    all.plan.G = p.plan.G;
-    all.plan.Hkv = p.plan.Hkv;
-    e = q8                  ? join<128, kQ8, kRowKinds>(call, all, part, p.whole, st)
-        : c.head_dim == 128 ? join<128, kBf16, 1>(call, all, part, p.whole, st)
-                            : join<64, kBf16, 1>(call, all, part, p.whole, st);
-  }
+  if (e == cudaSuccess)
+    e = q8                  ? join<128, kQ8, kRowKinds>(call, p, part, st)
+        : c.head_dim == 128 ? join<128, kBf16, 1>(call, p, part, st)
+                            : join<64, kBf16, 1>(call, p, part, st);
   return e == cudaSuccess ? MK_OK : chunk_fail(MK_ERR_CUDA, "attention over parts of the cache: %s", cudaGetErrorString(e));
 }
 

@@ -4,11 +4,26 @@
 
 #include <algorithm>
 
-#include "mk_schedule.h"
-
 namespace mk {
 
 namespace {
+
+// Costs in tenths of a microsecond, from timelines of a block's segments: a position tile, and what a segment adds to
+// its tiles (the first scores and weights, the epilogue), for segments of one tile of rows, of two, and of one of two KV
+// heads (both heads' tiles).  Of q8_0 the tiles' are what decoding takes.
+enum { kOneTile, kTwoTiles, kTwoHeads };
+struct Costs {
+  int tile[3], segment[3];
+};
+constexpr Costs kCosts[kRowKinds] = {{{11, 17, 21}, {42, 46, 42}}, {{11, 17, 0}, {42, 46, 0}}, {{13, 0, 0}, {45, 0, 0}}};
+constexpr Costs kQ8Costs = {{25, 34, 50}, {50, 60, 50}};
+const Costs& costs(const mk_cache_shape& c, int kind) {
+  return kind == kPageRows && (c.flags & MK_FLAG_KV_Q8) ? kQ8Costs : kCosts[kind];
+}
+// What cut items cost besides: the second kernel, and the bytes of partials that it and the first one move in a tenth.
+constexpr int64_t kJoinCost = 45, kJoinBytes = 250000;
+constexpr int kMinRange = 3;                 // position tiles a block is worth
+constexpr int kMaxRuns = 4096;               // units beyond which whole items are even enough
 
 // Launches are of one kind of operand each (SpanCall); a sequence's rows take
 //   kFewRows  over q8_0, where its units have at most 32 rows of a KV head,
@@ -94,7 +109,7 @@ struct Builder {
       SpanPlan& pl = call->plan[k];
       fill(&pl);
       size_t floats = 0;
-      if (!make_plan(c, &pl, &floats)) return false;
+      if (!make_plan(c, k, &pl, &floats)) return false;
       call->part0[k] = at;
       at += floats;
     }
@@ -111,7 +126,7 @@ void reset(const mk_cache_shape& c, int window, int sinks, SpanCall* call) {
     pl.sinks = sinks;
     pl.box = span_box(c);
   }
-  call->staged = call->stage_tiles = call->joins = 0;
+  call->staged = call->stage_tiles = call->joins = call->jobs = 0;
   call->stage_bytes = 0;
   call->whole_rows = 0;
 }
@@ -138,34 +153,120 @@ SpanEntry entry_of(const ChunkSeqs& q, int s) {
 
 }  // namespace
 
-bool make_plan(const mk_cache_shape& c, SpanPlan* pl, size_t* floats) {
+bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) {
   pl->blocks = pl->ranged = pl->cuts = 0;
   *floats = 0;
-  int most = 0;
-  bool any_two = false;
-  int64_t items = 0;
+  const Costs& cost = costs(c, kind);
+  // runs of items that are alike: a unit's KV heads
+  struct Run {
+    int32_t tiles, items;
+    int16_t type, rows;
+    int32_t whole;                   // 1: its items write the output unless they are cut
+  };
+  Run run[kMaxRuns];
+  int runs = 0, most = 0;
+  int64_t items = 0, tiles = 0, work = 0;
   for (int i = 0; i < pl->n; ++i) {
     SpanEntry& e = pl->e[i];
     most = std::max(most, std::min(e.rows, 2 * pl->TT) << e.pair);
-    any_two |= e.rows > pl->TT;
     e.item0 = static_cast<int32_t>(items);
-    items += static_cast<int64_t>(e.units) * (pl->Hkv >> e.pair);
+    const int heads = pl->Hkv >> e.pair;
+    items += static_cast<int64_t>(e.units) * heads;
     if (items >= (int64_t(1) << 31)) return false;
+    if (e.units > kMaxRuns - runs) {
+      runs = kMaxRuns + 1;
+      continue;
+    }
+    Segment g;
+    for (int u = e.units - 1; u >= 0; --u) {
+      unit_of(*pl, i, u, 0, g);
+      const int type = g.two ? kTwoTiles : g.pair ? kTwoHeads : kOneTile;
+      run[runs++] = {g.tiles, heads, static_cast<int16_t>(type), static_cast<int16_t>(g.ntok * pl->G << e.pair), e.part0 < 0};
+      tiles += static_cast<int64_t>(g.tiles) * heads;
+      work += (static_cast<int64_t>(g.tiles) * cost.tile[type] + cost.segment[type]) * heads;
+    }
   }
   pl->urows = most * pl->G;
   pl->items = static_cast<int32_t>(items);
-  auto each = [&](auto&& visit) {
-    int item = 0;
-    Segment g;
-    for (int i = 0; i < pl->n; ++i)
-      for (int u = pl->e[i].units - 1; u >= 0; --u) {
-        unit_of(*pl, i, u, 0, g);
-        const int kind = g.two ? kTwoTiles : g.pair ? kTwoHeads : kOneTile;
-        for (int h = 0; h < pl->Hkv >> pl->e[i].pair; ++h) visit(item++, g.tiles, kind);
+  pl->blocks = std::min<int32_t>(pl->items, kMaxBlocks);
+  if (items > 0 && runs <= kMaxRuns) {
+    // the slowest block of whole items
+    int64_t load[kMaxBlocks] = {};
+    for (int i = 0, b = 0, step = 1; i < runs; ++i)
+      for (int k = 0; k < run[i].items; ++k) {
+        load[b] += static_cast<int64_t>(run[i].tiles) * cost.tile[run[i].type] + cost.segment[run[i].type];
+        b += step;                           // 0..B-1, then B-1..0
+        if (b == pl->blocks || b < 0) {
+          step = -step;
+          b += step;
+        }
       }
-  };
-  schedule(pl, any_two, c.head_dim, floats, each,
-           [&](int item) { return pl->e[entry_of_item(*pl, item)].part0 < 0; });
+    const int64_t whole = *std::max_element(load, load + pl->blocks);
+    const int nb = static_cast<int>(std::min<int64_t>(kMaxBlocks, (tiles + kMinRange - 1) / kMinRange));
+    // Ranges: each block takes segments up to `limit`.  Whether that is enough for all items; `keep`: as the plan.
+    int64_t partials = 0;
+    auto cut = [&](int64_t limit, bool keep) {
+      int b = 0;
+      int64_t left = limit;
+      partials = 0;
+      if (keep) pl->start[0].item = pl->start[0].tile = 0;
+      for (int i = 0, item = 0; i < runs; ++i) {
+        const int per = cost.tile[run[i].type], own = cost.segment[run[i].type];
+        for (int k = 0; k < run[i].items; ++k, ++item) {
+          const int all = run[i].tiles;
+          for (int at = 0; at < all;) {
+            int64_t n = left < own ? 0 : (left - own) / per;
+            if (n + 1 >= all - at) n = all - at;         // (a last tile is not worth a segment)
+            if (n == 0 || (n < 2 && at == 0 && left < limit)) {
+              if (++b >= nb) return false;
+              left = limit;
+              if (keep) {
+                pl->start[b].item = item;
+                pl->start[b].tile = at;
+              }
+              if (n == 0 && limit < own + per) return false;
+              continue;
+            }
+            if (at + n < all || at > 0) partials += run[i].rows;
+            at += static_cast<int>(n);
+            left -= own + n * per;
+          }
+        }
+      }
+      if (keep) {
+        pl->blocks = b + 1;
+        pl->start[b + 1].item = pl->items;
+        pl->start[b + 1].tile = 0;
+      }
+      return true;
+    };
+    int64_t lo = work / nb, hi = lo + 2 * 60 + 2 * 50;
+    while (hi - lo > 4 + lo / 256) {
+      const int64_t mid = (lo + hi) / 2;
+      if (cut(mid, false)) hi = mid;
+      else lo = mid;
+    }
+    if (cut(hi, false) && hi + kJoinCost + partials * (c.head_dim + 4) * 8 / kJoinBytes < whole) {
+      pl->ranged = 1;
+      cut(hi, true);
+      *floats = static_cast<size_t>(2) * pl->blocks * pl->urows * (c.head_dim + 4);
+    }
+  }
+  for (int b = 0, i = 0; b < pl->blocks; ++b) {
+    const int item = pl->ranged ? pl->start[b].item : b;
+    while (i + 1 < pl->n && pl->e[i + 1].item0 <= item) ++i;
+    pl->start[b].entry = i;
+    // an item that is cut and writes the output: by its first block, with the blocks whose ranges begin inside it
+    if (!pl->ranged || pl->start[b + 1].tile == 0) continue;
+    const int last = pl->start[b + 1].item;
+    if (pl->start[b].item == last && pl->start[b].tile > 0) continue;
+    int e = i, n = 2;
+    while (e + 1 < pl->n && pl->e[e + 1].item0 <= last) ++e;
+    if (pl->e[e].part0 >= 0) continue;
+    while (b + n <= pl->blocks && pl->start[b + n].item == last) ++n;
+    pl->cut_block[pl->cuts] = static_cast<uint8_t>(b);
+    pl->cut_parts[pl->cuts++] = static_cast<uint8_t>(n);
+  }
   return true;
 }
 
@@ -184,16 +285,17 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
   Builder build(c, call);
   const int UT = build.UT;
   // Runs of a group's sequences whose rows do not fill a unit of their own (with others', they share one), between those
-  // that do.  A run's rows go over the shared positions together where that saves its blocks more time (the costs of
-  // mk_schedule.h, over all blocks) than the second kernel takes with the partials of its rows.
+  // that do.  A run's rows go over the shared positions together where that saves its blocks more time (over all
+  // of them) than the second kernel takes with the partials of its rows.
   int32_t common[kMaxSeqs];                              // whole pages that a sequence's run goes over together, or 0
   EntryRef over[kMaxSeqs];
   for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++]) {
     const int positions = prefix_lens[i] / c.page_size * c.page_size, tiles = (positions + kTile - 1) / kTile;
+    const Costs& x = costs(c, kPageRows);
     auto cost = [&](int rows, int item) {                // (a unit of more than half its rows has two tiles)
       const int full = rows / UT + (rows % UT > UT / 2), rest = rows % UT > 0 && rows % UT <= UT / 2;
-      return static_cast<int64_t>(full) * (tiles * kTileCost[kTwoTiles] + item * kItemCost[kTwoTiles]) +
-             rest * (tiles * kTileCost[kOneTile] + item * kItemCost[kOneTile]);
+      return static_cast<int64_t>(full) * (tiles * x.tile[kTwoTiles] + item * x.segment[kTwoTiles]) +
+             rest * (tiles * x.tile[kOneTile] + item * x.segment[kOneTile]);
     };
     for (int s = s0, end = s0 + group_seqs[i]; s < end;) {
       const int first = s;
@@ -207,7 +309,7 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
       const int rows = q.row0[s] - q.row0[first];
       if (with > 1 && tiles > 0) {
         const int64_t saved = (apart - cost(rows, 1)) * c.num_kv_heads / kMaxBlocks;
-        const int64_t bytes = static_cast<int64_t>(rows) * c.num_q_heads * (c.head_dim + 4) * 16;
+        const int64_t bytes = static_cast<int64_t>(rows) * c.num_q_heads * (c.head_dim + 4) * 8;
         if (saved > kJoinCost + bytes / kJoinBytes) {
           SpanEntry e = {};
           e.seq = first;

@@ -48,20 +48,10 @@ struct SpanPlan {
   int32_t by_G;
   int32_t window, sinks, box;        // box: positions of a copy, a power of two
   SpanEntry e[kMaxEntries];
-  struct { int32_t item, tile; } start[kMaxBlocks + 1];
+  struct { int32_t item, tile, entry; } start[kMaxBlocks + 1];   // (entry: of the block's first item, in ranges or not)
   int32_t cuts;                      // cut items that write the output
   uint8_t cut_block[kMaxBlocks], cut_parts[kMaxBlocks];
 };
-
-__host__ __device__ inline int entry_of_item(const SpanPlan& pl, int item) {
-  int lo = 0, hi = pl.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pl.e[mid].item0 <= item) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 
 __host__ __device__ inline void unit_of(const SpanPlan& pl, int i, int unit, int kvh, Segment& g) {
   const SpanEntry& e = pl.e[i];
@@ -87,20 +77,24 @@ __host__ __device__ inline void unit_of(const SpanPlan& pl, int i, int unit, int
   g.tiles = (end - g.gap + kTile - 1) / kTile;
 }
 
-__host__ __device__ inline void item_of(const SpanPlan& pl, const ChunkSeqs&, int item, Segment& g) {
-  const int i = entry_of_item(pl, item), rem = item - pl.e[i].item0, heads = pl.Hkv >> pl.e[i].pair, back = rem / heads;
+__host__ __device__ inline void item_of_entry(const SpanPlan& pl, int i, int item, Segment& g) {
+  const int rem = item - pl.e[i].item0, heads = pl.Hkv >> pl.e[i].pair, back = rem / heads;
   unit_of(pl, i, pl.e[i].units - 1 - back, (rem - back * heads) << pl.e[i].pair, g);
 }
 
-// Fills items and schedule of pl (all else of which is given); *floats is the size of
-// the cut items' partials.  False: more items than a call takes.
-bool make_plan(const mk_cache_shape& c, SpanPlan* pl, size_t* floats);
+inline int entry_of_item(const SpanPlan& pl, int item) {
+  int i = 0;
+  while (i + 1 < pl.n && pl.e[i + 1].item0 <= item) ++i;
+  return i;
+}
 
 // A call: a launch for each kind of rows that it has, and what joins them.
 enum { kPageRows, kStagedRows, kFewRows, kRowKinds };
 constexpr int kFewUnit = 32;         // rows of a unit of kFewRows
-// tenths of a microsecond that the second kernel takes, and bytes of partials that it and the first one move in one
-constexpr int64_t kJoinCost = 60, kJoinBytes = 500000;
+// Fills items and schedule of pl, a launch of that kind (all else of which is given); *floats is the size of
+// the cut items' partials.  False: more items than a call takes.
+bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats);
+
 struct EntryRef {
   int8_t kind, entry;
 };
