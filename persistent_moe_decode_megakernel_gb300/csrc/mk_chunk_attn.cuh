@@ -74,7 +74,8 @@ constexpr int kFew = 32;
 constexpr int kRawFew = 2;                     // raw stages of K and of V there
 
 constexpr int kRawBytes = kTile * (128 + 8);   // q8_0: the codes and scales of a K or V tile
-constexpr int kMasks = 8;           // tiles whose page masks are kept (more than can be in flight)
+constexpr int kMasks = 16;          // tiles whose page masks are kept (more than can be in flight)
+constexpr int kMaxStages = 12;      // of a ring (heads of 64)
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // The staged sequences and their tiles' numbers.
@@ -291,14 +292,14 @@ struct Layout {
   static constexpr int kRawStages = M == kQ8Few ? 2 * kRawFew : 3;
   static constexpr int kRaw = (M == kQ8Few ? 1 : 2) * kTileBytes;   // behind the Q tiles
   static constexpr int kKv = (kRaw + (kDecodes<M> ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
-  static constexpr int kStages = kDecodes<M> ? 3 : D == 128 ? 5 : 8;
+  static constexpr int kStages = kDecodes<M> ? 3 : D == 128 ? 5 : kMaxStages;
   static constexpr int kCtl = kKv + kStages * kTileBytes;
   static constexpr int kThreads = M == kQ8Few ? 640 : M == kQ8 ? 512 : 384;
 };
 
 struct Ctl {
-  uint64_t full[8], empty[8];        // K and V tiles, a ring (see entry_of)
-  uint64_t raw_full[8], raw_empty[8];
+  uint64_t full[kMaxStages], empty[kMaxStages];   // K and V tiles, a ring (see entry_of)
+  uint64_t raw_full[4], raw_empty[4];
   uint64_t qraw[2], qbar[2], qfree;  // query tiles: landed, in the operand type (bf16: qraw itself), read by the last S
   uint64_t sfull[2], pfull[2][2];    // S of a tile (stream); the halves of its P
   uint64_t landed, trim;             // a last V tile to be trimmed: landed, trimmed
@@ -1436,9 +1437,11 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) {                   // (q8_0: a K or V tile is the decode warps' work)
+    for (int i = 0; i < kMaxStages; ++i) {          // (q8_0: a K or V tile is the decode warps' work)
       mbar_init(smem_u32(&ctl->full[i]), kDecodes<M> ? 4 : 1);
       mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&ctl->raw_full[i]), 1);
       mbar_init(smem_u32(&ctl->raw_empty[i]), 4);
     }

@@ -11,9 +11,9 @@ namespace {
 // Joins partials: of a cut item's rows (in block order), and of the rows of groups, which have those of their own
 // sequence's positions and then those of the shared ones, each in one piece or cut.
 //
-// 8 rows lie side by side in a partial, so 8 lanes read 128 bytes of one.  Few rows (kSplit): the warp's other lanes
-// take every fourth partial each, a warp has 4 columns, a block half of all, and every read is on its way before any is waited for: what it
-// takes is the latency of one.  Many rows: they take other columns, and a block goes over several groups of 8 rows.
+// 8 rows lie side by side in a partial, so 8 lanes read 128 bytes of one; the warp's other lanes take other columns.
+// What it takes is latency.  Few rows (kDeep): two blocks an SM are all there is, and a lane has 12 partials on their way
+// before it waits for the first.  Many rows: more blocks, each over several groups of 8 rows.
 //
 // The launch brings just what is looked up, and a block copies it into shared memory at once, before it waits for the
 // kernel that writes the partials (walked where it lies, in the constant bank, each step of a search was a miss of its
@@ -92,11 +92,10 @@ __device__ __forceinline__ PartSet parts_of(const Joins<KINDS>& a, const JoinEnt
   return s;
 }
 
-template <int D, int M, int KINDS, bool kSplit>
-__global__ void __launch_bounds__(kSplit ? 4 * D : 2 * D, kSplit ? 256 / D : 512 / D)
+template <int D, int M, int KINDS, bool kDeep>
+__global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
     join_kernel(const __grid_constant__ JoinParams p, const __grid_constant__ Joins<KINDS> given) {
-  constexpr int kThreads = kSplit ? 4 * D : 2 * D, kEvery = kSplit ? 4 : 1;   // a lane takes every kEvery-th partial,
-  constexpr int kAhead = kSplit ? 5 : 3;                                      // that many at once
+  constexpr int kThreads = 2 * D, kAhead = kDeep ? 12 : 3;
   __shared__ Joins<KINDS> a;
   __shared__ PartSet sets[2][8][2];
   for (unsigned i = threadIdx.x; i < sizeof a / 8; i += kThreads) {
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kSplit ? 4 * D : 2 * D, kSplit ? 256 / D : 512
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, UT = a.UT;
-  const int chunk = kSplit ? static_cast<int>(blockIdx.z) * (D / 8) + warp : warp * 4 + (lane >> 3), mine = kSplit ? lane >> 3 : 0;
+  const int chunk = warp * 4 + (lane >> 3);
   const bool cut = static_cast<int>(blockIdx.x) < a.cuts;
   int lo = 0, unit = 0, kvh, hrows, rows, r0;
   if (cut) {
@@ -162,20 +161,15 @@ __global__ void __launch_bounds__(kSplit ? 4 * D : 2 * D, kSplit ? 256 / D : 512
     float2 held_ml[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int k = mine + i * kEvery;
-      held_ml[i] = k < n ? ml(k) : make_float2(-INFINITY, 0.f);
-      held[i] = k < n ? columns(k) : make_float4(0.f, 0.f, 0.f, 0.f);
+      held_ml[i] = i < n ? ml(i) : make_float2(-INFINITY, 0.f);
+      held[i] = i < n ? columns(i) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     find(row0 + gridDim.y * 8, turn ^ 1);
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) top = fmaxf(top, held_ml[i].x);
-#pragma unroll 4
-    for (int k = mine + kAhead * kEvery; k < n; k += kEvery) top = fmaxf(top, ml(k).x);
-    if constexpr (kSplit) {
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-    }
+#pragma unroll 8
+    for (int k = kAhead; k < n; ++k) top = fmaxf(top, ml(k).x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
     auto add = [&](const float4 x, const float2 ml) {
@@ -188,21 +182,11 @@ __global__ void __launch_bounds__(kSplit ? 4 * D : 2 * D, kSplit ? 256 / D : 512
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) add(held[i], held_ml[i]);
-#pragma unroll 4
-    for (int k = mine + kAhead * kEvery; k < n; k += kEvery) add(columns(k), ml(k));
-    if constexpr (kSplit) {
-#pragma unroll
-      for (int w = 8; w < 32; w <<= 1) {
-        L += __shfl_xor_sync(~0u, L, w);
-        acc.x += __shfl_xor_sync(~0u, acc.x, w);
-        acc.y += __shfl_xor_sync(~0u, acc.y, w);
-        acc.z += __shfl_xor_sync(~0u, acc.z, w);
-        acc.w += __shfl_xor_sync(~0u, acc.w, w);
-      }
-    }
+#pragma unroll 8
+    for (int k = kAhead; k < n; ++k) add(columns(k), ml(k));
     const float inv = L == 0.f ? 0.f : 1.0f / L;
     acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (live && mine == 0)
+    if (live)
       *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
           make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
     // (as in merge_kernel; a row's columns are several warps')
@@ -274,9 +258,9 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
   }
   const int jobs = a.cuts + call.jobs;
   if (jobs == 0) return cudaSuccess;
-  // few: blocks of half the columns, all at once or nearly; many: some ten blocks an SM, each over several groups of rows
-  if (groups <= kMaxBlocks * (256 / D))
-    return launch_after(join_kernel<D, M, KINDS, true>, dim3(jobs, (most + 7) / 8, 2), 4 * D, 0, st, p, a);
+  // few: two blocks an SM at once; many: some ten blocks an SM, each over several groups of rows
+  if (groups <= 2 * kMaxBlocks)
+    return launch_after(join_kernel<D, M, KINDS, true>, dim3(jobs, (most + 7) / 8), 2 * D, 0, st, p, a);
   const int y = std::max(1, std::min((most + 7) / 8, (10 * kMaxBlocks + jobs - 1) / jobs));
   return launch_after(join_kernel<D, M, KINDS, false>, dim3(jobs, y), 2 * D, 0, st, p, a);
 }

@@ -15,7 +15,7 @@ enum { kOneTile, kTwoTiles, kTwoHeads };
 struct Costs {
   int tile[3], segment[3];
 };
-constexpr Costs kCosts[kRowKinds] = {{{11, 17, 21}, {42, 46, 42}}, {{11, 17, 0}, {42, 46, 0}}, {{13, 0, 0}, {45, 0, 0}}};
+constexpr Costs kCosts[kRowKinds] = {{{9, 16, 18}, {38, 42, 20}}, {{9, 16, 0}, {38, 42, 0}}, {{13, 0, 0}, {45, 0, 0}}};
 constexpr Costs kQ8Costs = {{25, 34, 50}, {50, 60, 50}};
 const Costs& costs(const mk_cache_shape& c, int kind) {
   return kind == kPageRows && (c.flags & MK_FLAG_KV_Q8) ? kQ8Costs : kCosts[kind];
@@ -216,8 +216,8 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
           const int all = run[i].tiles;
           for (int at = 0; at < all;) {
             int64_t n = left < own ? 0 : (left - own) / per;
-            if (n + 1 >= all - at) n = all - at;         // (a last tile is not worth a segment)
-            if (n == 0 || (n < 2 && at == 0 && left < limit)) {
+            if (n > 0 && n + 1 >= all - at) n = all - at;   // (a last tile is not worth a segment,
+            if (n == 0 || (n == 1 && n < all - at && left < limit)) {   // nor is a first one)
               if (++b >= nb) return false;
               left = limit;
               if (keep) {
