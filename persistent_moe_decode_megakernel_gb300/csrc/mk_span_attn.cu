@@ -205,6 +205,9 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
 }
 template <int D, int M, int KINDS>
 cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const float* const* part, cudaStream_t st) {
+  int cuts = 0;
+  for (int k = 0; k < KINDS; ++k) cuts += call.plan[k].items > 0 ? call.plan[k].cuts : 0;
+  if (cuts + call.jobs == 0) return cudaSuccess;
   Joins<KINDS> a;
   static_assert(sizeof a % 8 == 0, "");
   const int UT = 2 * call.plan[0].TT, G = call.plan[0].G;
@@ -257,7 +260,6 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
     groups += static_cast<int64_t>(a.join[k].own.units) * a.Hkv * ((rows + 7) / 8);
   }
   const int jobs = a.cuts + call.jobs;
-  if (jobs == 0) return cudaSuccess;
   // few: two blocks an SM at once; many: some ten blocks an SM, each over several groups of rows
   if (groups <= 2 * kMaxBlocks)
     return launch_after(join_kernel<D, M, KINDS, true>, dim3(jobs, (most + 7) / 8), 2 * D, 0, st, p, a);

@@ -22,6 +22,7 @@ const Costs& costs(const mk_cache_shape& c, int kind) {
 }
 // What cut items cost besides: the second kernel, and the bytes of partials that it and the first one move in a tenth.
 constexpr int64_t kJoinCost = 45, kJoinBytes = 250000;
+constexpr int kMostTile = 50, kMostSegment = 60, kLeastSegment = 20;   // of these costs
 constexpr int kMinRange = 3;                 // position tiles a block is worth
 constexpr int kMaxRuns = 4096;               // units beyond which whole items are even enough
 
@@ -157,11 +158,10 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
   pl->blocks = pl->ranged = pl->cuts = 0;
   *floats = 0;
   const Costs& cost = costs(c, kind);
-  // runs of items that are alike: a unit's KV heads
+  // runs of items that are alike: a unit's KV heads, and those of units behind it
   struct Run {
     int32_t tiles, items;
     int16_t type, rows;
-    int32_t whole;                   // 1: its items write the output unless they are cut
   };
   Run run[kMaxRuns];
   int runs = 0, most = 0;
@@ -181,7 +181,10 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
     for (int u = e.units - 1; u >= 0; --u) {
       unit_of(*pl, i, u, 0, g);
       const int type = g.two ? kTwoTiles : g.pair ? kTwoHeads : kOneTile;
-      run[runs++] = {g.tiles, heads, static_cast<int16_t>(type), static_cast<int16_t>(g.ntok * pl->G << e.pair), e.part0 < 0};
+      const int16_t rows = static_cast<int16_t>(g.ntok * pl->G << e.pair);
+      Run* last = run + runs - 1;
+      if (runs > 0 && last->tiles == g.tiles && last->type == type && last->rows == rows) last->items += heads;
+      else run[runs++] = {g.tiles, heads, static_cast<int16_t>(type), rows};
       tiles += static_cast<int64_t>(g.tiles) * heads;
       work += (static_cast<int64_t>(g.tiles) * cost.tile[type] + cost.segment[type]) * heads;
     }
@@ -192,44 +195,55 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
   if (items > 0 && runs <= kMaxRuns) {
     // the slowest block of whole items
     int64_t load[kMaxBlocks] = {};
-    for (int i = 0, b = 0, step = 1; i < runs; ++i)
+    for (int i = 0, b = 0, step = 1; i < runs; ++i) {
+      const int64_t x = static_cast<int64_t>(run[i].tiles) * cost.tile[run[i].type] + cost.segment[run[i].type];
       for (int k = 0; k < run[i].items; ++k) {
-        load[b] += static_cast<int64_t>(run[i].tiles) * cost.tile[run[i].type] + cost.segment[run[i].type];
+        load[b] += x;
         b += step;                           // 0..B-1, then B-1..0
         if (b == pl->blocks || b < 0) {
           step = -step;
           b += step;
         }
       }
+    }
     const int64_t whole = *std::max_element(load, load + pl->blocks);
     const int nb = static_cast<int>(std::min<int64_t>(kMaxBlocks, (tiles + kMinRange - 1) / kMinRange));
     // Ranges: each block takes segments up to `limit`.  Whether that is enough for all items; `keep`: as the plan.
     int64_t partials = 0;
-    auto cut = [&](int64_t limit, bool keep) {
-      int b = 0;
-      int64_t left = limit;
+    auto cut = [&](int32_t limit, bool keep) {
+      int b = 0, item = 0;
+      int32_t left = limit;
       partials = 0;
       if (keep) pl->start[0].item = pl->start[0].tile = 0;
-      for (int i = 0, item = 0; i < runs; ++i) {
-        const int per = cost.tile[run[i].type], own = cost.segment[run[i].type];
-        for (int k = 0; k < run[i].items; ++k, ++item) {
-          const int all = run[i].tiles;
-          for (int at = 0; at < all;) {
-            int64_t n = left < own ? 0 : (left - own) / per;
-            if (n > 0 && n + 1 >= all - at) n = all - at;   // (a last tile is not worth a segment,
-            if (n == 0 || (n == 1 && n < all - at && left < limit)) {   // nor is a first one)
-              if (++b >= nb) return false;
-              left = limit;
-              if (keep) {
-                pl->start[b].item = item;
-                pl->start[b].tile = at;
-              }
-              if (n == 0 && limit < own + per) return false;
-              continue;
+      for (int i = 0; i < runs; ++i) {
+        const int32_t per = cost.tile[run[i].type], own = cost.segment[run[i].type], all = run[i].tiles;
+        const int64_t one = own + static_cast<int64_t>(per) * all;
+        for (int k = 0, at = 0; k < run[i].items;) {
+          if (at == 0 && left >= one) {                    // whole items
+            const int fit = std::min<int32_t>(run[i].items - k, left / static_cast<int32_t>(one));
+            k += fit;
+            item += fit;
+            left -= fit * static_cast<int32_t>(one);
+            continue;
+          }
+          int32_t n = left < own ? 0 : (left - own) / per;
+          if (n > 0 && n + 1 >= all - at) n = all - at;    // (a last tile is not worth a segment,
+          if (n == 0 || (n == 1 && n < all - at && left < limit)) {   // nor is a first one)
+            if (++b >= nb || (n == 0 && limit < own + per)) return false;
+            left = limit;
+            if (keep) {
+              pl->start[b].item = item;
+              pl->start[b].tile = at;
             }
-            if (at + n < all || at > 0) partials += run[i].rows;
-            at += static_cast<int>(n);
-            left -= own + n * per;
+            continue;
+          }
+          if (n < all) partials += run[i].rows;
+          at += n;
+          left -= own + n * per;
+          if (at == all) {
+            at = 0;
+            ++k;
+            ++item;
           }
         }
       }
@@ -240,16 +254,20 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
       }
       return true;
     };
-    int64_t lo = work / nb, hi = lo + 2 * 60 + 2 * 50;
-    while (hi - lo > 4 + lo / 256) {
-      const int64_t mid = (lo + hi) / 2;
-      if (cut(mid, false)) hi = mid;
-      else lo = mid;
-    }
-    if (cut(hi, false) && hi + kJoinCost + partials * (c.head_dim + 4) * 8 / kJoinBytes < whole) {
-      pl->ranged = 1;
-      cut(hi, true);
-      *floats = static_cast<size_t>(2) * pl->blocks * pl->urows * (c.head_dim + 4);
+    // A block takes a piece of one segment more than its share of the work, about; no plan below that is looked for.
+    const int64_t share = work / nb;
+    int64_t lo = share, hi = share + 2 * kMostSegment + 2 * kMostTile;
+    if (share + kLeastSegment / 2 + kJoinCost < whole && hi < (int64_t(1) << 30)) {
+      while (hi - lo > 8 + share / 64) {
+        const int64_t mid = (lo + hi) / 2;
+        if (cut(static_cast<int32_t>(mid), false)) hi = mid;
+        else lo = mid;
+      }
+      if (cut(static_cast<int32_t>(hi), false) && hi + kJoinCost + partials * (c.head_dim + 4) * 8 / kJoinBytes < whole) {
+        pl->ranged = 1;
+        cut(static_cast<int32_t>(hi), true);
+        *floats = static_cast<size_t>(2) * pl->blocks * pl->urows * (c.head_dim + 4);
+      }
     }
   }
   for (int b = 0, i = 0; b < pl->blocks; ++b) {
