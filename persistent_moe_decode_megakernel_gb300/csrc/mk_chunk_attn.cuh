@@ -532,6 +532,7 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
   const int lane = threadIdx.x & 31;
   const int r = p.box, nbox = kTile / r;                       // copies of a tile
   const bool mine = lane < nbox;
+  if constexpr (Plan::kSpans && M == kStaged) asm volatile("griddepcontrol.wait;" ::: "memory");   // for stage_kernel
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
   uint32_t jg = 0, c0 = 0;                                     // position tiles and ring entries so far
@@ -1504,6 +1505,8 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
     decode<D, M>(p, base, ctl, (warp - 12) >> 2);
   }
   __syncwarp();
+  // (launch_after: whoever waits for this kernel counts on the ones before it, too)
+  if constexpr (Plan::kSpans) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_before();
   __syncthreads();
   tc_after();
@@ -1789,7 +1792,7 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, unsigned threads, s
 }
 
 template <int D, int M, class Plan>
-cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
+cudaError_t launch(const Params<Plan>& p, cudaStream_t st, bool after = false) {
   // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -1802,6 +1805,7 @@ cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
+  if (after) return launch_after(attn_kernel<D, M, Plan>, dim3(p.plan.blocks), Layout<D, M>::kThreads, smem_bytes<D, M>(), st, p);
   attn_kernel<D, M, Plan><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
   return cudaGetLastError();
 }

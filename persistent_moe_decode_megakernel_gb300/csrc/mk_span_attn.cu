@@ -31,7 +31,7 @@ struct JoinEntry {
   int16_t pad;
 };
 template <int KINDS>
-struct Joins {
+struct alignas(16) Joins {
   // of each launch: where its blocks' ranges begin, item * 2 + whether inside the item (whole items: no block)
   int32_t start[KINDS][kMaxBlocks + 1], blocks[KINDS], urows[KINDS];
   const float* part[KINDS];
@@ -49,9 +49,10 @@ struct PartSet {                     // the partials of one row: `first`, then n
   __device__ __forceinline__ float2 ml(int k) const {
     return reinterpret_cast<const float2*>(at(k) + static_cast<size_t>(stride) * D)[row];
   }
-  __device__ __forceinline__ float4 columns(int k, int chunk) const {
-    return reinterpret_cast<const float4*>(at(k))[static_cast<size_t>(chunk) * stride + row];
+  __device__ __forceinline__ const float4* address(int k, int chunk) const {
+    return reinterpret_cast<const float4*>(at(k)) + static_cast<size_t>(chunk) * stride + row;
   }
+  __device__ __forceinline__ float4 columns(int k, int chunk) const { return *address(k, chunk); }
 };
 // of a cut item that block b begins
 template <int D, int KINDS>
@@ -98,11 +99,19 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
   constexpr int kThreads = 2 * D, kAhead = kDeep ? 12 : 3;
   __shared__ Joins<KINDS> a;
   __shared__ PartSet sets[2][8][2];
-  for (unsigned i = threadIdx.x; i < sizeof a / 8; i += kThreads) {
-    uint2 w;                         // (by their generic address: constant reads would go one lane at a time)
-    asm volatile("ld.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(reinterpret_cast<const uint2*>(&given) + i));
-    reinterpret_cast<uint2*>(&a)[i] = w;
+  // (by their generic address: constant reads would go one lane at a time; and all at once)
+  constexpr int kWords = sizeof a / 16, kReads = (kWords + kThreads - 1) / kThreads;
+  uint4 w[kReads];
+#pragma unroll
+  for (int i = 0; i < kReads; ++i) {
+    const int at = min(static_cast<int>(threadIdx.x) + i * kThreads, kWords - 1);
+    asm volatile("ld.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                 : "l"(reinterpret_cast<const uint4*>(&given) + at));
   }
+#pragma unroll
+  for (int i = 0; i < kReads; ++i)
+    reinterpret_cast<uint4*>(&a)[min(static_cast<int>(threadIdx.x) + i * kThreads, kWords - 1)] = w[i];
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, UT = a.UT;
   const int chunk = warp * 4 + (lane >> 3);
@@ -164,6 +173,9 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
       held_ml[i] = i < n ? ml(i) : make_float2(-INFINITY, 0.f);
       held[i] = i < n ? columns(i) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    if constexpr (kDeep)
+      for (int k = kAhead; k < n; ++k)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(k < own.n ? own.address(k, chunk) : over.address(k - own.n, chunk)));
     find(row0 + gridDim.y * 8, turn ^ 1);
     float top = -INFINITY;
 #pragma unroll
@@ -209,7 +221,7 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
   for (int k = 0; k < KINDS; ++k) cuts += call.plan[k].items > 0 ? call.plan[k].cuts : 0;
   if (cuts + call.jobs == 0) return cudaSuccess;
   Joins<KINDS> a;
-  static_assert(sizeof a % 8 == 0, "");
+  static_assert(sizeof a % 16 == 0, "");
   const int UT = 2 * call.plan[0].TT, G = call.plan[0].G;
   JoinParams p;                         // what the rows that are worked out again need
   static_cast<CallParams&>(p) = given;
@@ -282,6 +294,9 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
   float* floats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + call.stage_bytes);
   p.whole = floats + call.whole0;
   const float* part[kRowKinds];
+  // Launches of the call but the first may begin while the one before still runs: none reads what another of them writes,
+  // but the staged tiles and the partials, for which their readers wait (launch_after).
+  bool first = true;
   cudaError_t e = cudaSuccess;
   for (int k = 0; k < kRowKinds && e == cudaSuccess; ++k) {
     part[k] = floats + call.part0[k];
@@ -303,13 +318,14 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
       stage_kernel<128><<<dim3(call.stage_tiles, 2 * c.num_kv_heads), kStageThreads, 0, st>>>(
           p, static_cast<__half*>(workspace), t);
       e = cudaGetLastError();
-      if (e == cudaSuccess) e = launch<128, kStaged>(p, st);
+      if (e == cudaSuccess) e = launch<128, kStaged>(p, st, true);
     } else {
-      e = k == kFewRows       ? launch<128, kQ8Few>(p, st)
-          : q8                ? launch<128, kQ8>(p, st)
-          : c.head_dim == 128 ? launch<128, kBf16>(p, st)
-                              : launch<64, kBf16>(p, st);
+      e = k == kFewRows       ? launch<128, kQ8Few>(p, st, !first)
+          : q8                ? launch<128, kQ8>(p, st, !first)
+          : c.head_dim == 128 ? launch<128, kBf16>(p, st, !first)
+                              : launch<64, kBf16>(p, st, !first);
     }
+    first = false;
   }
   if (e == cudaSuccess)
     e = q8                  ? join<128, kQ8, kRowKinds>(call, p, part, st)

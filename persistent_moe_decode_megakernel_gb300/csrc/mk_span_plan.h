@@ -41,7 +41,7 @@ struct SpanEntry {
 struct SpanPlan {
   static constexpr bool kSpans = true;
   static constexpr int kWholeSlot = 2 * kMaxBlocks;      // Segment.slot of a whole item that writes a partial
-  int32_t n;                         // entries: shared ones, sequences that write the output, sequences of groups
+  int32_t n;                         // entries: of shared positions, of sequences (those with most positions first)
   int32_t items, blocks, ranged;
   int32_t G, TT, Hkv;
   int32_t urows;                     // rows of a cut item's partial
