@@ -105,6 +105,8 @@ struct Params : CallParams {
   float* whole;                     // and (parts of the cache) of whole items that are joined with another
   int32_t stage0[Plan::kSpans ? 1 : kMaxSeqs];   // staged sequences: first tile in the workspace (entries hold their own)
   int32_t box;                      // positions of one copy: a power of two that divides ps
+  int32_t first;                    // (parts of the cache) the call's first kernel: nothing but its parameters is read before the
+                                    // kernel in front of it is done
   float c;                          // log2(e) / sqrt(D)
 
   // the unit's first packed row
@@ -988,6 +990,14 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
     }
     return true;
   };
+  // (waited for before the epilogue, the rows of short segments held it up by as much as their loads took)
+  auto q_here = [&](const Segment& n) {
+    if constexpr (M != kBf16) {
+      if (!n.two && !pairs<Plan>(n) && t == 1) return true;
+      return __all_sync(~0u, mbar_try(smem_u32(&ctl->qraw[t]), qr & 1)) != 0;
+    }
+    return true;
+  };
   if (have && !take_q(g)) return;
   while (have) {
     const int trows = p.plan.TT * p.plan.G;
@@ -1114,8 +1124,9 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
     tc_after();
     jg += g.n;
     if (!have) let_next_start<Plan>();
-    // the next segment's rows, so that its first scores run under this one's epilogue
-    if (have && !take_q(next)) return;
+    // the next segment's rows, so that its first scores run under this one's epilogue -- if they are here already
+    const bool early = have && q_here(next);
+    if (early && !take_q(next)) return;
 
     // m and l in powers of two; a row without a position has m = -inf and l = 0
     m = m == -INFINITY ? m : m * c;
@@ -1223,6 +1234,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
         exact_row<D, M>(p, rr, hh, &ctl->beat);
       }
     }
+    if (have && !early && !take_q(next)) return;
     ++seg;
     g = next;
   }
@@ -1358,7 +1370,8 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
     jg += g.n;
     have = walk.next(p.plan, p.seqs, next);
     if (!have) let_next_start<Plan>();
-    if (have && t == 0 && !take_q()) return;
+    const bool early = have && t == 0 && __all_sync(~0u, mbar_try(smem_u32(&ctl->qraw[0]), taken & 1));   // (as in softmax)
+    if (early && !take_q()) return;
 
     // m and l in powers of two; a part without a position has m = -inf and l = 0
     ctl->ml[t][row] = make_float2(m == -INFINITY ? m : m * c, l);
@@ -1421,6 +1434,7 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
       const int who = __ffs(todo) - 1;
       exact_row<D, kQ8Few>(p, __shfl_sync(~0u, r, who), __shfl_sync(~0u, h, who), &ctl->beat);
     }
+    if (have && t == 0 && !early && !take_q()) return;
     ++seg;
     g = next;
   }
@@ -1473,6 +1487,8 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if constexpr (Plan::kSpans)
+    if (p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_before();
   __syncthreads();
   tc_after();
@@ -1628,6 +1644,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
                                                               const __grid_constant__ StageTiles st) {
   constexpr int CH = D / 16, kRows = kStageThreads / CH;       // chunks of a row, rows of a pass
   const int tile = blockIdx.x, vh = blockIdx.y;                // vh: K heads, then V heads
+  if constexpr (Plan::kSpans) asm volatile("griddepcontrol.wait;" ::: "memory");
   int i = 0;
   while (i + 1 < st.n && st.first[i + 1] <= tile) ++i;
   int s = st.seq[i], t = tile - st.first[i], len;
@@ -1792,7 +1809,7 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, unsigned threads, s
 }
 
 template <int D, int M, class Plan>
-cudaError_t launch(const Params<Plan>& p, cudaStream_t st, bool after = false) {
+cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
   // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -1805,7 +1822,7 @@ cudaError_t launch(const Params<Plan>& p, cudaStream_t st, bool after = false) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  if (after) return launch_after(attn_kernel<D, M, Plan>, dim3(p.plan.blocks), Layout<D, M>::kThreads, smem_bytes<D, M>(), st, p);
+  if constexpr (Plan::kSpans) return launch_after(attn_kernel<D, M, Plan>, dim3(p.plan.blocks), Layout<D, M>::kThreads, smem_bytes<D, M>(), st, p);
   attn_kernel<D, M, Plan><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
   return cudaGetLastError();
 }

@@ -294,14 +294,17 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
   float* floats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + call.stage_bytes);
   p.whole = floats + call.whole0;
   const float* part[kRowKinds];
-  // Launches of the call but the first may begin while the one before still runs: none reads what another of them writes,
-  // but the staged tiles and the partials, for which their readers wait (launch_after).
+  // Each launch may begin while the kernel before it still runs (launch_after).  The first kernel of the call sets itself
+  // up and then waits for that one.  The others need not: none reads what another of them writes, but the staged tiles
+  // and the partials, for which their readers wait; and each waits at its end, so that whoever waits for the last one
+  // waits for all.
   bool first = true;
   cudaError_t e = cudaSuccess;
   for (int k = 0; k < kRowKinds && e == cudaSuccess; ++k) {
     part[k] = floats + call.part0[k];
     if (call.plan[k].items == 0) continue;
     p.plan = call.plan[k];
+    p.first = first && k != kStagedRows;
     p.part = floats + call.part0[k];
     rc = encode_queries(c, p.plan.G, k == kFewRows ? kFew / p.plan.G : p.plan.TT, q, q_stride, rows, &p.qmap);
     if (!rc && k == kStagedRows) rc = encode_pages(128, c.num_kv_heads, kTile, call.stage_tiles, false, workspace, p.box, &p.map);
@@ -315,15 +318,14 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
         t.first[i] = p.plan.e[t.seq[i]].stage0;
       }
       t.first[t.n] = call.stage_tiles;
-      stage_kernel<128><<<dim3(call.stage_tiles, 2 * c.num_kv_heads), kStageThreads, 0, st>>>(
-          p, static_cast<__half*>(workspace), t);
-      e = cudaGetLastError();
-      if (e == cudaSuccess) e = launch<128, kStaged>(p, st, true);
+      e = launch_after(stage_kernel<128, SpanPlan>, dim3(call.stage_tiles, 2 * c.num_kv_heads), kStageThreads, 0, st, p,
+                       static_cast<__half*>(workspace), t);
+      if (e == cudaSuccess) e = launch<128, kStaged>(p, st);
     } else {
-      e = k == kFewRows       ? launch<128, kQ8Few>(p, st, !first)
-          : q8                ? launch<128, kQ8>(p, st, !first)
-          : c.head_dim == 128 ? launch<128, kBf16>(p, st, !first)
-                              : launch<64, kBf16>(p, st, !first);
+      e = k == kFewRows       ? launch<128, kQ8Few>(p, st)
+          : q8                ? launch<128, kQ8>(p, st)
+          : c.head_dim == 128 ? launch<128, kBf16>(p, st)
+                              : launch<64, kBf16>(p, st);
     }
     first = false;
   }

@@ -16,7 +16,7 @@ struct Costs {
   int tile[3], segment[3];
 };
 constexpr Costs kCosts[kRowKinds] = {{{9, 16, 18}, {38, 42, 20}}, {{9, 16, 0}, {38, 42, 0}}, {{13, 0, 0}, {45, 0, 0}}};
-constexpr Costs kQ8Costs = {{25, 34, 50}, {50, 60, 50}};
+constexpr Costs kQ8Costs = {{16, 20, 32}, {40, 32, 40}};
 const Costs& costs(const mk_cache_shape& c, int kind) {
   return kind == kPageRows && (c.flags & MK_FLAG_KV_Q8) ? kQ8Costs : kCosts[kind];
 }
