@@ -22,7 +22,8 @@ const Costs& costs(const mk_cache_shape& c, int kind) {
 }
 // What cut items cost besides: the second kernel, and the bytes of partials that it and the first one move in a tenth.
 constexpr int64_t kJoinCost = 45, kJoinBytes = 250000;
-constexpr int kMostTile = 50, kMostSegment = 60, kLeastSegment = 20;   // of these costs
+constexpr int kLeastSegment = 20;            // of these costs
+constexpr int kMostTries = 24;
 constexpr int kMinRange = 3;                 // position tiles a block is worth
 constexpr int kMaxRuns = 4096;               // units beyond which whole items are even enough
 
@@ -234,13 +235,13 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
     }
     const int64_t whole = *std::max_element(load, load + pl->blocks);
     const int nb = static_cast<int>(std::min<int64_t>(kMaxBlocks, (tiles + kMinRange - 1) / kMinRange));
-    // Ranges: each block takes segments up to `limit`.  Whether that is enough for all items; `keep`: as the plan.
+    // Ranges: each block takes segments up to `limit`.  Whether that is enough for all items.
     int64_t partials = 0;
-    auto cut = [&](int32_t limit, bool keep) {
+    auto cut = [&](int32_t limit) {
       int b = 0, item = 0;
       int32_t left = limit;
       partials = 0;
-      if (keep) pl->start[0].item = pl->start[0].tile = 0;
+      pl->start[0].item = pl->start[0].tile = 0;
       for (int i = 0; i < runs; ++i) {
         const int32_t per = cost.tile[run[i].type], own = cost.segment[run[i].type], all = run[i].tiles;
         const int64_t one = own + static_cast<int64_t>(per) * all;
@@ -257,10 +258,8 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
           if (n == 0 || (n == 1 && n < all - at && left < limit)) {   // nor is a first one)
             if (++b >= nb || (n == 0 && limit < own + per)) return false;
             left = limit;
-            if (keep) {
-              pl->start[b].item = item;
-              pl->start[b].tile = at;
-            }
+            pl->start[b].item = item;
+            pl->start[b].tile = at;
             continue;
           }
           if (n < all) partials += run[i].rows;
@@ -273,26 +272,29 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
           }
         }
       }
-      if (keep) {
-        pl->blocks = b + 1;
-        pl->start[b + 1].item = pl->items;
-        pl->start[b + 1].tile = 0;
-      }
+      pl->blocks = b + 1;
+      pl->start[b + 1].item = pl->items;
+      pl->start[b + 1].tile = 0;
       return true;
     };
-    // A block takes a piece of one segment more than its share of the work, about; no plan below that is looked for.
+    // Every block but the first begins inside an item, about: a segment more than its share of the work.  From a little
+    // below that the limit rises until it is enough.
     const int64_t share = work / nb;
-    int64_t lo = share, hi = share + 2 * kMostSegment + 2 * kMostTile;
-    if (share + kLeastSegment / 2 + kJoinCost < whole && hi < (int64_t(1) << 30)) {
-      while (hi - lo > 8 + share / 64) {
-        const int64_t mid = (lo + hi) / 2;
-        if (cut(static_cast<int32_t>(mid), false)) hi = mid;
-        else lo = mid;
-      }
-      if (cut(static_cast<int32_t>(hi), false) && hi + kJoinCost + partials * (c.head_dim + 4) * 8 / kJoinBytes < whole) {
+    int64_t more = 0;
+    for (int i = 0; i < runs; ++i)
+      more += static_cast<int64_t>(run[i].tiles) * cost.tile[run[i].type] * run[i].items / std::max<int64_t>(share, 1) *
+              cost.segment[run[i].type];
+    more = more / nb * 3 / 4;
+    int64_t limit = share + std::max<int64_t>(more, kLeastSegment / 2);
+    if (limit + kJoinCost < whole && limit < (int64_t(1) << 30)) {
+      const int64_t step = std::max<int64_t>(limit / 64, 4);
+      bool enough = false;
+      for (int i = 0; i < kMostTries && !(enough = cut(static_cast<int32_t>(limit))); ++i) limit += step;
+      if (enough && limit + kJoinCost + partials * (c.head_dim + 4) * 8 / kJoinBytes < whole) {
         pl->ranged = 1;
-        cut(static_cast<int32_t>(hi), true);
         *floats = static_cast<size_t>(2) * pl->blocks * pl->urows * (c.head_dim + 4);
+      } else {
+        pl->blocks = std::min<int32_t>(pl->items, kMaxBlocks);
       }
     }
   }
