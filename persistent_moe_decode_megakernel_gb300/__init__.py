@@ -83,7 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         import torch
         tdir = os.path.dirname(torch.__file__)
         bind_obj = os.path.join(_BUILD, "mk_torch.o")
-        cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", _INC, "-isystem", os.path.join(tdir, "include"),
+        cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", _INC, "-I", _CSRC, "-isystem", os.path.join(tdir, "include"),
                      "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"), "-isystem",
                      os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], "-c",
                      os.path.join(_BIND, "mk_torch.cpp"), "-o", bind_obj])
@@ -393,8 +393,7 @@ def _native():
             spec.loader.exec_module(m)
             m.init(MkError, *(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
                 "mk_append_chunk", "mk_chunk_attention_workspace", "mk_chunk_attention", "mk_read_cache", "mk_last_error",
-                "mk_window_attention_workspace", "mk_window_attention", "mk_prefix_attention_workspace",
-                "mk_prefix_attention")))
+                "mk_window_attention_in", "mk_prefix_attention_in")))
             _bind = m
     return _bind
 

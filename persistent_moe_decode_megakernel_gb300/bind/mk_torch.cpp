@@ -15,8 +15,10 @@
 
 #include <algorithm>
 #include <cstring>
+#include <exception>
 
 #include "mk_chunk.h"
+#include "mk_span_call.h"
 
 namespace {
 
@@ -29,10 +31,8 @@ struct {
   decltype(&mk_chunk_attention) attention;
   decltype(&mk_read_cache) read;
   decltype(&mk_last_error) last_error;
-  decltype(&mk_window_attention_workspace) window_workspace;
-  decltype(&mk_window_attention) window;
-  decltype(&mk_prefix_attention_workspace) prefix_workspace;
-  decltype(&mk_prefix_attention) prefix;
+  decltype(&mk_window_attention_in) window;
+  decltype(&mk_prefix_attention_in) prefix;
 } g_mk = {};
 
 // Other Python threads run while a call launches or allocates: a launch waits when the device's queue is
@@ -260,45 +260,81 @@ PyObject* append_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The three attention calls: (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status, ..)
-// with what is their own behind that.  bytes(c, &n): the workspace's size; attend(c, q, stride, out, ws, bytes, status, on).
-template <class Bytes, class Attend>
-PyObject* attention(PyObject* const* a, const Call& c, Bytes&& need_bytes, Attend&& attend) {
-  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
-  const at::Tensor& q = tensor(a[1], "q: a tensor");
-  const int64_t stride = c.rows_of(q, c.shape.num_q_heads,
-                                   "q: bf16 rows of num_q_heads heads of head_dim contiguous values on the cache's device, one "
-                                   "for each new token at least");
-  int32_t* status = c.status(a[8]);
-  const at::Tensor out = c.out(a[6], c.shape.num_q_heads, "out: contiguous bf16 [rows, num_q_heads, head_dim] on the cache's device");
-  at::Tensor ws;
-  if (a[7] != Py_None) {
+// What the attention calls share: (shape, q, chunk_lens, seq_lens, block_tables, kv_layer, out, workspace, status, ..)
+// with what is their own behind that.
+struct Rows {
+  const at::Tensor& q;
+  const int64_t stride;
+  int32_t* const status;
+  const at::Tensor out;
+  at::Tensor ws;               // as given
+  Rows(PyObject* const* a, const Call& c)
+      : q(tensor(a[1], "q: a tensor")),
+        stride(c.rows_of(q, c.shape.num_q_heads,
+                         "q: bf16 rows of num_q_heads heads of head_dim contiguous values on the cache's device, one for each "
+                         "new token at least")),
+        status(c.status(a[8])),
+        out(c.out(a[6], c.shape.num_q_heads, "out: contiguous bf16 [rows, num_q_heads, head_dim] on the cache's device")) {
+    if (a[7] == Py_None) return;
     ws = tensor(a[7], "workspace: a tensor or None");
     need(ws.is_cuda() && ws.get_device() == c.dev && ws.is_contiguous(), "workspace: contiguous tensor on the cache's device");
-  } else {
-    size_t bytes = 0;
-    run([&] { return need_bytes(&bytes); });
-    if (bytes) ws = c.make({static_cast<int64_t>(bytes)}, at::kByte);
   }
-  const mk_stream_t on = c.stream();
-  run([&] {
-    return attend(q.data_ptr(), stride, out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
-                  status, on);
-  });
-  return keep(a[6], out);
-}
+  void* ws_ptr() const { return ws.defined() ? ws.data_ptr() : nullptr; }
+  size_t ws_bytes() const { return ws.defined() ? ws.nbytes() : 0; }
+};
 
+// chunk_attention(.., status)
 PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 9)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Call c(a);
-    return attention(
-        a, c, [&](size_t* bytes) { return g_mk.workspace(&c.shape, c.n(), c.chunk.v, c.len.v, bytes); },
-        [&](const void* q, int64_t stride, void* out, void* ws, size_t ws_bytes, int32_t* status, mk_stream_t on) {
-          return g_mk.attention(&c.shape, c.n(), c.chunk.v, c.len.v, c.tables(), q, stride, c.kv.data_ptr(), out, ws, ws_bytes,
-                                status, on);
-        });
+    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+    Rows r(a, c);
+    if (!r.ws.defined()) {
+      size_t bytes = 0;
+      run([&] { return g_mk.workspace(&c.shape, c.n(), c.chunk.v, c.len.v, &bytes); });
+      if (bytes) r.ws = c.make({static_cast<int64_t>(bytes)}, at::kByte);
+    }
+    const mk_stream_t on = c.stream();
+    run([&] {
+      return g_mk.attention(&c.shape, c.n(), c.chunk.v, c.len.v, c.tables(), r.q.data_ptr(), r.stride, c.kv.data_ptr(),
+                            r.out.data_ptr(), r.ws_ptr(), r.ws_bytes(), r.status, on);
+    });
+    return keep(a[6], r.out);
   });
+}
+
+// A workspace that the call asks for (inside `run`, so without the interpreter's lock).
+struct Taken {
+  const Call& c;
+  at::Tensor ws;
+  std::exception_ptr failed;
+  static void* take(void* self, size_t bytes) noexcept {
+    Taken& t = *static_cast<Taken*>(self);
+    try {
+      t.ws = at::empty({static_cast<int64_t>(bytes)}, t.c.kv.options().dtype(at::kByte));
+      return t.ws.data_ptr();
+    } catch (...) {
+      t.failed = std::current_exception();
+      return nullptr;
+    }
+  }
+};
+template <class Attend>
+PyObject* span_attention(PyObject* const* a, const Call& c, Attend&& attend) {
+  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.dev));
+  const Rows r(a, c);
+  Taken taken{c, {}, {}};
+  const mk_span_workspace ws = {r.ws_ptr(), r.ws_bytes(), r.ws.defined() ? nullptr : Taken::take, &taken};
+  const mk_stream_t on = c.stream();
+  int rc;
+  {
+    Unlocked u;
+    rc = attend(r, &ws, on);
+  }
+  if (taken.failed) std::rethrow_exception(taken.failed);
+  if (rc != MK_OK) raise(rc, g_mk.last_error());
+  return keep(a[6], r.out);
 }
 
 int32_t number(PyObject* o, const char* what) {
@@ -312,22 +348,20 @@ int32_t number(PyObject* o, const char* what) {
   return static_cast<int32_t>(v);
 }
 
-// .., window, sinks)
+// window_attention(.., status, window, sinks)
 PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 11)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Call c(a);
     const int32_t window = number(a[9], "window: a whole number of 32 bits"), sinks = number(a[10], "sinks: a whole number of 32 bits");
-    return attention(
-        a, c, [&](size_t* bytes) { return g_mk.window_workspace(&c.shape, c.n(), c.chunk.v, c.len.v, window, sinks, bytes); },
-        [&](const void* q, int64_t stride, void* out, void* ws, size_t ws_bytes, int32_t* status, mk_stream_t on) {
-          return g_mk.window(&c.shape, c.n(), c.chunk.v, c.len.v, window, sinks, c.tables(), q, stride, c.kv.data_ptr(), out, ws,
-                             ws_bytes, status, on);
-        });
+    return span_attention(a, c, [&](const Rows& r, const mk_span_workspace* ws, mk_stream_t on) {
+      return g_mk.window(&c.shape, c.n(), c.chunk.v, c.len.v, window, sinks, c.tables(), r.q.data_ptr(), r.stride,
+                         c.kv.data_ptr(), r.out.data_ptr(), ws, r.status, on);
+    });
   });
 }
 
-// .., group_seqs, prefix_lens)
+// prefix_attention(.., status, group_seqs, prefix_lens)
 PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 11)) return nullptr;
   return guarded([&]() -> PyObject* {
@@ -336,15 +370,10 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Lengths seqs = lengths(a[9], what, where), shared = lengths(a[10], what, where);
     need(seqs.n == shared.n, "group_seqs and prefix_lens: one number per group each");
     const int groups = static_cast<int>(std::min<int64_t>(seqs.n, kMaxSeqs + 1));
-    return attention(
-        a, c,
-        [&](size_t* bytes) {
-          return g_mk.prefix_workspace(&c.shape, c.n(), c.chunk.v, c.len.v, groups, seqs.v, shared.v, bytes);
-        },
-        [&](const void* q, int64_t stride, void* out, void* ws, size_t ws_bytes, int32_t* status, mk_stream_t on) {
-          return g_mk.prefix(&c.shape, c.n(), c.chunk.v, c.len.v, groups, seqs.v, shared.v, c.tables(), q, stride, c.kv.data_ptr(),
-                             out, ws, ws_bytes, status, on);
-        });
+    return span_attention(a, c, [&](const Rows& r, const mk_span_workspace* ws, mk_stream_t on) {
+      return g_mk.prefix(&c.shape, c.n(), c.chunk.v, c.len.v, groups, seqs.v, shared.v, c.tables(), r.q.data_ptr(), r.stride,
+                         c.kv.data_ptr(), r.out.data_ptr(), ws, r.status, on);
+    });
   });
 }
 
@@ -369,13 +398,13 @@ PyObject* read_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(the exception class, called with (code, text); the addresses of the nine calls in the order of g_mk)
+// init(the exception class, called with (code, text); the addresses of the seven calls in the order of g_mk)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 10)) return nullptr;
-  void* f[9];
-  for (int i = 0; i < 9; ++i) f[i] = PyLong_AsVoidPtr(a[1 + i]);
+  if (!count(n, 8)) return nullptr;
+  void* f[7];
+  for (int i = 0; i < 7; ++i) f[i] = PyLong_AsVoidPtr(a[1 + i]);
   if (PyErr_Occurred()) return nullptr;
-  static_assert(sizeof f == sizeof g_mk, "nine calls");
+  static_assert(sizeof f == sizeof g_mk, "seven calls");
   std::memcpy(&g_mk, f, sizeof f);
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);

@@ -4,6 +4,7 @@
 
 #include "mk_chunk_attn.cuh"
 #include "mk_debug.h"
+#include "mk_span_call.h"
 
 namespace mk {
 namespace {
@@ -280,11 +281,15 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
 }
 
 int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, const int32_t* block_tables, const void* q,
-           int64_t q_stride, const void* kv_layer, void* out, void* workspace, size_t workspace_bytes, int32_t* status_out,
+           int64_t q_stride, const void* kv_layer, void* out, const mk_span_workspace& given, int32_t* status_out,
            mk_stream_t stream) {
-  int rc = check_attention(c, p.seqs, block_tables, q, q_stride, kv_layer, out, workspace, workspace_bytes, call.bytes());
+  const bool take = given.take != nullptr && call.bytes() > 0;
+  int rc = check_attention(c, p.seqs, block_tables, q, q_stride, kv_layer, out, given.ptr, given.bytes, take ? 0 : call.bytes());
   if (rc) return rc;
   const int rows = p.seqs.row0[p.seqs.n];
+  void* workspace = take ? given.take(given.ctx, call.bytes()) : given.ptr;
+  if (take && !workspace) return chunk_fail(MK_ERR_OOM, "no workspace of %zu bytes", call.bytes());
+  if (misaligned(workspace, 16)) return chunk_fail(MK_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = clear_status(status_out, st);
   if (rc || rows == 0) return rc;
@@ -379,17 +384,26 @@ extern "C" int mk_window_attention_workspace(const mk_cache_shape* shape, int32_
   return MK_OK;
 }
 
-extern "C" int mk_window_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
-                                   const int32_t* seq_lens, int32_t window, int32_t sinks, const int32_t* block_tables,
-                                   const void* q, int64_t q_stride, const void* kv_layer, void* out, void* workspace,
-                                   size_t workspace_bytes, int32_t* status_out, mk_stream_t stream) {
+extern "C" int mk_window_attention_in(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                      const int32_t* seq_lens, int32_t window, int32_t sinks, const int32_t* block_tables,
+                                      const void* q, int64_t q_stride, const void* kv_layer, void* out,
+                                      const mk_span_workspace* workspace, int32_t* status_out, mk_stream_t stream) {
   Params<SpanPlan> p;
   int rc = check_chunk(shape, num_seqs, chunk_lens, seq_lens, &p.seqs);
   if (!rc) rc = check_window(window, sinks);
   if (rc) return rc;
   SpanCall call;
   if (!plan_window(*shape, p.seqs, window, sinks, &call)) return too_many();
-  return attend(*shape, call, p, block_tables, q, q_stride, kv_layer, out, workspace, workspace_bytes, status_out, stream);
+  return attend(*shape, call, p, block_tables, q, q_stride, kv_layer, out, *workspace, status_out, stream);
+}
+
+extern "C" int mk_window_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                   const int32_t* seq_lens, int32_t window, int32_t sinks, const int32_t* block_tables,
+                                   const void* q, int64_t q_stride, const void* kv_layer, void* out, void* workspace,
+                                   size_t workspace_bytes, int32_t* status_out, mk_stream_t stream) {
+  const mk_span_workspace given = {workspace, workspace_bytes, nullptr, nullptr};
+  return mk_window_attention_in(shape, num_seqs, chunk_lens, seq_lens, window, sinks, block_tables, q, q_stride, kv_layer, out,
+                                &given, status_out, stream);
 }
 
 extern "C" int mk_prefix_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
@@ -406,18 +420,28 @@ extern "C" int mk_prefix_attention_workspace(const mk_cache_shape* shape, int32_
   return MK_OK;
 }
 
-extern "C" int mk_prefix_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
-                                   const int32_t* seq_lens, int32_t num_groups, const int32_t* group_seqs,
-                                   const int32_t* prefix_lens, const int32_t* block_tables, const void* q, int64_t q_stride,
-                                   const void* kv_layer, void* out, void* workspace, size_t workspace_bytes,
-                                   int32_t* status_out, mk_stream_t stream) {
+extern "C" int mk_prefix_attention_in(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                      const int32_t* seq_lens, int32_t num_groups, const int32_t* group_seqs,
+                                      const int32_t* prefix_lens, const int32_t* block_tables, const void* q, int64_t q_stride,
+                                      const void* kv_layer, void* out, const mk_span_workspace* workspace, int32_t* status_out,
+                                      mk_stream_t stream) {
   Params<SpanPlan> p;
   int rc = check_chunk(shape, num_seqs, chunk_lens, seq_lens, &p.seqs);
   if (!rc) rc = check_groups(p.seqs, num_groups, group_seqs, prefix_lens);
   if (rc) return rc;
   SpanCall call;
   if (!plan_prefix(*shape, p.seqs, num_groups, group_seqs, prefix_lens, &call)) return too_many();
-  return attend(*shape, call, p, block_tables, q, q_stride, kv_layer, out, workspace, workspace_bytes, status_out, stream);
+  return attend(*shape, call, p, block_tables, q, q_stride, kv_layer, out, *workspace, status_out, stream);
+}
+
+extern "C" int mk_prefix_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
+                                   const int32_t* seq_lens, int32_t num_groups, const int32_t* group_seqs,
+                                   const int32_t* prefix_lens, const int32_t* block_tables, const void* q, int64_t q_stride,
+                                   const void* kv_layer, void* out, void* workspace, size_t workspace_bytes,
+                                   int32_t* status_out, mk_stream_t stream) {
+  const mk_span_workspace given = {workspace, workspace_bytes, nullptr, nullptr};
+  return mk_prefix_attention_in(shape, num_seqs, chunk_lens, seq_lens, num_groups, group_seqs, prefix_lens, block_tables, q,
+                                q_stride, kv_layer, out, &given, status_out, stream);
 }
 
 extern "C" int mk_plan_span_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
