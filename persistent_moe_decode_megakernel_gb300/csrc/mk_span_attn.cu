@@ -13,8 +13,9 @@ namespace {
 // sequence's positions and then those of the shared ones, each in one piece or cut.
 //
 // 8 rows lie side by side in a partial, so 8 lanes read 128 bytes of one; the warp's other lanes take other columns.
-// What it takes is latency.  Few rows (kDeep): two blocks an SM are all there is, and a lane has 12 partials on their way
-// before it waits for the first.  Many rows: more blocks, each over several groups of 8 rows.
+// What it takes is latency.  Few rows: a block's 8 warps take every eighth partial each of 16 columns (kSplit).  More: a warp
+// has 16 columns and all partials, 12 of them on their way before it waits for the first, two blocks an SM (kDeep).  Many
+// rows: more and lighter blocks, each over several groups of 8 rows (kMany).
 //
 // The launch brings just what is looked up, and a block copies it into shared memory at once, before it waits for the
 // kernel that writes the partials (walked where it lies, in the constant bank, each step of a search was a miss of its
@@ -26,6 +27,7 @@ struct Sight {
 struct JoinParams : CallParams {     // what the rows that are worked out again need
   Sight plan;
 };
+enum { kSplit, kDeep, kMany };
 struct JoinEntry {
   int32_t row0, rows, units, item0, part0;
   int8_t kind, pair;
@@ -94,10 +96,11 @@ __device__ __forceinline__ PartSet parts_of(const Joins<KINDS>& a, const JoinEnt
   return s;
 }
 
-template <int D, int M, int KINDS, bool kDeep>
-__global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
+template <int D, int M, int KINDS, int kMode>
+__global__ void __launch_bounds__(kMode == kSplit ? 256 : 2 * D, kMode == kSplit ? 3 : kMode == kDeep ? 256 / D : 512 / D)
     join_kernel(const __grid_constant__ JoinParams p, const __grid_constant__ Joins<KINDS> given) {
-  constexpr int kThreads = 2 * D, kAhead = kDeep ? 12 : 3;
+  constexpr int kThreads = kMode == kSplit ? 256 : 2 * D, kAhead = kMode == kSplit ? 5 : kMode == kDeep ? 12 : 3;
+  constexpr int kEvery = kMode == kSplit ? 8 : 1;
   __shared__ Joins<KINDS> a;
   __shared__ PartSet sets[2][8][2];
   // (by their generic address: constant reads would go one lane at a time; and all at once)
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
     reinterpret_cast<uint4*>(&a)[min(static_cast<int>(threadIdx.x) + i * kThreads, kWords - 1)] = w[i];
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, UT = a.UT;
-  const int chunk = warp * 4 + (lane >> 3);
+  const int chunk = (kMode == kSplit ? static_cast<int>(blockIdx.z) : warp) * 4 + (lane >> 3), mine = kMode == kSplit ? warp : 0;
   const bool cut = static_cast<int>(blockIdx.x) < a.cuts;
   int lo = 0, unit = 0, kvh, hrows, rows, r0;
   if (cut) {
@@ -171,10 +174,11 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
     float2 held_ml[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      held_ml[i] = i < n ? ml(i) : make_float2(-INFINITY, 0.f);
-      held[i] = i < n ? columns(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int k = mine + i * kEvery;
+      held_ml[i] = k < n ? ml(k) : make_float2(-INFINITY, 0.f);
+      held[i] = k < n ? columns(k) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if constexpr (kDeep)
+    if constexpr (kMode == kDeep)
       for (int k = kAhead; k < n; ++k)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(k < own.n ? own.address(k, chunk) : over.address(k - own.n, chunk)));
     find(row0 + gridDim.y * 8, turn ^ 1);
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) top = fmaxf(top, held_ml[i].x);
 #pragma unroll 8
-    for (int k = kAhead; k < n; ++k) top = fmaxf(top, ml(k).x);
+    for (int k = mine + kAhead * kEvery; k < n; k += kEvery) top = fmaxf(top, ml(k).x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
     auto add = [&](const float4 x, const float2 ml) {
@@ -196,15 +200,30 @@ __global__ void __launch_bounds__(2 * D, kDeep ? 256 / D : 512 / D)
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) add(held[i], held_ml[i]);
 #pragma unroll 8
-    for (int k = kAhead; k < n; ++k) add(columns(k), ml(k));
+    for (int k = mine + kAhead * kEvery; k < n; k += kEvery) add(columns(k), ml(k));
+    if constexpr (kMode == kSplit) {
+      // the warps' sums, each relative to its own maximum, in the warps' order
+      __shared__ float4 sums[8][32];
+      __shared__ float2 scale[8][32];
+      sums[warp][lane] = acc;
+      scale[warp][lane] = make_float2(top, L);
+      __syncthreads();
+      top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, scale[w][lane].x);
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      L = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) add(sums[w][lane], scale[w][lane]);
+    }
     const float inv = L == 0.f ? 0.f : 1.0f / L;
     acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (live)
+    if (live && mine == 0)
       *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(r) * p.Hq + h) * D + chunk * 4) =
           make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
     // (as in merge_kernel; a row's columns are several warps')
     const float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
-    const bool odd = live && (L == 0.f || !(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
+    const bool odd = live && mine == 0 && (L == 0.f || !(big <= 3.3e38f) || acc.x != acc.x || acc.y != acc.y || acc.z != acc.z || acc.w != acc.w);
     if (__syncthreads_or(odd)) {
       uint32_t done = 0;
       for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
@@ -230,7 +249,7 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
   p.plan.Hkv = call.plan[0].Hkv;
   p.plan.window = call.plan[0].window;
   p.plan.sinks = call.plan[0].sinks;
-  int most = 0;
+  int most = 0, parts = 0;           // rows of a job, partials of a row
   int64_t groups = 0;                // of 8 rows
   a.cuts = 0;
   for (int k = 0; k < KINDS; ++k) {
@@ -255,6 +274,7 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
       const int rows = g.ntok * G << x.pair;
       most = std::max(most, rows);
       groups += (rows + 7) / 8;
+      parts = std::max<int>(parts, x.parts);
     }
   }
   a.whole = given.whole;
@@ -271,13 +291,22 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
     const int rows = std::min(a.join[k].own.rows, UT) * G;
     most = std::max(most, rows);
     groups += static_cast<int64_t>(a.join[k].own.units) * a.Hkv * ((rows + 7) / 8);
+    // (the blocks that begin among the group's items, over these)
+    const JoinEntry& o = a.join[k].over;
+    if (k > 0 && o.row0 == a.join[k - 1].over.row0) continue;
+    const int64_t items = static_cast<int64_t>(o.units) * (a.Hkv >> o.pair);
+    int64_t in = 0;
+    for (int b = 0; b < a.blocks[o.kind]; ++b) in += a.start[o.kind][b] / 2 >= o.item0 && a.start[o.kind][b] / 2 < o.item0 + items;
+    parts = std::max<int>(parts, static_cast<int>(2 + in / items));
   }
   const int jobs = a.cuts + call.jobs;
-  // few: two blocks an SM at once; many: some ten blocks an SM, each over several groups of rows
-  if (groups <= 2 * kMaxBlocks)
-    return launch_after(join_kernel<D, M, KINDS, true>, dim3(jobs, (most + 7) / 8), 2 * D, 0, st, p, a);
+  const dim3 all(jobs, (most + 7) / 8);
+  // (one token through 32768: 32 us so, 65 deep; 16 through 8192, whose rows have 5 partials: 68 and 66)
+  if (groups <= kMaxBlocks / 2 && parts > 12)
+    return launch_after(join_kernel<D, M, KINDS, kSplit>, dim3(all.x, all.y, D / 16), 256, 0, st, p, a);
+  if (groups <= 2 * kMaxBlocks) return launch_after(join_kernel<D, M, KINDS, kDeep>, all, 2 * D, 0, st, p, a);
   const int y = std::max(1, std::min((most + 7) / 8, (10 * kMaxBlocks + jobs - 1) / jobs));
-  return launch_after(join_kernel<D, M, KINDS, false>, dim3(jobs, y), 2 * D, 0, st, p, a);
+  return launch_after(join_kernel<D, M, KINDS, kMany>, dim3(jobs, y), 2 * D, 0, st, p, a);
 }
 
 int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, const int32_t* block_tables, const void* q,

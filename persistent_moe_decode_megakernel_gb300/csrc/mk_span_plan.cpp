@@ -22,6 +22,10 @@ const Costs& costs(const mk_cache_shape& c, int kind) {
 }
 // What cut items cost besides: the second kernel, and the bytes of partials that it and the first one move in a tenth.
 constexpr int64_t kJoinCost = 45, kJoinBytes = 250000;
+// What going over shared positions together costs besides: that, and the smaller pieces.  (8 sequences of 5 rows behind 8192
+// positions, 7.7 us less work together: 30 us apart, 40 together; 32 tokens behind 2048, 11.3 less: 31 and 30; 16 behind 8192,
+// 22.6 less: 44 and 28.)
+constexpr int64_t kShareCost = 95, kRunCost = 10;
 constexpr int kLeastSegment = 20;            // of these costs
 constexpr int kMostTries = 24;
 constexpr int kMinRange = 3;                 // position tiles a block is worth
@@ -29,10 +33,11 @@ constexpr int kMaxRuns = 4096;               // units beyond which whole items a
 
 // Launches are of one kind of operand each (SpanCall); a sequence's rows take
 //   kFewRows  over q8_0, where its units have at most 32 rows of a KV head,
-//   kStagedRows  over q8_0, where its units together decode each position kStageTimes or more often: decoding it once
-//             is less work (kStageBytes of decoded positions at most in a call),
+//   kStagedRows  over q8_0, where decoding their positions once, into the workspace, is less work than every unit's
+//             block doing it: that costs a block 0.8 us a tile more (over all blocks), staging a launch, 5 us, and its
+//             bytes, 0.025 us a tile and KV head.  (1024 rows of 16384 through 2048: 47 us, staged 42; 512 of 8192 through
+//             256: 22 and 26.)  kStageBytes of decoded positions at most in a call;
 //   kPageRows  else.
-constexpr int kStageTimes = 4;
 constexpr size_t kStageBytes = size_t(1) << 30;
 constexpr int kPairTiles = 4;
 constexpr int kGatherTiles = 40;
@@ -86,7 +91,9 @@ struct Builder {
       times += g.tiles;
     }
     const size_t bytes = static_cast<size_t>(own) * 2 * c.num_kv_heads * kTile * c.head_dim * 2;
-    if (times < static_cast<int64_t>(kStageTimes) * own || call->stage_bytes + bytes > kStageBytes) return false;
+    if (times * c.num_kv_heads * 8 / kMaxBlocks <= 50 + static_cast<int64_t>(own) * c.num_kv_heads / 4 ||
+        call->stage_bytes + bytes > kStageBytes)
+      return false;
     e->stage0 = call->stage_tiles;
     call->stage_tiles += own;
     call->stage_bytes += bytes;
@@ -331,8 +338,11 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
   Builder build(c, call);
   const int UT = build.UT;
   // Runs of a group's sequences whose rows do not fill a unit of their own (with others', they share one), between those
-  // that do.  A run's rows go over the shared positions together where that saves its blocks more time (over all
-  // of them) than the second kernel takes with the partials of its rows.
+  // that do.  A run's rows may go over the shared positions together where that saves blocks time (over all of them), and
+  // the runs of which that holds do so if they save more than that costs.
+  struct { int32_t first, end, positions; } run[kMaxSeqs];
+  int runs = 0;
+  int64_t total = 0;
   int32_t common[kMaxSeqs];                              // whole pages that a sequence's run goes over together, or 0
   EntryRef over[kMaxSeqs];
   for (int i = 0, s0 = 0; i < num_groups; s0 += group_seqs[i++]) {
@@ -356,22 +366,26 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
       if (with > 1 && tiles > 0) {
         const int64_t saved = (apart - cost(rows, 1)) * c.num_kv_heads / kMaxBlocks;
         const int64_t bytes = static_cast<int64_t>(rows) * c.num_q_heads * (c.head_dim + 4) * 8;
-        if (saved > kJoinCost + bytes / kJoinBytes) {
-          SpanEntry e = {};
-          e.seq = first;
-          e.row0 = q.row0[first];
-          e.rows = rows;
-          e.before = e.len = positions;
-          e.part0 = call->whole_rows;
-          call->whole_rows += rows;
-          const EntryRef at = build.add(e);
-          for (int k = first; k < s; ++k) {
-            common[k] = positions;
-            over[k] = at;
-          }
+        if (saved > kRunCost + bytes / kJoinBytes) {
+          run[runs++] = {first, s, positions};
+          total += saved - bytes / kJoinBytes;
         }
       }
       if (s < end && s == first) common[s++] = 0;         // fills units of its own
+    }
+  }
+  for (int i = 0; i < runs && total > kShareCost; ++i) {
+    SpanEntry e = {};
+    e.seq = run[i].first;
+    e.row0 = q.row0[run[i].first];
+    e.rows = q.row0[run[i].end] - e.row0;
+    e.before = e.len = run[i].positions;
+    e.part0 = call->whole_rows;
+    call->whole_rows += e.rows;
+    const EntryRef at = build.add(e);
+    for (int k = run[i].first; k < run[i].end; ++k) {
+      common[k] = run[i].positions;
+      over[k] = at;
     }
   }
   // after the shared positions, sequences that write the output and then those of runs (the order of SpanPlan)
