@@ -184,6 +184,82 @@ def test_window_with_every_score_minus_infinity_is_nan():
     assert torch.all(out.isnan())
 
 
+@pytest.mark.parametrize("hq,hkv,d,q8", [(32, 4, 128, False), (32, 4, 128, True), (14, 2, 64, False), (6, 3, 128, False)])
+def test_window_few_rows_of_many_partials(hq, hkv, d, q8):
+    # long windows of one and two rows, cut over all blocks; and of more of them
+    for lens, news, window in (([40000], [1], 30000), ([20000, 31000], [2, 1], 25000), ([9000] * 12, [1] * 12, 8000)):
+        st = R.Setup(hq, hkv, d, 64, lens, news, q8=q8, seed=17)
+        hide(st, window, 4)
+        check_window(st, window, 4)
+
+
+def test_window_three_launches():
+    # q8_0: a prompt that is decoded once, forty rows, and tokens too many to go with these
+    lens = [4500, 9000] + [9000 + 13 * i for i in range(40)]
+    st = R.Setup(32, 4, 128, 64, lens, [4096, 40] + [1] * 40, q8=True, seed=18)
+    hide(st, 8192, 4)
+    seg = mk.plan_span_attention(st.shape(mk), st.news, st.lens, 8192, 4)
+    assert sorted(set(seg[:, 0].tolist())) == [0, 1, 2]
+    check_window(st, 8192, 4)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_window_of_a_poisoned_position_in_cut_items(q8):
+    # a NaN behind the sinks is nobody's, one in the window of a token whose item is cut is that token's alone
+    st = R.Setup(32, 4, 128, 16, [20000] * 3, [1] * 3, q8=q8, seed=19)
+    q = st.normal(3, 32, 128, std=1.5)
+    ref, *scale = S.attention(st, q, st.kv, 9000, 4)
+    bound = R.attention_bound(ref, *scale, q8)
+    for s, pos in ((0, 5), (1, 15000)):
+        page, off = int(st.bt[s, pos // 16]), pos % 16
+        if q8:
+            st.planes()[1][page, :, :, off] = float("nan")
+        else:
+            st.kv[page, :, :, off] = float("nan")
+    out = mk.window_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, 9000, 4)
+    good = torch.tensor([True, False, True], device="cuda")
+    assert torch.all(((out.double() - ref).abs() <= bound)[good]) and torch.all(out[1].isnan())
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_offsets_beyond_32_bits(q8):
+    # a pool of more than 4 GiB, of which the sequences have the last pages and the first ones
+    hq, hkv, d, ps = 16, 8, 128, 128
+    P = (9 << 29) // (hkv * ps * d) if q8 else (9 << 28) // (hkv * ps * d)
+    small = R.Setup(hq, hkv, d, ps, [1500, 1500, 900], [3, 1, 200], q8=q8, seed=20)
+    S.share(small, [2, 1], [1280, 0])
+    n = P * 2 * hkv * ps * d
+    kv = torch.zeros(n + n // 16, dtype=torch.uint8, device="cuda") if q8 else torch.zeros(P, 2, hkv, ps, d, dtype=torch.bfloat16,
+                                                                                       device="cuda")
+    assert kv.nbytes > 1 << 32
+    to = torch.tensor([P - 1 - i if i % 2 else i for i in range(small.P)], device="cuda")
+    if q8:
+        codes = kv[:n].view(torch.int8).view(P, 2, hkv, ps, d)
+        scales = kv[n:].view(torch.float16).view(P, 2, hkv, ps, d // 32)
+        a, b = small.planes()
+        codes[to], scales.view(torch.int16)[to] = a, b.view(torch.int16)
+    else:
+        kv[to] = small.kv
+    q = small.normal(small.rows, hq, d, std=1.5)
+    bt = torch.where(small.bt >= 0, to[small.bt.clamp(min=0).long()].to(torch.int32), small.bt)
+    sh = mk.CacheShape(hq, hkv, d, ps, P, small.maxpg, mk.FLAG_KV_Q8 if q8 else 0)
+    for call in (lambda s, t, k: mk.window_attention(s, q, small.news, small.lens, t, k, 700, 4),
+                 lambda s, t, k: mk.prefix_attention(s, q, small.news, small.lens, t, k, [2, 1], [1280, 0])):
+        want = call(small.shape(mk), small.bt, small.kv)
+        assert torch.equal(call(sh, bt, kv), want) and not want.isnan().any()
+
+
+def test_output_aligned_to_16_bytes():
+    st = R.Setup(16, 2, 128, 16, [900, 3000], [300, 1], seed=21)
+    q = st.normal(301, 16, 128, std=1.5)
+    for off in (8, 16, 24):
+        buf = torch.full((301 * 2048 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[off:off + 301 * 2048].view(301, 16, 128)
+        want = mk.window_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, 500, 4)
+        mk.window_attention(st.shape(mk), q, st.news, st.lens, st.bt, st.kv, 500, 4, out=out)
+        assert torch.equal(out, want) and torch.all(buf[:off] == 7.0) and torch.all(buf[off + 301 * 2048:] == 7.0)
+
+
 # ---------------------------------------------------------------- shared prefixes
 PREFIX_SHAPES = [
     # hq, hkv, d, ps, groups, shared, own lengths (repeated), news (repeated)
@@ -230,6 +306,23 @@ def test_prefix_long(std, q8):
 def test_prefix_with_prompts_among_single_tokens(q8):
     st = prefix_setup(16, 2, 128, 16, [12, 4], [5000, 3000], [300, 20, 700], [260, 1, 1, 513], q8, seed=33)
     check_prefix(st, [12, 4], [5000, 3000])
+
+
+@pytest.mark.parametrize("hq,hkv,d,q8", [(32, 4, 128, False), (32, 4, 128, True), (4, 1, 64, False), (7, 1, 128, False)])
+def test_prefix_with_many_rows_to_join(hq, hkv, d, q8):
+    # rows of several 8s a unit, several blocks of them; and few rows of many partials
+    for n, news, shared in ((64, 9, 6000), (48, 16, 9000), (3, 1, 60000)):
+        st = prefix_setup(hq, hkv, d, 16, [n], [shared], [40, 21], [news], q8, seed=36)
+        check_prefix(st, [n], [shared])
+
+
+def test_prefix_groups_with_empty_sequences():
+    # sequences without new tokens stand in groups (first, last and between), and a whole group of them
+    lens = [5000] * 24 + [40, 900, 700]
+    news = [0] + [1] * 10 + [0] * 2 + [1] * 10 + [0] + [0, 0, 5]
+    st = R.Setup(32, 4, 128, 16, lens, news, seed=37)
+    S.share(st, [24, 2, 1], [4800, 32, 0])
+    check_prefix(st, [24, 2, 1], [4800, 32, 0])
 
 
 @pytest.mark.parametrize("q8", [False, True])
@@ -310,6 +403,53 @@ def test_calls_are_repeatable_captured_and_on_other_streams(q8):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.all(a == 0) for a in got)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_two_graphs_share_a_workspace(q8):
+    # one after the other on a stream, each many times, with other calls between: a call owns the workspace while it runs
+    st = prefix_setup(16, 2, 128, 16, [40], [6000], [60, 9], [1], q8, seed=44)
+    q = st.normal(st.rows, 16, 128, std=1.5)
+    args = (st.shape(mk), q, st.news, st.lens, st.bt, st.kv)
+    need = max(mk.prefix_attention_workspace(*[args[i] for i in (0, 2, 3)], [40], [6000]),
+               mk.window_attention_workspace(*[args[i] for i in (0, 2, 3)], 5000, 4))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = mk.prefix_attention(*args, [40], [6000]), mk.window_attention(*args, 5000, 4)
+    graphs, got = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g, call in zip(graphs, (lambda: mk.prefix_attention(*args, [40], [6000], workspace=ws),
+                                lambda: mk.window_attention(*args, 5000, 4, workspace=ws))):
+        call()
+        with torch.cuda.graph(g):
+            got.append(call())
+    for i in (0, 1, 0, 0, 1, 1, 0, 1):
+        got[i].zero_()
+        graphs[i].replay()
+        mk.chunk_attention(*args)
+        graphs[1 - i].replay()
+        ws.fill_(0xff)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_calls_follow_each_other_without_a_pause():
+    # each call's first kernel may set itself up while the one before ends: what it reads is what that one wrote
+    st = prefix_setup(16, 2, 128, 16, [20], [3000], [60, 9], [1], False, seed=45)
+    args = (st.shape(mk), st.news, st.lens, st.bt, st.kv)
+    first = st.normal(st.rows, 16, 128, std=1.5)
+
+    def chain(wait):
+        q = first.clone()
+        for _ in range(12):
+            q = mk.window_attention(args[0], q * 3, *args[1:], 700, 4)
+            if wait:
+                torch.cuda.synchronize()
+            q = mk.prefix_attention(args[0], q, *args[1:], [20], [3000])
+            if wait:
+                torch.cuda.synchronize()
+        return q
+    want = chain(True)
+    for _ in range(3):
+        assert torch.equal(chain(False), want)
 
 
 def test_calls_of_several_threads():

@@ -299,3 +299,87 @@ def test_plans_of_the_largest_calls():
     segs = segments(sh, [1, 1], [1 << 30, 1 << 30], group_seqs=[2], prefix_lens=[(1 << 30) - 1])
     # 2^30 - 16 shared positions, and 16 of each sequence's own
     assert heads(segs) == 2 * (1 << 23) + 2 * 2
+
+
+def blocks_of(segs):
+    """Position tiles over all KV heads, and segments, of each launch's blocks."""
+    load = {}
+    for g in segs:
+        at = load.setdefault((g["launch"], g["block"]), [0, 0])
+        at[0] += g["n"] * (1 + g["pair"])
+        at[1] += 1
+    return load
+
+
+@pytest.mark.parametrize("cl,sl,kw", [
+    ([1] * 64, [9000] * 64, dict(window=4096, sinks=4)), ([1], [1 << 17], dict(window=1 << 16, sinks=4)),
+    ([1] * 20, [5000 + 700 * i for i in range(20)], dict(window=1 << 20)),
+    ([1] * 64, [40000] * 64, dict(group_seqs=[64], prefix_lens=[32768]))])
+@pytest.mark.parametrize("flags", [0, mk.FLAG_KV_Q8])
+def test_cuts_are_even(cl, sl, kw, flags):
+    # a launch whose items are cut: no block has much more than its share (the costs differ by kind, by less than 2)
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 14, flags=flags)
+    segs = segments(sh, cl, sl, **kw)
+    assert any(0 <= g["slot"] < WHOLE for g in segs)
+    load = blocks_of(segs)
+    work = [t + 4 * n for t, n in load.values()]
+    assert max(work) <= 2 * sum(work) / 152 + 4
+
+
+def test_sequences_that_fill_units_read_for_themselves():
+    # 30 tokens and two prompts behind 8192 shared positions: the tokens' runs go over these together, the prompts do not
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 12)
+    cl = [1] * 10 + [500] + [1] * 15 + [400] + [1] * 5
+    segs = segments(sh, cl, [8192 + 900] * 32, group_seqs=[32], prefix_lens=[8192])
+    row0 = np.concatenate([[0], np.cumsum(cl)])
+    runs = sorted({(g["row0"], g["ntok"]) for g in segs if g["len"] == 8192})
+    assert runs == [(0, 10), (510, 15), (int(row0[27]), 5)]
+    for s in (10, 26):
+        mine = [g for g in segs if row0[s] <= g["row0"] < row0[s + 1]]
+        assert mine and all(g["len"] == 9092 and g["slot"] != WHOLE and g["table"] == s for g in mine)
+
+
+def test_runs_share_where_they_save_enough_together():
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 12)
+
+    def shared(n, rows, prefix, groups=1):
+        segs = segments(sh, [rows] * (n * groups), [prefix + 200] * (n * groups), group_seqs=[n] * groups,
+                        prefix_lens=[prefix] * groups)
+        return any(g["len"] == prefix for g in segs)
+    assert shared(64, 1, 8192) and shared(16, 1, 8192) and not shared(64, 1, 512) and not shared(4, 1, 2048)
+    assert not shared(8, 5, 8192) and shared(8, 5, 8192, groups=2)     # two groups for the price of one kernel
+
+
+def test_q8_launches():
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 14, flags=mk.FLAG_KV_Q8)
+
+    def launches(cl, sl, **kw):
+        return sorted({g["launch"] for g in segments(sh, cl, sl, **kw)})
+    assert launches([1] * 8, [5000] * 8, window=1000) == [2]                       # few rows of a unit
+    assert launches([40], [5000], window=1000) == [0]
+    assert launches([1] * 8 + [40], [5000] * 9, window=1000) == [0]                # with the launch that there is
+    assert launches([1] * 60 + [40], [20000] * 61, window=16384) == [0, 2]         # but not so much of it
+    assert launches([4096], [8192], window=512) == [1]                             # decoded once
+    assert launches([512], [8192], window=256) == [0]
+    assert launches([1] * 60 + [40, 4096], [20000] * 62, window=16384) == [0, 1, 2]
+
+
+def test_staged_bytes_are_bounded():
+    # 8 KV heads: a tile of 128 positions is half a MiB decoded; beyond a GiB sequences are read from their pages
+    sh = shape(num_q_heads=64, num_kv_heads=8, max_pages_per_seq=1 << 16, flags=mk.FLAG_KV_Q8)
+    segs = segments(sh, [2000] * 3, [1600 * 128, 600 * 128, 400 * 128], window=1 << 20)
+    assert {g["table"]: g["launch"] for g in segs} == {0: 1, 1: 0, 2: 1}
+    assert mk.window_attention_workspace(sh, [2000] * 3, [1600 * 128, 600 * 128, 400 * 128], 1 << 20) >= 2000 << 19
+
+
+@pytest.mark.parametrize("kw", [dict(window=50, sinks=3), dict(group_seqs=[2, 1], prefix_lens=[64, 0])])
+def test_workspace_is_what_the_plan_needs(kw):
+    sh = shape(max_pages_per_seq=1 << 12)
+    cl, sl = [3, 0, 5], [70, 64, 9]
+    call = mk.window_attention_workspace if "window" in kw else mk.prefix_attention_workspace
+    assert call(sh, cl, sl, *kw.values()) == 0                                     # whole items that write the output
+    big = [1] * 64, [60000] * 64
+    kw = dict(window=1 << 20, sinks=0) if "window" in kw else dict(group_seqs=[64], prefix_lens=[50000])
+    segs = segments(sh, *big, **kw)
+    cut = max(g["slot"] for g in segs if g["slot"] < WHOLE)
+    assert call(sh, *big, *kw.values()) >= (cut + 1) * 4 * 132 * 4
