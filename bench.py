@@ -502,11 +502,11 @@ def main():
 
 
 def _kernel_hash():
-    """Of the step's sources (the chunk operators, mk_chunk*, are no part of it)."""
+    """Of the step's sources (the chunk and span operators, mk_chunk* and mk_span*, are no part of it)."""
     import hashlib
     h = hashlib.sha256()
     d = os.path.join(ROOT, "persistent_moe_decode_megakernel_gb300", "csrc")
-    for f in sorted(f for f in os.listdir(d) if not f.startswith("mk_chunk")):
+    for f in sorted(f for f in os.listdir(d) if not f.startswith(("mk_chunk", "mk_span"))):
         h.update(open(os.path.join(d, f), "rb").read())
     return h.hexdigest()[:16]
 
