@@ -20,9 +20,15 @@
 // Roles.  Warps 0-3 and 4-7: softmax and epilogue of tile (stream) 0 and 1.  Warps 8 and 11: K and V
 // loads.  Warp 9: issues the MMAs.  Warp 10: query rows and V tails.  Over a q8_0 cache warps 12-15
 // decode codes into fp16 operand tiles (units of at most 32 rows: two groups, warps 12-15 K and 16-19 V);
-// sequences whose tiles many blocks would decode are decoded once before (stage_kernel).  Blocks are persistent (mk_chunk_plan.h): loads and scores of the next segment
-// run under the epilogue of this one.  Every wait is bounded: one that runs out raises the block's abort
-// flag, every role leaves its loop, copies in flight are let land and tensor memory is returned.
+// sequences whose tiles many blocks would decode are decoded once before (stage_kernel).  Blocks are persistent
+// (mk_chunk_plan.h): loads and scores of the next segment run under the epilogue of this one.  Every wait is bounded: one
+// that runs out raises the block's abort flag, every role leaves its loop, copies in flight are let land and tensor memory
+// is returned.
+//
+// Parts of the cache (Plan::kSpans; mk_span_plan.h).  The same roles go over a unit's places instead of its sequence's
+// positions; masks hide what lies before a row's window too; a unit of one tile may be two KV heads, a stream each; a
+// segment may write the partial of a whole item, which join_kernel (mk_span_attn.cu) puts together with another's; and the
+// kernel may be launched while the one before it on the stream still runs (launch_after).
 //
 // What bounds it.  Units of two tiles: 4 * 128^3 multiply-adds a position tile need 2048 tensor-core
 // cycles and as many of shared memory (192 KB of operands read, 64 KB written, at 128 B a cycle); about
@@ -30,7 +36,13 @@
 // 32768 tokens: 635 us, 1.68).  Units of one tile: HBM, 160 KB of copies in flight a block (one token, 131072
 // positions: 49.5 us, 5.4 TB/s).  Few rows over a q8_0 cache: the decode, whose two products and byte
 // permute per two codes take the half-precision pipe as long as the copies take HBM (one token, 262144
-// positions: 71.9 us; without the two products 61, without any work 56).
+// positions: 71.9 us; without the two products 61, without any work 56).  A block's segments besides (timelines; parts of
+// the cache): units of two tiles 1.65 us a tile, 2.1 over q8_0, and 4.2 a segment, of which the epilogue is 1.9; two KV heads
+// 1.75 a tile of both (1.5 from HBM at heads of 128) and 2 a segment; before the first scores 4 to 7 us from cold memory.
+// Tried on the 1.65 and slower: two warpgroups a tile with half the columns each (+18 %: more instructions in all), a part of
+// the exponentials as polynomials on the fma pipe (+6 to +30 %: they are not what binds here), the next scores' second half
+// before this tile's products (+17 %: the query tile is read twice, and shared memory binds), and a last tile of half the
+// places as half a tile (+6 %: its code, when fetched, displaces the rest).
 //
 // Operands.  bf16 cache: Q, K, V as they are, P rounded to bf16 (2^-8; its sum uses the unrounded
 // values).  q8_0 cache: fp16, whose 2^-11 keeps a decoded value three bits better than bf16 would

@@ -388,7 +388,7 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
       over[k] = at;
     }
   }
-  // after the shared positions, sequences that write the output and then those of runs (the order of SpanPlan)
+  // behind the shared positions (the longest entries), sequences that write the output, then those of runs
   int order[kMaxSeqs];
   const int n = by_length(q, order);
   for (int pass = 0; pass < 2; ++pass) {
