@@ -167,8 +167,8 @@ int mk_window_attention(const mk_cache_shape* shape, int32_t num_seqs, const int
  *                group_seqs[0] sequences, and so on
  *   prefix_lens: HOST int32 [num_groups]: first positions that a group's sequences share, >= 0 and at most
  *                seq_lens[s] - chunk_lens[s] of each of them (no new token is among them)
- * The first prefix_len / page_size (rounded down) entries of a group's block tables must be the same pages, and
- * are read in the table of any of its sequences; positions behind these pages are each sequence's own.  (Tables that
+ * The first prefix_len / page_size (rounded down) entries of the block tables of a group's sequences with rows must be
+ * the same pages, and are read in the table of any of these; positions behind these pages are each sequence's own.  (Tables that
  * differ there make the group's rows those of one or the other table; no page out of range is touched.)
  * Every other argument, limit, rounding and report is as for mk_chunk_attention, of which the sums' order differs.
  * mk_prefix_attention_workspace gives the bytes of workspace (0: none): beside what mk_chunk_attention's holds,

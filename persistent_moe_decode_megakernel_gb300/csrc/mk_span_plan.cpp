@@ -376,7 +376,8 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
   }
   for (int i = 0; i < runs && total > kShareCost; ++i) {
     SpanEntry e = {};
-    e.seq = run[i].first;
+    e.seq = run[i].first;                                 // (the first with rows: another's table is not read)
+    while (q.row0[e.seq + 1] == q.row0[e.seq]) ++e.seq;
     e.row0 = q.row0[run[i].first];
     e.rows = q.row0[run[i].end] - e.row0;
     e.before = e.len = run[i].positions;

@@ -326,6 +326,16 @@ def test_prefix_groups_with_empty_sequences():
 
 
 @pytest.mark.parametrize("q8", [False, True])
+def test_prefix_group_led_by_sequences_without_rows(q8):
+    # their tables name no page: they are not read, and nothing is reported
+    lens, news = [5000] * 30, [0, 0] + [1] * 27 + [0]
+    st = R.Setup(32, 4, 128, 16, lens, news, q8=q8, seed=38)
+    S.share(st, [30], [4800])
+    st.bt[[0, 1, 29]] = -1
+    check_prefix(st, [30], [4800])
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_prefix_skips_pages_out_of_range(q8):
     # in the shared part (every row of the group skips them), and in one sequence's own
     for shared in (3200, 160):

@@ -383,3 +383,13 @@ def test_workspace_is_what_the_plan_needs(kw):
     segs = segments(sh, *big, **kw)
     cut = max(g["slot"] for g in segs if g["slot"] < WHOLE)
     assert call(sh, *big, *kw.values()) >= (cut + 1) * 4 * 132 * 4
+
+
+def test_a_group_reads_the_table_of_a_sequence_with_rows():
+    # sequences without new tokens stand first: nothing is read through their tables
+    sh = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 12)
+    cl = [0, 0] + [1] * 30
+    segs = segments(sh, cl, [8192 + 100] * 32, group_seqs=[32], prefix_lens=[8192])
+    joint = [g for g in segs if g["len"] == 8192]
+    assert joint and all(g["table"] == 2 and (g["row0"], g["ntok"]) == (0, 30) for g in joint)
+    assert all(cl[g["table"]] > 0 for g in segs)
