@@ -36,13 +36,13 @@
 // 32768 tokens: 635 us, 1.68).  Units of one tile: HBM, 160 KB of copies in flight a block (one token, 131072
 // positions: 49.5 us, 5.4 TB/s).  Few rows over a q8_0 cache: the decode, whose two products and byte
 // permute per two codes take the half-precision pipe as long as the copies take HBM (one token, 262144
-// positions: 71.9 us; without the two products 61, without any work 56).  A block's segments besides (timelines; parts of
-// the cache): units of two tiles 1.65 us a tile, 2.1 over q8_0, and 4.2 a segment, of which the epilogue is 1.9; two KV heads
-// 1.75 a tile of both (1.5 from HBM at heads of 128) and 2 a segment; before the first scores 4 to 7 us from cold memory.
-// Tried on the 1.65 and slower: two warpgroups a tile with half the columns each (+18 %: more instructions in all), a part of
-// the exponentials as polynomials on the fma pipe (+6 to +30 %: they are not what binds here), the next scores' second half
-// before this tile's products (+17 %: the query tile is read twice, and shared memory binds), and a last tile of half the
-// places as half a tile (+6 %: its code, when fetched, displaces the rest).
+// positions: 71.9 us; without the two products 61, without any work 56).  A block's segments (timelines of
+// calls over parts of the cache): units of two tiles 1.65 us a tile, 2.04 over q8_0, and an epilogue of 1.9; two KV heads 0.87
+// us a head's tile, 1.6 over q8_0; before a launch's first scores 4 to 8 us from cold memory.
+// Tried on units of two tiles and slower (a prompt of 8192 through a window of 1024, 119 us): two warpgroups a tile with half
+// of the columns each, 139; 4 to 11 of 16 pairs of exponentials as polynomials on the fma pipe, 125 to 155; the second half of
+// the next scores before this tile's values (which reads the query tile twice), 138; a last tile of half the places as half
+// a tile, 126.
 //
 // Operands.  bf16 cache: Q, K, V as they are, P rounded to bf16 (2^-8; its sum uses the unrounded
 // values).  q8_0 cache: fp16, whose 2^-11 keeps a decoded value three bits better than bf16 would
@@ -1052,8 +1052,8 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
         for (int k = 0; k < kTile; k += 32) tc_ld32(ts + k, s + k);
         tc_wait_ld();
         if (edge || lower || mask != 0xffffu) {
-          // 32 columns at a time, those that some row of the warp does not see whole (a comparison or three for every
-          // column of the tile instead cost an 8192-token prompt through a window of 1024 11 us of 126)
+          // 32 columns at a time, those that some row of the warp does not see whole (a prompt of 8192 through a window of
+          // 1024: 120 us; with a comparison or three for every column of the tile 126)
 #pragma unroll
           for (int k = 0; k < kTile; k += 32) {
             const uint32_t m = seen32(limit - k, below - k, sinks - k, mask >> (k >> 3));

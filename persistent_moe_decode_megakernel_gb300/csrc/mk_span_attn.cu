@@ -301,7 +301,8 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
   }
   const int jobs = a.cuts + call.jobs;
   const dim3 all(jobs, (most + 7) / 8);
-  // (one token through 32768: 32 us so, 65 deep; 16 through 8192, whose rows have 5 partials: 68 and 66)
+  // (one token through 32768: 32 us split, 65 deep; 16 through 8192, whose rows have 5 partials: 68 and 66.  Deep and many: 64
+  // tokens behind 32768 64.6 and 68.7, 32 chunks of 5 behind 8192 50.3 and 52.3)
   if (groups <= kMaxBlocks / 2 && parts > 12)
     return launch_after(join_kernel<D, M, KINDS, kSplit>, dim3(all.x, all.y, D / 16), 256, 0, st, p, a);
   if (groups <= 2 * kMaxBlocks) return launch_after(join_kernel<D, M, KINDS, kDeep>, all, 2 * D, 0, st, p, a);

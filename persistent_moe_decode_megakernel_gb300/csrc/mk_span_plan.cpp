@@ -35,11 +35,15 @@ constexpr int kMaxRuns = 4096;               // units beyond which whole items a
 //   kFewRows  over q8_0, where its units have at most 32 rows of a KV head,
 //   kStagedRows  over q8_0, where decoding their positions once, into the workspace, is less work than every unit's
 //             block doing it: that costs a block 0.8 us a tile more (over all blocks), staging a launch, 5 us, and its
-//             bytes, 0.025 us a tile and KV head.  (1024 rows of 16384 through 2048: 47 us, staged 42; 512 of 8192 through
-//             256: 22 and 26.)  kStageBytes of decoded positions at most in a call;
+//             bytes, 0.025 us a tile and KV head.  (1024 rows of 16384 through 2048: 44.5 us, staged 42.5; 4096 of 8192
+//             through 512: 81 and 71; 512 of 8192 through 256, which this rule leaves: 21.6 and 25.7.)  kStageBytes of decoded positions at most in a call;
 //   kPageRows  else.
 constexpr size_t kStageBytes = size_t(1) << 30;
+// Position tiles a block from which on items are of two KV heads.  (64 tokens through 128: 21.6 us with a head an item, 15.5
+// with two; heads of 64 through 2048: 50.3 and 44.2.  The other way: one token through 32768, 29.8 and 31.9.)
 constexpr int kPairTiles = 4;
+// Position tiles a block of few rows up to which they go with another launch.  (A token of each of 63 sequences and a chunk
+// of 40 through 1024: 75 us in launches of their own, 42 together; through 4096, beyond: 132 and 134.)
 constexpr int kGatherTiles = 40;
 
 struct Builder {
