@@ -148,13 +148,14 @@ int mk_plan_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs, const
 
 /*
  * The schedule of mk_prefix_attention (num_groups > 0) or mk_window_attention (num_groups == 0) for these lengths
- * (host only): *n_out segments, the first max_segments of them written as 19 int32 each, block by block in the order
+ * (host only): *n_out segments, the first max_segments of them written as 21 int32 each, block by block in the order
  * a block runs them: launch (0: from the pages; 1: q8_0 positions decoded into the workspace first; 2: q8_0, few rows
  * a unit), block, entry, sequence whose table is read, first packed row, tokens, KV head; the unit's places: place v is
  * position v below `head` and position v + `gap` from there on; place of its first token, places up to the end of
  * what it may read; first tile of 128 places, tiles, tiles of the unit; partial written (-1: the segment writes the
  * output; 304: the whole unit's); of a decoded entry its first tile in the workspace, and the position tile that
- * follows the first n there, and n; 1 if the segment runs the next KV head too.
+ * follows the first n there, and n; 1 if the segment runs the next KV head too; of a decoded entry the first of the
+ * positions that are not looked up in its table, and their number.
  */
 int mk_plan_span_attention(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
                            const int32_t* seq_lens, int32_t window, int32_t sinks, int32_t num_groups,

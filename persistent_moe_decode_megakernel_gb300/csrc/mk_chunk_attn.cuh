@@ -1661,10 +1661,13 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
   int i = 0;
   while (i + 1 < st.n && st.first[i + 1] <= tile) ++i;
   int s = st.seq[i], t = tile - st.first[i], len;
+  int unseen = 0, unseen_n = 0;                                // (their pages may be another sequence's by now: zeros)
   if constexpr (Plan::kSpans) {                                // (an entry's number)
     const SpanEntry& e = p.plan.e[s];
     if (t >= e.stage_head) t += e.stage_tile0 - e.stage_head;
     len = e.len;
+    unseen = e.unseen;
+    unseen_n = e.unseen_n;
     s = e.seq;
   } else {
     len = p.seqs.len[s];
@@ -1679,6 +1682,9 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
     w[k] = make_uint4(0u, 0u, 0u, 0u);
     sc[k] = 0;
     if (pos >= len) continue;
+    if constexpr (Plan::kSpans) {
+      if (pos >= unseen && pos - unseen < unseen_n) continue;
+    }
     const int page = __ldg(bt + pos / p.ps);
     if (page < 0 || page >= p.P) {
       if (p.status) *p.status = MK_ERR_DEVICE_BOUNDS;

@@ -35,7 +35,8 @@ struct SpanEntry {
   int32_t pair;                      // 1: an item is two KV heads
   int32_t part0;                     // rows of partials before its own, -1: it writes the output
   int32_t stage0, stage_tile0, stage_head;   // q8_0 staged: its first tile in the workspace; the position tile that
-                                             // follows the first stage_head ones there
+                                             // follows the first stage_head ones there; of these tiles the
+  int32_t unseen, unseen_n;                  // positions [unseen, unseen + unseen_n) are no row's: not looked up
 };
 
 struct SpanPlan {

@@ -203,6 +203,18 @@ def test_window_three_launches():
     check_window(st, 8192, 4)
 
 
+@pytest.mark.parametrize("lens,news,window,sinks,ps", [
+    ([16384], [1024], 2048, 4, 16), ([9000], [4096], 512, 4, 16), ([12345], [4096], 512, 0, 8), ([9000, 40, 5000], [4096, 1, 2000], 500, 130, 40)])
+def test_window_decoded_before_with_pages_given_back(lens, news, window, sinks, ps):
+    # q8_0 prompts that are decoded once: what lies between the sinks and the first window is given back, inside the
+    # tiles of 128 positions that these share too, and nothing is reported
+    st = R.Setup(32, 4, 128, ps, lens, news, q8=True, seed=22)
+    hide(st, window, sinks)
+    seg = mk.plan_span_attention(st.shape(mk), st.news, st.lens, window, sinks)
+    assert 1 in seg[:, 0]
+    check_window(st, window, sinks)
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_window_of_a_poisoned_position_in_cut_items(q8):
     # a NaN behind the sinks is nobody's, one in the window of a token whose item is cut is that token's alone

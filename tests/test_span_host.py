@@ -393,3 +393,48 @@ def test_a_group_reads_the_table_of_a_sequence_with_rows():
     joint = [g for g in segs if g["len"] == 8192]
     assert joint and all(g["table"] == 2 and (g["row0"], g["ntok"]) == (0, 30) for g in joint)
     assert all(cl[g["table"]] > 0 for g in segs)
+
+
+def decoded(sh, cl, sl, window, sinks):
+    """The positions that each sequence of launch 1 has looked up and decoded before it (none: not in that launch)."""
+    out = {}
+    for row in mk.plan_span_attention(sh, cl, sl, window=window, sinks=sinks).tolist():
+        g = dict(zip(COLS + ("unseen", "unseen_n"), row))
+        if g["launch"] == 1:
+            pos = np.arange(sl[g["table"]])
+            tile = (pos // 128 < g["stage_head"]) | (pos // 128 >= g["stage_tile0"])
+            out[g["table"]] = tile & ~((pos >= g["unseen"]) & (pos < g["unseen"] + g["unseen_n"]))
+    return out
+
+
+def check_decoded(sh, cl, sl, window, sinks):
+    got = decoded(sh, cl, sl, window, sinks)
+    for s, looked in got.items():
+        row, pos = np.arange(sl[s] - cl[s], sl[s])[:, None], np.arange(sl[s])[None, :]
+        seen = ((pos <= row) & ((pos > row - window) | (pos < sinks))).any(0)
+        pages = np.zeros(-(-sl[s] // sh.page_size), dtype=bool)
+        pages[np.arange(sl[s])[seen] // sh.page_size] = True
+        assert np.all(looked[seen])
+        extra = np.unique(np.arange(sl[s])[looked] // sh.page_size)
+        assert pages[extra].all(), (s, extra[~pages[extra]])
+    return len(got)
+
+
+@pytest.mark.parametrize("cl,sl,window,sinks,ps", [
+    ([1024], [16384], 2048, 4, 16), ([4096], [12345], 512, 0, 16), ([4096], [9000], 512, 4, 16), ([4096, 3000], [9001, 8190], 700, 140, 8),
+    ([4096], [9000], 512, 4, 64), ([4096], [9000], 500, 300, 40), ([3000], [20000], 900, 130, 256)])
+def test_what_is_decoded_before_looks_up_no_page_that_no_row_sees(cl, sl, window, sinks, ps):
+    # the window's beginning and the sinks' end lie inside tiles of 128 positions: the pages between are not looked up
+    sh = shape(num_q_heads=32, num_kv_heads=4, page_size=ps, max_pages_per_seq=1 << 12, flags=mk.FLAG_KV_Q8)
+    assert check_decoded(sh, cl, sl, window, sinks) == len(cl)
+
+
+def test_what_is_decoded_before_over_random_windows():
+    g, n = np.random.default_rng(5), 0
+    for _ in range(400):
+        hkv, G = int(g.choice([1, 2, 4])), int(g.integers(1, 9))
+        sh = shape(num_q_heads=hkv * G, num_kv_heads=hkv, page_size=int(g.choice([8, 16, 24, 40, 64, 128, 256])),
+                   max_pages_per_seq=2048, flags=mk.FLAG_KV_Q8)
+        ln = int(g.integers(2000, 9000))
+        n += check_decoded(sh, [int(g.integers(1, ln + 1))], [ln], int(np.exp(g.uniform(3, 8))), int(g.choice([0, 1, 4, 100, 128, 300])))
+    assert n > 20
