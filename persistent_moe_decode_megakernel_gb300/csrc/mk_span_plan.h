@@ -24,7 +24,9 @@ namespace mk {
 
 constexpr int kMaxGroups = kMaxSeqs / 2;                 // groups of two sequences or more
 constexpr int kMaxEntries = kMaxSeqs + kMaxGroups;
-constexpr int32_t kNoWindow = 1 << 30;                   // no sequence is longer
+// Reaches back to position 0 from every row: no sequence is longer than 2^30, but rows that go over shared positions together
+// stand behind these one after the other, up to kMaxSeqs times a unit's 2 * kTile.
+constexpr int32_t kNoWindow = (1 << 30) + kMaxSeqs * 2 * kTile;
 
 struct SpanEntry {
   int32_t seq;                       // whose block table it reads

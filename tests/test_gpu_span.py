@@ -314,6 +314,34 @@ def test_prefix_long(std, q8):
     check_prefix(st, [40, 8], [20000, 9999], std=std)
 
 
+def test_prefix_of_the_most_positions():
+    # 2^30 - 128 shared positions: the rows of a second unit stand beyond 2^30, and still see the first page.  That holds
+    # about half of the weight (64 e^16.625 against 2^30) and -1, every other position 1; its pages are one that repeats.
+    n, rows, ps, ln = 5, 100, 64, 1 << 30
+    kv = torch.zeros(2 + 2 * n, 2, 1, ps, 64, dtype=torch.bfloat16, device="cuda")
+    kv[:, 1] = 1.0
+    kv[0, 0], kv[0, 1] = 2.078125, -1.0                  # (q . k / 8 = 16.625, exactly)
+    bt = torch.ones(n, ln // ps, dtype=torch.int32, device="cuda")
+    bt[:, 0] = 0
+    bt[:, -2:] = torch.arange(2, 2 + 2 * n, device="cuda", dtype=torch.int32).view(n, 2)
+    sh = mk.CacheShape(1, 1, 64, ps, kv.shape[0], ln // ps, 0)
+    args = (sh, [rows] * n, [ln] * n)
+    q = torch.ones(n * rows, 1, 64, dtype=torch.bfloat16, device="cuda")
+    seg = mk.plan_span_attention(*args, group_seqs=[n], prefix_lens=[ln - rows])
+    assert {256} <= set(seg[:, 4].tolist())              # (the group's second unit of rows)
+    status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+    out = mk.prefix_attention(sh, q, *args[1:], bt, kv, [n], [ln - rows], status=status)
+    assert int(status) == mk.MK_OK
+    first = 64 * np.exp(16.625)
+    rest = torch.arange(ln - rows, ln, device="cuda", dtype=torch.float64).repeat(n) + 1 - 64
+    want = (rest - first) / (rest + first)
+    # weights are powers of 2 times 1, so sums below 2^24 are exact; the segment that holds the first page may lose its
+    # others' (2^-24 of that page's each), which moves numerator and denominator by as much; bf16 rounds to 2^-8
+    lost = int(seg[:, 12].max()) * 128 / (ln + first)
+    assert lost < 0.02
+    assert torch.all((out[:, 0].double() - want[:, None]).abs() <= 2 * lost + 2.0 ** -8)
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_prefix_with_prompts_among_single_tokens(q8):
     st = prefix_setup(16, 2, 128, 16, [12, 4], [5000, 3000], [300, 20, 700], [260, 1, 1, 513], q8, seed=33)

@@ -438,3 +438,12 @@ def test_what_is_decoded_before_over_random_windows():
         ln = int(g.integers(2000, 9000))
         n += check_decoded(sh, [int(g.integers(1, ln + 1))], [ln], int(np.exp(g.uniform(3, 8))), int(g.choice([0, 1, 4, 100, 128, 300])))
     assert n > 20
+
+
+def test_rows_behind_the_most_shared_positions_see_the_first():
+    # the second unit of 500 rows stands beyond 2^30 positions: its places begin at position 0 as the first one's do
+    sh = shape(num_q_heads=1, num_kv_heads=1, head_dim=64, page_size=64, max_pages_per_seq=1 << 24)
+    segs = segments(sh, [100] * 5, [1 << 30] * 5, group_seqs=[5], prefix_lens=[(1 << 30) - 100])
+    joint = [g for g in segs if g["len"] == (1 << 30) - 128]
+    assert {(g["row0"], g["ntok"], g["pos0"]) for g in joint} == {(0, 256, (1 << 30) - 128), (256, 244, (1 << 30) + 128)}
+    assert all(g["head"] == g["gap"] == 0 for g in joint) and sum(g["n"] for g in joint) == 2 * ((1 << 23) - 1)
