@@ -442,9 +442,10 @@ __host__ __device__ constexpr bool ring_holds(int N) {
 // --------------------------------------------------------------------------- one row, plainly
 // Row r, query head h by one warp: 32 positions at a time, a lane per position for the scores,
 // D/32 dims per lane for the output; fp32, and no position beyond the row's own is touched.
-// `beat`: counted every 1024 positions (the rest of the block may be waiting), or NULL.
-template <int D, int M, class P>
-__device__ __noinline__ void exact_row(const P& p, int r, int h, volatile uint32_t* beat) {
+// `beat`: counted every 1024 positions (the rest of the block may be waiting), or NULL.  COLS < D: writes that many
+// columns from col0 on (the others are another block's to write).
+template <int D, int M, int COLS = D, class P>
+__device__ __noinline__ void exact_row(const P& p, int r, int h, volatile uint32_t* beat, int col0 = 0) {
   const int lane = threadIdx.x & 31, kvh = h / p.plan.G, s = seq_of_row(p.seqs, r);
   int n = p.seqs.len[s] - p.seqs.row0[s + 1] + r + 1, first = 0, skip = 0;
   if constexpr (decltype(p.plan)::kSpans) {                      // the first positions, and those of the window
@@ -531,7 +532,8 @@ __device__ __noinline__ void exact_row(const P& p, int r, int h, volatile uint32
   uint16_t* out = p.out + (static_cast<size_t>(r) * p.Hq + h) * D;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
-    out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(seen == 0u ? 0.f : o[i] / sum));
+    if (COLS == D || (32 * i + lane >= col0 && 32 * i + lane < col0 + COLS))
+      out[32 * i + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(seen == 0u ? 0.f : o[i] / sum));
 }
 
 // --------------------------------------------------------------------------- loads (warp 8: K, warp 11: V)

@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kMode == kSplit ? 256 : 2 * D, kMode == kSplit
       for (uint32_t todo = __ballot_sync(~0u, odd); todo; todo &= todo - 1) {
         const int who = __ffs(todo) - 1, lr = who & 7;
         const int rr = __shfl_sync(~0u, r, who), hh = __shfl_sync(~0u, h, who);
-        if (!((done >> lr) & 1u)) exact_row<D, M>(p, rr, hh, nullptr);
+        // (a split row's columns are several blocks': each writes its own, so that no two results of a value meet)
+        if (!((done >> lr) & 1u)) exact_row<D, M, kMode == kSplit ? 16 : D>(p, rr, hh, nullptr, kMode == kSplit ? blockIdx.z * 16 : 0);
         done |= 1u << lr;
       }
     }

@@ -233,6 +233,34 @@ def test_window_of_a_poisoned_position_in_cut_items(q8):
     assert torch.all(((out.double() - ref).abs() <= bound)[good]) and torch.all(out[1].isnan())
 
 
+@pytest.mark.parametrize("d,q8", [(128, False), (128, True), (64, False)])
+def test_infinite_values_of_a_row_that_many_blocks_join(d, q8):
+    # one token through a long window: 16 columns a block in the join.  Columns that are worked out again, those of a block
+    # that has one which is not finite, are written by that block alone: the others keep what was joined, in every run
+    st = R.Setup(32, 4, d, 64, [60000], [1], q8=q8, seed=23)
+    q = st.normal(1, 32, d, std=1.5)
+    args = (st.shape(mk), q, st.news, st.lens, st.bt, st.kv, 50000, 4)
+    clean = mk.window_attention(*args)
+    page, off = int(st.bt[0, 59000 // 64]), 59000 % 64
+    if q8:
+        st.planes()[1][page, 1, 2, off, 1] = float("inf")          # dims 32..63 of KV head 2
+        hit = slice(32, 64)
+    else:
+        st.kv[page, 1, 2, off, 37] = float("inf")
+        hit = slice(32, 48)
+    out = mk.window_attention(*args)
+    other = torch.ones(1, 32, d, dtype=torch.bool, device="cuda")
+    other[:, 16:24, hit] = False                                   # (KV head 2's query heads)
+    assert torch.equal(out[other], clean[other]) and not torch.any(out[:, 16:24, 37].isfinite())
+    if not q8:
+        ref, *scale = S.attention(st, q, torch.where(st.kv.isinf(), 0.0, st.kv), 50000, 4)
+        near = (out.double() - ref).abs() <= R.attention_bound(ref, *scale, q8)
+        near[:, 16:24, 37] = True
+        assert torch.all(near)
+    for _ in range(20):
+        assert torch.equal(mk.window_attention(*args).view(torch.int16), out.view(torch.int16))
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_offsets_beyond_32_bits(q8):
     # a pool of more than 4 GiB, of which the sequences have the last pages and the first ones
