@@ -89,6 +89,7 @@ constexpr int kRawBytes = kTile * (128 + 8);   // q8_0: the codes and scales of 
 constexpr int kMasks = 16;          // tiles whose page masks are kept (more than can be in flight)
 constexpr int kMaxStages = 12;      // of a ring (heads of 64)
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kBeatTiles = 8192;    // K tiles from one sign of life to the next: some 20 ms
 
 // The staged sequences and their tiles' numbers.
 struct StageTiles {
@@ -319,7 +320,7 @@ struct Ctl {
   uint64_t landed, trim;             // a last V tile to be trimmed: landed, trimmed
   uint64_t ofull[2], join;           // O of a tile (stream) is complete
   uint32_t tmem, abort;
-  uint32_t beat;                     // counts while a softmax warp works a row out plainly (exact_row)
+  uint32_t beat;                     // counts while a softmax warp works a row out plainly (exact_row), and with the K tiles
   uint32_t mask[kMasks];             // per tile, a bit per 8 positions: the page is in range
   float2 ml[2][kTile];               // streams' (m, l) when they join
 };
@@ -339,8 +340,8 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<128, kBf16>() <= 232448 && smem_bytes<128, kQ8>() <= 232448 && smem_bytes<128, kStaged>() <= 232448 &&
               smem_bytes<128, kQ8Few>() <= 232448 && smem_bytes<64, kBf16>() <= 232448, "");
 
-// Waits for the phase of `bar` with this parity, at most kWaitNs from the block's last sign of life in
-// exact_row; false once the block gives up.
+// Waits for the phase of `bar` with this parity, at most kWaitNs from the block's last sign of life (Ctl::beat); false
+// once the block gives up.
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status) {
   volatile uint32_t *abort = &ctl->abort, *beat = &ctl->beat;
   uint64_t t0 = globaltimer();
@@ -569,7 +570,11 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
       const uint32_t ok = __ballot_sync(~0u, good);
       uint32_t mask = 0;                                       // a bit per 8 positions
       if (only == 0 || M == kQ8Few) mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
-      if (only == 0 && lane == 0) ctl->mask[jg % kMasks] = mask;
+      if (only == 0 && lane == 0) {
+        ctl->mask[jg % kMasks] = mask;
+        // the query and trim waits last a segment, which may be longer than kWaitNs (2^23 tiles: 14 s)
+        if (j % kBeatTiles == kBeatTiles - 1) *static_cast<volatile uint32_t*>(&ctl->beat) = ctl->beat + 1;
+      }
       const uint32_t e = c0 + entry_of(g, only, j);
       if constexpr (M == kStaged && Plan::kSpans) {
         // copies of the workspace's tiles of 128 positions

@@ -300,6 +300,33 @@ def test_output_aligned_to_16_bytes():
         assert torch.equal(out, want) and torch.all(buf[:off] == 7.0) and torch.all(buf[off + 301 * 2048:] == 7.0)
 
 
+@pytest.mark.parametrize("window", [None, 1 << 30])
+def test_segments_of_seconds(window):
+    # 152 units over 3 * 2^27 positions: each block goes over 3 * 2^20 tiles in one segment, some 3 s, and the waits that last as
+    # long (for the next query rows, for the last values) do not give up.  All scores are 0; values are 1 in every 64th
+    # page and 0 in the others, so the sums of values are whole numbers up to 3 * 2^21, exact in fp32 in whatever groups they
+    # are added, and those of weights multiples of 128 up to 3 * 2^27, exact too; two pages that repeat.
+    rows, ps, ln = 152 * 256, 64, 3 << 27
+    kv = torch.zeros(2, 2, 1, ps, 64, dtype=torch.bfloat16, device="cuda")
+    kv[1, 1] = 1.0
+    bt = (torch.arange(ln // ps, device="cuda", dtype=torch.int32) % 64 == 63).to(torch.int32)[None].contiguous()
+    sh = mk.CacheShape(1, 1, 64, ps, 2, ln // ps, 0)
+    q = torch.ones(rows, 1, 64, dtype=torch.bfloat16, device="cuda")
+    status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+    if window is None:
+        seg = mk.plan_chunk_attention(sh, [rows], [ln])[:, 6]
+        out = mk.chunk_attention(sh, q, [rows], [ln], bt, kv, status=status)
+    else:
+        seg = mk.plan_span_attention(sh, [rows], [ln], window=window)[:, 12]
+        out = mk.window_attention(sh, q, [rows], [ln], bt, kv, window, status=status)
+    assert seg.max() > 3_000_000 and int(status) == mk.MK_OK
+    seen = torch.arange(ln - rows, ln, device="cuda") + 1
+    want = (seen // 4096 * 64 + (seen % 4096 - 63 * 64).clamp(min=0)).double() / seen
+    # (a row's last tile may hold any whole number of weights: the sum of all is off by at most 2^-24 there; the output
+    # rounds to 2^-8)
+    assert torch.all((out[:, 0].double() - want[:, None]).abs() <= want[:, None] * (2.0 ** -8 + 2.0 ** -20))
+
+
 # ---------------------------------------------------------------- shared prefixes
 PREFIX_SHAPES = [
     # hq, hkv, d, ps, groups, shared, own lengths (repeated), news (repeated)
