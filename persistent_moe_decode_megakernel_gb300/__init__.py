@@ -499,9 +499,10 @@ def plan_span_attention(shape: CacheShape, chunk_lens, seq_lens, window: int = 1
     """The schedule of :func:`prefix_attention`, or without groups of :func:`window_attention`
     (``mk_plan_span_attention``): int32 [segments, 21]."""
     cl, sl = _lengths(chunk_lens, seq_lens)
-    gs, pl = (np.array(x, dtype=np.int32) for x in (group_seqs, prefix_lens))
+    gs, pl = _lengths(group_seqs, prefix_lens, ("group_seqs", "prefix_lens"), "group")
     n = ctypes.c_int32()
-    args = (ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, window, sinks, gs.size, gs.ctypes.data, pl.ctypes.data)
+    args = (ctypes.byref(shape), cl.size, cl.ctypes.data, sl.ctypes.data, _number(window, "window"), _number(sinks, "sinks"),
+            gs.size, gs.ctypes.data, pl.ctypes.data)
     _check(lib().mk_plan_span_attention(*args, None, 0, ctypes.byref(n)))
     out = np.zeros((n.value, 21), dtype=np.int32)
     _check(lib().mk_plan_span_attention(*args, out.ctypes.data, n.value, ctypes.byref(n)))

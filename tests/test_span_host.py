@@ -447,3 +447,17 @@ def test_rows_behind_the_most_shared_positions_see_the_first():
     joint = [g for g in segs if g["len"] == (1 << 30) - 128]
     assert {(g["row0"], g["ntok"], g["pos0"]) for g in joint} == {(0, 256, (1 << 30) - 128), (256, 244, (1 << 30) + 128)}
     assert all(g["head"] == g["gap"] == 0 for g in joint) and sum(g["n"] for g in joint) == 2 * ((1 << 23) - 1)
+
+
+def test_schedule_refuses_arguments_that_do_not_pair_up():
+    sh = shape()
+    for kw in (dict(group_seqs=[1, 1], prefix_lens=[0]), dict(group_seqs=[2], prefix_lens=[]), dict(group_seqs=[2.0], prefix_lens=[0]),
+               dict(group_seqs=[[2]], prefix_lens=[[0]]), dict(group_seqs=[2], prefix_lens=[1 << 40])):
+        with pytest.raises(mk.MkError) as e:
+            mk.plan_span_attention(sh, [1, 1], [5, 6], **kw)
+        assert e.value.code == BAD and "group_seqs" in str(e.value)
+    for kw in (dict(window=1 << 32), dict(window=2.5), dict(window=None), dict(window=3, sinks=1 << 31), dict(window=3, sinks="1")):
+        with pytest.raises(mk.MkError) as e:
+            mk.plan_span_attention(sh, [1, 1], [5, 6], **kw)
+        assert e.value.code == BAD and "whole number" in str(e.value)
+    assert len(mk.plan_span_attention(sh, [1, 1], [5, 6], window=3)) == len(mk.plan_span_attention(sh, [1, 1], [5, 6], group_seqs=[2], prefix_lens=[0]))
