@@ -111,7 +111,7 @@ struct CallParams {
 };
 template <class Plan>
 struct Params : CallParams {
-  CUtensorMap map;                  // bf16 pages (see encode_pages)
+  CUtensorMap map;                  // bf16 pages or staged tiles (see encode_pages); none where the block decodes
   CUtensorMap qmap;                 // query rows (see encode_queries)
   Plan plan;
   float* part;                      // partials of cut items, two slots a block
@@ -1501,7 +1501,8 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
   }
   if constexpr (Plan::kSpans) {
     if (threadIdx.x == 320) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.qmap));
-    if (threadIdx.x == 256) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.map));
+    if constexpr (!kDecodes<M>)                    // (which copy without a map: none is encoded)
+      if (threadIdx.x == 256) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.map));
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
