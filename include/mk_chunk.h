@@ -128,7 +128,9 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  * Products run on the tensor cores: over a bf16 cache with bf16 operands (the softmax weights are
  * rounded to bf16), over a q8_0 cache with fp16 ones (weights, decoded values and scaled query rows
  * are rounded to fp16; rows that fp16 cannot hold are computed in fp32 instead).  Scores, softmax
- * statistics and outputs are accumulated in fp32 and rounded once.
+ * statistics and outputs are accumulated in fp32 and rounded once.  (The tensor cores cut their sums off instead of
+ * rounding them: over values of one sign, weighted alike, a row loses some 0.5 % a million positions that one block goes
+ * over, 2 % at 4 million, 9 % at 16 million.  Values of both signs lose far less.)
  * Rows never see later positions, whatever NaN or infinity these hold.  Scores beyond fp32's range
  * count as infinite: +inf makes its row NaN, -inf is no weight, and a row whose scores are all -inf is
  * NaN.  Every row that NaN or infinity reaches, or fp16 cannot hold, costs an fp32 pass over its

@@ -302,8 +302,12 @@ cudaError_t join(const SpanCall& call, const Params<SpanPlan>& given, const floa
   }
   const int jobs = a.cuts + call.jobs;
   const dim3 all(jobs, (most + 7) / 8);
-  // (one token through 32768: 32 us split, 65 deep; 16 through 8192, whose rows have 5 partials: 68 and 66.  Deep and many: 64
-  // tokens behind 32768 64.6 and 68.7, 32 chunks of 5 behind 8192 50.3 and 52.3)
+  // Calls of 32 / 4 heads of 128, as in mk_span_plan.cpp.  Split and deep: one token through 32768 26 us and 55; one, two and four
+  // through 8192 (16 partials a row) 13.7 and 17.5, 16 and 20, 25 and 28; six to twelve (11 to 6) alike within 0.3; 16 (6)
+  // 61 and 59; 12 tokens behind 30000 33 and 68, behind 8192 19 and 22, 16 there 24 and 22; 64 behind 32768 (256 groups) 70 and 53.
+  // Deep and many: 64 tokens behind 32768 (256 groups) 53 and 57, 24 sequences of 3 rows behind 8192 (288) 32 and 35, 32 of 5
+  // (640) 47.5 and 45.5, 64 of 9 behind 6000 104 and 85, 64 of 25 behind 9000 263 and 201.  Many, blocks over all, 6, 10 or 20
+  // an SM: 64 of 9 85, 85 and 87, 64 of 25 202, 202 and 207.
   if (groups <= kMaxBlocks / 2 && parts > 12)
     return launch_after(join_kernel<D, M, KINDS, kSplit>, dim3(all.x, all.y, D / 16), 256, 0, st, p, a);
   if (groups <= 2 * kMaxBlocks) return launch_after(join_kernel<D, M, KINDS, kDeep>, all, 2 * D, 0, st, p, a);

@@ -22,28 +22,40 @@ const Costs& costs(const mk_cache_shape& c, int kind) {
 }
 // What cut items cost besides: the second kernel, and the bytes of partials that it and the first one move in a tenth.
 constexpr int64_t kJoinCost = 45, kJoinBytes = 250000;
+// Measured below: calls of 32 / 4 heads of 128 and pages of 64, over bf16 unless said, each after a pass over 512 MB, less
+// that pass.
+//
 // What going over shared positions together costs besides: that, and the smaller pieces.  (8 sequences of 5 rows behind 8192
-// positions, 7.7 us less work together: 30 us apart, 40 together; 32 tokens behind 2048, 11.3 less: 31 and 30; 16 behind 8192,
-// 22.6 less: 44 and 28.)
+// positions, 7.7 us less work together: 23 us apart, 34 together; 32 tokens behind 2048, 11.3 less: 23 and 25, over q8_0 29
+// and 28; 64 behind 1024: 26 and 25; 8 behind 8192: 22 and 18; 16 behind 8192, 22.6 less: 33 and 24.)  A run has to save kRunCost
+// by itself.  (16 groups of 4 tokens behind 4096: 82 us apart, 44 together, and apart if a run had to save 4 us; 20 groups
+// of 3 behind 2048, which this leaves apart: 40, together 38; 32 groups of 2: alike either way.)
 constexpr int64_t kShareCost = 95, kRunCost = 10;
-constexpr int kLeastSegment = 20;            // of these costs
+constexpr int kLeastSegment = 20;            // of these costs.  (From 1 to 60 alike; 120: one token through 4096 12.8 us for 11.7,
+                                             // 64 tokens through 4096 99 for 103.)
 constexpr int kMostTries = 24;
-constexpr int kMinRange = 3;                 // position tiles a block is worth
+// Position tiles a block is worth.  (One token through 8192: 14.0 us with 1, 13.3 with 3, 12.8 with 5, 15.8 with 8; through
+// 1024 10.4, 10.7, 13.4 and 13.2.  Over q8_0 2 would be better: one token through 4096 18.9 us, 20.5 with 3, 26.1 with 8.)
+constexpr int kMinRange = 3;
 constexpr int kMaxRuns = 4096;               // units beyond which whole items are even enough
 
 // Launches are of one kind of operand each (SpanCall); a sequence's rows take
 //   kFewRows  over q8_0, where its units have at most 32 rows of a KV head,
 //   kStagedRows  over q8_0, where decoding their positions once, into the workspace, is less work than every unit's
 //             block doing it: that costs a block 0.8 us a tile more (over all blocks), staging a launch, 5 us, and its
-//             bytes, 0.025 us a tile and KV head.  (1024 rows of 16384 through 2048: 44.5 us, staged 42.5; 4096 of 8192
-//             through 512: 81 and 71; 512 of 8192 through 256, which this rule leaves: 21.6 and 25.7.)  kStageBytes of decoded positions at most in a call;
+//             bytes, 0.025 us a tile and KV head.  (1024 rows of 16384 through 2048: 44 us, staged 43; 4096 of 8192
+//             through 512: 74 and 64; 512 through 4096: 64 and 55.  Left by this rule: 512 through 256, 16 and 21; 2048
+//             through 512, 40 and 39.)  kStageBytes of decoded positions at most in a call;
 //   kPageRows  else.
 constexpr size_t kStageBytes = size_t(1) << 30;
-// Position tiles a block from which on items are of two KV heads.  (64 tokens through 128: 21.6 us with a head an item, 15.5
-// with two; heads of 64 through 2048: 50.3 and 44.2.  The other way: one token through 32768, 29.8 and 31.9.)
+// Position tiles a block from which on items are of two KV heads.  (64 tokens through 128: 19.2 us with a head an item, 14.6
+// with two; through 1024: 39 and 37; q8_0, 64 sequences of 5 rows through 1024: 42 and 35; 16 / 4 heads of 64, 64 tokens
+// through 2048: 40 and 36: these have more items than blocks.  By their tiles alone: q8_0, 20 sequences of 5 rows through 2048,
+// 36 and 34; but 71 and 74 through 8000 (over q8_0 69 and 71), 38 through 1000, an item a block, 25 and 28 (over q8_0 23.5 and
+// 36), and one token through 32768 22.7 and 26.1.  So this half of the rule loses more often than it gains.)
 constexpr int kPairTiles = 4;
 // Position tiles a block of few rows up to which they go with another launch.  (A token of each of 63 sequences and a chunk
-// of 40 through 1024: 75 us in launches of their own, 42 together; through 4096, beyond: 132 and 134.)
+// of 40 through 1024: 68 us in launches of their own, 36 together; through 2048 92 and 57; through 4096, beyond: 119 and 118.)
 constexpr int kGatherTiles = 40;
 
 struct Builder {
@@ -290,8 +302,9 @@ bool make_plan(const mk_cache_shape& c, int kind, SpanPlan* pl, size_t* floats) 
       pl->start[b + 1].tile = 0;
       return true;
     };
-    // Every block but the first begins inside an item, about: a segment more than its share of the work.  From a little
-    // below that the limit rises until it is enough.
+    // Every block but the first begins inside an item, about: a segment more than its share of the work.  From three quarters
+    // of that (a quarter to all of it: within 1 % over bf16; half as much again: 64 tokens behind 32768 54 us for 52) the
+    // limit rises until it is enough.
     const int64_t share = work / nb;
     int64_t more = 0;
     for (int i = 0; i < runs; ++i)
