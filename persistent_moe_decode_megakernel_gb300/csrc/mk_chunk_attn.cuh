@@ -89,7 +89,9 @@ constexpr int kRawBytes = kTile * (128 + 8);   // q8_0: the codes and scales of 
 constexpr int kMasks = 16;          // tiles whose page masks are kept (more than can be in flight)
 constexpr int kMaxStages = 12;      // of a ring (heads of 64)
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kBeatTiles = 8192;    // K tiles from one sign of life to the next: some 20 ms
+// Waits that last a segment of n position tiles (up to 2^23, 14 s) have kTileNs a tile more, several times what one takes.
+// (A fault ends them sooner: the roles that wait for a tile give up for the block.)
+constexpr uint64_t kTileNs = 10000;
 
 // The staged sequences and their tiles' numbers.
 struct StageTiles {
@@ -320,7 +322,7 @@ struct Ctl {
   uint64_t landed, trim;             // a last V tile to be trimmed: landed, trimmed
   uint64_t ofull[2], join;           // O of a tile (stream) is complete
   uint32_t tmem, abort;
-  uint32_t beat;                     // counts while a softmax warp works a row out plainly (exact_row), and with the K tiles
+  uint32_t beat;                     // counts while a softmax warp works a row out plainly (exact_row)
   uint32_t mask[kMasks];             // per tile, a bit per 8 positions: the page is in range
   float2 ml[2][kTile];               // streams' (m, l) when they join
 };
@@ -340,9 +342,9 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<128, kBf16>() <= 232448 && smem_bytes<128, kQ8>() <= 232448 && smem_bytes<128, kStaged>() <= 232448 &&
               smem_bytes<128, kQ8Few>() <= 232448 && smem_bytes<64, kBf16>() <= 232448, "");
 
-// Waits for the phase of `bar` with this parity, at most kWaitNs from the block's last sign of life (Ctl::beat); false
-// once the block gives up.
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status) {
+// Waits for the phase of `bar` with this parity, at most `limit` (kWaitNs) from the block's last sign of life in
+// exact_row; false once the block gives up.
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status, uint64_t limit = kWaitNs) {
   volatile uint32_t *abort = &ctl->abort, *beat = &ctl->beat;
   uint64_t t0 = globaltimer();
   uint32_t b0 = *beat;
@@ -353,7 +355,7 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ct
       b0 = b;
       t0 = globaltimer();
     }
-    if (globaltimer() - t0 > kWaitNs) {
+    if (globaltimer() - t0 > limit) {
       *abort = 1u;
       if (status) *status = MK_ERR_TIMEOUT;
       return false;
@@ -362,8 +364,8 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ct
   return true;
 }
 // The whole warp waits and agrees on the outcome (and is converged for what follows).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status) {
-  return __all_sync(~0u, mbar_try(bar, parity) || mbar_wait_slow(bar, parity, ctl, status));
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status, uint64_t limit = kWaitNs) {
+  return __all_sync(~0u, mbar_try(bar, parity) || mbar_wait_slow(bar, parity, ctl, status, limit));
 }
 
 // The block is in its last epilogue: a kernel behind this one that waits for it itself may be launched meanwhile.
@@ -570,11 +572,7 @@ __device__ __forceinline__ void produce(const Params<Plan>& p, uint32_t base, Ct
       const uint32_t ok = __ballot_sync(~0u, good);
       uint32_t mask = 0;                                       // a bit per 8 positions
       if (only == 0 || M == kQ8Few) mask = __ballot_sync(~0u, lane < 16 && ((ok >> (lane * 8 / r)) & 1u));
-      if (only == 0 && lane == 0) {
-        ctl->mask[jg % kMasks] = mask;
-        // the query and trim waits last a segment, which may be longer than kWaitNs (2^23 tiles: 14 s)
-        if (j % kBeatTiles == kBeatTiles - 1) *static_cast<volatile uint32_t*>(&ctl->beat) = ctl->beat + 1;
-      }
+      if (only == 0 && lane == 0) ctl->mask[jg % kMasks] = mask;
       const uint32_t e = c0 + entry_of(g, only, j);
       if constexpr (M == kStaged && Plan::kSpans) {
         // copies of the workspace's tiles of 128 positions
@@ -655,8 +653,10 @@ __device__ __forceinline__ void produce_q(const Params<Plan>& p, uint32_t base, 
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
   uint32_t k = 0, trimmed = 0, c0 = 0;
+  uint64_t limit = 0;                              // of waits for the segment's end
   while (walk.next(p.plan, p.seqs, g)) {
-    if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status)) return;
+    if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status, limit)) return;
+    limit = kWaitNs + kTileNs * g.n;
     ++k;
     if (M == kQ8Few && lane == 0) {                // the rows four times, once for each warp of a warpgroup
       const uint32_t bar = smem_u32(&ctl->qraw[0]), rows = kFew / p.plan.G * p.plan.G;
@@ -678,7 +678,7 @@ __device__ __forceinline__ void produce_q(const Params<Plan>& p, uint32_t base, 
     if (trims<M>(p, g)) {
       for (int k = pairs<Plan>(g) ? 1 : 0; k >= 0; --k) {
         const uint32_t c = c0 + entry_of(g, 1, g.n - 1 - k);
-        if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status)) return;
+        if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status, limit)) return;
         ++trimmed;
         const int first = g.len - p.tile_at(g, g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
         const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
