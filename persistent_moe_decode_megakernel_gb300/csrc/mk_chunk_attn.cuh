@@ -1674,8 +1674,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
     const SpanEntry& e = p.plan.e[s];
     if (t >= e.stage_head) t += e.stage_tile0 - e.stage_head;
     len = e.len;
-    unseen = e.unseen;
-    unseen_n = e.unseen_n;
+    unseen_of(p.plan, s, unseen, unseen_n);
     s = e.seq;
   } else {
     len = p.seqs.len[s];

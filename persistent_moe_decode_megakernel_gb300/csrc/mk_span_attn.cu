@@ -501,9 +501,11 @@ extern "C" int mk_plan_span_attention(const mk_cache_shape* shape, int32_t num_s
       while (walk.next(pl, seqs, g)) {
         if (n < max_segments) {
           const SpanEntry& e = pl.e[g.entry];
+          int unseen = 0, unseen_n = 0;
+          if (k == kStagedRows) unseen_of(pl, g.entry, unseen, unseen_n);
           const int32_t row[21] = {k,     b,       g.entry, g.s,  g.row0,  g.ntok, g.kvh,    g.head,         g.gap,
                                    g.pos0, g.len,  g.tile0, g.pair ? g.n / 2 : g.n,  g.tiles, g.slot, e.stage0, e.stage_tile0, e.stage_head, g.pair,
-                                   e.unseen, e.unseen_n};
+                                   unseen, unseen_n};
           std::copy(row, row + 21, segments + 21 * static_cast<size_t>(n));
         }
         ++n;

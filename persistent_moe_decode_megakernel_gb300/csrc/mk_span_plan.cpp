@@ -68,7 +68,7 @@ struct Builder {
   EntryRef add(SpanEntry e) {
     int kind = kPageRows;
     e.units = (e.rows + UT - 1) / UT;
-    e.pair = e.stage0 = e.stage_tile0 = e.stage_head = e.unseen = e.unseen_n = 0;
+    e.pair = e.stage0 = e.stage_tile0 = e.stage_head = 0;
     if (c.flags & MK_FLAG_KV_Q8) {
       if (std::min(e.rows, UT) * G <= kFewUnit) kind = kFewRows;
       else if (stage(&e)) kind = kStagedRows;
@@ -100,8 +100,6 @@ struct Builder {
     e->stage_tile0 = (g.head + g.gap) / kTile;
     if (g.gap == 0) e->stage_tile0 = 0;
     e->stage_head = std::min(head, e->stage_tile0);
-    e->unseen = g.head;
-    e->unseen_n = g.gap;
     const int own = e->stage_head + (e->len + kTile - 1) / kTile - e->stage_tile0;
     int64_t times = 0;
     for (int u = 0; u < e->units; ++u) {

@@ -37,8 +37,7 @@ struct SpanEntry {
   int32_t pair;                      // 1: an item is two KV heads
   int32_t part0;                     // rows of partials before its own, -1: it writes the output
   int32_t stage0, stage_tile0, stage_head;   // q8_0 staged: its first tile in the workspace; the position tile that
-                                             // follows the first stage_head ones there; of these tiles the
-  int32_t unseen, unseen_n;                  // positions [unseen, unseen + unseen_n) are no row's: not looked up
+                                             // follows the first stage_head ones there
 };
 
 struct SpanPlan {
@@ -83,6 +82,15 @@ __host__ __device__ inline void unit_of(const SpanPlan& pl, int i, int unit, int
 __host__ __device__ inline void item_of_entry(const SpanPlan& pl, int i, int item, Segment& g) {
   const int rem = item - pl.e[i].item0, heads = pl.Hkv >> pl.e[i].pair, back = rem / heads;
   unit_of(pl, i, pl.e[i].units - 1 - back, (rem - back * heads) << pl.e[i].pair, g);
+}
+
+// Of a decoded entry's positions those that no row sees, [first, first + n): its first unit, which reaches back furthest, has
+// them between its first positions and its others.  They are not looked up.
+__host__ __device__ inline void unseen_of(const SpanPlan& pl, int i, int& first, int& n) {
+  Segment g;
+  unit_of(pl, i, 0, 0, g);
+  first = g.head;
+  n = g.gap;
 }
 
 inline int entry_of_item(const SpanPlan& pl, int item) {
