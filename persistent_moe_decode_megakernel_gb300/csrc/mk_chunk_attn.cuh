@@ -342,9 +342,9 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<128, kBf16>() <= 232448 && smem_bytes<128, kQ8>() <= 232448 && smem_bytes<128, kStaged>() <= 232448 &&
               smem_bytes<128, kQ8Few>() <= 232448 && smem_bytes<64, kBf16>() <= 232448, "");
 
-// Waits for the phase of `bar` with this parity, at most `limit` (kWaitNs) from the block's last sign of life in
-// exact_row; false once the block gives up.
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status, uint64_t limit = kWaitNs) {
+// Waits for the phase of `bar` with this parity, at most kWaitNs, and kTileNs for each of `tiles`, from the
+// block's last sign of life in exact_row; false once the block gives up.
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status, uint32_t tiles = 0) {
   volatile uint32_t *abort = &ctl->abort, *beat = &ctl->beat;
   uint64_t t0 = globaltimer();
   uint32_t b0 = *beat;
@@ -355,7 +355,7 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ct
       b0 = b;
       t0 = globaltimer();
     }
-    if (globaltimer() - t0 > limit) {
+    if (globaltimer() - t0 > kWaitNs + kTileNs * tiles) {
       *abort = 1u;
       if (status) *status = MK_ERR_TIMEOUT;
       return false;
@@ -364,8 +364,8 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ct
   return true;
 }
 // The whole warp waits and agrees on the outcome (and is converged for what follows).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status, uint64_t limit = kWaitNs) {
-  return __all_sync(~0u, mbar_try(bar, parity) || mbar_wait_slow(bar, parity, ctl, status, limit));
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Ctl* ctl, int32_t* status, uint32_t tiles = 0) {
+  return __all_sync(~0u, mbar_try(bar, parity) || mbar_wait_slow(bar, parity, ctl, status, tiles));
 }
 
 // The block is in its last epilogue: a kernel behind this one that waits for it itself may be launched meanwhile.
@@ -653,10 +653,10 @@ __device__ __forceinline__ void produce_q(const Params<Plan>& p, uint32_t base, 
   SegmentWalk walk(p.plan, blockIdx.x);
   Segment g;
   uint32_t k = 0, trimmed = 0, c0 = 0;
-  uint64_t limit = 0;                              // of waits for the segment's end
+  uint32_t before = 0;                             // tiles of the segment before
   while (walk.next(p.plan, p.seqs, g)) {
-    if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status, limit)) return;
-    limit = kWaitNs + kTileNs * g.n;
+    if (k > 0 && !mbar_wait(smem_u32(&ctl->qfree), (k - 1) & 1, ctl, p.status, before)) return;
+    before = g.n;
     ++k;
     if (M == kQ8Few && lane == 0) {                // the rows four times, once for each warp of a warpgroup
       const uint32_t bar = smem_u32(&ctl->qraw[0]), rows = kFew / p.plan.G * p.plan.G;
@@ -678,7 +678,7 @@ __device__ __forceinline__ void produce_q(const Params<Plan>& p, uint32_t base, 
     if (trims<M>(p, g)) {
       for (int k = pairs<Plan>(g) ? 1 : 0; k >= 0; --k) {
         const uint32_t c = c0 + entry_of(g, 1, g.n - 1 - k);
-        if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status, limit)) return;
+        if (!mbar_wait(smem_u32(&ctl->landed), trimmed & 1, ctl, p.status, g.n)) return;
         ++trimmed;
         const int first = g.len - p.tile_at(g, g.n - 1) * kTile, last = (first + p.box - 1) / p.box * p.box;
         const uint32_t v = base + L::kKv + c % L::kStages * L::kTileBytes + (lane / 8 % (D / 64)) * 1024 + (lane & 7) * 16;
