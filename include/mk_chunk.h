@@ -111,8 +111,9 @@ int mk_append_chunk(const mk_cache_shape* shape, int32_t num_seqs, const int32_t
 /*
  * Bytes of device workspace that mk_chunk_attention needs for these lengths (0 when it needs
  * none), written to bytes_out.  Host only.  It holds the partial outputs of contexts split over
- * blocks (at most 42 MB) and, for q8_0 sequences with many new tokens, their cache decoded to fp16
- * (4 bytes a position, KV head and dim; at most 1 GiB in a call).
+ * blocks (at most 42 MB), for q8_0 sequences with many new tokens their cache decoded to fp16
+ * (4 bytes a position, KV head and dim; at most 1 GiB in a call), and where a block goes over more than
+ * 2^18 positions at once its sums (at most 21 MB).
  */
 int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, const int32_t* chunk_lens,
                                  const int32_t* seq_lens, size_t* bytes_out);
@@ -128,9 +129,9 @@ int mk_chunk_attention_workspace(const mk_cache_shape* shape, int32_t num_seqs, 
  * Products run on the tensor cores: over a bf16 cache with bf16 operands (the softmax weights are
  * rounded to bf16), over a q8_0 cache with fp16 ones (weights, decoded values and scaled query rows
  * are rounded to fp16; rows that fp16 cannot hold are computed in fp32 instead).  Scores, softmax
- * statistics and outputs are accumulated in fp32 and rounded once.  (The tensor cores cut their sums off instead of
- * rounding them: over values of one sign, weighted alike, a row loses some 0.5 % a million positions that one block goes
- * over, 2 % at 4 million, 9 % at 16 million.  Values of both signs lose far less.)
+ * statistics and outputs are accumulated in fp32 and rounded once.  (The tensor cores cut sums off instead of rounding
+ * them, which over values of one sign, weighted alike, is 0.1 % in 2^18 positions; sums over more are put together with
+ * rounding from pieces of at most so many.)
  * Rows never see later positions, whatever NaN or infinity these hold.  Scores beyond fp32's range
  * count as infinite: +inf makes its row NaN, -inf is no weight, and a row whose scores are all -inf is
  * NaN.  Every row that NaN or infinity reaches, or fp16 cannot hold, costs an fp32 pass over its

@@ -18,8 +18,9 @@ struct CallPlan {
   AttnPlan direct, staged;           // the two launches' (q8_0 only: staged.items may be 0, as direct.items)
   StageTiles tiles;
   int32_t stage0[kMaxSeqs];
-  size_t stage_bytes, floats;        // workspace: staged tiles, then partials (the launches follow each other)
-  size_t bytes() const { return stage_bytes + floats * sizeof(float); }
+  size_t stage_bytes, floats;        // workspace: staged tiles, then (floats) partials and folds (the launches follow each other)
+  size_t direct_folds, staged_folds;
+  size_t bytes() const { return stage_bytes + (floats + std::max(direct_folds, staged_folds)) * sizeof(float); }
 };
 
 bool plan_call(const mk_cache_shape& c, const ChunkSeqs& q, CallPlan* cp) {
@@ -46,6 +47,8 @@ bool plan_call(const mk_cache_shape& c, const ChunkSeqs& q, CallPlan* cp) {
   size_t a = 0, b = 0;
   if (!make_plan(c, q, direct, &cp->direct, &a) || !make_plan(c, q, staged, &cp->staged, &b)) return false;
   cp->floats = std::max(a, b);
+  cp->direct_folds = fold_floats(cp->direct, q, c.head_dim);
+  cp->staged_folds = fold_floats(cp->staged, q, c.head_dim);
   return true;
 }
 
@@ -90,6 +93,7 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   cudaError_t e = cudaSuccess;
   if (plan.direct.items > 0) {
     p.plan = plan.direct;
+    p.folds = plan.direct_folds ? p.part + plan.floats : nullptr;
     const bool few = q8 && p.plan.urows <= kFew;
     rc = encode_queries(c, p.plan.G, few ? kFew / p.plan.G : p.plan.TT, q, q_stride, rows, &p.qmap);
     if (rc) return rc;
@@ -104,6 +108,7 @@ extern "C" int mk_chunk_attention(const mk_cache_shape* shape, int32_t num_seqs,
   }
   if (e == cudaSuccess && plan.staged.items > 0) {
     p.plan = plan.staged;
+    p.folds = plan.staged_folds ? p.part + plan.floats : nullptr;
     rc = encode_queries(c, p.plan.G, p.plan.TT, q, q_stride, rows, &p.qmap);
     if (!rc) rc = encode_pages(128, c.num_kv_heads, kTile, plan.tiles.first[plan.tiles.n], false, workspace, kTile, &p.map);
     if (rc) return rc;

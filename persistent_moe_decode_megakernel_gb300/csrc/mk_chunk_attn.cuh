@@ -123,6 +123,7 @@ struct Params : CallParams {
   int32_t first;                    // (parts of the cache) the call's first kernel: nothing but its parameters is read before the
                                     // kernel in front of it is done
   float c;                          // log2(e) / sqrt(D)
+  float* folds;                     // where long segments' sums go (see fold), or NULL: no segment is so long
 
   // the unit's first packed row
   __device__ __forceinline__ int first_row(const Segment& g) const {
@@ -962,6 +963,62 @@ __device__ __forceinline__ float convert_q(uint32_t tile, int row) {
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
+// The tensor cores cut a sum's low bits off as they add to it: values of one sign lose some 0.5 % over a million positions
+// (2 % over four million; from 2^27 on nothing is added any more).  So O and l move into the workspace every kFoldTiles position
+// tiles, where they are added up with rounding, and come back at the segment's end.  A stream's 128 rows: [D/4][128] of 4
+// columns, then [128] of (m, l) that go with them.  Kernels of their own (LONG): a test in each tile cost the others 1 to 4 %
+// (the last 2048 of 32768 tokens: 650 us, 664 with it).
+template <class Plan, int D>
+__device__ __forceinline__ float4* fold_at(const Params<Plan>& p, int t, int row) {
+  return reinterpret_cast<float4*>(p.folds) + (static_cast<size_t>(blockIdx.x) * 2 + t) * kTile * (D / 4 + 1) + row;
+}
+template <int D>
+__device__ __noinline__ void fold(uint32_t o, float4* at, float m, float l, float c, bool first) {
+  const float4 had = first ? make_float4(m, 0.f, 0.f, 0.f) : at[D / 4 * kTile];
+  const float f = had.x == -INFINITY ? 0.f : ex2((had.x - m) * c);
+  at[D / 4 * kTile] = make_float4(m, had.y * f + l, 0.f, 0.f);
+#pragma unroll 1
+  for (int k = 0; k < D; k += 16) {
+    float x[16];
+    tc_ld16(o + k, x);
+    tc_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float4* to = at + (k + e) / 4 * kTile;
+      float4 s = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
+      s = make_float4(s.x * f + x[e], s.y * f + x[e + 1], s.z * f + x[e + 2], s.w * f + x[e + 3]);
+      *to = s;
+      x[e] = x[e + 1] = x[e + 2] = x[e + 3] = 0.f;
+    }
+    tc_st16(o + k, x);
+  }
+  tc_wait_st();
+}
+// l of the whole segment
+template <int D>
+__device__ __noinline__ float unfold(uint32_t o, const float4* at, float m, float l, float c) {
+  const float4 had = at[D / 4 * kTile];
+  const float f = had.x == -INFINITY ? 0.f : ex2((had.x - m) * c);
+#pragma unroll 1
+  for (int k = 0; k < D; k += 16) {
+    float x[16];
+    tc_ld16(o + k, x);
+    tc_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const float4 s = at[(k + e) / 4 * kTile];
+      x[e] += s.x * f;
+      x[e + 1] += s.y * f;
+      x[e + 2] += s.z * f;
+      x[e + 3] += s.w * f;
+    }
+    tc_st16(o + k, x);
+  }
+  tc_wait_st();
+  tc_before();
+  return had.y * f + l;
+}
+
 // The columns of 32 that a row sees, a bit each: those up to `limit`, without those from `sinks` to `below`, of pages
 // in range (a bit of `mask` for 8 columns).
 __device__ __forceinline__ uint32_t first_bits(int n) {       // n <= 0: none; n >= 32: all
@@ -979,7 +1036,7 @@ __device__ __forceinline__ void hide32(float* s, uint32_t seen) {
     if (!((seen >> k) & 1u)) s[k] = -INFINITY;
 }
 
-template <int D, int M, class Plan>
+template <int D, int M, bool LONG, class Plan>
 __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ctl* ctl) {
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
@@ -1053,6 +1110,10 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
       ++phase;
       if (any) {                                   // (warps without rows leave their lanes as they are)
         tc_after();
+        if (LONG && i % kFoldTiles == 0 && i > 0) {   // (what P V adds up to so far is complete: see below)
+          fold<D>(to + t * D, fold_at<Plan, D>(p, t, row), m, l, c, i == kFoldTiles);
+          l = 0.f;
+        }
         const uint32_t mask = ctl->mask[(jg + j) % kMasks];
         float s[kTile];
 #pragma unroll
@@ -1147,6 +1208,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
     // the next segment's rows, so that its first scores run under this one's epilogue -- if they are here already
     const bool early = have && q_here(next);
     if (early && !take_q(next)) return;
+    if (LONG && mine > kFoldTiles && any) l = unfold<D>(to + t * D, fold_at<Plan, D>(p, t, row), m, l, c);
 
     // m and l in powers of two; a row without a position has m = -inf and l = 0
     m = m == -INFINITY ? m : m * c;
@@ -1155,6 +1217,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
       // two streams of the same rows: both warpgroups read both outputs, each half of the columns
       ctl->ml[t][row] = make_float2(m, l);
       if (!join()) return;
+      if (LONG) tc_after();
       const float2 a = ctl->ml[0][row], b = ctl->ml[1][row];
       m = fmaxf(a.x, b.x);
       f[0] = a.x == -INFINITY ? 0.f : ex2(a.x - m);
@@ -1267,7 +1330,7 @@ __device__ __forceinline__ void softmax(const Params<Plan>& p, uint32_t base, Ct
 // own positions.  The eight parts of a row (two streams, four warps), each with its m and l, are
 // joined through shared memory.  (One token at 262144 positions, with the two groups of decode warps that the
 // saved registers pay for: 87.0 -> 81.3 us.)
-template <int D, class Plan>
+template <int D, bool LONG, class Plan>
 __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base, Ctl* ctl) {
   CtlFew* few = static_cast<CtlFew*>(ctl);
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127, lane = row & 31, warp = __shfl_sync(~0u, row >> 5, 0);
@@ -1324,6 +1387,10 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
       if (!mbar_wait(smem_u32(&ctl->sfull[t]), phase & 1, ctl, p.status)) return;
       ++phase;
       tc_after();
+      if (LONG && i % kFoldTiles == 0 && i > 0) {    // (as in softmax)
+        fold<D>(to + t * D, fold_at<Plan, D>(p, t, row), m, l, c, i == kFoldTiles);
+        l = 0.f;
+      }
       const uint32_t mask = ctl->mask[(jg + j) % kMasks] >> (4 * warp) & 15u;
       float s[32];
       tc_ld32(ts + 32 * warp, s);
@@ -1392,10 +1459,12 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
     if (!have) let_next_start<Plan>();
     const bool early = have && t == 0 && __all_sync(~0u, mbar_try(smem_u32(&ctl->qraw[0]), taken & 1));   // (as in softmax)
     if (early && !take_q()) return;
+    if (LONG && mine > kFoldTiles) l = unfold<D>(to + t * D, fold_at<Plan, D>(p, t, row), m, l, c);
 
     // m and l in powers of two; a part without a position has m = -inf and l = 0
     ctl->ml[t][row] = make_float2(m == -INFINITY ? m : m * c, l);
     if (!join()) return;
+    if (LONG) tc_after();
     m = -INFINITY;
     l = 0.f;
 #pragma unroll
@@ -1460,7 +1529,7 @@ __device__ __forceinline__ void softmax_few(const Params<Plan>& p, uint32_t base
   }
 }
 
-template <int D, int M, class Plan>
+template <int D, int M, bool LONG, class Plan>
 __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const __grid_constant__ Params<Plan> p) {
   using L = Layout<D, M>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1524,11 +1593,11 @@ __global__ void __launch_bounds__(Layout<D, M>::kThreads, 1) attn_kernel(const _
   if (warp < 8) {
     if constexpr (M == kQ8Few) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-      softmax_few<D>(p, base, ctl);
+      softmax_few<D, LONG>(p, base, ctl);
     } else {
       if constexpr (M == kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
       else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      softmax<D, M>(p, base, ctl);
+      softmax<D, M, LONG>(p, base, ctl);
     }
   } else if (warp < 12) {
     if constexpr (kDecodes<M>) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -1809,7 +1878,7 @@ void fill_params(const mk_cache_shape& c, const int32_t* block_tables, const voi
   p->q = static_cast<const uint16_t*>(q);
   p->q_stride = q_stride;
   p->out = static_cast<uint16_t*>(out);
-  p->part = p->whole = nullptr;
+  p->part = p->whole = p->folds = nullptr;
   p->code_bytes = static_cast<size_t>(c.num_pages) * 2 * c.num_kv_heads * c.page_size * c.head_dim;
   p->Hq = c.num_q_heads;
   p->ps = c.page_size;
@@ -1834,8 +1903,8 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, unsigned threads, s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int M, class Plan>
-cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
+template <int D, int M, bool LONG, class Plan>
+cudaError_t launch_kernel(const Params<Plan>& p, cudaStream_t st) {
   // once per device (a bit each; beyond 64 devices on every call): the attribute is the device's
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -1843,14 +1912,19 @@ cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(set.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(attn_kernel<D, M, Plan>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_kernel<D, M, LONG, Plan>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem_bytes<D, M>()));
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  if constexpr (Plan::kSpans) return launch_after(attn_kernel<D, M, Plan>, dim3(p.plan.blocks), Layout<D, M>::kThreads, smem_bytes<D, M>(), st, p);
-  attn_kernel<D, M, Plan><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
+  if constexpr (Plan::kSpans)
+    return launch_after(attn_kernel<D, M, LONG, Plan>, dim3(p.plan.blocks), Layout<D, M>::kThreads, smem_bytes<D, M>(), st, p);
+  attn_kernel<D, M, LONG, Plan><<<p.plan.blocks, Layout<D, M>::kThreads, smem_bytes<D, M>(), st>>>(p);
   return cudaGetLastError();
+}
+template <int D, int M, class Plan>
+cudaError_t launch(const Params<Plan>& p, cudaStream_t st) {
+  return p.folds ? launch_kernel<D, M, true>(p, st) : launch_kernel<D, M, false>(p, st);
 }
 
 // And the kernel that merges what its ranges cut.

@@ -19,6 +19,8 @@ namespace mk {
 
 constexpr int kTile = 128;           // positions of a tile, and rows of a tile
 constexpr int kMaxBlocks = 152;      // one block per SM
+// Position tiles that are summed in tensor memory before the sum moves into the workspace: see fold.
+constexpr int kFoldTiles = 2048;
 
 struct AttnPlan {
   static constexpr bool kSpans = false;
@@ -124,6 +126,30 @@ struct SegmentWalk {
     else return -1;
   }
 };
+
+// Floats of the workspace that a launch's blocks fold into, two streams of 128 rows each (0: no segment is so long).
+template <class Plan>
+size_t fold_floats(const Plan& pl, const ChunkSeqs& q, int head_dim) {
+  Segment g;
+  bool any = false;
+  if (!pl.ranged) {                  // (a window's last unit may have some tiles fewer than the others)
+    if constexpr (Plan::kSpans) {
+      for (int i = 0; i < pl.n; ++i) {
+        unit_of(pl, i, pl.e[i].units - 1, 0, g);
+        any |= g.tiles + 3 > kFoldTiles;
+      }
+    } else if (pl.items > 0) {
+      item_of(pl, q, 0, g);
+      any = g.tiles > kFoldTiles;
+    }
+  } else {
+    for (int b = 0; b < pl.blocks && !any; ++b) {
+      SegmentWalk walk(pl, b);
+      while (!any && walk.next(pl, q, g)) any = (g.two ? g.n : (g.n + 1) / 2) > kFoldTiles;
+    }
+  }
+  return any ? static_cast<size_t>(pl.blocks) * 2 * kTile * (head_dim + 4) : 0;
+}
 
 // Fills the plan of the sequences that `use` marks; *floats is the size of the partials (0: none).  False: more items
 // than a call takes.

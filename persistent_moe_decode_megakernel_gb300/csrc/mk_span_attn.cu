@@ -346,6 +346,7 @@ int attend(const mk_cache_shape& c, const SpanCall& call, Params<SpanPlan>& p, c
     p.plan = call.plan[k];
     p.first = first && k != kStagedRows;
     p.part = floats + call.part0[k];
+    p.folds = call.folds[k] ? floats + call.fold0[k] : nullptr;
     rc = encode_queries(c, p.plan.G, k == kFewRows ? kFew / p.plan.G : p.plan.TT, q, q_stride, rows, &p.qmap);
     if (!rc && k == kStagedRows) rc = encode_pages(128, c.num_kv_heads, kTile, call.stage_tiles, false, workspace, p.box, &p.map);
     if (!rc && !q8) rc = encode_pages(c.head_dim, c.num_kv_heads, c.page_size, c.num_pages, true, kv_layer, p.box, &p.map);

@@ -140,7 +140,7 @@ struct Builder {
         if (r->kind == kFewRows) *r = {kPageRows, static_cast<int8_t>(moved[r->entry])};
   }
 
-  bool finish() {
+  bool finish(const ChunkSeqs& q) {
     gather();
     size_t at = 0;
     // Two KV heads an item, where there are more items than blocks without that, or kPairTiles position tiles a block.
@@ -165,7 +165,12 @@ struct Builder {
       at += floats;
     }
     call->whole0 = at;
-    call->floats = at + static_cast<size_t>(call->whole_rows) * c.num_q_heads * (c.head_dim + 4);
+    at += static_cast<size_t>(call->whole_rows) * c.num_q_heads * (c.head_dim + 4);
+    for (int k = 0; k < kRowKinds; ++k) {
+      call->fold0[k] = at;
+      at += call->folds[k] = fold_floats(call->plan[k], q, c.head_dim);
+    }
+    call->floats = at;
     return true;
   }
 };
@@ -346,7 +351,7 @@ bool plan_window(const mk_cache_shape& c, const ChunkSeqs& q, int32_t window, in
   int order[kMaxSeqs];
   const int n = by_length(q, order);
   for (int i = 0; i < n; ++i) build.add(entry_of(q, order[i]));
-  return build.finish();
+  return build.finish(q);
 }
 
 bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups, const int32_t* group_seqs,
@@ -426,7 +431,7 @@ bool plan_prefix(const mk_cache_shape& c, const ChunkSeqs& q, int32_t num_groups
       j.over = over[s];
     }
   }
-  if (!build.finish()) return false;
+  if (!build.finish(q)) return false;
   // each unit and KV head of a joined sequence is a block's work of the second kernel
   int64_t jobs = 0;
   for (int k = 0; k < call->joins; ++k) {

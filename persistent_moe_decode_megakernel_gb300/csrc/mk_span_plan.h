@@ -120,8 +120,8 @@ struct SpanCall {
   int32_t joins, jobs;
   JoinSeq join[kMaxSeqs];
   int32_t whole_rows;
-  size_t stage_bytes;                // workspace: staged tiles, then (floats) each launch's cut partials, then whole ones
-  size_t part0[kRowKinds], whole0, floats;
+  size_t stage_bytes;                // workspace: staged tiles, then (floats) each launch's cut partials, whole ones, each one's folds
+  size_t part0[kRowKinds], whole0, fold0[kRowKinds], folds[kRowKinds], floats;
   size_t bytes() const { return stage_bytes + floats * sizeof(float); }
 };
 

@@ -327,6 +327,89 @@ def test_segments_of_seconds(window):
     assert torch.all((out[:, 0].double() - want[:, None]).abs() <= want[:, None] * (2.0 ** -8 + 2.0 ** -20))
 
 
+LONG = [
+    # rows, sequences, hq, hkv, positions, q8: two tiles of rows a unit; streams of one token, cut over all blocks; many
+    # tokens (two KV heads an item in a window); and over q8_0 few rows, more rows, and a prompt that is decoded before
+    (152 * 256, 1, 1, 1, 1 << 21, False), (1, 1, 1, 1, 1 << 27, False), (1, 64, 4, 4, 1 << 20, False),
+    (1, 1, 1, 1, 1 << 27, True), (5, 1, 8, 1, 1 << 27, True), (30000, 1, 1, 1, 1 << 20, True),
+]
+
+
+@pytest.mark.parametrize("window", [None, 1 << 30])
+@pytest.mark.parametrize("rows,seqs,hq,hkv,ln,q8", LONG)
+def test_sums_over_millions_of_positions(rows, seqs, hq, hkv, ln, q8, window):
+    # Three kinds of pages of 64 positions: most have scores of 0 and values of 1, one in 5000 scores of 7.5 and values of
+    # -3, one in 12000 scores of 11 and values of 2.  (All of the last lie further apart than what a block adds up before
+    # it moves its sums to the workspace.)
+    d, ps = (128 if q8 else 64), 64
+    n = 3 * 2 * hkv * ps * d
+    want_k, want_v = (0.0, 7.5 / d ** 0.5, 11 / d ** 0.5), (1.0, -3.0, 2.0)
+    if q8:
+        kv = torch.zeros(n + n // 16, dtype=torch.uint8, device="cuda")
+        x = kv[:n].view(torch.int8).view(3, 2, hkv, ps, d)
+        scale = kv[n:].view(torch.float16).view(3, 2, hkv, ps, d // 32)
+        x[...] = 64
+        for i in range(3):
+            scale[i, 0], scale[i, 1] = want_k[i] / 64, want_v[i] / 64
+        key = scale[:, 0, 0, 0, 0].double() * 64
+    else:
+        kv = torch.zeros(3, 2, hkv, ps, d, dtype=torch.bfloat16, device="cuda")
+        for i in range(3):
+            kv[i, 0], kv[i, 1] = want_k[i], want_v[i]
+        key = kv[:, 0, 0, 0, 0].double()
+    at = torch.arange(ln // ps, device="cuda")
+    kind = torch.where(at % 12000 == 7001, 2, torch.where(at % 5000 == 3001, 1, 0)).to(torch.int32)
+    kind[-(rows // ps + 1):] = 0
+    sh = mk.CacheShape(hq, hkv, d, ps, 3, ln // ps, mk.FLAG_KV_Q8 if q8 else 0)
+    cl, sl, bt = [rows] * seqs, [ln] * seqs, kind[None].repeat(seqs, 1)
+    q = torch.ones(rows * seqs, hq, d, dtype=torch.bfloat16, device="cuda")
+    status = torch.full((1,), -99, dtype=torch.int32, device="cuda")
+    if window is None:
+        seg = mk.plan_chunk_attention(sh, cl, sl)[:, 6]
+        out = mk.chunk_attention(sh, q, cl, sl, bt, kv, status=status)
+    else:
+        seg = mk.plan_span_attention(sh, cl, sl, window=window)[:, 12]
+        out = mk.window_attention(sh, q, cl, sl, bt, kv, window, status=status)
+    assert int(status) == mk.MK_OK and seg.max() > 4096
+    w = (key * d ** 0.5).exp()
+    value = torch.tensor(want_v, dtype=torch.float64, device="cuda")
+    special = [ps * int((kind == i).sum()) for i in (1, 2)]
+    common = (torch.arange(ln - rows, ln, device="cuda", dtype=torch.float64) + 1 - sum(special)).repeat(seqs)
+    mass = torch.stack([common, *(torch.full_like(common, float(s)) * w[i + 1] for i, s in enumerate(special))])
+    share = mass / mass.sum(0)
+    want = (share * value[:, None]).sum(0)
+    # A product adds 8 common weights and cuts off less than 2^-23 of the sum, which one page of the third kind makes up to
+    # 128 w: 128 w / 2^23 of every 8 common ones at most, with what the page of the second kind has about as much again.
+    # Weights round to 2^-8 (and to fp16, 2^-11, as do the q8_0 values), the output to 2^-8.
+    cut = 2 * 128 * float(w[2]) / 2 ** 23 / 8
+    assert cut < 0.25
+    bound = share[0] * cut + (share * value[:, None].abs()).sum(0) * (2.0 ** -8 + 2.0 ** -10) + want.abs() * 2.0 ** -8
+    assert torch.all((out.double() - want[:, None, None]).abs() <= bound[:, None, None])
+
+
+@pytest.mark.parametrize("window", [None, 1 << 30])
+@pytest.mark.parametrize("rows,seqs,hq,hkv,ln,q8", [(152 * 256, 1, 1, 1, 1 << 24, False), *LONG[1:]])
+def test_sums_of_values_of_one_sign(rows, seqs, hq, hkv, ln, q8, window):
+    # every score 0 and every value 1.3359375: a sum in one place loses 2 % of itself over four million positions
+    d, ps = (128 if q8 else 64), 64
+    n = 2 * hkv * ps * d
+    if q8:
+        kv = torch.zeros(n + n // 16, dtype=torch.uint8, device="cuda")
+        kv[n // 2:n] = 1
+        kv[n + n // 32:].view(torch.float16)[...] = 1.3359375
+    else:
+        kv = torch.zeros(1, 2, hkv, ps, d, dtype=torch.bfloat16, device="cuda")
+        kv[:, 1] = 1.3359375
+    sh = mk.CacheShape(hq, hkv, d, ps, 1, ln // ps, mk.FLAG_KV_Q8 if q8 else 0)
+    cl, sl = [rows] * seqs, [ln] * seqs
+    bt = torch.zeros(seqs, ln // ps, dtype=torch.int32, device="cuda")
+    q = torch.ones(rows * seqs, hq, d, dtype=torch.bfloat16, device="cuda")
+    out = mk.chunk_attention(sh, q, cl, sl, bt, kv) if window is None else mk.window_attention(sh, q, cl, sl, bt, kv, window)
+    # 2^18 positions are added up in one place, 8 at a time, each of which cuts off less than 2^-23 of a sum that is half of
+    # its last on average: 2^-9; the output rounds to 2^-8
+    assert torch.all((out.double() - 1.3359375).abs() <= 1.3359375 * (2.0 ** -8 + 2.0 ** -9))
+
+
 # ---------------------------------------------------------------- shared prefixes
 PREFIX_SHAPES = [
     # hq, hkv, d, ps, groups, shared, own lengths (repeated), news (repeated)
