@@ -131,18 +131,18 @@ struct SegmentWalk {
 template <class Plan>
 size_t fold_floats(const Plan& pl, const ChunkSeqs& q, int head_dim) {
   Segment g;
-  bool any = false;
-  if (!pl.ranged) {                  // (a window's last unit may have some tiles fewer than the others)
-    if constexpr (Plan::kSpans) {
-      for (int i = 0; i < pl.n; ++i) {
-        unit_of(pl, i, pl.e[i].units - 1, 0, g);
-        any |= g.tiles + 3 > kFoldTiles;
-      }
-    } else if (pl.items > 0) {
-      item_of(pl, q, 0, g);
-      any = g.tiles > kFoldTiles;
+  bool any = false;                  // an item is so long
+  if constexpr (Plan::kSpans) {      // (a window's last unit may have three tiles fewer than the others)
+    for (int i = 0; i < pl.n; ++i) {
+      unit_of(pl, i, pl.e[i].units - 1, 0, g);
+      any |= g.tiles + 3 > kFoldTiles;
     }
-  } else {
+  } else if (pl.items > 0) {
+    item_of(pl, q, 0, g);
+    any = g.tiles > kFoldTiles;
+  }
+  if (any && pl.ranged) {            // and what a block has of it
+    any = false;
     for (int b = 0; b < pl.blocks && !any; ++b) {
       SegmentWalk walk(pl, b);
       while (!any && walk.next(pl, q, g)) any = (g.two ? g.n : (g.n + 1) / 2) > kFoldTiles;

@@ -461,3 +461,23 @@ def test_schedule_refuses_arguments_that_do_not_pair_up():
             mk.plan_span_attention(sh, [1, 1], [5, 6], **kw)
         assert e.value.code == BAD and "whole number" in str(e.value)
     assert len(mk.plan_span_attention(sh, [1, 1], [5, 6], window=3)) == len(mk.plan_span_attention(sh, [1, 1], [5, 6], group_seqs=[2], prefix_lens=[0]))
+
+
+def test_long_segments_have_room_for_their_sums():
+    # more than 2048 position tiles of one row's in a segment: the workspace has [2][128][D + 4] floats for every block, and
+    # without such segments nothing of the kind
+    sh, long = shape(num_q_heads=32, num_kv_heads=4, max_pages_per_seq=1 << 20), 0
+    for cl, sl, w in (([4000], [1 << 18], 1 << 20), ([4000], [(1 << 18) + 129], 1 << 20), ([5000], [1 << 20], 1 << 20), ([1], [1 << 23], 1 << 23),
+                      ([1] * 64, [1 << 19] * 64, 1 << 20), ([4000], [1 << 20], 1 << 17), ([4000] * 2, [1 << 20] * 2, 300000),
+                      ([1] * 64, [1 << 19] * 64, 200000)):
+        segs = segments(sh, cl, sl, window=w)
+        most = max(g["n"] if g["ntok"] > 16 or g["pair"] else (g["n"] + 1) // 2 for g in segs)
+        cut = max((g["slot"] for g in segs if g["slot"] < WHOLE), default=-1)
+        rows = max(min(g["ntok"], 32) << g["pair"] for g in segs) * 8
+        blocks = len({g["block"] for g in segs})
+        parts = 0 if cut < 0 else 2 * blocks * rows * 132 * 4
+        folds = blocks * 2 * 128 * 132 * 4
+        need = mk.window_attention_workspace(sh, cl, sl, w)
+        long += most > 2048
+        assert need == parts + (folds if most > 2048 else 0) or (most > 2045 and need == parts + folds), (cl, sl, w, need, parts, folds)
+    assert long >= 3
